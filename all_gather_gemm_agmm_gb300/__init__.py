@@ -379,3 +379,7 @@ def all_gather_matmul(xs, y, my_id: int = 0, rhs_transpose: bool = False, out=No
         return out, xcat
     (plan.run_unfused if unfused else plan.run)(xs, y, out, my_id, workspace, stream)
     return out
+
+
+from .attention import (NormRopePlan, PromptPlan, TreePlan, prompt_attention, qkv_norm_rope,  # noqa: E402,F401
+                        rotary_axes, tree_attention, tree_mask)

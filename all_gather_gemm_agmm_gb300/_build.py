@@ -1,7 +1,8 @@
 """Build the sm_103a shared library ``libagmm.so`` in-tree with nvcc.
 
 The translation units (kernel variants in three groups, selection and launch,
-C ABI, allocation-free entry point) compile in parallel to objects under
+C ABI, allocation-free entry point; the attention operators' kernels and C ABI)
+compile in parallel to objects under
 ``_build/`` and link, with the CUDA runtime linked statically, into
 ``all_gather_gemm_agmm_gb300/libagmm.so``.  No cmake, one ``-gencode``.
 """
@@ -16,11 +17,13 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_ATTENTION = os.path.join(PKG, "csrc_attention")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libagmm.so")
 SOURCES = ["agmm_select_rows_a1.cu", "agmm_select_rows_a2.cu", "agmm_select_swap.cu", "agmm_kernels.cu",
            "agmm_api.cpp", "agmm_noalloc.cu"]
+ATTENTION_SOURCES = ["norm_rope.cu", "attn_simple.cu", "attn_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,8 +35,7 @@ def _nvcc() -> str:
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "agmm.h"))
+    files = [os.path.join(d, f) for d in (CSRC, CSRC_ATTENTION, INCLUDE) for f in os.listdir(d)]
     files.append(os.path.abspath(__file__))
     return files
 
@@ -50,13 +52,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
-    common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
+    common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-I", CSRC_ATTENTION]
     if ptxas_info:
         common += ["-Xptxas", "-v"]
 
     def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-        cmd = [nvcc] + common + ["-c", os.path.join(CSRC, src), "-o", obj]
+        obj = os.path.join(BUILD_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
+        cmd = [nvcc] + common + ["-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -66,8 +68,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
+    sources = [os.path.join(CSRC, f) for f in SOURCES] + [os.path.join(CSRC_ATTENTION, f) for f in ATTENTION_SOURCES]
+    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        objs = list(ex.map(compile_one, sources))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "--cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
