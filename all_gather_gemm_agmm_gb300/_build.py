@@ -23,7 +23,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libagmm.so")
 SOURCES = ["agmm_select_rows_a1.cu", "agmm_select_rows_a2.cu", "agmm_select_swap.cu", "agmm_kernels.cu",
            "agmm_api.cpp", "agmm_noalloc.cu"]
-ATTENTION_SOURCES = ["norm_rope.cu", "attn_simple.cu", "attn_api.cpp"]
+ATTENTION_SOURCES = ["norm_rope.cu", "attn_prompt.cu", "attn_tree.cu", "attn_launch.cu", "attn_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -47,7 +47,7 @@ class _TreeDesc(ctypes.Structure):
 # The *_args_t structs are 64-bit fields throughout, packed in one step.
 _NORM_ROPE_ARGS = struct.Struct("=23q")
 _PROMPT_ARGS = struct.Struct("=18q")
-_TREE_ARGS = struct.Struct("=21q")
+_TREE_ARGS = struct.Struct("=22q")
 
 _bound = None
 
@@ -354,7 +354,7 @@ class TreePlan(_AttentionPlan):
                 raise ValueError(f"mask must be contiguous int64 [{tokens}, words] on {self.device}")
             m_ptr, words = mask.data_ptr(), mask.shape[1]
         args = _TREE_ARGS.pack(tokens, sequences, q_ptr, q_ts, q_hs, kc, vc, shape[0], c_ps, c_ts, c_hs,
-                               page_table.data_ptr(), table[1], c_ptr, n_ptr, m_ptr, words, o_ptr, o_ts, o_hs,
+                               page_table.data_ptr(), table[1], page_table.stride(0), c_ptr, n_ptr, m_ptr, words, o_ptr, o_ts, o_hs,
                                self._workspace(workspace))
         st = self._run(self._h, args, self._stream(stream))
         if st:

@@ -7,7 +7,11 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
+#include <mutex>
 #include <new>
+
+#include <cudaTypedefs.h>
 
 #include "agmm_attention.h"
 #include "attn_params.h"
@@ -30,13 +34,15 @@ struct AttnPlan {
   bool f16;
   float scale;
   int device, num_sms;
+  AttnFn kernel;
+  int pack, tile_tokens, partial_rows;
+  uint64_t wait_limit_cycles;
+  int test_drop;
 };
 struct agmm_prompt_s : AttnPlan {};
 struct agmm_tree_s : AttnPlan {};
 
 namespace {
-
-constexpr size_t kStatusBytes = 256;
 
 agmm_status_t fail(agmm_status_t s, const char* fmt, ...) {
   char text[256];
@@ -74,7 +80,7 @@ agmm_status_t check_attention(int q_heads, int kv_heads, int head_dim, int dtype
     return fail(AGMM_ERR_INVALID_ARG, "q_heads (%d) must be a multiple of kv_heads (%d)", q_heads, kv_heads);
   if (head_dim != 64 && head_dim != 128)
     return fail(AGMM_ERR_UNSUPPORTED, "head_dim must be 64 or 128: %d", head_dim);
-  if (!std::isfinite(scale)) return fail(AGMM_ERR_INVALID_ARG, "scale is not finite");
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return fail(AGMM_ERR_INVALID_ARG, "scale must be positive and finite");
   return AGMM_OK;
 }
 
@@ -105,6 +111,108 @@ int shift_of(int64_t v) {  // log2, or -1
   int s = 0;
   while ((int64_t)1 << s < v) ++s;
   return s;
+}
+
+// What both attention plans hold, from the checked description.
+agmm_status_t fill_plan(AttnPlan* pl, int q_heads, int kv_heads, int head_dim, agmm_dtype_t dtype, float scale, bool tree) {
+  pl->q_heads = q_heads;
+  pl->kv_heads = kv_heads;
+  pl->head_dim = head_dim;
+  pl->f16 = dtype == AGMM_F16;
+  pl->scale = scale;
+  pl->pack = tree ? q_heads / kv_heads : 1;
+  pl->tile_tokens = kRows / pl->pack;
+  pl->kernel = tree ? tree_kernel(head_dim, pl->f16) : prompt_kernel(head_dim, pl->f16);
+  int khz = 0;
+  if (cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, pl->device) != cudaSuccess || khz <= 0) {
+    (void)cudaGetLastError();
+    khz = 2100000;  // above the part's 2.07 GHz peak
+  }
+  const char* ms = std::getenv("AGMM_WAIT_LIMIT_MS");
+  const int limit = ms && *ms ? std::atoi(ms) : 0;
+  pl->wait_limit_cycles = (uint64_t)(limit > 0 ? limit : 2000) * (uint64_t)khz;
+  const char* drop = std::getenv("AGMM_TEST_DROP_ARRIVE");
+  pl->test_drop = drop && std::atoi(drop) != 0;
+  const cudaError_t e = prepare_attention(pl->kernel);
+  if (e != cudaSuccess) return fail(AGMM_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(e));
+  return AGMM_OK;
+}
+
+// The plan's fields of a launch, and the Q tiles' tensor map.
+void fill_params(const AttnPlan* pl, AttnParams* p, void* workspace) {
+  p->q_heads = pl->q_heads;
+  p->kv_heads = pl->kv_heads;
+  p->group = pl->q_heads / pl->kv_heads;
+  p->pack = pl->pack;
+  p->tile_tokens = pl->tile_tokens;
+  p->scale_log2 = (float)((double)pl->scale * 1.4426950408889634074);  // log2(e)
+  p->wait_limit_cycles = pl->wait_limit_cycles;
+  p->test_drop_first_load = pl->test_drop;
+  p->status = static_cast<int*>(workspace);
+  p->counter = reinterpret_cast<int*>(static_cast<char*>(workspace) + kCounterOffset);
+}
+
+// Where the join records of a tree's workspace end and its partial results begin.
+size_t joins_end(const AttnPlan* pl) {
+  return (kAttnStatusBytes + (size_t)pl->num_sms * kJoinInts * sizeof(int) + 255) / 256 * 256;
+}
+
+agmm_status_t check_plan_device(int device) {
+  int now = -1;
+  const cudaError_t e = cudaGetDevice(&now);
+  if (e != cudaSuccess) return fail(AGMM_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (now != device) return fail(AGMM_ERR_INVALID_ARG, "the plan belongs to device %d, the current device is %d", device, now);
+  return AGMM_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A tensor map of 16-bit values whose boxes are 64 columns wide, 128-byte
+// swizzled, zero-filled outside.  dims, box: innermost first; strides of the
+// dimensions after the first, in elements.
+agmm_status_t encode(CUtensorMap* map, const char* name, const void* ptr, int rank, const int64_t* dims, const int64_t* strides,
+                     const int* box, bool f16) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(AGMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], es[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    es[i] = 1;
+    // a dimension of one value has no stride to speak of; the map wants some
+    if (i) st[i - 1] = (cuuint64_t)((dims[i] == 1 ? dims[0] : strides[i - 1]) * 2);
+  }
+  const CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                         const_cast<void*>(ptr), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(AGMM_ERR_CUDA, "tensor map of %s: cuTensorMapEncodeTiled gave %d", name, (int)r);
+  return AGMM_OK;
+}
+
+agmm_status_t encode_q(CUtensorMap* map, const AttnPlan* pl, const void* q, int64_t tokens, int64_t ts, int64_t hs) {
+  const int64_t dims[3] = {pl->head_dim, pl->q_heads, tokens}, strides[2] = {hs, ts};
+  const int box[3] = {64, pl->pack, pl->tile_tokens};
+  return encode(map, "q", q, 3, dims, strides, box, pl->f16);
+}
+
+// Keys or values: rows (tokens, or the places of a page), heads, pages.
+agmm_status_t encode_kv(CUtensorMap* map, const char* name, const AttnPlan* pl, const void* x, int64_t rows, int64_t pages,
+                        int64_t ts, int64_t hs, int64_t ps, int box_rows) {
+  const int64_t dims[4] = {pl->head_dim, rows, pl->kv_heads, pages}, strides[3] = {ts, hs, ps};
+  const int box[4] = {64, box_rows, 1, 1};
+  return encode(map, name, x, 4, dims, strides, box, pl->f16);
 }
 
 agmm_status_t launched(cudaError_t e, const char* what) {
@@ -176,6 +284,7 @@ agmm_status_t agmm_norm_rope_run(agmm_norm_rope_t plan, const agmm_norm_rope_arg
     AGMM_TRY(check_pointer("q_weight", a->q_weight, 16));
     AGMM_TRY(check_pointer("k_weight", a->k_weight, 16));
   }
+  AGMM_TRY(check_plan_device(plan->device));
   NormRopeParams p = plan->params;
   if (p.pairs) {
     if (a->position_bytes != 4 && a->position_bytes != 8)
@@ -233,21 +342,21 @@ agmm_status_t agmm_prompt_plan(const agmm_prompt_desc_t* d, agmm_prompt_t* out) 
   AGMM_TRY(check_device(&device, &sms));
   agmm_prompt_s* pl = new (std::nothrow) agmm_prompt_s();
   if (!pl) return fail(AGMM_ERR_NOMEM, "plan allocation");
-  pl->q_heads = d->q_heads;
-  pl->kv_heads = d->kv_heads;
-  pl->head_dim = d->head_dim;
   pl->causal = d->causal != 0;
-  pl->f16 = d->dtype == AGMM_F16;
-  pl->scale = d->scale;
   pl->device = device;
   pl->num_sms = sms;
+  const agmm_status_t st = fill_plan(pl, d->q_heads, d->kv_heads, d->head_dim, d->dtype, d->scale, false);
+  if (st != AGMM_OK) {
+    delete pl;
+    return st;
+  }
   *out = pl;
   return AGMM_OK;
 }
 
 void agmm_prompt_destroy(agmm_prompt_t plan) { delete plan; }
 
-size_t agmm_prompt_workspace_bytes(agmm_prompt_t plan) { return plan ? kStatusBytes : 0; }
+size_t agmm_prompt_workspace_bytes(agmm_prompt_t plan) { return plan ? kAttnStatusBytes : 0; }
 
 agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, void* stream) {
   if (!plan || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
@@ -264,29 +373,33 @@ agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, v
   AGMM_TRY(check_pointer("starts", a->starts, 4));
   if (a->kv_starts) AGMM_TRY(check_pointer("kv_starts", a->kv_starts, 4));
   AGMM_TRY(check_pointer("workspace", a->workspace, 16));
+  // row-tile pairs there can be, and items
+  const int64_t pairs = a->tokens / (2 * kRows) + (a->sequences < a->tokens ? a->sequences : a->tokens);
+  if (pairs * plan->q_heads >= INT_MAX / 2)
+    return fail(AGMM_ERR_UNSUPPORTED, "too many rows for one run: %lld tokens of %d heads", (long long)a->tokens, plan->q_heads);
+  AGMM_TRY(check_plan_device(plan->device));
   AttnParams p = {};
-  p.q = static_cast<const uint16_t*>(a->q);
-  p.k = static_cast<const uint16_t*>(a->k);
+  fill_params(plan, &p, a->workspace);
+  AGMM_TRY(encode_q(&p.qmap, plan, a->q, a->tokens, a->q_token_stride, a->q_head_stride));
+  if (a->kv_tokens) {
+    AGMM_TRY(encode_kv(&p.kmap, "k", plan, a->k, a->kv_tokens, 1, a->k_token_stride, a->k_head_stride, 0, kKeys));
+    AGMM_TRY(encode_kv(&p.vmap, "v", plan, a->v, a->kv_tokens, 1, a->v_token_stride, a->v_head_stride, 0, kKeys));
+  }
   p.v = static_cast<const uint16_t*>(a->v);
+  p.v_ts = a->v_token_stride;
+  p.v_hs = a->v_head_stride;
   p.out = static_cast<uint16_t*>(a->out);
+  p.out_ts = a->out_token_stride;
+  p.out_hs = a->out_head_stride;
   p.starts = a->starts;
   p.kv_starts = a->kv_starts ? a->kv_starts : a->starts;
   p.tokens = a->tokens;
   p.kv_tokens = a->kv_tokens;
-  p.sequences = a->sequences;
-  p.q_ts = a->q_token_stride;
-  p.q_hs = a->q_head_stride;
-  p.k_ts = a->k_token_stride;
-  p.k_hs = a->k_head_stride;
-  p.v_ts = a->v_token_stride;
-  p.v_hs = a->v_head_stride;
-  p.out_ts = a->out_token_stride;
-  p.out_hs = a->out_head_stride;
-  p.q_heads = plan->q_heads;
-  p.kv_heads = plan->kv_heads;
+  p.sequences = (int)a->sequences;
   p.causal = plan->causal;
-  p.scale = plan->scale;
-  return launched(launch_attention(p, plan->head_dim, plan->f16, false, static_cast<cudaStream_t>(stream)), "prompt");
+  const int64_t items = pairs * plan->q_heads;
+  const int ctas = (int)(items < plan->num_sms ? items : plan->num_sms);
+  return launched(launch_attention(plan->kernel, p, ctas, static_cast<cudaStream_t>(stream)), "prompt");
 }
 
 // ----------------------------------------------------------------------- tree
@@ -304,23 +417,28 @@ agmm_status_t agmm_tree_plan(const agmm_tree_desc_t* d, agmm_tree_t* out) {
   AGMM_TRY(check_device(&device, &sms));
   agmm_tree_s* pl = new (std::nothrow) agmm_tree_s();
   if (!pl) return fail(AGMM_ERR_NOMEM, "plan allocation");
-  pl->q_heads = d->q_heads;
-  pl->kv_heads = d->kv_heads;
-  pl->head_dim = d->head_dim;
   pl->causal = 1;
   pl->page_size = d->page_size;
   pl->max_nodes = d->max_nodes;
-  pl->f16 = d->dtype == AGMM_F16;
-  pl->scale = d->scale;
   pl->device = device;
   pl->num_sms = sms;
+  const agmm_status_t st = fill_plan(pl, d->q_heads, d->kv_heads, d->head_dim, d->dtype, d->scale, true);
+  if (st != AGMM_OK) {
+    delete pl;
+    return st;
+  }
+  pl->partial_rows = (d->max_nodes < 2 * pl->tile_tokens ? d->max_nodes : 2 * pl->tile_tokens) * pl->pack;
   *out = pl;
   return AGMM_OK;
 }
 
 void agmm_tree_destroy(agmm_tree_t plan) { delete plan; }
 
-size_t agmm_tree_workspace_bytes(agmm_tree_t plan) { return plan ? kStatusBytes : 0; }
+size_t agmm_tree_workspace_bytes(agmm_tree_t plan) {
+  if (!plan) return 0;
+  const size_t slots = (size_t)plan->num_sms * 2 * plan->partial_rows;
+  return joins_end(plan) + slots * ((size_t)plan->head_dim + 2) * sizeof(float);
+}
 
 agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* stream) {
   if (!plan || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
@@ -332,7 +450,8 @@ agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* s
   AGMM_TRY(check_operand("k_cache", a->k_cache, a->cache_token_stride, a->cache_head_stride));
   AGMM_TRY(check_operand("v_cache", a->v_cache, a->cache_page_stride, a->cache_head_stride));
   AGMM_TRY(check_range("pages", a->pages, 1, INT_MAX));
-  AGMM_TRY(check_range("table_stride", a->table_stride, 1, INT_MAX / plan->page_size));
+  AGMM_TRY(check_range("table_pages", a->table_pages, 1, INT_MAX / plan->page_size));
+  AGMM_TRY(check_range("table_stride", a->table_stride, 0, (int64_t)1 << 38));
   AGMM_TRY(check_pointer("page_table", a->page_table, 4));
   AGMM_TRY(check_pointer("context_lens", a->context_lens, 4));
   AGMM_TRY(check_pointer("node_starts", a->node_starts, 4));
@@ -341,34 +460,42 @@ agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* s
     AGMM_TRY(check_range("mask_words", a->mask_words, (plan->max_nodes + 63) / 64, 1 << 20));
   }
   AGMM_TRY(check_pointer("workspace", a->workspace, 16));
+  AGMM_TRY(check_plan_device(plan->device));
   AttnParams p = {};
-  p.q = static_cast<const uint16_t*>(a->q);
-  p.k = static_cast<const uint16_t*>(a->k_cache);
+  fill_params(plan, &p, a->workspace);
+  const int box_rows = plan->page_size < kKeys ? plan->page_size : kKeys;
+  AGMM_TRY(encode_q(&p.qmap, plan, a->q, a->tokens, a->q_token_stride, a->q_head_stride));
+  AGMM_TRY(encode_kv(&p.kmap, "k_cache", plan, a->k_cache, plan->page_size, a->pages, a->cache_token_stride,
+                     a->cache_head_stride, a->cache_page_stride, box_rows));
+  AGMM_TRY(encode_kv(&p.vmap, "v_cache", plan, a->v_cache, plan->page_size, a->pages, a->cache_token_stride,
+                     a->cache_head_stride, a->cache_page_stride, box_rows));
   p.v = static_cast<const uint16_t*>(a->v_cache);
+  p.v_ts = a->cache_token_stride;
+  p.v_hs = a->cache_head_stride;
+  p.v_ps = a->cache_page_stride;
   p.out = static_cast<uint16_t*>(a->out);
+  p.out_ts = a->out_token_stride;
+  p.out_hs = a->out_head_stride;
   p.starts = a->node_starts;
   p.context_lens = a->context_lens;
   p.page_table = a->page_table;
-  p.mask = a->mask;
-  p.tokens = a->tokens;
-  p.sequences = a->sequences;
-  p.q_ts = a->q_token_stride;
-  p.q_hs = a->q_head_stride;
-  p.k_ts = a->cache_token_stride;
-  p.k_hs = a->cache_head_stride;
-  p.out_ts = a->out_token_stride;
-  p.out_hs = a->out_head_stride;
-  p.page_stride = a->cache_page_stride;
+  p.table_pages = a->table_pages;
   p.table_stride = a->table_stride;
   p.pages = a->pages;
-  p.mask_words = (int)a->mask_words;
   p.page_shift = shift_of(plan->page_size);
-  p.q_heads = plan->q_heads;
-  p.kv_heads = plan->kv_heads;
+  p.mask = a->mask;
+  p.mask_words = (int)a->mask_words;
+  p.tokens = a->tokens;
+  p.sequences = (int)a->sequences;
   p.causal = 1;
   p.max_nodes = plan->max_nodes;
-  p.scale = plan->scale;
-  return launched(launch_attention(p, plan->head_dim, plan->f16, true, static_cast<cudaStream_t>(stream)), "tree");
+  p.partial_rows = plan->partial_rows;
+  char* const ws = static_cast<char*>(a->workspace);
+  p.joins = reinterpret_cast<int*>(ws + kAttnStatusBytes);
+  p.partial = reinterpret_cast<float*>(ws + joins_end(plan));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AGMM_TRY(launched(launch_attention(plan->kernel, p, plan->num_sms, s), "tree"));
+  return launched(launch_join(p, plan->head_dim, plan->f16, plan->num_sms, s), "tree join");
 }
 
 }  // extern "C"

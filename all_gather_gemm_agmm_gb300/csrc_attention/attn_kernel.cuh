@@ -1,0 +1,963 @@
+// attn_kernel.cuh -- the attention kernel: packed prompts, and drafted tokens
+// over a paged cache.
+//
+//   out_i = sum_j softmax_j(scale * q_i . k_j) v_j   over the keys j that row i sees
+//
+// in one pass over the keys: S = Q K^T for a tile of 128 rows and 128 keys, p =
+// 2^(c s - c m) with a reference m for each row, O += P V, l += sum p, and O /
+// l at the end.  m is the running maximum, but it follows only when it has grown by
+// more than 2^8 (the weights stay exact to their own rounding up to there, in
+// 16 bits as in 32), so the rescaling of O, a round trip through tensor
+// memory, is rare after the first keys.
+//
+// One persistent CTA per SM.  Two "streams" of 128 query rows each, so that
+// the tensor cores work on one while the other's weights are computed:
+//   warps 0-3, 4-7  the softmax of stream 0 and 1: a thread owns a row; S comes
+//                   from tensor memory, P goes back there (over S, as 16-bit
+//                   pairs) and is the second product's A operand;
+//   warp 8          TMA loads of Q tiles and of a ring of K and V tiles;
+//   warp 9          issues tcgen05.mma, P V of a tile and Q K^T of the next for
+//                   one stream, then for the other;
+//   warp 10         decides the work items.
+// Tensor memory (512 columns): S of both streams, O of both.
+//
+// A work item is paired (the streams hold two row tiles and share every key
+// tile) or, where there is one row tile only, alternating (the streams hold the
+// same rows and take even and odd key tiles; their sums are joined at the end).
+//
+// Prompts: an item is 256 rows of a sequence and a head, taken from a counter,
+// long ones first.  Trees: a tile packs the heads of a group (row = token *
+// group + head), so that each key is read once for all of them; the key tiles of
+// all (sequence, key head, rows) are laid out in a line that the CTAs cut into
+// equal parts.  A part that covers only some of its keys leaves O, m and l in
+// device memory, and attn_join sums the parts in order.
+//
+// What a row does not see never reaches it: its scores are replaced, not
+// added to; value rows past the end are cleared in shared memory; and in a
+// tile that only some rows see, values that are not finite are taken out of the
+// product and added at the end to the rows that see them.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_params.h"
+#include "attn_ptx.cuh"
+
+namespace agmm {
+namespace {
+
+constexpr int kItemSlots = 4;
+constexpr float kMaxGrowth = 8.0f;  // log2 of how far the weights may grow past 1
+
+template <int kD>
+struct Layout {
+  static constexpr int kHalves = kD / 64;                      // 64-column (128-byte) pieces of a row
+  static constexpr uint32_t kTileBytes = kRows * kD * 2;        // a Q, K or V tile
+  static constexpr uint32_t kHalfBytes = kRows * 128;           // its 64-column piece
+  static constexpr int kStages = kD == 128 ? 5 : 10;
+  static constexpr uint32_t kRing = 2 * kTileBytes;
+  static constexpr uint32_t kCtl = kRing + kStages * kTileBytes;
+  // control block
+  static constexpr uint32_t kBars = kCtl;
+  static constexpr uint32_t kItems = kCtl + 344;                // kItemSlots x 96 bytes
+  static constexpr uint32_t kFlags = kItems + kItemSlots * 96;  // abort, TMEM base, non-finite flag
+  static constexpr uint32_t kStats = kFlags + 16;               // [2 streams][128 rows][2] float
+  static constexpr size_t kBytes = kStats + 2 * 128 * 2 * 4;
+  static_assert(kBytes <= 232448, "more shared memory than a CTA can have");
+};
+
+struct Bars {
+  uint32_t base;
+  int stages;
+  __device__ __forceinline__ uint32_t full(int s) const { return base + 8 * s; }
+  __device__ __forceinline__ uint32_t empty(int s) const { return base + 8 * (10 + s); }
+  __device__ __forceinline__ uint32_t q_full(int x) const { return base + 8 * (20 + x); }
+  __device__ __forceinline__ uint32_t q_empty(int x) const { return base + 8 * (22 + x); }
+  __device__ __forceinline__ uint32_t s_full(int s) const { return base + 8 * (24 + s); }
+  __device__ __forceinline__ uint32_t p_ready(int s) const { return base + 8 * (26 + s); }
+  __device__ __forceinline__ uint32_t pv_done(int s) const { return base + 8 * (28 + s); }
+  __device__ __forceinline__ uint32_t o_free(int s) const { return base + 8 * (30 + s); }
+  __device__ __forceinline__ uint32_t item_full(int i) const { return base + 8 * (32 + i); }
+  __device__ __forceinline__ uint32_t item_empty(int i) const { return base + 8 * (36 + i); }
+  __device__ __forceinline__ uint32_t stats() const { return base + 8 * 40; }
+  __device__ __forceinline__ uint32_t drained() const { return base + 8 * 41; }
+};
+
+// A work item, written by the scheduler warp.
+struct __align__(8) Item {
+  int valid;
+  int alternate;    // the streams share the rows and take key tiles in turn
+  int n[2];         // key tiles of each stream
+  int tiles;        // key tiles loaded
+  int kv_tile;      // first of them in the sequence
+  int kv_len;       // keys of the sequence
+  int kv_row;       // prompts: its first key row
+  int seq;
+  int kv_head, head;  // head: of the tile's first row
+  int q0, q_len;      // the sequence's first query row, and how many
+  int off;            // row i sees keys below i + off + 1 (causal, chains); trees: the context
+  int tok[2], cnt[2];  // each stream's first token in the sequence, and how many
+  int slot;            // -1: the whole result; else where the partial one goes
+  int masked_from;     // the first place that not all rows see
+};
+static_assert(sizeof(Item) <= 96, "item slot too small");
+
+// Ring positions of an item's key and value tiles.  The tiles are loaded in the
+// order in which the MMA warp first waits for them: keys run `lead` tiles ahead.
+__device__ __forceinline__ int k_index(int t, int lead) { return t + max(0, t - lead); }
+__device__ __forceinline__ int v_index(int t, int lead, int tiles) { return t + min(t + 1 + lead, tiles); }
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------ scheduler
+struct Sequence {
+  int q0, q_len, kv_row, kv_len, off;
+};
+
+template <bool kPaged>
+__device__ __forceinline__ Sequence sequence_of(const AttnParams& p, int s) {
+  Sequence x;
+  const int64_t a = min(max((int64_t)__ldg(p.starts + s), (int64_t)0), p.tokens);
+  const int64_t b = min(max((int64_t)__ldg(p.starts + s + 1), a), p.tokens);
+  x.q0 = (int)a;
+  x.q_len = (int)(b - a);
+  if constexpr (kPaged) {
+    x.q_len = min(x.q_len, p.max_nodes);
+    const int64_t most = p.table_pages << p.page_shift;
+    const int64_t ctx = max(__ldg(p.context_lens + s), 0);
+    x.kv_row = 0;
+    x.kv_len = (int)min(ctx + x.q_len, most);
+    x.off = (int)min(ctx, most);
+  } else {
+    const int64_t c = min(max((int64_t)__ldg(p.kv_starts + s), (int64_t)0), p.kv_tokens);
+    const int64_t d = min(max((int64_t)__ldg(p.kv_starts + s + 1), c), p.kv_tokens);
+    x.kv_row = (int)c;
+    x.kv_len = (int)(d - c);
+    x.off = x.kv_len - x.q_len;
+  }
+  return x;
+}
+
+// Prompts: the key tiles that the rows before token `end` need.
+__device__ __forceinline__ int key_tiles(const AttnParams& p, const Sequence& x, int end) {
+  return ceil_div(p.causal ? min(x.kv_len, max(end + x.off, 0)) : x.kv_len, kKeys);
+}
+
+// An alternating item's key tiles: stream 0 takes the even ones.
+__device__ __forceinline__ void share_tiles(Item& it) {
+  it.n[0] = (it.tiles + 1) / 2;
+  it.n[1] = it.tiles / 2;
+}
+
+__device__ __forceinline__ void fill_rows(const AttnParams& p, const Sequence& x, int tok, Item& it) {
+  it.tok[0] = tok;
+  it.cnt[0] = min(p.tile_tokens, x.q_len - tok);
+  it.alternate = x.q_len - tok <= p.tile_tokens;
+  it.tok[1] = it.alternate ? tok : tok + p.tile_tokens;
+  it.cnt[1] = it.alternate ? it.cnt[0] : min(x.q_len - it.tok[1], p.tile_tokens);
+  it.q0 = x.q0;
+  it.q_len = x.q_len;
+  it.kv_len = x.kv_len;
+  it.kv_row = x.kv_row;
+  it.off = x.off;
+}
+
+// Prompts: items in the order of their row tile's place in its sequence, last
+// ones first (they see the most keys), then by sequence, then by head.
+struct PromptWork {
+  int level, base, count;  // row-tile pairs `level` of all sequences have the ranks [base, base + count)
+  int total;               // row-tile pairs
+  int lane;
+
+  __device__ __forceinline__ int pairs_of(const AttnParams& p, int s) const {
+    const int64_t a = min(max((int64_t)__ldg(p.starts + s), (int64_t)0), p.tokens);
+    const int64_t b = min(max((int64_t)__ldg(p.starts + s + 1), a), p.tokens);
+    return (int)((b - a + 2 * kRows - 1) / (2 * kRows));
+  }
+  __device__ __forceinline__ void init(const AttnParams& p) {
+    lane = threadIdx.x & 31;
+    int most = 0, sum = 0;
+    for (int s = lane; s < p.sequences; s += 32) {
+      const int n = pairs_of(p, s);
+      most = max(most, n);
+      sum += n;
+    }
+    total = __reduce_add_sync(0xffffffffu, sum);
+    level = __reduce_max_sync(0xffffffffu, most);
+    base = count = 0;
+  }
+  // The sequence and row-tile pair of a rank; ranks come in rising order.
+  __device__ __forceinline__ void find(const AttnParams& p, int rank, int& seq, int& pair) {
+    while (rank >= base + count) {
+      base += count;
+      --level;
+      int c = 0;
+      for (int s = lane; s < p.sequences; s += 32) c += pairs_of(p, s) > level;
+      count = __reduce_add_sync(0xffffffffu, c);
+    }
+    int left = rank - base;
+    seq = 0;
+    pair = level;
+    for (int s0 = 0; s0 < p.sequences; s0 += 32) {
+      const int s = s0 + lane;
+      const uint32_t has = __ballot_sync(0xffffffffu, s < p.sequences && pairs_of(p, s) > level);
+      const int n = __popc(has);
+      if (left < n) {
+        seq = s0 + __fns(has, 0, left + 1);
+        return;
+      }
+      left -= n;
+    }
+  }
+};
+
+// Trees: key tiles of (sequence, key head, row tiles) in a line.
+struct TreeWork {
+  __device__ static __forceinline__ int row_sets(const AttnParams& p, const Sequence& x) {
+    return ceil_div(ceil_div(x.q_len, p.tile_tokens), 2);  // one tile, or pairs of tiles
+  }
+  __device__ static __forceinline__ int64_t units(const AttnParams& p, const Sequence& x) {
+    return x.q_len > 0 ? (int64_t)p.kv_heads * row_sets(p, x) * ceil_div(x.kv_len, kKeys) : 0;
+  }
+};
+
+template <bool kPaged>
+__device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars, Item* slots, const Waiter& wait) {
+  const int lane = threadIdx.x & 31;
+  int k = 0;
+  auto publish = [&](const Item& it) -> bool {
+    const int slot = k % kItemSlots;
+    if (k >= kItemSlots && !wait(bars.item_empty(slot), (uint32_t)(k / kItemSlots - 1) & 1u, k)) return false;
+    if (lane == 0) {
+      slots[slot] = it;
+      ptx::mbar_arrive(bars.item_full(slot));
+    }
+    ++k;
+    return true;
+  };
+  Item it = {};
+  it.valid = 1;
+  it.slot = -1;
+  if constexpr (!kPaged) {
+    PromptWork work;
+    work.init(p);
+    const int items = work.total * p.q_heads;
+    int next = blockIdx.x;
+    while (next < items) {
+      const int rank = next / p.q_heads;
+      it.head = next - rank * p.q_heads;
+      it.kv_head = it.head / p.group;
+      int pair;
+      work.find(p, rank, it.seq, pair);
+      const Sequence x = sequence_of<false>(p, it.seq);
+      fill_rows(p, x, pair * 2 * kRows, it);
+      it.n[0] = key_tiles(p, x, it.tok[0] + it.cnt[0]);
+      it.n[1] = key_tiles(p, x, it.tok[1] + it.cnt[1]);
+      it.tiles = max(it.n[0], it.n[1]);
+      if (it.alternate) share_tiles(it);
+      it.masked_from = p.causal ? min(x.kv_len, max(it.tok[0] + x.off + 1, 0)) : x.kv_len;
+      // The CTA that draws the last number puts the counter back to zero.
+      if (lane == 0) {
+        next = atomicAdd(p.counter, 1);
+        if (next == items - 1) atomicExch(p.counter, 0);
+        next += gridDim.x;
+      }
+      next = __shfl_sync(0xffffffffu, next, 0);
+      if (!publish(it)) return;
+    }
+  } else {
+    // the length of the line, then this CTA's part of it
+    int64_t sum = 0;
+    for (int s = lane; s < p.sequences; s += 32) sum += TreeWork::units(p, sequence_of<true>(p, s));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int64_t total = sum;
+    const int64_t parts = min((int64_t)gridDim.x, total);
+    int* const join = p.joins + (size_t)blockIdx.x * kJoinInts;
+    if (lane == 0) join[0] = 0;
+    if ((int64_t)blockIdx.x < parts) {
+      int64_t u = total * blockIdx.x / parts;
+      const int64_t hi = total * (blockIdx.x + 1) / parts;
+      // the sequence that u lies in
+      int seq = 0;
+      int64_t first = 0;  // its first unit
+      for (int s0 = 0; s0 < p.sequences; s0 += 32) {
+        const int64_t mine = s0 + lane < p.sequences ? TreeWork::units(p, sequence_of<true>(p, s0 + lane)) : 0;
+        int64_t run = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, first + run > u);
+        if (past) {
+          const int at = __ffs(past) - 1;
+          seq = s0 + at;
+          first += __shfl_sync(0xffffffffu, run - mine, at);
+          break;
+        }
+        first += __shfl_sync(0xffffffffu, run, 31);
+      }
+      while (u < hi) {
+        const Sequence x = sequence_of<true>(p, seq);
+        const int64_t have = TreeWork::units(p, x);
+        if (u >= first + have) {  // on to the next sequence
+          first += have;
+          ++seq;
+          continue;
+        }
+        const int keys = ceil_div(x.kv_len, kKeys), sets = TreeWork::row_sets(p, x);
+        const int64_t in = u - first;
+        const int t0 = (int)(in % keys);
+        const int which = (int)(in / keys);
+        const int set = which % sets, head = which / sets;
+        const int t1 = (int)min((int64_t)keys, t0 + (hi - u));
+        it.seq = seq;
+        it.kv_head = head;
+        it.head = head * p.group;
+        fill_rows(p, x, set * 2 * p.tile_tokens, it);
+        it.kv_tile = t0;
+        it.tiles = it.n[0] = it.n[1] = t1 - t0;
+        if (it.alternate) share_tiles(it);
+        it.masked_from = p.mask ? min(x.off, x.kv_len) : min(x.kv_len, it.tok[0] + x.off + 1);
+        const bool whole = t0 == 0 && t1 == keys;
+        it.slot = whole ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
+        if (!whole && t0 == 0 && lane == 0) {
+          // this CTA holds the first keys of an item that goes on: the record of its join
+          const int64_t end = u - t0 + keys;  // unit after the item's last
+          join[1] = (int)((end * parts - 1) / total);  // the CTA of its last unit
+          join[2] = x.q0 + it.tok[0];
+          join[3] = (it.alternate ? it.cnt[0] : it.cnt[0] + it.cnt[1]) * p.pack;  // rows
+          join[4] = it.head;
+          join[0] = 1;
+        }
+        u += it.tiles;
+        if (!publish(it)) return;
+      }
+    }
+  }
+  Item end = {};
+  publish(end);
+}
+
+// ------------------------------------------------------------------- producer
+template <int kD, bool kPaged>
+__device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, const Item* slots, uint32_t smem,
+                                         const Waiter& wait) {
+  using L = Layout<kD>;
+  const int lane = threadIdx.x & 31;
+  uint32_t fills = 0;
+  uint32_t q_uses[2] = {0, 0};
+  bool drop = p.test_drop_first_load != 0;
+  const int page_rows = kPaged ? min(1 << p.page_shift, kKeys) : kKeys;
+  const int pages_per_tile = kKeys / page_rows;
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % kItemSlots;
+    if (!wait(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
+    const Item it = slots[slot];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bars.item_empty(slot));
+    if (!it.valid) break;
+    if (it.tiles == 0) continue;
+    for (int s = 0; s < 2 && ok; ++s) {
+      if (s == 1 && it.alternate) break;
+      if (it.n[s] == 0) continue;
+      ok = wait(bars.q_empty(s), (q_uses[s] & 1u) ^ 1u, 1000 + s);
+      if (!ok) break;
+      ++q_uses[s];
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)(p.tile_tokens * p.pack) * 128u;
+        ptx::mbar_arrive_expect_tx(bars.q_full(s), bytes * L::kHalves);
+#pragma unroll
+        for (int h = 0; h < L::kHalves; ++h)
+          ptx::tma_load_3d(smem + s * L::kTileBytes + h * L::kHalfBytes, &p.qmap, bars.q_full(s), h * 64, it.head,
+                           it.q0 + it.tok[s]);
+      }
+      __syncwarp();
+    }
+    if (!ok) break;
+    const int lead = it.alternate ? 2 : 1;
+    // loads in ring order: key tile t + lead, value tile t
+    auto load = [&](const CUtensorMap* map, int t) -> bool {
+      const int st = (int)(fills % L::kStages);
+      if (!wait(bars.empty(st), ((fills / L::kStages) & 1u) ^ 1u, 2000 + st)) return false;
+      ++fills;
+      const uint32_t dst = smem + L::kRing + st * L::kTileBytes, bar = bars.full(st);
+      const int place = (it.kv_tile + t) * kKeys;
+      if (drop) {  // test hook
+        drop = false;
+        return true;
+      }
+      if constexpr (kPaged) {
+        const int mine = place + lane * page_rows;
+        const bool there = lane < pages_per_tile && mine < it.kv_len;
+        const int n = __popc(__ballot_sync(0xffffffffu, there));
+        int page = 0;
+        if (there) page = __ldg(p.page_table + it.seq * p.table_stride + (mine >> p.page_shift));
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(n * page_rows) * 128u * L::kHalves);
+        __syncwarp();
+        if (there) {
+#pragma unroll
+          for (int h = 0; h < L::kHalves; ++h)
+            ptx::tma_load_4d(dst + h * L::kHalfBytes + lane * page_rows * 128, map, bar, h * 64,
+                             mine & ((1 << p.page_shift) - 1), it.kv_head, page);
+        }
+      } else if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar, L::kTileBytes);
+#pragma unroll
+        for (int h = 0; h < L::kHalves; ++h)
+          ptx::tma_load_4d(dst + h * L::kHalfBytes, map, bar, h * 64, it.kv_row + place, it.kv_head, 0);
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int t = 0; t < lead && t < it.tiles && ok; ++t) ok = load(&p.kmap, t);
+    for (int t = 0; t < it.tiles && ok; ++t) {
+      if (t + lead < it.tiles) ok = load(&p.kmap, t + lead);
+      if (ok) ok = load(&p.vmap, t);
+    }
+  }
+  if (*wait.abort) {
+    // copies in flight end before the CTA does
+    for (int st = 0; st < L::kStages; ++st) {
+      if (p.test_drop_first_load && st == 0) continue;  // never filled
+      if (fills > (uint32_t)st) {  // its last fill
+        const uint32_t last = (fills - 1 - st) / L::kStages;
+        wait.drain(bars.full(st), last & 1u);
+      }
+    }
+    for (int s = 0; s < 2; ++s)
+      if (q_uses[s]) wait.drain(bars.q_full(s), (q_uses[s] - 1) & 1u);
+  }
+}
+
+// ------------------------------------------------------------------------ MMA
+template <int kD, bool kF16>
+__device__ __forceinline__ void mma_issuer(const AttnParams& p, const Bars& bars, const Item* slots, uint32_t smem,
+                                           uint32_t tmem, const Waiter& wait) {
+  using L = Layout<kD>;
+  const bool leader = ptx::elect_one();
+  constexpr uint32_t kIdescS = ptx::idesc_f16kind_f32(kRows, kKeys, false, false, kF16);
+  constexpr uint32_t kIdescO = ptx::idesc_f16kind_f32(kRows, kD, false, true, kF16);
+  uint32_t fills = 0;  // of earlier items
+  uint32_t q_uses[2] = {0, 0}, o_uses[2] = {0, 0}, steps[2] = {0, 0};
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % kItemSlots;
+    if (!wait(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
+    const Item it = slots[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bars.item_empty(slot));
+    if (!it.valid) break;
+    if (it.tiles == 0) continue;
+    const int lead = it.alternate ? 2 : 1;
+
+    // S = Q K^T of stream s, its key tile i
+    auto scores = [&](int s, int i) -> bool {
+      const int t = it.alternate ? 2 * i + s : i;
+      const int x = it.alternate ? 0 : s;
+      if (i == 0 && !wait(bars.q_full(x), q_uses[x] & 1u, 1000 + s)) return false;
+      const uint32_t f = fills + (uint32_t)k_index(t, lead);
+      const int st = (int)(f % L::kStages);
+      if (!wait(bars.full(st), (f / L::kStages) & 1u, 2000 + st)) return false;
+      ptx::tc_fence_after();
+      if (leader) {
+        const uint64_t a = ptx::smem_desc_sw128(smem + x * L::kTileBytes, 16u, 1024u);
+        const uint64_t b = ptx::smem_desc_sw128(smem + L::kRing + st * L::kTileBytes, 16u, 1024u);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          // 16 columns further: 32 bytes in the 128-byte row, then the next 64-column piece
+          const uint64_t step = (uint64_t)((kk / 4) * L::kHalfBytes + (kk % 4) * 32u) >> 4;
+          ptx::mma_bf16(tmem + s * kKeys, a + step, b + step, kIdescS, kk > 0);
+        }
+        const bool last_reader = it.alternate || s == 1 || it.n[1] <= t;
+        if (last_reader) ptx::mma_commit(bars.empty(st));
+        ptx::mma_commit(bars.s_full(s));
+        if (it.alternate ? t == it.tiles - 1 : i == it.n[s] - 1) ptx::mma_commit(bars.q_empty(x));
+      }
+      __syncwarp();
+      return true;
+    };
+    // O += P V of stream s, its key tile i
+    auto values = [&](int s, int i) -> bool {
+      const int t = it.alternate ? 2 * i + s : i;
+      const uint32_t f = fills + (uint32_t)v_index(t, lead, it.tiles);
+      const int st = (int)(f % L::kStages);
+      if (!wait(bars.full(st), (f / L::kStages) & 1u, 3000 + st)) return false;
+      if (i == 0) {
+        if (!wait(bars.o_free(s), (o_uses[s] & 1u) ^ 1u, 4000 + s)) return false;
+        ++o_uses[s];
+      }
+      if (!wait(bars.p_ready(s), steps[s] & 1u, 5000 + s)) return false;
+      ++steps[s];
+      ptx::tc_fence_after();
+      if (leader) {
+        const uint64_t b = ptx::smem_desc_sw128(smem + L::kRing + st * L::kTileBytes, L::kHalfBytes, 1024u);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          ptx::mma_f16_ts(tmem + 2 * kKeys + s * kD, tmem + s * kKeys + kk * 8, b + (uint64_t)(kk * 2048u >> 4), kIdescO,
+                          i > 0 || kk > 0);
+        const bool last_reader = it.alternate || s == 1 || it.n[1] <= t;
+        if (last_reader) ptx::mma_commit(bars.empty(st));
+        ptx::mma_commit(bars.pv_done(s));
+      }
+      __syncwarp();
+      return true;
+    };
+
+    for (int s = 0; s < 2 && ok; ++s)
+      if (it.n[s] > 0) ok = scores(s, 0);
+    const int most = max(it.n[0], it.n[1]);
+    for (int i = 0; i < most && ok; ++i) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (i < it.n[s] && ok) {
+          ok = values(s, i);
+          if (ok && i + 1 < it.n[s]) ok = scores(s, i + 1);
+        }
+      }
+    }
+    fills += 2u * (uint32_t)it.tiles;
+    if (it.alternate) {
+      ++q_uses[0];
+    } else {
+      q_uses[0] += it.n[0] > 0;
+      q_uses[1] += it.n[1] > 0;
+    }
+  }
+  // every product issued has ended before the CTA does
+  if (leader) ptx::mma_commit(bars.drained());
+  __syncwarp();
+  wait.drain(bars.drained(), 0);
+}
+
+// -------------------------------------------------------------------- softmax
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kF16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <bool kF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (kF16)
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <bool kF16>
+__device__ __forceinline__ float value16(uint16_t b) {
+  if constexpr (kF16)
+    return __half2float(__ushort_as_half(b));
+  else
+    return __bfloat162float(__ushort_as_bfloat16(b));
+}
+
+// Bits [at, at + 32) of a row of mask words; at >= 0.
+__device__ __forceinline__ uint32_t mask_window(const int64_t* row, int words, int at) {
+  const int w = at >> 6, sh = at & 63;
+  if (w >= words) return 0;
+  uint64_t v = (uint64_t)__ldg(row + w) >> sh;
+  if (sh > 32 && w + 1 < words) v |= (uint64_t)__ldg(row + w + 1) << (64 - sh);
+  return (uint32_t)v;
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Which of the places [place, place + 32) a row sees.  `row` (trees with a
+// mask): its mask words; else `limit` is the first place that it does not see.
+__device__ __forceinline__ uint32_t seen32(const Item& it, const int64_t* row, int words, int limit, int place) {
+  if (row == nullptr) return low_bits(limit - place);
+  uint32_t bits = low_bits(it.off - place);
+  const int node = place - it.off;
+  if (node >= 0)
+    bits = mask_window(row, words, node);
+  else if (node > -32)
+    bits |= mask_window(row, words, 0) << -node;
+  return bits & low_bits(it.kv_len - place);
+}
+
+// One 16-byte piece of 16-bit values with those that are not finite set to 0.
+template <bool kF16>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  constexpr uint32_t kExp = kF16 ? 0x7c00u : 0x7f80u;
+  if ((w & kExp) == kExp) w &= 0xffff0000u;
+  if ((w >> 16 & kExp) == kExp) w &= 0x0000ffffu;
+  return w;
+}
+
+// Row r of a V tile (key `place`): cleared if it lies past the keys; else
+// values that are not finite are cleared and reported.
+template <int kD, bool kF16>
+__device__ __forceinline__ void clean_value_row(uint8_t* tile, int r, bool past, volatile int* flag) {
+  using L = Layout<kD>;
+  constexpr uint32_t kInf2 = kF16 ? 0x7c007c00u : 0x7f807f80u;
+#pragma unroll
+  for (int h = 0; h < L::kHalves; ++h) {
+    uint4* const row = reinterpret_cast<uint4*>(tile + h * L::kHalfBytes + r * 128);
+    if (past) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) row[(c + r) & 7] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 v = row[(c + r) & 7];
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                   __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    if (__vcmpgeu2(top, kInf2)) {
+      *flag = 1;
+      __threadfence_block();
+      for (int c = 0; c < 8; ++c) {
+        uint4 v = row[c];
+        v.x = finite_only<kF16>(v.x);
+        v.y = finite_only<kF16>(v.y);
+        v.z = finite_only<kF16>(v.z);
+        v.w = finite_only<kF16>(v.w);
+        row[c] = v;
+      }
+    }
+  }
+}
+
+// Adds to columns [col, col + 32) of a row the values that are not finite of
+// the places [from, to) that it sees: they were left out of the products there.
+template <bool kF16, bool kPaged>
+__device__ __noinline__ void add_not_finite(const AttnParams& p, const Item& it, const int64_t* row, int limit, int from,
+                                            int to, int col, float (&o)[32]) {
+  constexpr uint16_t kExp = kF16 ? 0x7c00u : 0x7f80u;
+  for (int place = from; place < to; ++place) {
+    if (!(seen32(it, row, p.mask_words, limit, place) & 1u)) continue;
+    const uint16_t* v;
+    if constexpr (kPaged) {
+      const int64_t page = __ldg(p.page_table + it.seq * p.table_stride + (place >> p.page_shift));
+      if (page < 0 || page >= p.pages) continue;
+      v = p.v + page * p.v_ps + (int64_t)(place & ((1 << p.page_shift) - 1)) * p.v_ts;
+    } else {
+      v = p.v + ((int64_t)it.kv_row + place) * p.v_ts;
+    }
+    v += it.kv_head * p.v_hs + col;
+    for (int c = 0; c < 32; ++c)
+      if ((v[c] & kExp) == kExp) o[c] += value16<kF16>(v[c]);
+  }
+}
+
+template <int kD, bool kF16, bool kPaged>
+__device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, const Item* slots, uint8_t* smem, uint32_t tmem,
+                                        const Waiter& wait, int s, float* stats, volatile int* flag) {
+  using L = Layout<kD>;
+  const int lane = threadIdx.x & 31;
+  const int r = threadIdx.x & 127;  // the row this thread owns
+  const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;  // its warp's quarter of the TMEM lanes
+  const uint32_t t_s = tmem + lanes + s * kKeys;
+  const uint32_t t_o = tmem + lanes + 2 * kKeys;
+  const float c = p.scale_log2;
+  uint32_t fills = 0, steps[2] = {0, 0};
+  uint32_t joint = 0;  // alternating items so far
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % kItemSlots;
+    if (!wait(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
+    const Item it = slots[slot];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bars.item_empty(slot));
+    if (!it.valid) break;
+    const int n = it.n[s];
+    const int lead = it.alternate ? 2 : 1;
+    const bool there = r < it.cnt[s] * p.pack;
+    const bool any = __any_sync(0xffffffffu, there);
+    const int token = it.tok[s] + (p.pack == 1 ? r : r / p.pack);
+    const int64_t* const mask_row =
+        kPaged && p.mask && there ? p.mask + (int64_t)(it.q0 + token) * p.mask_words : nullptr;
+    const bool masked = kPaged && p.mask != nullptr;
+    // the first place that this row does not see (rows under a mask: seen32)
+    int limit = it.kv_len;
+    if (!masked && p.causal) limit = min(limit, max(token + it.off + 1, 0));
+    if (masked && !there) limit = 0;
+    // tiles that end before this place are seen by all rows of the stream
+    const int clear = masked ? min(it.off, it.kv_len) : p.causal ? min(it.kv_len, max(it.tok[s] + it.off + 1, 0)) : it.kv_len;
+    float m = -INFINITY, l = 0.0f;
+
+    for (int i = 0; i < n; ++i) {
+      const int t = it.alternate ? 2 * i + s : i;
+      const int place = (it.kv_tile + t) * kKeys;
+      ok = wait(bars.s_full(s), (steps[s] + i) & 1u, 6000 + s);
+      if (!ok) break;
+      if (any) {
+        ptx::tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) ptx::tmem_ld_32x32b_x32(t_s + w * 32, v[w]);
+        ptx::tmem_ld_wait();
+        if (place + kKeys > clear) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = seen32(it, mask_row, p.mask_words, limit, place + 32 * w);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1u)) v[w][e] = 0xff800000u;  // -inf
+          }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            top[w] = fmaxf(fmaxf(top[w], __uint_as_float(v[w][e])), __uint_as_float(v[w][e + 1]));
+        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (i == 0) {
+          m = tile_top;
+        } else if (__any_sync(0xffffffffu, (tile_top - m) * c > kMaxGrowth)) {
+          const bool grows = (tile_top - m) * c > kMaxGrowth;  // also from -inf to anything
+          const float keep = grows ? ptx::exp2_approx((m - tile_top) * c) : 1.0f;
+          if (grows) m = tile_top;
+          l *= keep;
+          // the sums so far are complete once the last product with them is
+          ok = wait(bars.pv_done(s), (steps[s] + i - 1) & 1u, 7000 + s);
+          if (!ok) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int col = 0; col < kD; col += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld_32x32b_x16(t_o + s * kD + col, o);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+            ptx::tmem_st_32x32b_x16(t_o + s * kD + col, o);
+          }
+        }
+        const float shift = m == -INFINITY ? 0.0f : -m * c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int w = 2 * h + e / 16, x = 2 * (e % 16);
+            const float a = ptx::exp2_approx(fmaf(__uint_as_float(v[w][x]), c, shift));
+            const float b = ptx::exp2_approx(fmaf(__uint_as_float(v[w][x + 1]), c, shift));
+            pk[e] = pack2<kF16>(a, b);
+            const float2 back = unpack2<kF16>(pk[e]);
+            sum[e & 1] += back.x;
+            sum[2 + (e & 1)] += back.y;
+          }
+          ptx::tmem_st_32x32b_x32(t_s + h * 32, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        ptx::tmem_st_wait();
+      }
+      if (place + kKeys > clear) {
+        // the values of a tile that not all rows see
+        const uint32_t f = fills + (uint32_t)v_index(t, lead, it.tiles);
+        const int st = (int)(f % L::kStages);
+        ok = wait(bars.full(st), (f / L::kStages) & 1u, 8000 + st);
+        if (!ok) break;
+        clean_value_row<kD, kF16>(smem + L::kRing + st * L::kTileBytes, r, place + r >= it.kv_len, flag);
+        ptx::fence_proxy_async_smem();
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars.p_ready(s));
+    }
+    if (!ok) break;
+
+    // ---- the item's result
+    float scale0 = 0.0f, scale1 = 0.0f;  // of the streams' sums
+    int col0 = 0, col1 = kD;             // columns this thread writes
+    bool has0 = s == 0 && n > 0, has1 = s == 1 && n > 0;
+    if (n > 0) ok = wait(bars.pv_done(s), (steps[s] + n - 1) & 1u, 7100 + s);
+    if (!ok) break;
+    if (it.alternate) {
+      // The streams' maxima and sums change hands.  A stream that had keys has
+      // just seen its product end, which waited for all warps to be done with the
+      // item before: what it left here then has been read.
+      if (n > 0) *reinterpret_cast<float2*>(stats + 256 * s + 2 * r) = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars.stats());
+      ok = wait(bars.stats(), joint & 1u, 9000);
+      if (!ok) break;
+      ++joint;
+      float2 other = make_float2(-INFINITY, 0.0f);
+      if (it.n[s ^ 1] > 0) {
+        other = *reinterpret_cast<const float2*>(stats + 256 * (s ^ 1) + 2 * r);
+        ok = wait(bars.pv_done(s ^ 1), (steps[s ^ 1] + it.n[s ^ 1] - 1) & 1u, 7200 + s);
+        if (!ok) break;
+      }
+      const float both = fmaxf(m, other.x);
+      const float mine_w = m == -INFINITY ? (l != l ? 1.0f : 0.0f) : ptx::exp2_approx((m - both) * c);
+      const float other_w = other.x == -INFINITY ? (other.y != other.y ? 1.0f : 0.0f) : ptx::exp2_approx((other.x - both) * c);
+      l = l * mine_w + other.y * other_w;
+      m = both;
+      scale0 = s == 0 ? mine_w : other_w;
+      scale1 = s == 0 ? other_w : mine_w;
+      has0 = it.n[0] > 0;
+      has1 = it.n[1] > 0;
+      col0 = s * (kD / 2);
+      col1 = col0 + kD / 2;
+    } else {
+      scale0 = scale1 = 1.0f;
+    }
+    ptx::tc_fence_after();
+    __threadfence_block();
+    const bool repair = *flag != 0;
+    if (any) {
+      if (it.slot < 0) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        scale0 *= inv;
+        scale1 *= inv;
+      }
+      const int head = it.head + (p.pack == 1 ? 0 : r - (token - it.tok[s]) * p.pack);
+      uint16_t* const out = p.out + (int64_t)(it.q0 + token) * p.out_ts + head * p.out_hs;
+      const int row = (it.alternate ? 0 : s * p.tile_tokens * p.pack) + r;
+      float* const part = kPaged ? p.partial + ((size_t)it.slot * p.partial_rows + row) * kD : nullptr;
+      for (int col = col0; col < col1; col += 32) {
+        float o[32];
+        uint32_t a[32];
+        if (has0) {
+          ptx::tmem_ld_32x32b_x32(t_o + col, a);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(a[e]) * scale0;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+        }
+        if (has1) {
+          ptx::tmem_ld_32x32b_x32(t_o + kD + col, a);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(a[e]) * scale1;
+        }
+        if (repair && there) {
+          const int from = max(it.masked_from / kKeys, it.kv_tile) * kKeys;
+          const int to = min(it.kv_len, (it.kv_tile + it.tiles) * kKeys);
+          add_not_finite<kF16, kPaged>(p, it, mask_row, limit, from, to, col, o);
+        }
+        __syncwarp();
+        if (there) {
+          if (kPaged && it.slot >= 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(part + col + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(out + col + e) =
+                  make_uint4(pack2<kF16>(o[e], o[e + 1]), pack2<kF16>(o[e + 2], o[e + 3]),
+                             pack2<kF16>(o[e + 4], o[e + 5]), pack2<kF16>(o[e + 6], o[e + 7]));
+          }
+        }
+      }
+      if (kPaged && it.slot >= 0 && there && col0 == 0) {
+        float* const ml =
+            p.partial + (size_t)gridDim.x * 2 * p.partial_rows * kD + ((size_t)it.slot * p.partial_rows + row) * 2;
+        ml[0] = m;
+        ml[1] = l;
+      }
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (has0) ptx::mbar_arrive_n(bars.o_free(0), it.alternate ? 1 : 2);
+      if (has1) ptx::mbar_arrive_n(bars.o_free(1), it.alternate ? 1 : 2);
+    }
+    fills += 2u * (uint32_t)it.tiles;
+    steps[0] += it.n[0];
+    steps[1] += it.n[1];
+  }
+}
+
+// --------------------------------------------------------------------- kernel
+template <int kD, bool kF16, bool kPaged>
+__global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_constant__ AttnParams p) {
+  using L = Layout<kD>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t smem = ptx::smem_addr(raw);
+  uint8_t* const base = raw;
+  if (smem & 1023u) {  // the swizzled tiles need the alignment that `raw` asks for
+    if (threadIdx.x == 0 && atomicCAS(p.status, 0, 4) == 0) p.status[1] = 0;
+    return;
+  }
+  const Bars bars{smem + L::kBars, L::kStages};
+  Item* const slots = reinterpret_cast<Item*>(base + L::kItems);
+  int* const flags = reinterpret_cast<int*>(base + L::kFlags);  // [0] abort, [1] TMEM base, [2] values that are not finite were taken out
+  float* const stats = reinterpret_cast<float*>(base + L::kStats);
+
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_addr(&flags[1]), 512);
+    ptx::tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    flags[0] = flags[2] = 0;
+    for (int i = 0; i < L::kStages; ++i) {
+      ptx::mbar_init(bars.full(i), 1);
+      ptx::mbar_init(bars.empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars.q_full(i), 1);
+      ptx::mbar_init(bars.q_empty(i), 1);
+      ptx::mbar_init(bars.s_full(i), 1);
+      ptx::mbar_init(bars.p_ready(i), 4);
+      ptx::mbar_init(bars.pv_done(i), 1);
+      ptx::mbar_init(bars.o_free(i), 8);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      ptx::mbar_init(bars.item_full(i), 1);
+      ptx::mbar_init(bars.item_empty(i), 10);  // producer, MMA and eight softmax warps
+    }
+    ptx::mbar_init(bars.stats(), 8);
+    ptx::mbar_init(bars.drained(), 1);
+    ptx::fence_mbar_init();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = flags[1];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+
+  Waiter wait{flags, p.wait_limit_cycles, p.status, 3};
+  if (warp < 8) {
+    softmax<kD, kF16, kPaged>(p, bars, slots, base, tmem, wait, warp >> 2, stats, flags + 2);
+  } else if (warp == 8) {
+    if (lane == 0) {
+      ptx::prefetch_tensormap(&p.qmap);
+      if (kPaged || p.kv_tokens > 0) {  // else there are no such maps
+        ptx::prefetch_tensormap(&p.kmap);
+        ptx::prefetch_tensormap(&p.vmap);
+      }
+    }
+    wait.role = 1;
+    producer<kD, kPaged>(p, bars, slots, smem, wait);
+  } else if (warp == 9) {
+    wait.role = 2;
+    mma_issuer<kD, kF16>(p, bars, slots, smem, tmem, wait);
+  } else {
+    wait.role = 4;
+    scheduler<kPaged>(p, bars, slots, wait);
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+}  // namespace agmm
+
+#define AGMM_ATTN_VARIANT(D, F16, PAGED) \
+  AttnFn { &agmm_attention<D, F16, PAGED>, Layout<D>::kBytes }

@@ -35,26 +35,60 @@ struct NormRopeParams {
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, bool f16, cudaStream_t stream);
 
-// One attention problem.  Prompts: packed rows, `paged` false.  Trees: a
-// paged cache.
-struct AttnParams {
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
+constexpr int kRows = 128;        // query rows of a tile (MMA M, TMEM lanes)
+constexpr int kKeys = 128;        // keys of a tile
+constexpr int kAttnThreads = 352;  // 2 x 4 softmax warps, then producer, MMA and scheduler warps
+
+// Workspace: status words, the prompt scheduler's counter, then (trees) a
+// join record per CTA and the partial results of split work.
+constexpr size_t kAttnStatusBytes = 256;
+constexpr size_t kCounterOffset = 128;
+constexpr int kJoinInts = 8;
+
+// One attention problem.  Prompts: packed rows of keys and values.  Trees: a
+// paged cache, whose places take the part of the key rows.
+struct __align__(128) AttnParams {
+  CUtensorMap qmap;  // {head_dim, q_heads, tokens}: a box is 64 columns of one tile's rows
+  CUtensorMap kmap;  // {head_dim, tokens or places, kv_heads, pages}: 64 columns of up to 128 rows
+  CUtensorMap vmap;
+  const uint16_t* v;  // the values again, for plain loads
   uint16_t* out;
   const int32_t* starts;     // query rows of each sequence (nodes of a tree)
   const int32_t* kv_starts;  // prompts: key rows of each sequence
   const int32_t* context_lens;
   const int32_t* page_table;
   const int64_t* mask;
-  int64_t tokens, kv_tokens, sequences;
-  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, out_ts, out_hs;
-  int64_t page_stride, table_stride, pages;
+  int* status;
+  int* counter;   // prompts: next item
+  int* joins;     // trees: [CTAs][kJoinInts]
+  float* partial;  // trees: [CTAs][2][rows][head_dim], then [CTAs][2][rows][2] (maximum, sum)
+  int64_t tokens, kv_tokens;
+  int64_t v_ts, v_hs, v_ps;  // token (place), head and page strides of v
+  int64_t out_ts, out_hs;
+  int64_t table_stride, table_pages, pages;
+  uint64_t wait_limit_cycles;
+  int sequences;
   int mask_words, page_shift;
-  int q_heads, kv_heads, causal, max_nodes;
-  float scale;
+  int q_heads, kv_heads, group;  // group: query heads of a key head
+  int pack;                      // heads a tile packs per token: group for trees, 1 for prompts
+  int tile_tokens;               // tokens of a row tile: 128 / pack
+  int causal, max_nodes;
+  int partial_rows;              // rows of a partial slot
+  float scale_log2;              // scale * log2(e)
+  int test_drop_first_load;      // test hook: the producer skips its first load, so a wait runs out
 };
 
-cudaError_t launch_attention(const AttnParams& p, int head_dim, bool f16, bool paged, cudaStream_t stream);
+// One instantiation of the kernel, and its shared memory.
+struct AttnFn {
+  void (*fn)(AttnParams);
+  size_t smem;
+};
+AttnFn prompt_kernel(int head_dim, bool f16);
+AttnFn tree_kernel(int head_dim, bool f16);
+
+cudaError_t prepare_attention(const AttnFn& k);
+cudaError_t launch_attention(const AttnFn& k, const AttnParams& p, int ctas, cudaStream_t stream);
+// Sums the parts of split work (trees), after launch_attention on the same stream.
+cudaError_t launch_join(const AttnParams& p, int head_dim, bool f16, int ctas, cudaStream_t stream);
 
 }  // namespace agmm

@@ -100,7 +100,7 @@ typedef struct {
   int head_dim;          /* 64 or 128                      */
   int causal;
   agmm_dtype_t dtype;    /* AGMM_BF16 or AGMM_F16          */
-  float scale;
+  float scale;           /* > 0                            */
 } agmm_prompt_desc_t;
 
 typedef struct {
@@ -142,7 +142,7 @@ typedef struct {
   int page_size;         /* a power of two, 8..256                 */
   int max_nodes;         /* 1..1024                                */
   agmm_dtype_t dtype;    /* AGMM_BF16 or AGMM_F16                  */
-  float scale;
+  float scale;           /* > 0                                    */
 } agmm_tree_desc_t;
 
 typedef struct {
@@ -152,8 +152,9 @@ typedef struct {
   const void* k_cache;          /* [pages, page_size, kv_heads, head_dim]   */
   const void* v_cache;          /* the same shape and strides               */
   int64_t pages, cache_page_stride, cache_token_stride, cache_head_stride;
-  const int32_t* page_table;    /* [sequences, table_stride]                */
-  int64_t table_stride;         /* pages a sequence can have                */
+  const int32_t* page_table;    /* [sequences, table_pages]                 */
+  int64_t table_pages;          /* pages a sequence can have                */
+  int64_t table_stride;         /* entries from one sequence to the next    */
   const int32_t* context_lens;  /* [sequences]                              */
   const int32_t* node_starts;   /* [sequences + 1], not falling             */
   const int64_t* mask;          /* [tokens, mask_words] or NULL             */
