@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -113,6 +114,21 @@ int shift_of(int64_t v) {  // log2, or -1
   return s;
 }
 
+// The device's peak clock.  Asked once per device: the driver takes most of a
+// millisecond to answer.
+int peak_clock_khz(int device) {
+  static std::atomic<int> known[64];
+  const bool cached = device >= 0 && device < 64;
+  int khz = cached ? known[device].load(std::memory_order_relaxed) : 0;
+  if (khz > 0) return khz;
+  if (cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, device) != cudaSuccess || khz <= 0) {
+    (void)cudaGetLastError();
+    khz = 2100000;  // above the part's 2.07 GHz peak
+  }
+  if (cached) known[device].store(khz, std::memory_order_relaxed);
+  return khz;
+}
+
 // What both attention plans hold, from the checked description.
 agmm_status_t fill_plan(AttnPlan* pl, int q_heads, int kv_heads, int head_dim, agmm_dtype_t dtype, float scale, bool tree) {
   pl->q_heads = q_heads;
@@ -123,11 +139,7 @@ agmm_status_t fill_plan(AttnPlan* pl, int q_heads, int kv_heads, int head_dim, a
   pl->pack = tree ? q_heads / kv_heads : 1;
   pl->tile_tokens = kRows / pl->pack;
   pl->kernel = tree ? tree_kernel(head_dim, pl->f16) : prompt_kernel(head_dim, pl->f16);
-  int khz = 0;
-  if (cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, pl->device) != cudaSuccess || khz <= 0) {
-    (void)cudaGetLastError();
-    khz = 2100000;  // above the part's 2.07 GHz peak
-  }
+  const int khz = peak_clock_khz(pl->device);
   const char* ms = std::getenv("AGMM_WAIT_LIMIT_MS");
   const int limit = ms && *ms ? std::atoi(ms) : 0;
   pl->wait_limit_cycles = (uint64_t)(limit > 0 ? limit : 2000) * (uint64_t)khz;

@@ -47,7 +47,7 @@
 namespace agmm {
 namespace {
 
-constexpr int kItemSlots = 4;
+constexpr int kItemSlots = 2;
 constexpr float kMaxGrowth = 8.0f;  // log2 of how far the weights may grow past 1
 
 template <int kD>
@@ -168,6 +168,7 @@ __device__ __forceinline__ void fill_rows(const AttnParams& p, const Sequence& x
 struct PromptWork {
   int level, base, count;  // row-tile pairs `level` of all sequences have the ranks [base, base + count)
   int total;               // row-tile pairs
+  bool drawn;              // the first item, its own number, is taken
   int lane;
 
   __device__ __forceinline__ int pairs_of(const AttnParams& p, int s) const {
@@ -186,6 +187,7 @@ struct PromptWork {
     total = __reduce_add_sync(0xffffffffu, sum);
     level = __reduce_max_sync(0xffffffffu, most);
     base = count = 0;
+    drawn = false;
   }
   // The sequence and row-tile pair of a rank; ranks come in rising order.
   __device__ __forceinline__ void find(const AttnParams& p, int rank, int& seq, int& pair) {
@@ -226,15 +228,15 @@ template <bool kPaged>
 __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars, Item* slots, const Waiter& wait) {
   const int lane = threadIdx.x & 31;
   int k = 0;
-  auto publish = [&](const Item& it) -> bool {
-    const int slot = k % kItemSlots;
-    if (k >= kItemSlots && !wait(bars.item_empty(slot), (uint32_t)(k / kItemSlots - 1) & 1u, k)) return false;
+  auto room = [&]() -> bool {
+    return k < kItemSlots || wait(bars.item_empty(k % kItemSlots), (uint32_t)(k / kItemSlots - 1) & 1u, k);
+  };
+  auto publish = [&](const Item& it) {
     if (lane == 0) {
-      slots[slot] = it;
-      ptx::mbar_arrive(bars.item_full(slot));
+      slots[k % kItemSlots] = it;
+      ptx::mbar_arrive(bars.item_full(k % kItemSlots));
     }
     ++k;
-    return true;
   };
   Item it = {};
   it.valid = 1;
@@ -244,7 +246,21 @@ __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars,
     work.init(p);
     const int items = work.total * p.q_heads;
     int next = blockIdx.x;
-    while (next < items) {
+    while (true) {
+      // An item is drawn when there is room for it, two ahead of the one at
+      // work at most: a CTA that drew more would hold them from the others.
+      if (!room()) return;
+      if (work.drawn) {
+        // The CTA that draws the last number puts the counter back to zero.
+        if (lane == 0) {
+          next = atomicAdd(p.counter, 1);
+          if (next == items - 1) atomicExch(p.counter, 0);
+          next += gridDim.x;
+        }
+        next = __shfl_sync(0xffffffffu, next, 0);
+      }
+      work.drawn = true;
+      if (next >= items) break;
       const int rank = next / p.q_heads;
       it.head = next - rank * p.q_heads;
       it.kv_head = it.head / p.group;
@@ -257,14 +273,7 @@ __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars,
       it.tiles = max(it.n[0], it.n[1]);
       if (it.alternate) share_tiles(it);
       it.masked_from = p.causal ? min(x.kv_len, max(it.tok[0] + x.off + 1, 0)) : x.kv_len;
-      // The CTA that draws the last number puts the counter back to zero.
-      if (lane == 0) {
-        next = atomicAdd(p.counter, 1);
-        if (next == items - 1) atomicExch(p.counter, 0);
-        next += gridDim.x;
-      }
-      next = __shfl_sync(0xffffffffu, next, 0);
-      if (!publish(it)) return;
+      publish(it);
     }
   } else {
     // the length of the line, then this CTA's part of it
@@ -333,12 +342,13 @@ __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars,
           join[0] = 1;
         }
         u += it.tiles;
-        if (!publish(it)) return;
+        if (!room()) return;
+        publish(it);
       }
     }
   }
-  Item end = {};
-  publish(end);
+  if (!room()) return;
+  publish(Item{});
 }
 
 // ------------------------------------------------------------------- producer
@@ -546,14 +556,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <bool kF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (kF16)
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  else
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
-template <bool kF16>
 __device__ __forceinline__ float value16(uint16_t b) {
   if constexpr (kF16)
     return __half2float(__ushort_as_half(b));
@@ -633,7 +635,7 @@ __device__ __forceinline__ void clean_value_row(uint8_t* tile, int r, bool past,
 // Adds to columns [col, col + 32) of a row the values that are not finite of
 // the places [from, to) that it sees: they were left out of the products there.
 template <bool kF16, bool kPaged>
-__device__ __noinline__ void add_not_finite(const AttnParams& p, const Item& it, const int64_t* row, int limit, int from,
+__device__ __forceinline__ void add_not_finite(const AttnParams& p, const Item& it, const int64_t* row, int limit, int from,
                                             int to, int col, float (&o)[32]) {
   constexpr uint16_t kExp = kF16 ? 0x7c00u : 0x7f80u;
   for (int place = from; place < to; ++place) {
@@ -708,13 +710,14 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
               if (!(bits >> e & 1u)) v[w][e] = 0xff800000u;  // -inf
           }
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float top[4];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
+        for (int w = 0; w < 4; ++w) top[w] = fmaxf(__uint_as_float(v[w][0]), __uint_as_float(v[w][1]));
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            top[w] = fmaxf(fmaxf(top[w], __uint_as_float(v[w][e])), __uint_as_float(v[w][e + 1]));
-        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        for (int e = 2; e < 32; e += 2)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) top[w] = ptx::max3(top[w], __uint_as_float(v[w][e]), __uint_as_float(v[w][e + 1]));
+        const float tile_top = ptx::max3(fmaxf(top[0], top[1]), top[2], top[3]);
         if (i == 0) {
           m = tile_top;
         } else if (__any_sync(0xffffffffu, (tile_top - m) * c > kMaxGrowth)) {
@@ -737,6 +740,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
           }
         }
         const float shift = m == -INFINITY ? 0.0f : -m * c;
+        const uint64_t c2 = ptx::pair(c, c), shift2 = ptx::pair(shift, shift);
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -744,12 +748,12 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int w = 2 * h + e / 16, x = 2 * (e % 16);
-            const float a = ptx::exp2_approx(fmaf(__uint_as_float(v[w][x]), c, shift));
-            const float b = ptx::exp2_approx(fmaf(__uint_as_float(v[w][x + 1]), c, shift));
-            pk[e] = pack2<kF16>(a, b);
-            const float2 back = unpack2<kF16>(pk[e]);
-            sum[e & 1] += back.x;
-            sum[2 + (e & 1)] += back.y;
+            const float2 y =
+                ptx::unpair(ptx::fma_pair(ptx::pair(__uint_as_float(v[w][x]), __uint_as_float(v[w][x + 1])), c2, shift2));
+            pk[e] = pack2<kF16>(ptx::exp2_approx(y.x), ptx::exp2_approx(y.y));
+            // The sum is of the rounded weights, those that multiply V: a row with
+            // one weight that counts gives exactly its value.
+            ptx::add_halves<kF16>(sum[e & 1], sum[2 + (e & 1)], pk[e]);
           }
           ptx::tmem_st_32x32b_x32(t_s + h * 32, pk);
         }
@@ -928,6 +932,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
   ptx::griddep_wait();
 
   Waiter wait{flags, p.wait_limit_cycles, p.status, 3};
+  // Of the 168 registers a thread that 384 threads start with, the third
+  // warpgroup gives up 96 and the softmax warps take 48 more each:
+  // 2 x 216 + 72 = 504 = 3 x 168.
+  if (warp < 8)
+    ptx::more_registers<216>();
+  else
+    ptx::fewer_registers<72>();
   if (warp < 8) {
     softmax<kD, kF16, kPaged>(p, bars, slots, base, tmem, wait, warp >> 2, stats, flags + 2);
   } else if (warp == 8) {
@@ -943,7 +954,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
   } else if (warp == 9) {
     wait.role = 2;
     mma_issuer<kD, kF16>(p, bars, slots, smem, tmem, wait);
-  } else {
+  } else if (warp == 10) {
     wait.role = 4;
     scheduler<kPaged>(p, bars, slots, wait);
   }

@@ -37,7 +37,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, bool f16, cu
 
 constexpr int kRows = 128;        // query rows of a tile (MMA M, TMEM lanes)
 constexpr int kKeys = 128;        // keys of a tile
-constexpr int kAttnThreads = 352;  // 2 x 4 softmax warps, then producer, MMA and scheduler warps
+constexpr int kAttnThreads = 384;  // 2 x 4 softmax warps, then producer, MMA and scheduler warps and an idle one
 
 // Workspace: status words, the prompt scheduler's counter, then (trees) a
 // join record per CTA and the partial results of split work.

@@ -61,6 +61,50 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Registers of the warps of a warpgroup from here on (all its warps run it).
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Two float32 values in a 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// acc + each 16-bit half of w, in float32.
+template <bool kF16>
+__device__ __forceinline__ void add_halves(float& acc0, float& acc1, uint32_t w) {
+  if constexpr (kF16)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.f16 %0, l, %0;\n\tadd.f32.f16 %1, h, %1;\n\t}"
+        : "+f"(acc0), "+f"(acc1)
+        : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(acc0), "+f"(acc1)
+        : "r"(w));
+}
+
 }  // namespace ptx
 
 // Bounded waits.  A wait that runs out raises the CTA's abort flag and records
@@ -73,7 +117,7 @@ struct Waiter {
   int role;
 
   // A converged warp waits; every lane gets the same answer.
-  __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity, int where) const {
+  __device__ __forceinline__ bool retry(uint32_t bar, uint32_t parity, int where) const {
     const uint64_t t0 = ptx::clock_cycles();
     for (;;) {
       if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000))) return true;
@@ -89,9 +133,10 @@ struct Waiter {
     __syncwarp();
     return false;
   }
+  // Everything inline: a call with a tile's scores live would spill them.
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int where) const {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-    return slow(bar, parity, where);
+    return retry(bar, parity, where);
   }
   // Waits for work in flight, whatever the abort flag says.
   __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const {
