@@ -16,8 +16,8 @@
 //                   from tensor memory, P goes back there (over S, as 16-bit
 //                   pairs) and is the second product's A operand;
 //   warp 8          TMA loads of Q tiles and of a ring of K and V tiles;
-//   warp 9          issues tcgen05.mma, P V of a tile and Q K^T of the next for
-//                   one stream, then for the other;
+//   warps 9, 11     issue tcgen05.mma for stream 0 and 1: P V of a tile, then
+//                   Q K^T of the next;
 //   warp 10         decides the work items.
 // Tensor memory (512 columns): S of both streams, O of both.
 //
@@ -41,6 +41,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attn_params.h"
 #include "attn_ptx.cuh"
 
@@ -60,7 +62,7 @@ struct Layout {
   static constexpr uint32_t kCtl = kRing + kStages * kTileBytes;
   // control block
   static constexpr uint32_t kBars = kCtl;
-  static constexpr uint32_t kItems = kCtl + 344;                // kItemSlots x 96 bytes
+  static constexpr uint32_t kItems = kCtl + 360;                // kItemSlots x 96 bytes
   static constexpr uint32_t kFlags = kItems + kItemSlots * 96;  // abort, TMEM base, non-finite flag
   static constexpr uint32_t kStats = kFlags + 16;               // [2 streams][128 rows][2] float
   static constexpr size_t kBytes = kStats + 2 * 128 * 2 * 4;
@@ -75,13 +77,15 @@ struct Bars {
   __device__ __forceinline__ uint32_t q_full(int x) const { return base + 8 * (20 + x); }
   __device__ __forceinline__ uint32_t q_empty(int x) const { return base + 8 * (22 + x); }
   __device__ __forceinline__ uint32_t s_full(int s) const { return base + 8 * (24 + s); }
-  __device__ __forceinline__ uint32_t p_ready(int s) const { return base + 8 * (26 + s); }
-  __device__ __forceinline__ uint32_t pv_done(int s) const { return base + 8 * (28 + s); }
-  __device__ __forceinline__ uint32_t o_free(int s) const { return base + 8 * (30 + s); }
-  __device__ __forceinline__ uint32_t item_full(int i) const { return base + 8 * (32 + i); }
+  __device__ __forceinline__ uint32_t p_ready(int s, int h) const { return base + 8 * (26 + 2 * s + h); }
+  __device__ __forceinline__ uint32_t o_full(int s) const { return base + 8 * (30 + s); }
+  __device__ __forceinline__ uint32_t o_free(int s) const { return base + 8 * (32 + s); }
+  __device__ __forceinline__ uint32_t item_full(int i) const { return base + 8 * (34 + i); }
   __device__ __forceinline__ uint32_t item_empty(int i) const { return base + 8 * (36 + i); }
-  __device__ __forceinline__ uint32_t stats() const { return base + 8 * 40; }
-  __device__ __forceinline__ uint32_t drained() const { return base + 8 * 41; }
+  __device__ __forceinline__ uint32_t stats() const { return base + 8 * 38; }
+  __device__ __forceinline__ uint32_t drained(int s) const { return base + 8 * (39 + s); }
+  __device__ __forceinline__ uint32_t v_there(int s) const { return base + 8 * (41 + s); }
+  __device__ __forceinline__ uint32_t turn(int s) const { return base + 8 * (43 + s); }
 };
 
 // A work item, written by the scheduler warp.
@@ -179,6 +183,7 @@ struct PromptWork {
   __device__ __forceinline__ void init(const AttnParams& p) {
     lane = threadIdx.x & 31;
     int most = 0, sum = 0;
+#pragma unroll 1
     for (int s = lane; s < p.sequences; s += 32) {
       const int n = pairs_of(p, s);
       most = max(most, n);
@@ -195,12 +200,14 @@ struct PromptWork {
       base += count;
       --level;
       int c = 0;
+#pragma unroll 1
       for (int s = lane; s < p.sequences; s += 32) c += pairs_of(p, s) > level;
       count = __reduce_add_sync(0xffffffffu, c);
     }
     int left = rank - base;
     seq = 0;
     pair = level;
+#pragma unroll 1
     for (int s0 = 0; s0 < p.sequences; s0 += 32) {
       const int s = s0 + lane;
       const uint32_t has = __ballot_sync(0xffffffffu, s < p.sequences && pairs_of(p, s) > level);
@@ -229,7 +236,7 @@ __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars,
   const int lane = threadIdx.x & 31;
   int k = 0;
   auto room = [&]() -> bool {
-    return k < kItemSlots || wait(bars.item_empty(k % kItemSlots), (uint32_t)(k / kItemSlots - 1) & 1u, k);
+    return k < kItemSlots || wait.compact(bars.item_empty(k % kItemSlots), (uint32_t)(k / kItemSlots - 1) & 1u, k);
   };
   auto publish = [&](const Item& it) {
     if (lane == 0) {
@@ -278,6 +285,7 @@ __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars,
   } else {
     // the length of the line, then this CTA's part of it
     int64_t sum = 0;
+#pragma unroll 1
     for (int s = lane; s < p.sequences; s += 32) sum += TreeWork::units(p, sequence_of<true>(p, s));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -291,6 +299,7 @@ __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars,
       // the sequence that u lies in
       int seq = 0;
       int64_t first = 0;  // its first unit
+#pragma unroll 1
       for (int s0 = 0; s0 < p.sequences; s0 += 32) {
         const int64_t mine = s0 + lane < p.sequences ? TreeWork::units(p, sequence_of<true>(p, s0 + lane)) : 0;
         int64_t run = mine;
@@ -365,7 +374,7 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
   bool ok = true;
   for (int k = 0; ok; ++k) {
     const int slot = k % kItemSlots;
-    if (!wait(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
+    if (!wait.compact(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
     const Item it = slots[slot];
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bars.item_empty(slot));
@@ -374,7 +383,7 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
     for (int s = 0; s < 2 && ok; ++s) {
       if (s == 1 && it.alternate) break;
       if (it.n[s] == 0) continue;
-      ok = wait(bars.q_empty(s), (q_uses[s] & 1u) ^ 1u, 1000 + s);
+      ok = wait.compact(bars.q_empty(s), (q_uses[s] & 1u) ^ 1u, 1000 + s);
       if (!ok) break;
       ++q_uses[s];
       if (lane == 0) {
@@ -388,18 +397,24 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
       __syncwarp();
     }
     if (!ok) break;
+    // loads in ring order: key tile t + lead, then value tile t
     const int lead = it.alternate ? 2 : 1;
-    // loads in ring order: key tile t + lead, value tile t
-    auto load = [&](const CUtensorMap* map, int t) -> bool {
+#pragma unroll 1
+    for (int f = -2 * lead; f < 2 * it.tiles && ok; ++f) {
+      const bool value = f & 1;
+      const int t = value ? f >> 1 : (f >> 1) + lead;
+      if (t < 0 || t >= it.tiles) continue;
+      const CUtensorMap* const map = value ? &p.vmap : &p.kmap;
       const int st = (int)(fills % L::kStages);
-      if (!wait(bars.empty(st), ((fills / L::kStages) & 1u) ^ 1u, 2000 + st)) return false;
+      ok = wait.compact(bars.empty(st), ((fills / L::kStages) & 1u) ^ 1u, 2000 + st);
+      if (!ok) break;
       ++fills;
-      const uint32_t dst = smem + L::kRing + st * L::kTileBytes, bar = bars.full(st);
-      const int place = (it.kv_tile + t) * kKeys;
       if (drop) {  // test hook
         drop = false;
-        return true;
+        continue;
       }
+      const uint32_t dst = smem + L::kRing + st * L::kTileBytes, bar = bars.full(st);
+      const int place = (it.kv_tile + t) * kKeys;
       if constexpr (kPaged) {
         const int mine = place + lane * page_rows;
         const bool there = lane < pages_per_tile && mine < it.kv_len;
@@ -421,12 +436,6 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
           ptx::tma_load_4d(dst + h * L::kHalfBytes, map, bar, h * 64, it.kv_row + place, it.kv_head, 0);
       }
       __syncwarp();
-      return true;
-    };
-    for (int t = 0; t < lead && t < it.tiles && ok; ++t) ok = load(&p.kmap, t);
-    for (int t = 0; t < it.tiles && ok; ++t) {
-      if (t + lead < it.tiles) ok = load(&p.kmap, t + lead);
-      if (ok) ok = load(&p.vmap, t);
     }
   }
   if (*wait.abort) {
@@ -444,103 +453,153 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
 }
 
 // ------------------------------------------------------------------------ MMA
-template <int kD, bool kF16>
-__device__ __forceinline__ void mma_issuer(const AttnParams& p, const Bars& bars, const Item* slots, uint32_t smem,
-                                           uint32_t tmem, const Waiter& wait) {
+// A place in the ring: stage, and the parity of its full barrier's phase.
+template <int kStages>
+struct RingPos {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ RingPos after(int n) const {
+    RingPos x = *this;
+    x.stage += n;
+    if (x.stage >= kStages) {
+      x.stage -= kStages;
+      x.parity ^= 1u;
+    }
+    return x;
+  }
+};
+
+// The products of stream kS.  Each stream has a warp of its own: a warp can run
+// only a product or two ahead of the tensor cores, so what it spends on waits
+// and commits is lost to them unless another warp's products run meanwhile.
+//
+// The two take turns, a tile each: left to themselves they fall into step, both
+// streams' weights being computed while the tensor cores wait and the other way
+// round.
+//
+// The warp runs converged and one elected lane issues; the operands of
+// tcgen05.mma are uniform registers, so everything that they come from is
+// uniform too: constants, the kernel's shared-memory address (the CTA has all of
+// tensor memory, from address 0), and loop counters whose bounds are broadcast.
+//
+// Both warps see every fill of every stage, used or not, and a stage is free
+// when both have let go of it: neither can take one fill for another.
+template <int kD, bool kF16, int kS>
+__device__ __forceinline__ void mma_issuer(const Bars& bars, const Item* slots, uint32_t smem, const Waiter& wait) {
   using L = Layout<kD>;
-  const bool leader = ptx::elect_one();
+  using Pos = RingPos<L::kStages>;
   constexpr uint32_t kIdescS = ptx::idesc_f16kind_f32(kRows, kKeys, false, false, kF16);
   constexpr uint32_t kIdescO = ptx::idesc_f16kind_f32(kRows, kD, false, true, kF16);
-  uint32_t fills = 0;  // of earlier items
-  uint32_t q_uses[2] = {0, 0}, o_uses[2] = {0, 0}, steps[2] = {0, 0};
+  constexpr uint32_t kTmemS = kS * kKeys, kTmemO = 2 * kKeys + kS * kD;
+  const bool leader = ptx::elect_one();
+  Pos pos;  // of the next load in ring order
+  uint32_t q_parity = 0, o_parity = 1, p_parity = 0;  // of the next phases (q: bit x of Q tile x)
+  uint32_t turn_parity = kS == 0 ? 1 : 0;             // stream 0 has the first turn
   bool ok = true;
   for (int k = 0; ok; ++k) {
     const int slot = k % kItemSlots;
-    if (!wait(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
-    const Item it = slots[slot];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bars.item_empty(slot));
-    if (!it.valid) break;
-    if (it.tiles == 0) continue;
-    const int lead = it.alternate ? 2 : 1;
-
-    // S = Q K^T of stream s, its key tile i
-    auto scores = [&](int s, int i) -> bool {
-      const int t = it.alternate ? 2 * i + s : i;
-      const int x = it.alternate ? 0 : s;
-      if (i == 0 && !wait(bars.q_full(x), q_uses[x] & 1u, 1000 + s)) return false;
-      const uint32_t f = fills + (uint32_t)k_index(t, lead);
-      const int st = (int)(f % L::kStages);
-      if (!wait(bars.full(st), (f / L::kStages) & 1u, 2000 + st)) return false;
-      ptx::tc_fence_after();
-      if (leader) {
-        const uint64_t a = ptx::smem_desc_sw128(smem + x * L::kTileBytes, 16u, 1024u);
-        const uint64_t b = ptx::smem_desc_sw128(smem + L::kRing + st * L::kTileBytes, 16u, 1024u);
-#pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk) {
-          // 16 columns further: 32 bytes in the 128-byte row, then the next 64-column piece
-          const uint64_t step = (uint64_t)((kk / 4) * L::kHalfBytes + (kk % 4) * 32u) >> 4;
-          ptx::mma_bf16(tmem + s * kKeys, a + step, b + step, kIdescS, kk > 0);
+    if (!wait.compact(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
+    const Item& it = slots[slot];
+    const int valid = __shfl_sync(0xffffffffu, it.valid, 0), alternate = __shfl_sync(0xffffffffu, it.alternate, 0);
+    const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0), mine = __shfl_sync(0xffffffffu, it.n[kS], 0);
+    const uint32_t q_used = __shfl_sync(0xffffffffu, (it.n[0] > 0 ? 1u : 0u) | (!it.alternate && it.n[1] > 0 ? 2u : 0u), 0);
+    if (leader) ptx::mbar_arrive(bars.item_empty(slot));
+    if (!valid) break;
+    if (tiles == 0) continue;
+    const int x = alternate ? 0 : kS;  // this stream's Q tile
+    for (int y = 0; y < 2 && ok; ++y)
+      if (q_used >> y & 1u) {
+        ok = wait.compact(bars.q_full(y), q_parity >> y & 1u, 1000 + y);
+        if (ok && leader && (y != x || mine == 0)) ptx::mbar_arrive(bars.q_empty(y));  // not for this stream
+      }
+    q_parity ^= q_used;
+    // At t the ring holds key tile t + lead, then value tile t.  This stream takes
+    // the first `mine` tiles, or every second one.
+    const int lead = alternate ? 2 : 1;
+    int done_k = 0, done_v = 0;
+#pragma unroll 1
+    for (int t = -lead; t < tiles && ok; ++t) {
+      const bool has_k = t + lead < tiles, has_v = t >= 0;
+      const Pos at_k = pos, at_v = pos.after(has_k);
+      pos = at_v.after(has_v);
+      const bool own = alternate ? (t & 1) == kS : true;
+      const bool with_k = has_k && own && done_k < mine, with_v = has_v && own && done_v < mine;
+      if (has_v) {
+        if (!(ok = wait.compact(bars.full(at_v.stage), at_v.parity, 3000 + at_v.stage))) break;
+        if (!with_v && leader) ptx::mbar_arrive(bars.empty(at_v.stage));
+      }
+      if (has_k) {
+        if (!(ok = wait.compact(bars.full(at_k.stage), at_k.parity, 2000 + at_k.stage))) break;
+        if (!with_k && leader) ptx::mbar_arrive(bars.empty(at_k.stage));
+      }
+      if (with_v) {
+        // O += P V, in halves of the keys as their weights come.  The softmax warps
+        // learn here that the value tile is there.
+        if (leader) ptx::mbar_arrive(bars.v_there(kS));
+        if (done_v == 0) {
+          if (!(ok = wait.compact(bars.o_free(kS), o_parity, 4000 + kS))) break;
+          o_parity ^= 1u;
         }
-        const bool last_reader = it.alternate || s == 1 || it.n[1] <= t;
-        if (last_reader) ptx::mma_commit(bars.empty(st));
-        ptx::mma_commit(bars.s_full(s));
-        if (it.alternate ? t == it.tiles - 1 : i == it.n[s] - 1) ptx::mma_commit(bars.q_empty(x));
-      }
-      __syncwarp();
-      return true;
-    };
-    // O += P V of stream s, its key tile i
-    auto values = [&](int s, int i) -> bool {
-      const int t = it.alternate ? 2 * i + s : i;
-      const uint32_t f = fills + (uint32_t)v_index(t, lead, it.tiles);
-      const int st = (int)(f % L::kStages);
-      if (!wait(bars.full(st), (f / L::kStages) & 1u, 3000 + st)) return false;
-      if (i == 0) {
-        if (!wait(bars.o_free(s), (o_uses[s] & 1u) ^ 1u, 4000 + s)) return false;
-        ++o_uses[s];
-      }
-      if (!wait(bars.p_ready(s), steps[s] & 1u, 5000 + s)) return false;
-      ++steps[s];
-      ptx::tc_fence_after();
-      if (leader) {
-        const uint64_t b = ptx::smem_desc_sw128(smem + L::kRing + st * L::kTileBytes, L::kHalfBytes, 1024u);
+        const uint64_t b = ptx::smem_desc_sw128(smem + L::kRing + at_v.stage * L::kTileBytes, L::kHalfBytes, 1024u);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          ptx::mma_f16_ts(tmem + 2 * kKeys + s * kD, tmem + s * kKeys + kk * 8, b + (uint64_t)(kk * 2048u >> 4), kIdescO,
-                          i > 0 || kk > 0);
-        const bool last_reader = it.alternate || s == 1 || it.n[1] <= t;
-        if (last_reader) ptx::mma_commit(bars.empty(st));
-        ptx::mma_commit(bars.pv_done(s));
-      }
-      __syncwarp();
-      return true;
-    };
-
-    for (int s = 0; s < 2 && ok; ++s)
-      if (it.n[s] > 0) ok = scores(s, 0);
-    const int most = max(it.n[0], it.n[1]);
-    for (int i = 0; i < most && ok; ++i) {
+        for (int h = 0; h < 2; ++h) {
+          if (!(ok = wait.compact(bars.p_ready(kS, h), p_parity, 5000 + 2 * kS + h))) break;
+          if (h == 0 && !(ok = wait.compact(bars.turn(kS), turn_parity, 5500 + kS))) break;
+          ptx::tc_fence_after();
+          if (leader) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (i < it.n[s] && ok) {
-          ok = values(s, i);
-          if (ok && i + 1 < it.n[s]) ok = scores(s, i + 1);
+            for (int kk = h * kKeys / 32; kk < (h + 1) * kKeys / 32; ++kk)
+              ptx::mma_f16_ts(kTmemO, kTmemS + kk * 8, b + (uint64_t)(kk * 2048u >> 4), kIdescO, done_v > 0 || kk > 0);
+          }
+          __syncwarp();
         }
+        if (!ok) break;
+        p_parity ^= 1u;
+        ++done_v;
+        if (leader) {
+          ptx::mma_commit(bars.empty(at_v.stage));
+          if (done_v == mine) ptx::mma_commit(bars.o_full(kS));
+        }
+        __syncwarp();
+      }
+      if (own && !with_v && !(ok = wait.compact(bars.turn(kS), turn_parity, 5600 + kS))) break;
+      if (with_k) {
+        // S = Q K^T
+        ptx::tc_fence_after();
+        ++done_k;
+        if (leader) {
+          const uint64_t a = ptx::smem_desc_sw128(smem + x * L::kTileBytes, 16u, 1024u);
+          const uint64_t b = ptx::smem_desc_sw128(smem + L::kRing + at_k.stage * L::kTileBytes, 16u, 1024u);
+#pragma unroll
+          for (int kk = 0; kk < kD / 16; ++kk) {
+            // 16 columns further: 32 bytes in the 128-byte row, then the next 64-column piece
+            const uint64_t step = (uint64_t)((kk / 4) * L::kHalfBytes + (kk % 4) * 32u) >> 4;
+            ptx::mma_bf16(kTmemS, a + step, b + step, kIdescS, kk > 0);
+          }
+          // This barrier also says that the product before it, P V of the tile
+          // before, has ended.
+          ptx::mma_commit(bars.s_full(kS));
+          ptx::mma_commit(bars.empty(at_k.stage));
+          if (done_k == mine) ptx::mma_commit(bars.q_empty(x));
+        }
+        __syncwarp();
+      }
+      if (own) {
+        turn_parity ^= 1u;
+        if (leader) ptx::mbar_arrive(bars.turn(kS ^ 1));
       }
     }
-    fills += 2u * (uint32_t)it.tiles;
-    if (it.alternate) {
-      ++q_uses[0];
-    } else {
-      q_uses[0] += it.n[0] > 0;
-      q_uses[1] += it.n[1] > 0;
+    if (kS == 1 && alternate && (tiles & 1) && ok) {
+      // stream 0 had a tile more: this turn is passed on
+      ok = wait.compact(bars.turn(1), turn_parity, 5700);
+      turn_parity ^= 1u;
+      if (leader) ptx::mbar_arrive(bars.turn(0));
     }
   }
   // every product issued has ended before the CTA does
-  if (leader) ptx::mma_commit(bars.drained());
+  if (leader) ptx::mma_commit(bars.drained(kS));
   __syncwarp();
-  wait.drain(bars.drained(), 0);
+  wait.drain(bars.drained(kS), 0);
 }
 
 // -------------------------------------------------------------------- softmax
@@ -574,16 +633,41 @@ __device__ __forceinline__ uint32_t mask_window(const int64_t* row, int words, i
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// Which of the places [place, place + 32) a row sees.  `row` (trees with a
-// mask): its mask words; else `limit` is the first place that it does not see.
-__device__ __forceinline__ uint32_t seen32(const Item& it, const int64_t* row, int words, int limit, int place) {
-  if (row == nullptr) return low_bits(limit - place);
+// A thread's row of an item.
+struct Row {
+  bool there;          // one of the tile's tokens, not padding
+  int token;           // in its sequence
+  int limit;           // the first place that it does not see, without a mask
+  const int64_t* mask;  // its mask words, or null
+};
+
+template <bool kPaged>
+__device__ __forceinline__ Row row_of(const AttnParams& p, const Item& it, int s, int r) {
+  Row x;
+  x.there = r < it.cnt[s] * p.pack;
+  x.token = it.tok[s] + (p.pack == 1 ? r : r / p.pack);
+  x.limit = it.kv_len;
+  x.mask = nullptr;
+  if (kPaged && p.mask != nullptr) {
+    if (x.there)
+      x.mask = p.mask + (int64_t)(it.q0 + x.token) * p.mask_words;
+    else
+      x.limit = 0;
+  } else if (p.causal) {
+    x.limit = min(x.limit, max(x.token + it.off + 1, 0));
+  }
+  return x;
+}
+
+// Which of the places [place, place + 32) a row sees.
+__device__ __forceinline__ uint32_t seen32(const Item& it, const Row& row, int words, int place) {
+  if (row.mask == nullptr) return low_bits(row.limit - place);
   uint32_t bits = low_bits(it.off - place);
   const int node = place - it.off;
   if (node >= 0)
-    bits = mask_window(row, words, node);
+    bits = mask_window(row.mask, words, node);
   else if (node > -32)
-    bits |= mask_window(row, words, 0) << -node;
+    bits |= mask_window(row.mask, words, 0) << -node;
   return bits & low_bits(it.kv_len - place);
 }
 
@@ -602,7 +686,7 @@ template <int kD, bool kF16>
 __device__ __forceinline__ void clean_value_row(uint8_t* tile, int r, bool past, volatile int* flag) {
   using L = Layout<kD>;
   constexpr uint32_t kInf2 = kF16 ? 0x7c007c00u : 0x7f807f80u;
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < L::kHalves; ++h) {
     uint4* const row = reinterpret_cast<uint4*>(tile + h * L::kHalfBytes + r * 128);
     if (past) {
@@ -620,6 +704,7 @@ __device__ __forceinline__ void clean_value_row(uint8_t* tile, int r, bool past,
     if (__vcmpgeu2(top, kInf2)) {
       *flag = 1;
       __threadfence_block();
+#pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint4 v = row[c];
         v.x = finite_only<kF16>(v.x);
@@ -632,26 +717,141 @@ __device__ __forceinline__ void clean_value_row(uint8_t* tile, int r, bool past,
   }
 }
 
-// Adds to columns [col, col + 32) of a row the values that are not finite of
-// the places [from, to) that it sees: they were left out of the products there.
+// Adds to columns [col0, col1) of a row's result, where it has been written, the
+// values that are not finite of the places [from, to) that the row sees: they
+// were left out of the products there.  `part`: the result in float32, else `out`.
 template <bool kF16, bool kPaged>
-__device__ __forceinline__ void add_not_finite(const AttnParams& p, const Item& it, const int64_t* row, int limit, int from,
-                                            int to, int col, float (&o)[32]) {
+__device__ __noinline__ void add_not_finite(const AttnParams* p, const Item* it, Row row, int from, int to, int col0, int col1,
+                                            uint16_t* out, float* part) {
   constexpr uint16_t kExp = kF16 ? 0x7c00u : 0x7f80u;
+#pragma unroll 1
   for (int place = from; place < to; ++place) {
-    if (!(seen32(it, row, p.mask_words, limit, place) & 1u)) continue;
+    if (!(seen32(*it, row, p->mask_words, place) & 1u)) continue;
     const uint16_t* v;
     if constexpr (kPaged) {
-      const int64_t page = __ldg(p.page_table + it.seq * p.table_stride + (place >> p.page_shift));
-      if (page < 0 || page >= p.pages) continue;
-      v = p.v + page * p.v_ps + (int64_t)(place & ((1 << p.page_shift) - 1)) * p.v_ts;
+      const int64_t page = __ldg(p->page_table + it->seq * p->table_stride + (place >> p->page_shift));
+      if (page < 0 || page >= p->pages) continue;
+      v = p->v + page * p->v_ps + (int64_t)(place & ((1 << p->page_shift) - 1)) * p->v_ts;
     } else {
-      v = p.v + ((int64_t)it.kv_row + place) * p.v_ts;
+      v = p->v + ((int64_t)it->kv_row + place) * p->v_ts;
     }
-    v += it.kv_head * p.v_hs + col;
-    for (int c = 0; c < 32; ++c)
-      if ((v[c] & kExp) == kExp) o[c] += value16<kF16>(v[c]);
+    v += it->kv_head * p->v_hs;
+#pragma unroll 1
+    for (int c = col0; c < col1; ++c) {
+      if ((v[c] & kExp) != kExp) continue;
+      const float x = value16<kF16>(v[c]);
+      if (part)
+        part[c] += x;
+      else
+        out[c] = (uint16_t)pack2<kF16>(value16<kF16>(out[c]) + x, 0.0f);
+    }
   }
+}
+
+// The largest of 128 scores, in eight chains.
+__device__ __forceinline__ float row_max(const uint32_t (&v)[4][32]) {
+  float top[8];
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top[w] = fmaxf(__uint_as_float(v[w & 3][w >> 2]), __uint_as_float(v[w & 3][2 + (w >> 2)]));
+#pragma unroll
+  for (int e = 4; e < 32; e += 4)
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+      top[w] = ptx::max3(top[w], __uint_as_float(v[w & 3][e + (w >> 2)]), __uint_as_float(v[w & 3][e + 2 + (w >> 2)]));
+  return ptx::max3(ptx::max3(top[0], top[1], top[2]), ptx::max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
+}
+
+// The weights 2^(c s + shift) of 64 scores as 16-bit pairs, and their sums.  The
+// sums are of the rounded weights, those that multiply V: a row with one weight
+// that counts gives exactly its value.
+template <bool kF16>
+__device__ __forceinline__ void weights(const uint32_t (&a)[32], const uint32_t (&b)[32], float c, float shift, uint32_t (&pk)[32],
+                                        float (&sum)[4]) {
+  const uint64_t c2 = ptx::pair(c, c), shift2 = ptx::pair(shift, shift);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const uint32_t (&v)[32] = e < 16 ? a : b;
+    const float2 y = ptx::unpair(
+        ptx::fma_pair(ptx::pair(__uint_as_float(v[2 * (e & 15)]), __uint_as_float(v[2 * (e & 15) + 1])), c2, shift2));
+    pk[e] = ptx::round_pair<kF16>(ptx::exp2_approx(y.x), ptx::exp2_approx(y.y));
+    ptx::add_halves<kF16>(sum[e & 1], sum[2 + (e & 1)], pk[e]);
+  }
+}
+
+// The parts of a key tile's work that most tiles do not need are functions of
+// their own, called when no scores are held in registers: the key loop stays
+// short enough for the instruction cache and spills nothing.
+
+// A tile that not all rows of the item see.  Looks over its value tile in shared
+// memory, and puts -inf over the scores, in tensor memory, of the keys that this
+// thread's row does not see, whatever they were.
+template <int kD, bool kF16, bool kPaged>
+__device__ __noinline__ bool mask_tile(const AttnParams* p, const Item* it, const Waiter* wait, uint8_t* value_tile,
+                                       uint32_t value_bar, uint32_t parity, uint32_t t_s, int s, int place, bool any,
+                                       volatile int* flag) {
+  const int r = threadIdx.x & 127;
+  if (!(*wait)(value_bar, parity, 8000 + s)) return false;
+  clean_value_row<kD, kF16>(value_tile, r, place + r >= it->kv_len, flag);
+  ptx::fence_proxy_async_smem();
+  if (!any) return true;
+  const Row row = row_of<kPaged>(*p, *it, s, r);
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    uint32_t v[32];
+    ptx::tmem_ld_32x32b_x32(t_s + w * 32, v);
+    const uint32_t bits = seen32(*it, row, p->mask_words, place + 32 * w);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(bits >> e & 1u)) v[e] = 0xff800000u;
+    ptx::tmem_st_32x32b_x32(t_s + w * 32, v);
+  }
+  ptx::tmem_st_wait();
+  return true;
+}
+
+// The largest score of a row.
+__device__ __noinline__ float tile_max(uint32_t t_s) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int w = 0; w < 4; w += 2) {
+    uint32_t a[32], b[32];
+    ptx::tmem_ld_32x32b_x32(t_s + w * 32, a);
+    ptx::tmem_ld_32x32b_x32(t_s + w * 32 + 32, b);
+    ptx::tmem_ld_wait();
+    float t[4] = {top, top, top, top};
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      t[0] = ptx::max3(t[0], __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+      t[1] = ptx::max3(t[1], __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
+      t[2] = ptx::max3(t[2], __uint_as_float(b[e]), __uint_as_float(b[e + 1]));
+      t[3] = ptx::max3(t[3], __uint_as_float(b[e + 2]), __uint_as_float(b[e + 3]));
+    }
+    top = ptx::max3(fmaxf(t[0], t[1]), t[2], t[3]);
+  }
+  return top;
+}
+
+// O *= keep.  The last product into it has ended: the scores that showed the new
+// maximum were issued after it.
+template <int kD>
+__device__ __noinline__ void rescale(uint32_t t_o, float keep) {
+#pragma unroll 1
+  for (int col = 0; col < kD; col += 32) {
+    uint32_t o[32];
+    ptx::tmem_ld_32x32b_x32(t_o + col, o);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+    ptx::tmem_st_32x32b_x32(t_o + col, o);
+  }
+  ptx::tmem_st_wait();
+}
+
+__device__ __forceinline__ void load_scores(uint32_t t_s, uint32_t (&v)[4][32]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) ptx::tmem_ld_32x32b_x32(t_s + w * 32, v[w]);
+  ptx::tmem_ld_wait();
 }
 
 template <int kD, bool kF16, bool kPaged>
@@ -664,114 +864,73 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
   const uint32_t t_s = tmem + lanes + s * kKeys;
   const uint32_t t_o = tmem + lanes + 2 * kKeys;
   const float c = p.scale_log2;
-  uint32_t fills = 0, steps[2] = {0, 0};
+  uint32_t fills = 0, steps = 0, results = 0, results_other = 0;
   uint32_t joint = 0;  // alternating items so far
   bool ok = true;
   for (int k = 0; ok; ++k) {
     const int slot = k % kItemSlots;
     if (!wait(bars.item_full(slot), (uint32_t)(k / kItemSlots) & 1u, k)) break;
-    const Item it = slots[slot];
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bars.item_empty(slot));
+    // The item stays in shared memory until this warp has its results out: what
+    // the key loop does not need on every tile takes no register there.
+    const Item& it = slots[slot];
     if (!it.valid) break;
     const int n = it.n[s];
-    const int lead = it.alternate ? 2 : 1;
-    const bool there = r < it.cnt[s] * p.pack;
-    const bool any = __any_sync(0xffffffffu, there);
-    const int token = it.tok[s] + (p.pack == 1 ? r : r / p.pack);
-    const int64_t* const mask_row =
-        kPaged && p.mask && there ? p.mask + (int64_t)(it.q0 + token) * p.mask_words : nullptr;
-    const bool masked = kPaged && p.mask != nullptr;
-    // the first place that this row does not see (rows under a mask: seen32)
-    int limit = it.kv_len;
-    if (!masked && p.causal) limit = min(limit, max(token + it.off + 1, 0));
-    if (masked && !there) limit = 0;
-    // tiles that end before this place are seen by all rows of the stream
-    const int clear = masked ? min(it.off, it.kv_len) : p.causal ? min(it.kv_len, max(it.tok[s] + it.off + 1, 0)) : it.kv_len;
+    const int stride = it.alternate ? 2 * kKeys : kKeys;
+    const bool any = __any_sync(0xffffffffu, r < it.cnt[s] * p.pack);
+    const int edge = it.masked_from;  // tiles that end before this place are seen by all rows
+    int place = (it.kv_tile + (it.alternate ? s : 0)) * kKeys;
     float m = -INFINITY, l = 0.0f;
-
-    for (int i = 0; i < n; ++i) {
-      const int t = it.alternate ? 2 * i + s : i;
-      const int place = (it.kv_tile + t) * kKeys;
-      ok = wait(bars.s_full(s), (steps[s] + i) & 1u, 6000 + s);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, place += stride) {
+      ok = wait(bars.s_full(s), (steps + i) & 1u, 6000 + s);
       if (!ok) break;
-      if (any) {
-        ptx::tc_fence_after();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) ptx::tmem_ld_32x32b_x32(t_s + w * 32, v[w]);
-        ptx::tmem_ld_wait();
-        if (place + kKeys > clear) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t bits = seen32(it, mask_row, p.mask_words, limit, place + 32 * w);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(bits >> e & 1u)) v[w][e] = 0xff800000u;  // -inf
-          }
-        }
-        float top[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) top[w] = fmaxf(__uint_as_float(v[w][0]), __uint_as_float(v[w][1]));
-#pragma unroll
-        for (int e = 2; e < 32; e += 2)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) top[w] = ptx::max3(top[w], __uint_as_float(v[w][e]), __uint_as_float(v[w][e + 1]));
-        const float tile_top = ptx::max3(fmaxf(top[0], top[1]), top[2], top[3]);
-        if (i == 0) {
-          m = tile_top;
-        } else if (__any_sync(0xffffffffu, (tile_top - m) * c > kMaxGrowth)) {
-          const bool grows = (tile_top - m) * c > kMaxGrowth;  // also from -inf to anything
-          const float keep = grows ? ptx::exp2_approx((m - tile_top) * c) : 1.0f;
-          if (grows) m = tile_top;
-          l *= keep;
-          // the sums so far are complete once the last product with them is
-          ok = wait(bars.pv_done(s), (steps[s] + i - 1) & 1u, 7000 + s);
-          if (!ok) break;
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int col = 0; col < kD; col += 16) {
-            uint32_t o[16];
-            ptx::tmem_ld_32x32b_x16(t_o + s * kD + col, o);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-            ptx::tmem_st_32x32b_x16(t_o + s * kD + col, o);
-          }
-        }
-        const float shift = m == -INFINITY ? 0.0f : -m * c;
-        const uint64_t c2 = ptx::pair(c, c), shift2 = ptx::pair(shift, shift);
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int w = 2 * h + e / 16, x = 2 * (e % 16);
-            const float2 y =
-                ptx::unpair(ptx::fma_pair(ptx::pair(__uint_as_float(v[w][x]), __uint_as_float(v[w][x + 1])), c2, shift2));
-            pk[e] = pack2<kF16>(ptx::exp2_approx(y.x), ptx::exp2_approx(y.y));
-            // The sum is of the rounded weights, those that multiply V: a row with
-            // one weight that counts gives exactly its value.
-            ptx::add_halves<kF16>(sum[e & 1], sum[2 + (e & 1)], pk[e]);
-          }
-          ptx::tmem_st_32x32b_x32(t_s + h * 32, pk);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        ptx::tmem_st_wait();
-      }
-      if (place + kKeys > clear) {
-        // the values of a tile that not all rows see
-        const uint32_t f = fills + (uint32_t)v_index(t, lead, it.tiles);
-        const int st = (int)(f % L::kStages);
-        ok = wait(bars.full(st), (f / L::kStages) & 1u, 8000 + st);
+      ptx::tc_fence_after();
+      if (place + kKeys > edge) {
+        // Both streams look over the value tile of a key tile that either has rows
+        // which do not see all of: what one takes out, the other has to know of.
+        const uint32_t f = fills + (uint32_t)v_index(place / kKeys - it.kv_tile, it.alternate ? 2 : 1, it.tiles);
+        ok = mask_tile<kD, kF16, kPaged>(&p, &it, &wait, smem + L::kRing + (f % L::kStages) * L::kTileBytes, bars.v_there(s),
+                                         (steps + i) & 1u, t_s, s, place, any, flag);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        clean_value_row<kD, kF16>(smem + L::kRing + st * L::kTileBytes, r, place + r >= it.kv_len, flag);
-        ptx::fence_proxy_async_smem();
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars.p_ready(s));
+      // The weights, in halves of 64 keys, so that the first half's product runs
+      // while the second half's weights are computed.
+      if (any) {
+        if (i == 0) m = tile_max(t_s);
+        uint32_t v[4][32], pk[32];
+        float sum[4];
+        // The weights of the first half are computed with the reference there is,
+        // and the tile's maximum on the way: only where a row's maximum has grown
+        // too far, which is rare, they are computed again.
+        for (;;) {
+          load_scores(t_s, v);
+          sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
+          weights<kF16>(v[0], v[1], c, m == -INFINITY ? 0.0f : -m * c, pk, sum);
+          const float top = row_max(v);
+          const bool grows = (top - m) * c > kMaxGrowth;  // also from -inf to anything
+          if (!__any_sync(0xffffffffu, grows)) break;
+          const float keep = grows ? ptx::exp2_approx((m - top) * c) : 1.0f;
+          if (grows) m = top;
+          l *= keep;
+          rescale<kD>(t_o + s * kD, keep);
+        }
+        ptx::tmem_st_32x32b_x32(t_s, pk);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars.p_ready(s, 0));
+        weights<kF16>(v[2], v[3], c, m == -INFINITY ? 0.0f : -m * c, pk, sum);
+        ptx::tmem_st_32x32b_x32(t_s + 32, pk);
+        ptx::tmem_st_wait();
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars.p_ready(s, 1));
+      } else if (lane == 0) {
+        ptx::mbar_arrive(bars.p_ready(s, 0));
+        ptx::mbar_arrive(bars.p_ready(s, 1));
+      }
     }
     if (!ok) break;
 
@@ -779,7 +938,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
     float scale0 = 0.0f, scale1 = 0.0f;  // of the streams' sums
     int col0 = 0, col1 = kD;             // columns this thread writes
     bool has0 = s == 0 && n > 0, has1 = s == 1 && n > 0;
-    if (n > 0) ok = wait(bars.pv_done(s), (steps[s] + n - 1) & 1u, 7100 + s);
+    if (n > 0) ok = wait(bars.o_full(s), results & 1u, 7100 + s);
     if (!ok) break;
     if (it.alternate) {
       // The streams' maxima and sums change hands.  A stream that had keys has
@@ -794,7 +953,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
       float2 other = make_float2(-INFINITY, 0.0f);
       if (it.n[s ^ 1] > 0) {
         other = *reinterpret_cast<const float2*>(stats + 256 * (s ^ 1) + 2 * r);
-        ok = wait(bars.pv_done(s ^ 1), (steps[s ^ 1] + it.n[s ^ 1] - 1) & 1u, 7200 + s);
+        ok = wait(bars.o_full(s ^ 1), results_other & 1u, 7200 + s);
         if (!ok) break;
       }
       const float both = fmaxf(m, other.x);
@@ -815,15 +974,17 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
     __threadfence_block();
     const bool repair = *flag != 0;
     if (any) {
+      const Row own = row_of<kPaged>(p, it, s, r);
       if (it.slot < 0) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         scale0 *= inv;
         scale1 *= inv;
       }
-      const int head = it.head + (p.pack == 1 ? 0 : r - (token - it.tok[s]) * p.pack);
-      uint16_t* const out = p.out + (int64_t)(it.q0 + token) * p.out_ts + head * p.out_hs;
+      const int head = it.head + (p.pack == 1 ? 0 : r - (own.token - it.tok[s]) * p.pack);
+      uint16_t* const out = p.out + (int64_t)(it.q0 + own.token) * p.out_ts + head * p.out_hs;
       const int row = (it.alternate ? 0 : s * p.tile_tokens * p.pack) + r;
       float* const part = kPaged ? p.partial + ((size_t)it.slot * p.partial_rows + row) * kD : nullptr;
+#pragma unroll 1
       for (int col = col0; col < col1; col += 32) {
         float o[32];
         uint32_t a[32];
@@ -842,13 +1003,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(a[e]) * scale1;
         }
-        if (repair && there) {
-          const int from = max(it.masked_from / kKeys, it.kv_tile) * kKeys;
-          const int to = min(it.kv_len, (it.kv_tile + it.tiles) * kKeys);
-          add_not_finite<kF16, kPaged>(p, it, mask_row, limit, from, to, col, o);
-        }
-        __syncwarp();
-        if (there) {
+        if (own.there) {
           if (kPaged && it.slot >= 0) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
@@ -862,7 +1017,11 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
           }
         }
       }
-      if (kPaged && it.slot >= 0 && there && col0 == 0) {
+      if (repair && own.there)
+        add_not_finite<kF16, kPaged>(&p, &it, own, max(it.masked_from / kKeys, it.kv_tile) * kKeys,
+                                     min(it.kv_len, (it.kv_tile + it.tiles) * kKeys), col0, col1, out,
+                                     kPaged && it.slot >= 0 ? part : nullptr);
+      if (kPaged && it.slot >= 0 && own.there && col0 == 0) {
         float* const ml =
             p.partial + (size_t)gridDim.x * 2 * p.partial_rows * kD + ((size_t)it.slot * p.partial_rows + row) * 2;
         ml[0] = m;
@@ -876,8 +1035,11 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
       if (has1) ptx::mbar_arrive_n(bars.o_free(1), it.alternate ? 1 : 2);
     }
     fills += 2u * (uint32_t)it.tiles;
-    steps[0] += it.n[0];
-    steps[1] += it.n[1];
+    steps += n;
+    results += n > 0;
+    results_other += it.n[s ^ 1] > 0;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bars.item_empty(slot));
   }
 }
 
@@ -906,28 +1068,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
     flags[0] = flags[2] = 0;
     for (int i = 0; i < L::kStages; ++i) {
       ptx::mbar_init(bars.full(i), 1);
-      ptx::mbar_init(bars.empty(i), 1);
+      ptx::mbar_init(bars.empty(i), 2);  // both MMA warps
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars.q_full(i), 1);
-      ptx::mbar_init(bars.q_empty(i), 1);
+      ptx::mbar_init(bars.q_empty(i), 2);
       ptx::mbar_init(bars.s_full(i), 1);
-      ptx::mbar_init(bars.p_ready(i), 4);
-      ptx::mbar_init(bars.pv_done(i), 1);
+      ptx::mbar_init(bars.p_ready(i, 0), 4);
+      ptx::mbar_init(bars.p_ready(i, 1), 4);
+      ptx::mbar_init(bars.o_full(i), 1);
+      ptx::mbar_init(bars.v_there(i), 1);
+      ptx::mbar_init(bars.turn(i), 1);
       ptx::mbar_init(bars.o_free(i), 8);
     }
     for (int i = 0; i < kItemSlots; ++i) {
       ptx::mbar_init(bars.item_full(i), 1);
-      ptx::mbar_init(bars.item_empty(i), 10);  // producer, MMA and eight softmax warps
+      ptx::mbar_init(bars.item_empty(i), 11);  // all warps but the scheduler's
     }
     ptx::mbar_init(bars.stats(), 8);
-    ptx::mbar_init(bars.drained(), 1);
+    ptx::mbar_init(bars.drained(0), 1);
+    ptx::mbar_init(bars.drained(1), 1);
     ptx::fence_mbar_init();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = flags[1];
+  // All 512 columns are this CTA's, so they begin at 0; the MMA warp counts on it.
+  constexpr uint32_t tmem = 0;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
 
@@ -953,10 +1120,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
     producer<kD, kPaged>(p, bars, slots, smem, wait);
   } else if (warp == 9) {
     wait.role = 2;
-    mma_issuer<kD, kF16>(p, bars, slots, smem, tmem, wait);
+    mma_issuer<kD, kF16, 0>(bars, slots, smem, wait);
   } else if (warp == 10) {
     wait.role = 4;
     scheduler<kPaged>(p, bars, slots, wait);
+  } else {
+    wait.role = 2;
+    mma_issuer<kD, kF16, 1>(bars, slots, smem, wait);
   }
   __syncwarp();
   ptx::tc_fence_before();

@@ -92,17 +92,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Two values rounded to 16 bits, the first in the low half.
+template <bool kF16>
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+  uint32_t w;
+  if constexpr (kF16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
 // acc + each 16-bit half of w, in float32.
 template <bool kF16>
 __device__ __forceinline__ void add_halves(float& acc0, float& acc1, uint32_t w) {
   if constexpr (kF16)
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.f16 %0, l, %0;\n\tadd.f32.f16 %1, h, %1;\n\t}"
-        : "+f"(acc0), "+f"(acc1)
-        : "r"(w));
+                 : "+f"(acc0), "+f"(acc1)
+                 : "r"(w));
   else
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
-        : "+f"(acc0), "+f"(acc1)
-        : "r"(w));
+                 : "+f"(acc0), "+f"(acc1)
+                 : "r"(w));
 }
 
 }  // namespace ptx
@@ -133,10 +143,16 @@ struct Waiter {
     __syncwarp();
     return false;
   }
-  // Everything inline: a call with a tile's scores live would spill them.
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int where) const {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     return retry(bar, parity, where);
+  }
+  // The same with the retries as a call: for the warps with many waits, whose
+  // code would crowd the instruction cache.
+  __device__ __noinline__ bool retry_call(uint32_t bar, uint32_t parity, int where) const { return retry(bar, parity, where); }
+  __device__ __forceinline__ bool compact(uint32_t bar, uint32_t parity, int where) const {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return retry_call(bar, parity, where);
   }
   // Waits for work in flight, whatever the abort flag says.
   __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const {
