@@ -62,7 +62,7 @@ struct Layout {
   static constexpr uint32_t kCtl = kRing + kStages * kTileBytes;
   // control block
   static constexpr uint32_t kBars = kCtl;
-  static constexpr uint32_t kItems = kCtl + 360;                // kItemSlots x 96 bytes
+  static constexpr uint32_t kItems = kCtl + 376;                // kItemSlots x 96 bytes
   static constexpr uint32_t kFlags = kItems + kItemSlots * 96;  // abort, TMEM base, non-finite flag
   static constexpr uint32_t kStats = kFlags + 16;               // [2 streams][128 rows][2] float
   static constexpr size_t kBytes = kStats + 2 * 128 * 2 * 4;
@@ -84,8 +84,10 @@ struct Bars {
   __device__ __forceinline__ uint32_t item_empty(int i) const { return base + 8 * (36 + i); }
   __device__ __forceinline__ uint32_t stats() const { return base + 8 * 38; }
   __device__ __forceinline__ uint32_t drained(int s) const { return base + 8 * (39 + s); }
-  __device__ __forceinline__ uint32_t v_there(int s) const { return base + 8 * (41 + s); }
-  __device__ __forceinline__ uint32_t turn(int s) const { return base + 8 * (43 + s); }
+  // by parity of the stream's tile: the softmax warps wait for it before they
+  // know that the tile before had its arrival
+  __device__ __forceinline__ uint32_t v_there(int s, uint32_t tile) const { return base + 8 * (41 + 2 * s + (tile & 1u)); }
+  __device__ __forceinline__ uint32_t turn(int s) const { return base + 8 * (45 + s); }
 };
 
 // A work item, written by the scheduler warp.
@@ -493,7 +495,8 @@ __device__ __forceinline__ void mma_issuer(const Bars& bars, const Item* slots, 
   constexpr uint32_t kTmemS = kS * kKeys, kTmemO = 2 * kKeys + kS * kD;
   const bool leader = ptx::elect_one();
   Pos pos;  // of the next load in ring order
-  uint32_t q_parity = 0, o_parity = 1, p_parity = 0;  // of the next phases (q: bit x of Q tile x)
+  uint32_t q_parity = 0, o_parity = 1;     // of the next phases (q: bit x of Q tile x)
+  uint32_t steps = 0;                      // the stream's tiles so far
   uint32_t turn_parity = kS == 0 ? 1 : 0;             // stream 0 has the first turn
   bool ok = true;
   for (int k = 0; ok; ++k) {
@@ -535,7 +538,7 @@ __device__ __forceinline__ void mma_issuer(const Bars& bars, const Item* slots, 
       if (with_v) {
         // O += P V, in halves of the keys as their weights come.  The softmax warps
         // learn here that the value tile is there.
-        if (leader) ptx::mbar_arrive(bars.v_there(kS));
+        if (leader) ptx::mbar_arrive(bars.v_there(kS, steps));
         if (done_v == 0) {
           if (!(ok = wait.compact(bars.o_free(kS), o_parity, 4000 + kS))) break;
           o_parity ^= 1u;
@@ -543,7 +546,7 @@ __device__ __forceinline__ void mma_issuer(const Bars& bars, const Item* slots, 
         const uint64_t b = ptx::smem_desc_sw128(smem + L::kRing + at_v.stage * L::kTileBytes, L::kHalfBytes, 1024u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!(ok = wait.compact(bars.p_ready(kS, h), p_parity, 5000 + 2 * kS + h))) break;
+          if (!(ok = wait.compact(bars.p_ready(kS, h), steps & 1u, 5000 + 2 * kS + h))) break;
           if (h == 0 && !(ok = wait.compact(bars.turn(kS), turn_parity, 5500 + kS))) break;
           ptx::tc_fence_after();
           if (leader) {
@@ -554,7 +557,7 @@ __device__ __forceinline__ void mma_issuer(const Bars& bars, const Item* slots, 
           __syncwarp();
         }
         if (!ok) break;
-        p_parity ^= 1u;
+        ++steps;
         ++done_v;
         if (leader) {
           ptx::mma_commit(bars.empty(at_v.stage));
@@ -562,7 +565,7 @@ __device__ __forceinline__ void mma_issuer(const Bars& bars, const Item* slots, 
         }
         __syncwarp();
       }
-      if (own && !with_v && !(ok = wait.compact(bars.turn(kS), turn_parity, 5600 + kS))) break;
+      if (own && has_v && !with_v && !(ok = wait.compact(bars.turn(kS), turn_parity, 5600 + kS))) break;
       if (with_k) {
         // S = Q K^T
         ptx::tc_fence_after();
@@ -584,7 +587,7 @@ __device__ __forceinline__ void mma_issuer(const Bars& bars, const Item* slots, 
         }
         __syncwarp();
       }
-      if (own) {
+      if (own && has_v) {
         turn_parity ^= 1u;
         if (leader) ptx::mbar_arrive(bars.turn(kS ^ 1));
       }
@@ -782,24 +785,29 @@ __device__ __forceinline__ void weights(const uint32_t (&a)[32], const uint32_t 
 // their own, called when no scores are held in registers: the key loop stays
 // short enough for the instruction cache and spills nothing.
 
-// A tile that not all rows of the item see.  Looks over its value tile in shared
-// memory, and puts -inf over the scores, in tensor memory, of the keys that this
-// thread's row does not see, whatever they were.
-template <int kD, bool kF16, bool kPaged>
-__device__ __noinline__ bool mask_tile(const AttnParams* p, const Item* it, const Waiter* wait, uint8_t* value_tile,
-                                       uint32_t value_bar, uint32_t parity, uint32_t t_s, int s, int place, bool any,
-                                       volatile int* flag) {
+// Looks over the value tile of a key tile that not all rows of the item see
+// (while its scores are still being computed).
+template <int kD, bool kF16>
+__device__ __noinline__ bool clean_values(const Waiter* wait, uint32_t value_bar, uint32_t parity, uint8_t* value_tile, int place,
+                                          int kv_len, volatile int* flag) {
   const int r = threadIdx.x & 127;
-  if (!(*wait)(value_bar, parity, 8000 + s)) return false;
-  clean_value_row<kD, kF16>(value_tile, r, place + r >= it->kv_len, flag);
+  if (!(*wait)(value_bar, parity, 8000)) return false;
+  clean_value_row<kD, kF16>(value_tile, r, place + r >= kv_len, flag);
   ptx::fence_proxy_async_smem();
-  if (!any) return true;
-  const Row row = row_of<kPaged>(*p, *it, s, r);
+  return true;
+}
+
+// Puts -inf over the scores, in tensor memory, of the keys of such a tile that
+// this thread's row does not see, whatever they were.
+template <bool kPaged>
+__device__ __noinline__ void mask_scores(const AttnParams* p, const Item* it, uint32_t t_s, int s, int place) {
+  const Row row = row_of<kPaged>(*p, *it, s, threadIdx.x & 127);
 #pragma unroll 1
   for (int w = 0; w < 4; ++w) {
+    const uint32_t bits = seen32(*it, row, p->mask_words, place + 32 * w);
+    if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
     uint32_t v[32];
     ptx::tmem_ld_32x32b_x32(t_s + w * 32, v);
-    const uint32_t bits = seen32(*it, row, p->mask_words, place + 32 * w);
     ptx::tmem_ld_wait();
 #pragma unroll
     for (int e = 0; e < 32; ++e)
@@ -807,7 +815,6 @@ __device__ __noinline__ bool mask_tile(const AttnParams* p, const Item* it, cons
     ptx::tmem_st_32x32b_x32(t_s + w * 32, v);
   }
   ptx::tmem_st_wait();
-  return true;
 }
 
 // The largest score of a row.
@@ -830,6 +837,31 @@ __device__ __noinline__ float tile_max(uint32_t t_s) {
     top = ptx::max3(fmaxf(t[0], t[1]), t[2], t[3]);
   }
   return top;
+}
+
+// Lane 4 g + j has x[i] = piece i of row 4 g + j; afterwards x[i] = piece j of row
+// 4 g + i.
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+  auto exchange = [](uint4& send, int bit) {
+    send.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
+    send.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
+    send.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
+    send.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
+  };
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e & bit) continue;
+      // the lower lane keeps the lower piece and sends the upper one
+      const bool upper = lane & bit;
+      const uint4 keep = upper ? x[e | bit] : x[e];
+      uint4 send = upper ? x[e] : x[e | bit];
+      exchange(send, bit);
+      x[e] = upper ? send : keep;
+      x[e | bit] = upper ? keep : send;
+    }
+  }
 }
 
 // O *= keep.  The last product into it has ended: the scores that showed the new
@@ -882,18 +914,20 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
     float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
     for (int i = 0; i < n; ++i, place += stride) {
-      ok = wait(bars.s_full(s), (steps + i) & 1u, 6000 + s);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      if (place + kKeys > edge) {
+      const bool partly = place + kKeys > edge;
+      if (partly) {
         // Both streams look over the value tile of a key tile that either has rows
         // which do not see all of: what one takes out, the other has to know of.
         const uint32_t f = fills + (uint32_t)v_index(place / kKeys - it.kv_tile, it.alternate ? 2 : 1, it.tiles);
-        ok = mask_tile<kD, kF16, kPaged>(&p, &it, &wait, smem + L::kRing + (f % L::kStages) * L::kTileBytes, bars.v_there(s),
-                                         (steps + i) & 1u, t_s, s, place, any, flag);
+        ok = clean_values<kD, kF16>(&wait, bars.v_there(s, steps + i), (steps + i) >> 1 & 1u, smem + L::kRing + (f % L::kStages) * L::kTileBytes,
+                                    place, it.kv_len, flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
+      ok = wait(bars.s_full(s), (steps + i) & 1u, 6000 + s);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (partly && any) mask_scores<kPaged>(&p, &it, t_s, s, place);
       // The weights, in halves of 64 keys, so that the first half's product runs
       // while the second half's weights are computed.
       if (any) {
@@ -975,55 +1009,80 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
     const bool repair = *flag != 0;
     if (any) {
       const Row own = row_of<kPaged>(p, it, s, r);
-      if (it.slot < 0) {
+      const bool whole = !kPaged || it.slot < 0;
+      if (whole) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         scale0 *= inv;
         scale1 *= inv;
       }
-      const int head = it.head + (p.pack == 1 ? 0 : r - (own.token - it.tok[s]) * p.pack);
-      uint16_t* const out = p.out + (int64_t)(it.q0 + own.token) * p.out_ts + head * p.out_hs;
-      const int row = (it.alternate ? 0 : s * p.tile_tokens * p.pack) + r;
-      float* const part = kPaged ? p.partial + ((size_t)it.slot * p.partial_rows + row) * kD : nullptr;
+      const int tile_row = (it.alternate ? 0 : s * p.tile_tokens * p.pack) + r;
+      const int64_t out_at = (int64_t)(it.q0 + own.token) * p.out_ts +
+                             (it.head + (p.pack == 1 ? 0 : r - (own.token - it.tok[s]) * p.pack)) * p.out_hs;
+      float* const part = kPaged && !whole ? p.partial + ((size_t)it.slot * p.partial_rows + tile_row) * kD : nullptr;
+      // A row's results are in one lane.  Four lanes exchange theirs, so that each
+      // stores 16 bytes of all four rows and together 64 consecutive bytes of one:
+      // with a row a lane, every store would touch 32 lines.
+      const uint32_t rows_there = __ballot_sync(0xffffffffu, own.there);
 #pragma unroll 1
       for (int col = col0; col < col1; col += 32) {
-        float o[32];
-        uint32_t a[32];
+        uint32_t o[32];
         if (has0) {
-          ptx::tmem_ld_32x32b_x32(t_o + col, a);
+          ptx::tmem_ld_32x32b_x32(t_o + col, o);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(a[e]) * scale0;
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale0);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+          for (int e = 0; e < 32; ++e) o[e] = 0;
         }
         if (has1) {
+          uint32_t a[32];
           ptx::tmem_ld_32x32b_x32(t_o + kD + col, a);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(a[e]) * scale1;
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(a[e]), scale1, __uint_as_float(o[e])));
         }
-        if (own.there) {
-          if (kPaged && it.slot >= 0) {
+        if (whole) {
+          uint4 x[4];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(part + col + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else {
+          for (int e = 0; e < 4; ++e)
+            x[e] = make_uint4(pack2<kF16>(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+                              pack2<kF16>(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+                              pack2<kF16>(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+                              pack2<kF16>(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+          transpose4(x, lane);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(out + col + e) =
-                  make_uint4(pack2<kF16>(o[e], o[e + 1]), pack2<kF16>(o[e + 2], o[e + 3]),
-                             pack2<kF16>(o[e + 4], o[e + 5]), pack2<kF16>(o[e + 6], o[e + 7]));
+          for (int e = 0; e < 4; ++e) {
+            const int from = (lane & ~3) + e;  // the lane of the row that x[e] is of
+            const int64_t at = __shfl_sync(0xffffffffu, out_at, from);
+            if (rows_there >> from & 1u) *reinterpret_cast<uint4*>(p.out + at + col + (lane & 3) * 8) = x[e];
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint4 x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = make_uint4(o[16 * g + 4 * e], o[16 * g + 4 * e + 1], o[16 * g + 4 * e + 2], o[16 * g + 4 * e + 3]);
+            transpose4(x, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int from = (lane & ~3) + e;
+              if (rows_there >> from & 1u)
+                *reinterpret_cast<uint4*>(part + (from - lane) * kD + col + 16 * g + (lane & 3) * 4) = x[e];
+            }
           }
         }
       }
-      if (repair && own.there)
-        add_not_finite<kF16, kPaged>(&p, &it, own, max(it.masked_from / kKeys, it.kv_tile) * kKeys,
-                                     min(it.kv_len, (it.kv_tile + it.tiles) * kKeys), col0, col1, out,
-                                     kPaged && it.slot >= 0 ? part : nullptr);
-      if (kPaged && it.slot >= 0 && own.there && col0 == 0) {
+      if (repair) {
+        // reads what the other lanes of the four have stored of its row
+        __syncwarp();
+        if (own.there)
+          add_not_finite<kF16, kPaged>(&p, &it, own, max(it.masked_from / kKeys, it.kv_tile) * kKeys,
+                                       min(it.kv_len, (it.kv_tile + it.tiles) * kKeys), col0, col1, p.out + out_at, part);
+      }
+      if (kPaged && !whole && own.there && col0 == 0) {
         float* const ml =
-            p.partial + (size_t)gridDim.x * 2 * p.partial_rows * kD + ((size_t)it.slot * p.partial_rows + row) * 2;
+            p.partial + (size_t)gridDim.x * 2 * p.partial_rows * kD + ((size_t)it.slot * p.partial_rows + tile_row) * 2;
         ml[0] = m;
         ml[1] = l;
       }
@@ -1077,7 +1136,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
       ptx::mbar_init(bars.p_ready(i, 0), 4);
       ptx::mbar_init(bars.p_ready(i, 1), 4);
       ptx::mbar_init(bars.o_full(i), 1);
-      ptx::mbar_init(bars.v_there(i), 1);
+      ptx::mbar_init(bars.v_there(i, 0), 1);
+      ptx::mbar_init(bars.v_there(i, 1), 1);
       ptx::mbar_init(bars.turn(i), 1);
       ptx::mbar_init(bars.o_free(i), 8);
     }
