@@ -45,6 +45,12 @@ struct agmm_tree_s : AttnPlan {};
 
 namespace {
 
+// A part of a prompt's item is at least this many key tiles: its results make a
+// round trip through device memory, 256 rows in float32.
+constexpr int kMinPromptTiles = 4;
+// From this many items for each CTA on, prompts draw whole items.
+constexpr int kDrawnItems = 2;
+
 agmm_status_t fail(agmm_status_t s, const char* fmt, ...) {
   char text[256];
   va_list ap;
@@ -138,6 +144,7 @@ agmm_status_t fill_plan(AttnPlan* pl, int q_heads, int kv_heads, int head_dim, a
   pl->scale = scale;
   pl->pack = tree ? q_heads / kv_heads : 1;
   pl->tile_tokens = kRows / pl->pack;
+  pl->partial_rows = 2 * pl->tile_tokens * pl->pack;
   pl->kernel = tree ? tree_kernel(head_dim, pl->f16) : prompt_kernel(head_dim, pl->f16);
   const int khz = peak_clock_khz(pl->device);
   const char* ms = std::getenv("AGMM_WAIT_LIMIT_MS");
@@ -148,6 +155,16 @@ agmm_status_t fill_plan(AttnPlan* pl, int q_heads, int kv_heads, int head_dim, a
   const cudaError_t e = prepare_attention(pl->kernel);
   if (e != cudaSuccess) return fail(AGMM_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(e));
   return AGMM_OK;
+}
+
+// Where the join records of a workspace end and its partial results begin.
+size_t joins_end(const AttnPlan* pl) {
+  return (kAttnStatusBytes + (size_t)pl->num_sms * kJoinInts * sizeof(int) + 255) / 256 * 256;
+}
+
+size_t workspace_bytes(const AttnPlan* pl) {
+  const size_t rows = (size_t)pl->num_sms * 2 * pl->partial_rows;
+  return joins_end(pl) + rows * ((size_t)pl->head_dim + 2) * sizeof(float);
 }
 
 // The plan's fields of a launch, and the Q tiles' tensor map.
@@ -161,12 +178,11 @@ void fill_params(const AttnPlan* pl, AttnParams* p, void* workspace) {
   p->wait_limit_cycles = pl->wait_limit_cycles;
   p->test_drop_first_load = pl->test_drop;
   p->status = static_cast<int*>(workspace);
-  p->counter = reinterpret_cast<int*>(static_cast<char*>(workspace) + kCounterOffset);
-}
-
-// Where the join records of a tree's workspace end and its partial results begin.
-size_t joins_end(const AttnPlan* pl) {
-  return (kAttnStatusBytes + (size_t)pl->num_sms * kJoinInts * sizeof(int) + 255) / 256 * 256;
+  char* const ws = static_cast<char*>(workspace);
+  p->counter = reinterpret_cast<int*>(ws + kCounterOffset);
+  p->joins = reinterpret_cast<int*>(ws + kAttnStatusBytes);
+  p->partial = reinterpret_cast<float*>(ws + joins_end(pl));
+  p->partial_rows = pl->partial_rows;
 }
 
 agmm_status_t check_plan_device(int device) {
@@ -368,7 +384,7 @@ agmm_status_t agmm_prompt_plan(const agmm_prompt_desc_t* d, agmm_prompt_t* out) 
 
 void agmm_prompt_destroy(agmm_prompt_t plan) { delete plan; }
 
-size_t agmm_prompt_workspace_bytes(agmm_prompt_t plan) { return plan ? kAttnStatusBytes : 0; }
+size_t agmm_prompt_workspace_bytes(agmm_prompt_t plan) { return plan ? workspace_bytes(plan) : 0; }
 
 agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, void* stream) {
   if (!plan || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
@@ -385,7 +401,7 @@ agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, v
   AGMM_TRY(check_pointer("starts", a->starts, 4));
   if (a->kv_starts) AGMM_TRY(check_pointer("kv_starts", a->kv_starts, 4));
   AGMM_TRY(check_pointer("workspace", a->workspace, 16));
-  // row-tile pairs there can be, and items
+  // row-tile pairs there can be
   const int64_t pairs = a->tokens / (2 * kRows) + (a->sequences < a->tokens ? a->sequences : a->tokens);
   if (pairs * plan->q_heads >= INT_MAX / 2)
     return fail(AGMM_ERR_UNSUPPORTED, "too many rows for one run: %lld tokens of %d heads", (long long)a->tokens, plan->q_heads);
@@ -409,9 +425,16 @@ agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, v
   p.kv_tokens = a->kv_tokens;
   p.sequences = (int)a->sequences;
   p.causal = plan->causal;
-  const int64_t items = pairs * plan->q_heads;
-  const int ctas = (int)(items < plan->num_sms ? items : plan->num_sms);
-  return launched(launch_attention(plan->kernel, p, ctas, static_cast<cudaStream_t>(stream)), "prompt");
+  // Two heads share the keys of a one-tile item where there are enough items for
+  // all CTAs without.
+  p.pair_heads = p.group % 2 == 0 && pairs * plan->q_heads >= 2 * plan->num_sms;
+  p.min_tiles = kMinPromptTiles;
+  p.by_draw = pairs * plan->q_heads >= (int64_t)kDrawnItems * plan->num_sms;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AGMM_TRY(launched(launch_attention(plan->kernel, p, plan->num_sms, s), "prompt"));
+  // no cuts, or nothing long enough to be cut
+  if (p.by_draw || a->kv_tokens <= (2 * kMinPromptTiles - 1) * kKeys) return AGMM_OK;
+  return launched(launch_join(p, plan->head_dim, plan->f16, plan->num_sms, s), "prompt join");
 }
 
 // ----------------------------------------------------------------------- tree
@@ -446,11 +469,7 @@ agmm_status_t agmm_tree_plan(const agmm_tree_desc_t* d, agmm_tree_t* out) {
 
 void agmm_tree_destroy(agmm_tree_t plan) { delete plan; }
 
-size_t agmm_tree_workspace_bytes(agmm_tree_t plan) {
-  if (!plan) return 0;
-  const size_t slots = (size_t)plan->num_sms * 2 * plan->partial_rows;
-  return joins_end(plan) + slots * ((size_t)plan->head_dim + 2) * sizeof(float);
-}
+size_t agmm_tree_workspace_bytes(agmm_tree_t plan) { return plan ? workspace_bytes(plan) : 0; }
 
 agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* stream) {
   if (!plan || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
@@ -501,10 +520,7 @@ agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* s
   p.sequences = (int)a->sequences;
   p.causal = 1;
   p.max_nodes = plan->max_nodes;
-  p.partial_rows = plan->partial_rows;
-  char* const ws = static_cast<char*>(a->workspace);
-  p.joins = reinterpret_cast<int*>(ws + kAttnStatusBytes);
-  p.partial = reinterpret_cast<float*>(ws + joins_end(plan));
+  p.min_tiles = 1;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   AGMM_TRY(launched(launch_attention(plan->kernel, p, plan->num_sms, s), "tree"));
   return launched(launch_join(p, plan->head_dim, plan->f16, plan->num_sms, s), "tree join");

@@ -25,12 +25,13 @@
 // tile) or, where there is one row tile only, alternating (the streams hold the
 // same rows and take even and odd key tiles; their sums are joined at the end).
 //
-// Prompts: an item is 256 rows of a sequence and a head, taken from a counter,
-// long ones first.  Trees: a tile packs the heads of a group (row = token *
-// group + head), so that each key is read once for all of them; the key tiles of
-// all (sequence, key head, rows) are laid out in a line that the CTAs cut into
-// equal parts.  A part that covers only some of its keys leaves O, m and l in
-// device memory, and attn_join sums the parts in order.
+// Prompts: an item is up to 256 rows of a sequence for a head, or up to 128 rows
+// for two heads of a group.  Trees: a tile packs the heads of a group (row = token *
+// group + head), so that each key is read once for all of them.  The key tiles of all
+// items are laid out in a line that the CTAs cut into equal parts (struct Line).
+// A part that covers only some of an item's keys leaves O, m and l in device
+// memory, and agmm_attn_join sums the parts in order.  Prompts that have many items for
+// every CTA are not cut: the CTAs draw them from a counter (struct Draw).
 //
 // What a row does not see never reaches it: its scores are replaced, not
 // added to; value rows past the end are cleared in shared memory; and in a
@@ -101,6 +102,7 @@ struct __align__(8) Item {
   int kv_row;       // prompts: its first key row
   int seq;
   int kv_head, head;  // head: of the tile's first row
+  int head_step;      // stream 1 has the head after: 1 (the streams' tokens are the same), else 0
   int q0, q_len;      // the sequence's first query row, and how many
   int off;            // row i sees keys below i + off + 1 (causal, chains); trees: the context
   int tok[2], cnt[2];  // each stream's first token in the sequence, and how many
@@ -150,216 +152,306 @@ __device__ __forceinline__ int key_tiles(const AttnParams& p, const Sequence& x,
   return ceil_div(p.causal ? min(x.kv_len, max(end + x.off, 0)) : x.kv_len, kKeys);
 }
 
-// An alternating item's key tiles: stream 0 takes the even ones.
-__device__ __forceinline__ void share_tiles(Item& it) {
-  it.n[0] = (it.tiles + 1) / 2;
-  it.n[1] = it.tiles / 2;
-}
+// The work is laid out in a line: sequences, in each its sets of row tiles (one
+// or two tiles), for each the heads, for each item its key tiles.  In front of
+// its tiles an item has kItemCost places for what it takes besides them.  The
+// line is cut into a part for every CTA, equal but for cuts that would leave
+// less than p.min_tiles of an item on one side: those move to the item's edge.
+constexpr int kItemCost = 4;
 
-__device__ __forceinline__ void fill_rows(const AttnParams& p, const Sequence& x, int tok, Item& it) {
-  it.tok[0] = tok;
-  it.cnt[0] = min(p.tile_tokens, x.q_len - tok);
-  it.alternate = x.q_len - tok <= p.tile_tokens;
-  it.tok[1] = it.alternate ? tok : tok + p.tile_tokens;
-  it.cnt[1] = it.alternate ? it.cnt[0] : min(x.q_len - it.tok[1], p.tile_tokens);
-  it.q0 = x.q0;
-  it.q_len = x.q_len;
-  it.kv_len = x.kv_len;
-  it.kv_row = x.kv_row;
-  it.off = x.off;
-}
+struct Spot {
+  int seq, set, head;  // head: among the set's
+  int heads, len;      // items of the set, key tiles of each (at least 1)
+  int64_t start;       // the item's first place
+};
 
-// Prompts: items in the order of their row tile's place in its sequence, last
-// ones first (they see the most keys), then by sequence, then by head.
-struct PromptWork {
-  int level, base, count;  // row-tile pairs `level` of all sequences have the ranks [base, base + count)
-  int total;               // row-tile pairs
-  bool drawn;              // the first item, its own number, is taken
+template <bool kPaged>
+struct Line {
+  const AttnParams& p;
   int lane;
+  int64_t total;
+  int parts;  // CTAs that have work: no two cuts are the same place
 
-  __device__ __forceinline__ int pairs_of(const AttnParams& p, int s) const {
+  __device__ __forceinline__ int sets(const Sequence& x) const { return ceil_div(x.q_len, 2 * p.tile_tokens); }
+  __device__ __forceinline__ bool single(const Sequence& x, int set) const {
+    return x.q_len - set * 2 * p.tile_tokens <= p.tile_tokens;
+  }
+  // Items of a row set: a key head each (trees), a query head each, or two query
+  // heads of a group where the set is one tile.
+  __device__ __forceinline__ int heads(const Sequence& x, int set) const {
+    if (kPaged) return p.kv_heads;
+    return p.pair_heads && single(x, set) ? p.q_heads / 2 : p.q_heads;
+  }
+  __device__ __forceinline__ int length(const Sequence& x, int set) const {
+    if (kPaged) return ceil_div(x.kv_len, kKeys);
+    return max(1, key_tiles(p, x, min(x.q_len, (set + 1) * 2 * p.tile_tokens)));
+  }
+  __device__ __forceinline__ int64_t places(int seq) const {
+    if (seq >= p.sequences) return 0;
+    const Sequence x = sequence_of<kPaged>(p, seq);
+    int64_t sum = 0;
+    const int n = sets(x);
+#pragma unroll 1
+    for (int set = 0; set < n; ++set) sum += (int64_t)heads(x, set) * (length(x, set) + kItemCost);
+    return sum;
+  }
+  __device__ __forceinline__ void init() {
+    lane = threadIdx.x & 31;
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int s = lane; s < p.sequences; s += 32) sum += places(s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    total = sum;
+    parts = (int)min((int64_t)gridDim.x, total);
+  }
+  // The CTA whose part begins at or before place u, uncut by items.
+  __device__ __forceinline__ int cta_of(int64_t u) const { return (int)(((u + 1) * parts - 1) / total); }
+
+  // The item of place u (0 <= u < total).
+  __device__ __noinline__ Spot find(int64_t u) const {
+    Spot at = {};
+    int64_t first = 0;  // first place of the sequence
+#pragma unroll 1
+    for (int s0 = 0; s0 < p.sequences; s0 += 32) {
+      const int64_t mine = places(s0 + lane);
+      int64_t run = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, first + run > u);
+      if (past) {
+        const int j = __ffs(past) - 1;
+        at.seq = s0 + j;
+        first += __shfl_sync(0xffffffffu, run - mine, j);
+        break;
+      }
+      first += __shfl_sync(0xffffffffu, run, 31);
+    }
+    const Sequence x = sequence_of<kPaged>(p, at.seq);
+    for (;;) {
+      at.heads = heads(x, at.set);
+      at.len = length(x, at.set);
+      const int each = at.len + kItemCost;
+      if (u < first + (int64_t)at.heads * each || at.set + 1 >= sets(x)) {
+        at.head = (int)((u - first) / each);
+        at.start = first + (int64_t)at.head * each;
+        return at;
+      }
+      first += (int64_t)at.heads * each;
+      ++at.set;
+    }
+  }
+  // Where the part of CTA c begins, and the item that lies there.
+  __device__ __forceinline__ int64_t cut(int c, Spot& at) const {
+    if (c >= parts) return total;
+    const int64_t u = total * c / parts;
+    at = find(u);
+    const int t = (int)(u - at.start) - kItemCost;
+    if (t < p.min_tiles) return at.start;
+    if (at.len - t < p.min_tiles) return at.start + kItemCost + at.len;
+    return u;
+  }
+};
+
+// Prompts with many items for each CTA: whole items, drawn one at a time from a
+// counter, those of the last row set of their sequence first (they see the most
+// keys), then by sequence, then by head.  No result makes a round trip through
+// memory, and what the line's cost model misses evens out.
+struct Draw {
+  const AttnParams& p;
+  int lane;
+  int level, base, count;  // the row sets `level` of all sequences have the ranks [base, base + count)
+  int items, next;
+
+  __device__ __forceinline__ int sets_of(int s) const {
     const int64_t a = min(max((int64_t)__ldg(p.starts + s), (int64_t)0), p.tokens);
     const int64_t b = min(max((int64_t)__ldg(p.starts + s + 1), a), p.tokens);
     return (int)((b - a + 2 * kRows - 1) / (2 * kRows));
   }
-  __device__ __forceinline__ void init(const AttnParams& p) {
+  __device__ __forceinline__ void init() {
     lane = threadIdx.x & 31;
     int most = 0, sum = 0;
 #pragma unroll 1
     for (int s = lane; s < p.sequences; s += 32) {
-      const int n = pairs_of(p, s);
+      const int n = sets_of(s);
       most = max(most, n);
       sum += n;
     }
-    total = __reduce_add_sync(0xffffffffu, sum);
+    items = __reduce_add_sync(0xffffffffu, sum) * p.q_heads;
     level = __reduce_max_sync(0xffffffffu, most);
     base = count = 0;
-    drawn = false;
+    next = (int)blockIdx.x - (int)gridDim.x;  // the first item is this CTA's number
   }
-  // The sequence and row-tile pair of a rank; ranks come in rising order.
-  __device__ __forceinline__ void find(const AttnParams& p, int rank, int& seq, int& pair) {
+  // The next item, of Spot's seq, set and head (head: query head); false: none.
+  __device__ __forceinline__ bool draw(Spot& at) {
+    if (next < 0) {
+      next += gridDim.x;
+    } else {
+      // the CTA that draws the last number puts the counter back to zero
+      if (lane == 0) {
+        next = atomicAdd(p.counter, 1);
+        if (next == items - 1) atomicExch(p.counter, 0);
+        next += gridDim.x;
+      }
+      next = __shfl_sync(0xffffffffu, next, 0);
+    }
+    if (next >= items) return false;
+    const int rank = next / p.q_heads;
+    at.head = next - rank * p.q_heads;
     while (rank >= base + count) {
       base += count;
       --level;
       int c = 0;
 #pragma unroll 1
-      for (int s = lane; s < p.sequences; s += 32) c += pairs_of(p, s) > level;
+      for (int s = lane; s < p.sequences; s += 32) c += sets_of(s) > level;
       count = __reduce_add_sync(0xffffffffu, c);
     }
+    at.set = level;
     int left = rank - base;
-    seq = 0;
-    pair = level;
 #pragma unroll 1
     for (int s0 = 0; s0 < p.sequences; s0 += 32) {
       const int s = s0 + lane;
-      const uint32_t has = __ballot_sync(0xffffffffu, s < p.sequences && pairs_of(p, s) > level);
+      const uint32_t has = __ballot_sync(0xffffffffu, s < p.sequences && sets_of(s) > level);
       const int n = __popc(has);
       if (left < n) {
-        seq = s0 + __fns(has, 0, left + 1);
-        return;
+        at.seq = s0 + (int)__fns(has, 0, left + 1);
+        return true;
       }
       left -= n;
     }
+    return false;
   }
 };
 
-// Trees: key tiles of (sequence, key head, row tiles) in a line.
-struct TreeWork {
-  __device__ static __forceinline__ int row_sets(const AttnParams& p, const Sequence& x) {
-    return ceil_div(ceil_div(x.q_len, p.tile_tokens), 2);  // one tile, or pairs of tiles
+// Key tiles [t0, t1) of the item at a spot.
+template <bool kPaged>
+__device__ __noinline__ Item make_item(const AttnParams& p, const Line<kPaged>& line, const Sequence& x, const Spot& at, int t0,
+                                       int t1) {
+  Item it = {};
+  it.valid = 1;
+  it.slot = -1;
+  it.seq = at.seq;
+  it.q0 = x.q0;
+  it.q_len = x.q_len;
+  it.kv_len = x.kv_len;
+  it.kv_row = x.kv_row;
+  it.off = x.off;
+  it.kv_tile = t0;
+  const int tok = at.set * 2 * p.tile_tokens;
+  const bool single = line.single(x, at.set);
+  it.tok[0] = it.tok[1] = tok;
+  it.cnt[0] = it.cnt[1] = min(p.tile_tokens, x.q_len - tok);
+  if (!single) {
+    it.tok[1] = tok + p.tile_tokens;
+    it.cnt[1] = min(p.tile_tokens, x.q_len - it.tok[1]);
   }
-  __device__ static __forceinline__ int64_t units(const AttnParams& p, const Sequence& x) {
-    return x.q_len > 0 ? (int64_t)p.kv_heads * row_sets(p, x) * ceil_div(x.kv_len, kKeys) : 0;
+  it.alternate = single;
+  if (kPaged) {
+    it.kv_head = at.head;
+    it.head = at.head * p.group;
+    it.n[0] = it.n[1] = t1 - t0;
+    it.masked_from = p.mask ? min(x.off, x.kv_len) : min(x.kv_len, tok + x.off + 1);
+  } else {
+    if (single && p.pair_heads) {
+      it.alternate = 0;
+      it.head_step = 1;
+    }
+    it.head = at.head << it.head_step;
+    it.kv_head = it.head / p.group;
+    it.n[0] = max(0, min(key_tiles(p, x, it.tok[0] + it.cnt[0]), t1) - t0);
+    it.n[1] = max(0, min(key_tiles(p, x, it.tok[1] + it.cnt[1]), t1) - t0);
+    it.masked_from = p.causal ? min(x.kv_len, max(tok + x.off + 1, 0)) : x.kv_len;
   }
-};
+  it.tiles = max(it.n[0], it.n[1]);
+  if (it.alternate) {  // stream 0 takes the even tiles
+    it.n[0] = (it.tiles + 1) / 2;
+    it.n[1] = it.tiles / 2;
+  }
+  return it;
+}
 
 template <bool kPaged>
 __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars, Item* slots, const Waiter& wait) {
+  Line<kPaged> line{p};
+  Draw drawn{p};
   const int lane = threadIdx.x & 31;
+  const bool by_draw = !kPaged && p.by_draw;
+  int* const join = p.joins + (size_t)blockIdx.x * kJoinInts;
+  if (lane == 0) join[0] = 0;
+  int64_t u = 0, end = 0;
+  Spot at = {};
+  Sequence x = {};
+  if (by_draw) {
+    drawn.init();
+  } else {
+    line.init();
+    if ((int)blockIdx.x < line.parts) {
+      end = line.cut(blockIdx.x + 1, at);
+      u = line.cut(blockIdx.x, at);
+      x = sequence_of<kPaged>(p, at.seq);
+    }
+  }
   int k = 0;
-  auto room = [&]() -> bool {
-    return k < kItemSlots || wait.compact(bars.item_empty(k % kItemSlots), (uint32_t)(k / kItemSlots - 1) & 1u, k);
-  };
-  auto publish = [&](const Item& it) {
+  for (bool more = true; more;) {
+    // An item is drawn when there is room for it, two ahead of the one at work at
+    // most: a CTA that drew more would hold them from the others.
+    if (k >= kItemSlots && !wait.compact(bars.item_empty(k % kItemSlots), (uint32_t)(k / kItemSlots - 1) & 1u, k)) return;
+    Item it = {};
+    if (by_draw) {
+      do
+        more = drawn.draw(at);
+      while (more && p.pair_heads && (at.head & 1) && line.single(x = sequence_of<false>(p, at.seq), at.set));
+      if (more) {
+        x = sequence_of<kPaged>(p, at.seq);
+        if (p.pair_heads && line.single(x, at.set)) at.head /= 2;
+        it = make_item(p, line, x, at, 0, line.length(x, at.set));
+      }
+    } else {
+      // the item at u, where it is not one that ends there
+      while (u < end && u >= at.start + kItemCost + at.len) {
+        at.start += kItemCost + at.len;
+        if (++at.head < at.heads) continue;
+        at.head = 0;
+        if (++at.set >= line.sets(x)) {
+          at.set = 0;
+          do
+            x = sequence_of<kPaged>(p, ++at.seq);
+          while (x.q_len == 0);  // the line goes on: there is one more
+        }
+        at.heads = line.heads(x, at.set);
+        at.len = line.length(x, at.set);
+      }
+      more = u < end;
+      if (more) {
+        const int64_t tiles0 = at.start + kItemCost;
+        const int t0 = u <= at.start ? 0 : (int)(u - tiles0);
+        const int t1 = (int)min((int64_t)at.len, end - tiles0);
+        const bool whole = t0 == 0 && t1 == at.len;
+        u = tiles0 + t1;
+        it = make_item(p, line, x, at, t0, t1);
+        if (!whole) it.slot = 2 * (int)blockIdx.x + (t0 == 0);
+        if (!whole && t0 == 0 && lane == 0) {
+          // this CTA holds the first keys of an item that goes on: the record of its join
+          join[1] = x.q0 + it.tok[0];
+          join[2] = it.cnt[0] * p.pack;
+          join[3] = it.head;
+          join[4] = line.cta_of(tiles0 + at.len - p.min_tiles);  // the CTA of the item's last tiles
+          join[5] = x.q0 + it.tok[1];
+          join[6] = it.alternate ? 0 : it.cnt[1] * p.pack;
+          join[7] = it.head + it.head_step;
+          join[0] = 1;
+        }
+      }
+    }
     if (lane == 0) {
       slots[k % kItemSlots] = it;
       ptx::mbar_arrive(bars.item_full(k % kItemSlots));
     }
     ++k;
-  };
-  Item it = {};
-  it.valid = 1;
-  it.slot = -1;
-  if constexpr (!kPaged) {
-    PromptWork work;
-    work.init(p);
-    const int items = work.total * p.q_heads;
-    int next = blockIdx.x;
-    while (true) {
-      // An item is drawn when there is room for it, two ahead of the one at
-      // work at most: a CTA that drew more would hold them from the others.
-      if (!room()) return;
-      if (work.drawn) {
-        // The CTA that draws the last number puts the counter back to zero.
-        if (lane == 0) {
-          next = atomicAdd(p.counter, 1);
-          if (next == items - 1) atomicExch(p.counter, 0);
-          next += gridDim.x;
-        }
-        next = __shfl_sync(0xffffffffu, next, 0);
-      }
-      work.drawn = true;
-      if (next >= items) break;
-      const int rank = next / p.q_heads;
-      it.head = next - rank * p.q_heads;
-      it.kv_head = it.head / p.group;
-      int pair;
-      work.find(p, rank, it.seq, pair);
-      const Sequence x = sequence_of<false>(p, it.seq);
-      fill_rows(p, x, pair * 2 * kRows, it);
-      it.n[0] = key_tiles(p, x, it.tok[0] + it.cnt[0]);
-      it.n[1] = key_tiles(p, x, it.tok[1] + it.cnt[1]);
-      it.tiles = max(it.n[0], it.n[1]);
-      if (it.alternate) share_tiles(it);
-      it.masked_from = p.causal ? min(x.kv_len, max(it.tok[0] + x.off + 1, 0)) : x.kv_len;
-      publish(it);
-    }
-  } else {
-    // the length of the line, then this CTA's part of it
-    int64_t sum = 0;
-#pragma unroll 1
-    for (int s = lane; s < p.sequences; s += 32) sum += TreeWork::units(p, sequence_of<true>(p, s));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int64_t total = sum;
-    const int64_t parts = min((int64_t)gridDim.x, total);
-    int* const join = p.joins + (size_t)blockIdx.x * kJoinInts;
-    if (lane == 0) join[0] = 0;
-    if ((int64_t)blockIdx.x < parts) {
-      int64_t u = total * blockIdx.x / parts;
-      const int64_t hi = total * (blockIdx.x + 1) / parts;
-      // the sequence that u lies in
-      int seq = 0;
-      int64_t first = 0;  // its first unit
-#pragma unroll 1
-      for (int s0 = 0; s0 < p.sequences; s0 += 32) {
-        const int64_t mine = s0 + lane < p.sequences ? TreeWork::units(p, sequence_of<true>(p, s0 + lane)) : 0;
-        int64_t run = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, first + run > u);
-        if (past) {
-          const int at = __ffs(past) - 1;
-          seq = s0 + at;
-          first += __shfl_sync(0xffffffffu, run - mine, at);
-          break;
-        }
-        first += __shfl_sync(0xffffffffu, run, 31);
-      }
-      while (u < hi) {
-        const Sequence x = sequence_of<true>(p, seq);
-        const int64_t have = TreeWork::units(p, x);
-        if (u >= first + have) {  // on to the next sequence
-          first += have;
-          ++seq;
-          continue;
-        }
-        const int keys = ceil_div(x.kv_len, kKeys), sets = TreeWork::row_sets(p, x);
-        const int64_t in = u - first;
-        const int t0 = (int)(in % keys);
-        const int which = (int)(in / keys);
-        const int set = which % sets, head = which / sets;
-        const int t1 = (int)min((int64_t)keys, t0 + (hi - u));
-        it.seq = seq;
-        it.kv_head = head;
-        it.head = head * p.group;
-        fill_rows(p, x, set * 2 * p.tile_tokens, it);
-        it.kv_tile = t0;
-        it.tiles = it.n[0] = it.n[1] = t1 - t0;
-        if (it.alternate) share_tiles(it);
-        it.masked_from = p.mask ? min(x.off, x.kv_len) : min(x.kv_len, it.tok[0] + x.off + 1);
-        const bool whole = t0 == 0 && t1 == keys;
-        it.slot = whole ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
-        if (!whole && t0 == 0 && lane == 0) {
-          // this CTA holds the first keys of an item that goes on: the record of its join
-          const int64_t end = u - t0 + keys;  // unit after the item's last
-          join[1] = (int)((end * parts - 1) / total);  // the CTA of its last unit
-          join[2] = x.q0 + it.tok[0];
-          join[3] = (it.alternate ? it.cnt[0] : it.cnt[0] + it.cnt[1]) * p.pack;  // rows
-          join[4] = it.head;
-          join[0] = 1;
-        }
-        u += it.tiles;
-        if (!room()) return;
-        publish(it);
-      }
-    }
   }
-  if (!room()) return;
-  publish(Item{});
 }
 
 // ------------------------------------------------------------------- producer
@@ -393,8 +485,8 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
         ptx::mbar_arrive_expect_tx(bars.q_full(s), bytes * L::kHalves);
 #pragma unroll
         for (int h = 0; h < L::kHalves; ++h)
-          ptx::tma_load_3d(smem + s * L::kTileBytes + h * L::kHalfBytes, &p.qmap, bars.q_full(s), h * 64, it.head,
-                           it.q0 + it.tok[s]);
+          ptx::tma_load_3d(smem + s * L::kTileBytes + h * L::kHalfBytes, &p.qmap, bars.q_full(s), h * 64,
+                           it.head + s * it.head_step, it.q0 + it.tok[s]);
       }
       __syncwarp();
     }
@@ -839,31 +931,6 @@ __device__ __noinline__ float tile_max(uint32_t t_s) {
   return top;
 }
 
-// Lane 4 g + j has x[i] = piece i of row 4 g + j; afterwards x[i] = piece j of row
-// 4 g + i.
-__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
-  auto exchange = [](uint4& send, int bit) {
-    send.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
-    send.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
-    send.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
-    send.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
-  };
-#pragma unroll
-  for (int bit = 1; bit <= 2; bit <<= 1) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e & bit) continue;
-      // the lower lane keeps the lower piece and sends the upper one
-      const bool upper = lane & bit;
-      const uint4 keep = upper ? x[e | bit] : x[e];
-      uint4 send = upper ? x[e] : x[e | bit];
-      exchange(send, bit);
-      x[e] = upper ? send : keep;
-      x[e | bit] = upper ? keep : send;
-    }
-  }
-}
-
 // O *= keep.  The last product into it has ended: the scores that showed the new
 // maximum were issued after it.
 template <int kD>
@@ -1009,78 +1076,46 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
     const bool repair = *flag != 0;
     if (any) {
       const Row own = row_of<kPaged>(p, it, s, r);
-      const bool whole = !kPaged || it.slot < 0;
+      const bool whole = it.slot < 0;
       if (whole) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         scale0 *= inv;
         scale1 *= inv;
       }
       const int tile_row = (it.alternate ? 0 : s * p.tile_tokens * p.pack) + r;
-      const int64_t out_at = (int64_t)(it.q0 + own.token) * p.out_ts +
-                             (it.head + (p.pack == 1 ? 0 : r - (own.token - it.tok[s]) * p.pack)) * p.out_hs;
-      float* const part = kPaged && !whole ? p.partial + ((size_t)it.slot * p.partial_rows + tile_row) * kD : nullptr;
-      // A row's results are in one lane.  Four lanes exchange theirs, so that each
-      // stores 16 bytes of all four rows and together 64 consecutive bytes of one:
-      // with a row a lane, every store would touch 32 lines.
-      const uint32_t rows_there = __ballot_sync(0xffffffffu, own.there);
+      const int head = it.head + s * (it.alternate ? 0 : it.head_step) + (p.pack == 1 ? 0 : r - (own.token - it.tok[s]) * p.pack);
+      uint16_t* const out = p.out + (int64_t)(it.q0 + own.token) * p.out_ts + head * p.out_hs;
+      float* const part = whole ? nullptr : p.partial + ((size_t)it.slot * p.partial_rows + tile_row) * kD;
 #pragma unroll 1
-      for (int col = col0; col < col1; col += 32) {
-        uint32_t o[32];
-        if (has0) {
-          ptx::tmem_ld_32x32b_x32(t_o + col, o);
-          ptx::tmem_ld_wait();
+      for (int col = col0; col < col1; col += 16) {
+        uint32_t o[16], a[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale0);
-        } else {
+        for (int e = 0; e < 16; ++e) o[e] = a[e] = 0;
+        if (has0) ptx::tmem_ld_32x32b_x16(t_o + col, o);
+        if (has1) ptx::tmem_ld_32x32b_x16(t_o + kD + col, a);
+        ptx::tmem_ld_wait();
+        if (!own.there) continue;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
-        }
-        if (has1) {
-          uint32_t a[32];
-          ptx::tmem_ld_32x32b_x32(t_o + kD + col, a);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(a[e]), scale1, __uint_as_float(o[e])));
-        }
+        for (int e = 0; e < 16; ++e)
+          o[e] = __float_as_uint(fmaf(__uint_as_float(a[e]), scale1, __uint_as_float(o[e]) * scale0));
         if (whole) {
-          uint4 x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = make_uint4(pack2<kF16>(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-                              pack2<kF16>(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-                              pack2<kF16>(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-                              pack2<kF16>(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-          transpose4(x, lane);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int from = (lane & ~3) + e;  // the lane of the row that x[e] is of
-            const int64_t at = __shfl_sync(0xffffffffu, out_at, from);
-            if (rows_there >> from & 1u) *reinterpret_cast<uint4*>(p.out + at + col + (lane & 3) * 8) = x[e];
-          }
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(out + col + e) =
+                make_uint4(pack2<kF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                           pack2<kF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                           pack2<kF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
+                           pack2<kF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
         } else {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint4 x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = make_uint4(o[16 * g + 4 * e], o[16 * g + 4 * e + 1], o[16 * g + 4 * e + 2], o[16 * g + 4 * e + 3]);
-            transpose4(x, lane);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int from = (lane & ~3) + e;
-              if (rows_there >> from & 1u)
-                *reinterpret_cast<uint4*>(part + (from - lane) * kD + col + 16 * g + (lane & 3) * 4) = x[e];
-            }
-          }
+          for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(part + col + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-      if (repair) {
-        // reads what the other lanes of the four have stored of its row
-        __syncwarp();
-        if (own.there)
-          add_not_finite<kF16, kPaged>(&p, &it, own, max(it.masked_from / kKeys, it.kv_tile) * kKeys,
-                                       min(it.kv_len, (it.kv_tile + it.tiles) * kKeys), col0, col1, p.out + out_at, part);
-      }
-      if (kPaged && !whole && own.there && col0 == 0) {
+      __syncwarp();
+      if (repair && own.there)
+        add_not_finite<kF16, kPaged>(&p, &it, own, max(it.masked_from / kKeys, it.kv_tile) * kKeys,
+                                     min(it.kv_len, (it.kv_tile + it.tiles) * kKeys), col0, col1, out, part);
+      if (!whole && own.there && col0 == 0) {
         float* const ml =
             p.partial + (size_t)gridDim.x * 2 * p.partial_rows * kD + ((size_t)it.slot * p.partial_rows + tile_row) * 2;
         ml[0] = m;

@@ -39,11 +39,11 @@ constexpr int kRows = 128;        // query rows of a tile (MMA M, TMEM lanes)
 constexpr int kKeys = 128;        // keys of a tile
 constexpr int kAttnThreads = 384;  // 2 x 4 softmax warps, then producer, MMA and scheduler warps and an idle one
 
-// Workspace: status words, the prompt scheduler's counter, then (trees) a
-// join record per CTA and the partial results of split work.
+// Workspace: status words and the counter that prompts draw from, then a join
+// record per CTA and the partial results of split work.
 constexpr size_t kAttnStatusBytes = 256;
 constexpr size_t kCounterOffset = 128;
-constexpr int kJoinInts = 8;
+constexpr int kJoinInts = 8;  // 1 (or 0: no join); first tile's token, rows, head; last CTA; second tile's token, rows, head
 
 // One attention problem.  Prompts: packed rows of keys and values.  Trees: a
 // paged cache, whose places take the part of the key rows.
@@ -59,9 +59,9 @@ struct __align__(128) AttnParams {
   const int32_t* page_table;
   const int64_t* mask;
   int* status;
-  int* counter;   // prompts: next item
-  int* joins;     // trees: [CTAs][kJoinInts]
-  float* partial;  // trees: [CTAs][2][rows][head_dim], then [CTAs][2][rows][2] (maximum, sum)
+  int* counter;    // prompts: items drawn
+  int* joins;      // [CTAs][kJoinInts]
+  float* partial;  // [CTAs][2][rows][head_dim], then [CTAs][2][rows][2] (maximum, sum)
   int64_t tokens, kv_tokens;
   int64_t v_ts, v_hs, v_ps;  // token (place), head and page strides of v
   int64_t out_ts, out_hs;
@@ -73,6 +73,9 @@ struct __align__(128) AttnParams {
   int pack;                      // heads a tile packs per token: group for trees, 1 for prompts
   int tile_tokens;               // tokens of a row tile: 128 / pack
   int causal, max_nodes;
+  int pair_heads;                // prompts: one-tile items have two heads
+  int by_draw;                   // prompts: whole items from the counter, no cuts
+  int min_tiles;                 // least key tiles of an item on either side of a cut
   int partial_rows;              // rows of a partial slot
   float scale_log2;              // scale * log2(e)
   int test_drop_first_load;      // test hook: the producer skips its first load, so a wait runs out
@@ -88,7 +91,7 @@ AttnFn tree_kernel(int head_dim, bool f16);
 
 cudaError_t prepare_attention(const AttnFn& k);
 cudaError_t launch_attention(const AttnFn& k, const AttnParams& p, int ctas, cudaStream_t stream);
-// Sums the parts of split work (trees), after launch_attention on the same stream.
+// Sums the parts of split work, after launch_attention on the same stream.
 cudaError_t launch_join(const AttnParams& p, int head_dim, bool f16, int ctas, cudaStream_t stream);
 
 }  // namespace agmm
