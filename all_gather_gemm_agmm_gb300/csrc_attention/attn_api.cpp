@@ -413,6 +413,12 @@ agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, v
     AGMM_TRY(encode_kv(&p.kmap, "k", plan, a->k, a->kv_tokens, 1, a->k_token_stride, a->k_head_stride, 0, kKeys));
     AGMM_TRY(encode_kv(&p.vmap, "v", plan, a->v, a->kv_tokens, 1, a->v_token_stride, a->v_head_stride, 0, kKeys));
   }
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_ts = a->q_token_stride;
+  p.q_hs = a->q_head_stride;
+  p.k = static_cast<const uint16_t*>(a->k);
+  p.k_ts = a->k_token_stride;
+  p.k_hs = a->k_head_stride;
   p.v = static_cast<const uint16_t*>(a->v);
   p.v_ts = a->v_token_stride;
   p.v_hs = a->v_head_stride;
@@ -500,10 +506,14 @@ agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* s
                      a->cache_head_stride, a->cache_page_stride, box_rows));
   AGMM_TRY(encode_kv(&p.vmap, "v_cache", plan, a->v_cache, plan->page_size, a->pages, a->cache_token_stride,
                      a->cache_head_stride, a->cache_page_stride, box_rows));
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_ts = a->q_token_stride;
+  p.q_hs = a->q_head_stride;
+  p.k = static_cast<const uint16_t*>(a->k_cache);
   p.v = static_cast<const uint16_t*>(a->v_cache);
-  p.v_ts = a->cache_token_stride;
-  p.v_hs = a->cache_head_stride;
-  p.v_ps = a->cache_page_stride;
+  p.k_ts = p.v_ts = a->cache_token_stride;
+  p.k_hs = p.v_hs = a->cache_head_stride;
+  p.k_ps = p.v_ps = a->cache_page_stride;
   p.out = static_cast<uint16_t*>(a->out);
   p.out_ts = a->out_token_stride;
   p.out_hs = a->out_head_stride;

@@ -34,9 +34,9 @@
 // every CTA are not cut: the CTAs draw them from a counter (struct Draw).
 //
 // What a row does not see never reaches it: its scores are replaced, not
-// added to; value rows past the end are cleared in shared memory; and in a
-// tile that only some rows see, values that are not finite are taken out of the
-// product and added at the end to the rows that see them.
+// added to; value rows past the end are cleared in shared memory; and a row whose
+// result is not finite, in an item with a value that is not finite and that the row
+// does not see, is computed again without it.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -766,79 +766,88 @@ __device__ __forceinline__ uint32_t seen32(const Item& it, const Row& row, int w
   return bits & low_bits(it.kv_len - place);
 }
 
-// One 16-byte piece of 16-bit values with those that are not finite set to 0.
 template <bool kF16>
-__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-  constexpr uint32_t kExp = kF16 ? 0x7c00u : 0x7f80u;
-  if ((w & kExp) == kExp) w &= 0xffff0000u;
-  if ((w >> 16 & kExp) == kExp) w &= 0x0000ffffu;
-  return w;
+__device__ __forceinline__ bool not_finite(uint16_t b) {
+  constexpr uint16_t kExp = kF16 ? 0x7c00u : 0x7f80u;
+  return (b & kExp) == kExp;
 }
 
-// Row r of a V tile (key `place`): cleared if it lies past the keys; else
-// values that are not finite are cleared and reported.
-template <int kD, bool kF16>
-__device__ __forceinline__ void clean_value_row(uint8_t* tile, int r, bool past, volatile int* flag) {
-  using L = Layout<kD>;
-  constexpr uint32_t kInf2 = kF16 ? 0x7c007c00u : 0x7f807f80u;
-#pragma unroll 1
-  for (int h = 0; h < L::kHalves; ++h) {
-    uint4* const row = reinterpret_cast<uint4*>(tile + h * L::kHalfBytes + r * 128);
-    if (past) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) row[(c + r) & 7] = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint4 v = row[(c + r) & 7];
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                   __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-    }
-    if (__vcmpgeu2(top, kInf2)) {
-      *flag = 1;
-      __threadfence_block();
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint4 v = row[c];
-        v.x = finite_only<kF16>(v.x);
-        v.y = finite_only<kF16>(v.y);
-        v.z = finite_only<kF16>(v.z);
-        v.w = finite_only<kF16>(v.w);
-        row[c] = v;
-      }
-    }
+// Offset of (place, column 0) in keys (or values) with these strides; -1: a page
+// outside the cache, which reads as zeros.
+template <bool kPaged>
+__device__ __forceinline__ int64_t row_offset(const AttnParams& p, const Item& it, int place, int64_t ts, int64_t hs, int64_t ps) {
+  if constexpr (kPaged) {
+    const int64_t page = __ldg(p.page_table + it.seq * p.table_stride + (place >> p.page_shift));
+    if (page < 0 || page >= p.pages) return -1;
+    return page * ps + (int64_t)(place & ((1 << p.page_shift) - 1)) * ts + it.kv_head * hs;
+  } else {
+    return ((int64_t)it.kv_row + place) * ts + it.kv_head * hs;
   }
 }
 
-// Adds to columns [col0, col1) of a row's result, where it has been written, the
-// values that are not finite of the places [from, to) that the row sees: they
-// were left out of the products there.  `part`: the result in float32, else `out`.
-template <bool kF16, bool kPaged>
-__device__ __noinline__ void add_not_finite(const AttnParams* p, const Item* it, Row row, int from, int to, int col0, int col1,
-                                            uint16_t* out, float* part) {
-  constexpr uint16_t kExp = kF16 ? 0x7c00u : 0x7f80u;
+// The exact results of rows whose products came out not finite (`rows`: lanes of
+// this warp).  In a tile that a row does not see all of, a value that is not finite
+// times a weight of zero is not zero.  Where there is such a value that the row
+// does not see, its result is computed again, key by key, with the weights that it had
+// (m, l); else it stands.  A warp takes a row at a time: a lane takes a key's
+// score, then some columns of all 32 keys' values.  Slow (0.1 us a key and 32 rows) and rare.
+template <int kD, bool kF16, bool kPaged>
+__device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, int s, uint32_t rows, float m, float l, int col0,
+                                         int col1, uint16_t* out, float* part) {
+  constexpr int kN = kD / 32;
+  const int lane = threadIdx.x & 31;
+  const int begin = it->kv_tile * kKeys, end = min(it->kv_len, (it->kv_tile + it->tiles) * kKeys);
 #pragma unroll 1
-  for (int place = from; place < to; ++place) {
-    if (!(seen32(*it, row, p->mask_words, place) & 1u)) continue;
-    const uint16_t* v;
-    if constexpr (kPaged) {
-      const int64_t page = __ldg(p->page_table + it->seq * p->table_stride + (place >> p->page_shift));
-      if (page < 0 || page >= p->pages) continue;
-      v = p->v + page * p->v_ps + (int64_t)(place & ((1 << p->page_shift) - 1)) * p->v_ts;
-    } else {
-      v = p->v + ((int64_t)it->kv_row + place) * p->v_ts;
+  for (; rows; rows &= rows - 1) {
+    const int from = __ffs(rows) - 1;
+    const Row row = row_of<kPaged>(*p, *it, s, (threadIdx.x & 96) + from);
+    bool found = false;
+#pragma unroll 1
+    for (int place = max(it->masked_from / kKeys * kKeys, begin) + lane; place < end; place += 32) {
+      if (seen32(*it, row, p->mask_words, place) & 1u) continue;
+      const int64_t at = row_offset<kPaged>(*p, *it, place, p->v_ts, p->v_hs, p->v_ps);
+#pragma unroll 1
+      for (int c = col0; c < col1 && at >= 0; ++c) found |= not_finite<kF16>(p->v[at + c]);
     }
-    v += it->kv_head * p->v_hs;
+    if (!__any_sync(0xffffffffu, found)) continue;
+    const float row_m = __shfl_sync(0xffffffffu, m, from), row_l = __shfl_sync(0xffffffffu, l, from);
+    const float shift = row_m == -INFINITY ? 0.0f : -row_m * p->scale_log2;
+    const int head = it->head + s * (it->alternate ? 0 : it->head_step) +
+                     (p->pack == 1 ? 0 : (threadIdx.x & 96) + from - (row.token - it->tok[s]) * p->pack);
+    const uint16_t* const q = p->q + (int64_t)(it->q0 + row.token) * p->q_ts + head * p->q_hs;
+    float o[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) o[e] = 0.0f;
 #pragma unroll 1
-    for (int c = col0; c < col1; ++c) {
-      if ((v[c] & kExp) != kExp) continue;
-      const float x = value16<kF16>(v[c]);
-      if (part)
-        part[c] += x;
+    for (int place0 = begin; place0 < end; place0 += 32) {
+      float w = 0.0f;
+      int64_t v_at = -1;
+      if (place0 + lane < end && (seen32(*it, row, p->mask_words, place0 + lane) & 1u)) {
+        const int64_t k_at = row_offset<kPaged>(*p, *it, place0 + lane, p->k_ts, p->k_hs, p->k_ps);
+        v_at = row_offset<kPaged>(*p, *it, place0 + lane, p->v_ts, p->v_hs, p->v_ps);
+        float dot = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < kD && k_at >= 0; ++c) dot = fmaf(value16<kF16>(q[c]), value16<kF16>(p->k[k_at + c]), dot);
+        w = value16<kF16>((uint16_t)pack2<kF16>(ptx::exp2_approx(fmaf(dot, p->scale_log2, shift)), 0.0f));
+      }
+#pragma unroll 1
+      for (int j = 0; j < 32; ++j) {
+        const int64_t at = __shfl_sync(0xffffffffu, v_at, j);
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        if (at < 0) continue;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) o[e] = fmaf(wj, value16<kF16>(p->v[at + lane * kN + e]), o[e]);
+      }
+    }
+    uint16_t* const row_out = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(out), from));
+    float* const row_part = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(part), from));
+    if (lane * kN < col0 || lane * kN >= col1) continue;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      if (row_part)
+        row_part[lane * kN + e] = o[e];
       else
-        out[c] = (uint16_t)pack2<kF16>(value16<kF16>(out[c]) + x, 0.0f);
+        row_out[lane * kN + e] = (uint16_t)pack2<kF16>(row_l == 0.0f ? 0.0f : o[e] / row_l, 0.0f);
     }
   }
 }
@@ -877,15 +886,19 @@ __device__ __forceinline__ void weights(const uint32_t (&a)[32], const uint32_t 
 // their own, called when no scores are held in registers: the key loop stays
 // short enough for the instruction cache and spills nothing.
 
-// Looks over the value tile of a key tile that not all rows of the item see
-// (while its scores are still being computed).
-template <int kD, bool kF16>
-__device__ __noinline__ bool clean_values(const Waiter* wait, uint32_t value_bar, uint32_t parity, uint8_t* value_tile, int place,
-                                          int kv_len, volatile int* flag) {
+// Clears the rows of a value tile that lie past the keys: they may hold anything, and
+// a weight of zero does not make up for it.
+template <int kD>
+__device__ __noinline__ bool clear_past(const Waiter* wait, uint32_t value_bar, uint32_t parity, uint8_t* value_tile, int keys) {
+  using L = Layout<kD>;
   const int r = threadIdx.x & 127;
   if (!(*wait)(value_bar, parity, 8000)) return false;
-  clean_value_row<kD, kF16>(value_tile, r, place + r >= kv_len, flag);
-  ptx::fence_proxy_async_smem();
+  if (r >= keys) {
+#pragma unroll 1
+    for (int c = 0; c < kD / 8; ++c)
+      reinterpret_cast<uint4*>(value_tile + (c >> 3) * L::kHalfBytes + r * 128)[(c + r) & 7] = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+  }
   return true;
 }
 
@@ -899,8 +912,10 @@ __device__ __noinline__ void mask_scores(const AttnParams* p, const Item* it, ui
     const uint32_t bits = seen32(*it, row, p->mask_words, place + 32 * w);
     if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
     uint32_t v[32];
-    ptx::tmem_ld_32x32b_x32(t_s + w * 32, v);
-    ptx::tmem_ld_wait();
+    if (__any_sync(0xffffffffu, bits)) {
+      ptx::tmem_ld_32x32b_x32(t_s + w * 32, v);
+      ptx::tmem_ld_wait();
+    }
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (!(bits >> e & 1u)) v[e] = 0xff800000u;
@@ -931,6 +946,41 @@ __device__ __noinline__ float tile_max(uint32_t t_s) {
   return top;
 }
 
+// Stores kWords 32-bit words of each lane's row to `to`, the lane's own address.  Lane
+// 4 g + j has piece i (16 bytes) of row 4 g + j in words 4 i ..; after two
+// exchanges it has piece j of row 4 g + i.
+template <int kWords, typename T>
+__device__ __forceinline__ void store_rows(const uint32_t (&words)[kWords], int lane, uint32_t rows, T* to) {
+#pragma unroll
+  for (int w = 0; w < kWords; w += 16) {
+    uint32_t x[4][4];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e / 4][e % 4] = words[w + e];
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+      const bool upper = lane & bit;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (e & bit) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // the lower lane keeps the lower piece and sends the upper one
+          const uint32_t keep = upper ? x[e | bit][q] : x[e][q];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[e][q] : x[e | bit][q], bit);
+          x[e][q] = upper ? got : keep;
+          x[e | bit][q] = upper ? keep : got;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int from = (lane & ~3) + e;
+      T* const at = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(to), from));
+      if (rows >> from & 1u) reinterpret_cast<uint4*>(at)[w / 4 + (lane & 3)] = make_uint4(x[e][0], x[e][1], x[e][2], x[e][3]);
+    }
+  }
+}
+
 // O *= keep.  The last product into it has ended: the scores that showed the new
 // maximum were issued after it.
 template <int kD>
@@ -955,7 +1005,7 @@ __device__ __forceinline__ void load_scores(uint32_t t_s, uint32_t (&v)[4][32]) 
 
 template <int kD, bool kF16, bool kPaged>
 __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, const Item* slots, uint8_t* smem, uint32_t tmem,
-                                        const Waiter& wait, int s, float* stats, volatile int* flag) {
+                                        const Waiter& wait, int s, float* stats) {
   using L = Layout<kD>;
   const int lane = threadIdx.x & 31;
   const int r = threadIdx.x & 127;  // the row this thread owns
@@ -982,12 +1032,10 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
 #pragma unroll 1
     for (int i = 0; i < n; ++i, place += stride) {
       const bool partly = place + kKeys > edge;
-      if (partly) {
-        // Both streams look over the value tile of a key tile that either has rows
-        // which do not see all of: what one takes out, the other has to know of.
+      if (place + kKeys > it.kv_len) {
         const uint32_t f = fills + (uint32_t)v_index(place / kKeys - it.kv_tile, it.alternate ? 2 : 1, it.tiles);
-        ok = clean_values<kD, kF16>(&wait, bars.v_there(s, steps + i), (steps + i) >> 1 & 1u, smem + L::kRing + (f % L::kStages) * L::kTileBytes,
-                                    place, it.kv_len, flag);
+        ok = clear_past<kD>(&wait, bars.v_there(s, steps + i), (steps + i) >> 1 & 1u, smem + L::kRing + (f % L::kStages) * L::kTileBytes,
+                            it.kv_len - place);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
@@ -1072,8 +1120,6 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
       scale0 = scale1 = 1.0f;
     }
     ptx::tc_fence_after();
-    __threadfence_block();
-    const bool repair = *flag != 0;
     if (any) {
       const Row own = row_of<kPaged>(p, it, s, r);
       const bool whole = it.slot < 0;
@@ -1086,35 +1132,51 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
       const int head = it.head + s * (it.alternate ? 0 : it.head_step) + (p.pack == 1 ? 0 : r - (own.token - it.tok[s]) * p.pack);
       uint16_t* const out = p.out + (int64_t)(it.q0 + own.token) * p.out_ts + head * p.out_hs;
       float* const part = whole ? nullptr : p.partial + ((size_t)it.slot * p.partial_rows + tile_row) * kD;
+      // A row's results are in one lane.  Four lanes exchange theirs, so that each
+      // stores 16 bytes of all four rows and together 64 consecutive bytes of one: a
+      // store of 32 rows takes a cycle for each of 32 lines and more, 3400 cycles a tile
+      // against 1300.
+      const uint32_t rows_there = __ballot_sync(0xffffffffu, own.there);
+      uint32_t top = 0;  // of the results' magnitudes, as 16-bit pairs
 #pragma unroll 1
-      for (int col = col0; col < col1; col += 16) {
-        uint32_t o[16], a[16];
+      for (int col = col0; col < col1; col += 32) {
+        uint32_t o[32];
+        if (has0 != has1) {
+          ptx::tmem_ld_32x32b_x32(t_o + (has1 ? kD : 0) + col, o);
+          ptx::tmem_ld_wait();
+          const float scale = has1 ? scale1 : scale0;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = a[e] = 0;
-        if (has0) ptx::tmem_ld_32x32b_x16(t_o + col, o);
-        if (has1) ptx::tmem_ld_32x32b_x16(t_o + kD + col, a);
-        ptx::tmem_ld_wait();
-        if (!own.there) continue;
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+        } else if (has0) {
+          uint32_t a[32];
+          ptx::tmem_ld_32x32b_x32(t_o + col, o);
+          ptx::tmem_ld_32x32b_x32(t_o + kD + col, a);
+          ptx::tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          o[e] = __float_as_uint(fmaf(__uint_as_float(a[e]), scale1, __uint_as_float(o[e]) * scale0));
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            *reinterpret_cast<uint4*>(out + col + e) =
-                make_uint4(pack2<kF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                           pack2<kF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                           pack2<kF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
-                           pack2<kF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(fmaf(__uint_as_float(a[e]), scale1, __uint_as_float(o[e]) * scale0));
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(part + col + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; ++e) o[e] = 0;
         }
+        uint32_t packed[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          packed[e] = pack2<kF16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          top = __vmaxu2(top, packed[e] & 0x7fff7fffu);
+        }
+        if (whole)
+          store_rows(packed, lane, rows_there, out + col);
+        else
+          store_rows(o, lane, rows_there, part + col);
       }
-      __syncwarp();
-      if (repair && own.there)
-        add_not_finite<kF16, kPaged>(&p, &it, own, max(it.masked_from / kKeys, it.kv_tile) * kKeys,
-                                     min(it.kv_len, (it.kv_tile + it.tiles) * kKeys), col0, col1, out, part);
+      // (a weight sum that is NaN makes the row NaN, as it should be)
+      constexpr uint32_t kInf2 = kF16 ? 0x7c007c00u : 0x7f807f80u;
+      const uint32_t bad = __ballot_sync(0xffffffffu, own.there && l == l && __vcmpgeu2(top, kInf2) != 0);
+      if (bad) {
+        __syncwarp();  // the other lanes' stores come first
+        repair_rows<kD, kF16, kPaged>(&p, &it, s, bad, m, l, col0, col1, out, part);
+      }
       if (!whole && own.there && col0 == 0) {
         float* const ml =
             p.partial + (size_t)gridDim.x * 2 * p.partial_rows * kD + ((size_t)it.slot * p.partial_rows + tile_row) * 2;
@@ -1151,7 +1213,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
   }
   const Bars bars{smem + L::kBars, L::kStages};
   Item* const slots = reinterpret_cast<Item*>(base + L::kItems);
-  int* const flags = reinterpret_cast<int*>(base + L::kFlags);  // [0] abort, [1] TMEM base, [2] values that are not finite were taken out
+  int* const flags = reinterpret_cast<int*>(base + L::kFlags);  // [0] abort, [1] TMEM base
   float* const stats = reinterpret_cast<float*>(base + L::kStats);
 
   if (warp == 9) {
@@ -1159,7 +1221,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
     ptx::tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    flags[0] = flags[2] = 0;
+    flags[0] = 0;
     for (int i = 0; i < L::kStages; ++i) {
       ptx::mbar_init(bars.full(i), 1);
       ptx::mbar_init(bars.empty(i), 2);  // both MMA warps
@@ -1202,7 +1264,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
   else
     ptx::fewer_registers<72>();
   if (warp < 8) {
-    softmax<kD, kF16, kPaged>(p, bars, slots, base, tmem, wait, warp >> 2, stats, flags + 2);
+    softmax<kD, kF16, kPaged>(p, bars, slots, base, tmem, wait, warp >> 2, stats);
   } else if (warp == 8) {
     if (lane == 0) {
       ptx::prefetch_tensormap(&p.qmap);

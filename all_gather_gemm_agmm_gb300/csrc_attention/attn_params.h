@@ -51,7 +51,9 @@ struct __align__(128) AttnParams {
   CUtensorMap qmap;  // {head_dim, q_heads, tokens}: a box is 64 columns of one tile's rows
   CUtensorMap kmap;  // {head_dim, tokens or places, kv_heads, pages}: 64 columns of up to 128 rows
   CUtensorMap vmap;
-  const uint16_t* v;  // the values again, for plain loads
+  const uint16_t* q;  // the same again, for plain loads
+  const uint16_t* k;
+  const uint16_t* v;
   uint16_t* out;
   const int32_t* starts;     // query rows of each sequence (nodes of a tree)
   const int32_t* kv_starts;  // prompts: key rows of each sequence
@@ -63,7 +65,9 @@ struct __align__(128) AttnParams {
   int* joins;      // [CTAs][kJoinInts]
   float* partial;  // [CTAs][2][rows][head_dim], then [CTAs][2][rows][2] (maximum, sum)
   int64_t tokens, kv_tokens;
-  int64_t v_ts, v_hs, v_ps;  // token (place), head and page strides of v
+  int64_t q_ts, q_hs;        // token and head strides
+  int64_t k_ts, k_hs, k_ps;  // token (place), head and page strides
+  int64_t v_ts, v_hs, v_ps;
   int64_t out_ts, out_hs;
   int64_t table_stride, table_pages, pages;
   uint64_t wait_limit_cycles;
