@@ -23,7 +23,7 @@
 namespace agmm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kInFlight = 3;  // heads a thread loads before it works on the first
 
 template <bool kF16>
@@ -58,7 +58,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 template <int kD, bool kF16>
-__global__ void __launch_bounds__(kThreads) agmm_norm_rope(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, 8) agmm_norm_rope(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = kD / 16;            // lanes per head
   constexpr int kGroups = kThreads / kLanes;  // heads in flight per block
   __shared__ float s_cos[kD / 2], s_sin[kD / 2];
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) agmm_norm_rope(const __grid_constant
   int64_t slot = -1;
   if (p.k_cache) slot = p.slots[t];
 
+  static_assert(kD / 2 <= kThreads, "a thread for every pair");
   if ((int)threadIdx.x < p.pairs) {
     const int i = threadIdx.x;
     const int64_t at = (int64_t)p.axis[i] * p.position_axis_stride + t;
