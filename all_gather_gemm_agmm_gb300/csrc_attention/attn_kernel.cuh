@@ -51,6 +51,7 @@ namespace agmm {
 namespace {
 
 constexpr int kItemSlots = 2;
+constexpr int kDrawAhead = 3;  // key tiles still to be loaded when the next item is asked for
 constexpr float kMaxGrowth = 8.0f;  // log2 of how far the weights may grow past 1
 
 template <int kD>
@@ -63,7 +64,7 @@ struct Layout {
   static constexpr uint32_t kCtl = kRing + kStages * kTileBytes;
   // control block
   static constexpr uint32_t kBars = kCtl;
-  static constexpr uint32_t kItems = kCtl + 376;                // kItemSlots x 96 bytes
+  static constexpr uint32_t kItems = kCtl + 384;                // kItemSlots x 96 bytes
   static constexpr uint32_t kFlags = kItems + kItemSlots * 96;  // abort, TMEM base, non-finite flag
   static constexpr uint32_t kStats = kFlags + 16;               // [2 streams][128 rows][2] float
   static constexpr size_t kBytes = kStats + 2 * 128 * 2 * 4;
@@ -89,6 +90,7 @@ struct Bars {
   // know that the tile before had its arrival
   __device__ __forceinline__ uint32_t v_there(int s, uint32_t tile) const { return base + 8 * (41 + 2 * s + (tile & 1u)); }
   __device__ __forceinline__ uint32_t turn(int s) const { return base + 8 * (45 + s); }
+  __device__ __forceinline__ uint32_t next_item() const { return base + 8 * 47; }
 };
 
 // A work item, written by the scheduler warp.
@@ -258,35 +260,43 @@ struct Line {
 
 // Prompts with many items for each CTA: whole items, drawn one at a time from a
 // counter, those of the last row set of their sequence first (they see the most
-// keys), then by sequence, then by head.  No result makes a round trip through
-// memory, and what the line's cost model misses evens out.
+// keys), and of one such level the sets of two tiles first, then by sequence, then
+// by head.  No result makes a round trip through memory, and what the line's cost
+// model misses evens out.
 struct Draw {
   const AttnParams& p;
   int lane;
-  int level, base, count;  // the row sets `level` of all sequences have the ranks [base, base + count)
+  int level, base, pairs, singles;  // the level's items begin at `base`; sequences with a two-tile, a one-tile set there
   int items, next;
 
-  __device__ __forceinline__ int sets_of(int s) const {
+  // Row sets of a sequence; `single`: the last one is a tile that has two heads to an item.
+  __device__ __forceinline__ int sets_of(int s, bool& single) const {
+    single = false;
+    if (s >= p.sequences) return 0;
     const int64_t a = min(max((int64_t)__ldg(p.starts + s), (int64_t)0), p.tokens);
     const int64_t b = min(max((int64_t)__ldg(p.starts + s + 1), a), p.tokens);
-    return (int)((b - a + 2 * kRows - 1) / (2 * kRows));
+    const int n = (int)((b - a + 2 * kRows - 1) / (2 * kRows));
+    single = p.pair_heads && n > 0 && b - a <= (int64_t)(2 * n - 1) * kRows;
+    return n;
   }
+  __device__ __forceinline__ int level_items() const { return pairs * p.q_heads + singles * (p.q_heads / 2); }
   __device__ __forceinline__ void init() {
     lane = threadIdx.x & 31;
     int most = 0, sum = 0;
 #pragma unroll 1
     for (int s = lane; s < p.sequences; s += 32) {
-      const int n = sets_of(s);
+      bool single;
+      const int n = sets_of(s, single);
       most = max(most, n);
-      sum += n;
+      sum += n * p.q_heads - (single ? p.q_heads - p.q_heads / 2 : 0);
     }
-    items = __reduce_add_sync(0xffffffffu, sum) * p.q_heads;
+    items = __reduce_add_sync(0xffffffffu, sum);
     level = __reduce_max_sync(0xffffffffu, most);
-    base = count = 0;
+    base = pairs = singles = 0;
     next = (int)blockIdx.x - (int)gridDim.x;  // the first item is this CTA's number
   }
-  // The next item, of Spot's seq, set and head (head: query head); false: none.
-  __device__ __forceinline__ bool draw(Spot& at) {
+  // The next item, of Spot's seq, set and head (among the set's); false: none.
+  __device__ __noinline__ bool draw(Spot& at) {
     if (next < 0) {
       next += gridDim.x;
     } else {
@@ -299,28 +309,40 @@ struct Draw {
       next = __shfl_sync(0xffffffffu, next, 0);
     }
     if (next >= items) return false;
-    const int rank = next / p.q_heads;
-    at.head = next - rank * p.q_heads;
-    while (rank >= base + count) {
-      base += count;
+    while (next >= base + level_items()) {
+      base += level_items();
       --level;
-      int c = 0;
+      int c = 0, d = 0;
 #pragma unroll 1
-      for (int s = lane; s < p.sequences; s += 32) c += sets_of(s) > level;
-      count = __reduce_add_sync(0xffffffffu, c);
+      for (int s = lane; s < p.sequences; s += 32) {
+        bool single;
+        const int n = sets_of(s, single);
+        const bool one = single && n == level + 1;
+        c += n > level && !one;
+        d += one;
+      }
+      pairs = __reduce_add_sync(0xffffffffu, c);
+      singles = __reduce_add_sync(0xffffffffu, d);
     }
     at.set = level;
-    int left = rank - base;
+    int left = next - base;
+    const bool want_single = left >= pairs * p.q_heads;
+    if (want_single) left -= pairs * p.q_heads;
+    const int heads = want_single ? p.q_heads / 2 : p.q_heads;
+    int rank = left / heads;
+    at.head = left - rank * heads;
 #pragma unroll 1
     for (int s0 = 0; s0 < p.sequences; s0 += 32) {
-      const int s = s0 + lane;
-      const uint32_t has = __ballot_sync(0xffffffffu, s < p.sequences && sets_of(s) > level);
-      const int n = __popc(has);
-      if (left < n) {
-        at.seq = s0 + (int)__fns(has, 0, left + 1);
+      bool single;
+      const int n = sets_of(s0 + lane, single);
+      const bool mine = n > level && (single && n == level + 1) == want_single;
+      const uint32_t has = __ballot_sync(0xffffffffu, mine);
+      const uint32_t here = __ballot_sync(0xffffffffu, mine && __popc(has & ((1u << lane) - 1u)) == rank);
+      if (here) {
+        at.seq = s0 + __ffs(here) - 1;
         return true;
       }
-      left -= n;
+      rank -= __popc(has);
     }
     return false;
   }
@@ -396,17 +418,15 @@ __device__ __forceinline__ void scheduler(const AttnParams& p, const Bars& bars,
   }
   int k = 0;
   for (bool more = true; more;) {
-    // An item is drawn when there is room for it, two ahead of the one at work at
-    // most: a CTA that drew more would hold them from the others.
+    // An item is drawn when the last loads of the one before come up: a CTA that
+    // drew further ahead would hold items from the others.
+    if (k > 0 && !wait.compact(bars.next_item(), (uint32_t)(k - 1) & 1u, 100000 + k)) return;
     if (k >= kItemSlots && !wait.compact(bars.item_empty(k % kItemSlots), (uint32_t)(k / kItemSlots - 1) & 1u, k)) return;
     Item it = {};
     if (by_draw) {
-      do
-        more = drawn.draw(at);
-      while (more && p.pair_heads && (at.head & 1) && line.single(x = sequence_of<false>(p, at.seq), at.set));
+      more = drawn.draw(at);
       if (more) {
         x = sequence_of<kPaged>(p, at.seq);
-        if (p.pair_heads && line.single(x, at.set)) at.head /= 2;
         it = make_item(p, line, x, at, 0, line.length(x, at.set));
       }
     } else {
@@ -473,6 +493,7 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bars.item_empty(slot));
     if (!it.valid) break;
+    if (it.tiles <= kDrawAhead && lane == 0) ptx::mbar_arrive(bars.next_item());
     if (it.tiles == 0) continue;
     for (int s = 0; s < 2 && ok; ++s) {
       if (s == 1 && it.alternate) break;
@@ -498,6 +519,7 @@ __device__ __forceinline__ void producer(const AttnParams& p, const Bars& bars, 
       const bool value = f & 1;
       const int t = value ? f >> 1 : (f >> 1) + lead;
       if (t < 0 || t >= it.tiles) continue;
+      if (value && t == it.tiles - 1 - kDrawAhead && lane == 0) ptx::mbar_arrive(bars.next_item());
       const CUtensorMap* const map = value ? &p.vmap : &p.kmap;
       const int st = (int)(fills % L::kStages);
       ok = wait.compact(bars.empty(st), ((fills / L::kStages) & 1u) ^ 1u, 2000 + st);
@@ -1243,6 +1265,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
       ptx::mbar_init(bars.item_empty(i), 11);  // all warps but the scheduler's
     }
     ptx::mbar_init(bars.stats(), 8);
+    ptx::mbar_init(bars.next_item(), 1);
     ptx::mbar_init(bars.drained(0), 1);
     ptx::mbar_init(bars.drained(1), 1);
     ptx::fence_mbar_init();
