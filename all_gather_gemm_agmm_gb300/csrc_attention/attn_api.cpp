@@ -48,7 +48,11 @@ namespace {
 // A part of a prompt's item is at least this many key tiles: its results make a
 // round trip through device memory, 256 rows in float32.
 constexpr int kMinPromptTiles = 4;
-// From this many items for each CTA on, prompts draw whole items.
+// From this many items for each CTA on, prompts draw whole items; fewer are cut along
+// the keys.  Measured: 1.5 items (two pieces of 1024 and 700 tokens behind 8000 to
+// 15000 keys, 32 heads) 332 us drawn, 239 us cut; 4.1 items (prompts of 17 to 4001
+// tokens, 16 heads) 87 us drawn, 118 us cut; 6.7 items (one of 8191 tokens, 32 heads)
+// 341 us drawn, 418 us cut.
 constexpr int kDrawnItems = 2;
 
 agmm_status_t fail(agmm_status_t s, const char* fmt, ...) {
@@ -431,11 +435,10 @@ agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, v
   p.kv_tokens = a->kv_tokens;
   p.sequences = (int)a->sequences;
   p.causal = plan->causal;
-  // Two heads share the keys of a one-tile item where there are enough items for
-  // all CTAs without.
-  p.pair_heads = p.group % 2 == 0 && pairs * plan->q_heads >= 2 * plan->num_sms;
   p.min_tiles = kMinPromptTiles;
   p.by_draw = pairs * plan->q_heads >= (int64_t)kDrawnItems * plan->num_sms;
+  // then there are enough items for a one-tile set to take two heads, which share its keys
+  p.pair_heads = p.by_draw && p.group % 2 == 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   AGMM_TRY(launched(launch_attention(plan->kernel, p, plan->num_sms, s), "prompt"));
   // no cuts, or nothing long enough to be cut

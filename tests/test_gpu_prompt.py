@@ -185,6 +185,44 @@ def test_many_sequences(agmm):
     check(out.cpu(), want, bound)
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (6, 2, 64)], ids=str)
+def test_many_items_of_all_sizes(agmm, heads):
+    """Enough items that they are drawn, of many lengths: one and two tiles to a set, two heads to an item and one."""
+    hq, hk, d = heads
+    g = torch.Generator().manual_seed(hq)
+    lens = torch.randint(0, 280, (50,), generator=g).tolist() + [600, 1, 128, 129, 385, 384, 256, 0, 511]
+    kv_lens = [n + int(torch.randint(0, 200, (1,), generator=g)) for n in lens]
+    q, k, v = _make(lens, kv_lens, hq, hk, d, torch.bfloat16, seed=21)
+    want, bound = _ref(q, k, v, lens, kv_lens, True, d ** -0.5)
+    plan = agmm.PromptPlan(hq, hk, d)
+    ws = plan.new_workspace()
+    for _ in range(2):
+        out = torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+        plan.run(q.cuda(), k.cuda(), v.cuda(), _ints(_edges(lens)), out, ws, kv_starts=_ints(_edges(kv_lens)))
+        plan.query_status(ws)
+        check(out.cpu(), want, bound)
+
+
+def test_hidden_values_in_a_cut_prompt(agmm):
+    """A prompt that is cut along its keys, with values that are not finite near its end: earlier rows are as they were."""
+    dt, d, n = torch.bfloat16, 128, 3001
+    q, k, v = _make([n], [n], 2, 1, d, dt, seed=23)
+    rows = torch.tensor([0, 100, 1500, 2816, 2900, 2949, 2950, 2999, 3000])
+    seen = torch.arange(n)[None] <= rows[:, None]
+    refs = [attend(q[rows, h], k[:, 0], v[:, 0], seen, d ** -0.5, dt) for h in range(2)]
+    v[2950, 0, 7] = float("inf")
+    v[3000, 0, 9] = float("nan")
+    out = agmm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), _ints([0, n])).cpu()[rows]
+    for h in range(2):
+        want, bound = refs[h]
+        clear = [c for c in range(d) if c not in (7, 9)]
+        check(out[:, h][:, clear], want[:, clear], bound[:, clear], "other columns")
+        check(out[:6, h], want[:6], bound[:6], "rows before")
+        assert bool((out[6:, h, 7] == float("inf")).all())
+        check(out[6:8, h, 9:10], want[6:8, 9:10], bound[6:8, 9:10])
+        assert bool(torch.isnan(out[8, h, 9]))
+
+
 def test_same_bits_every_time_and_on_another_stream(agmm):
     dt, d, lens = torch.bfloat16, 128, [700, 90, 1100]
     q, k, v = (x.cuda() for x in _make(lens, lens, 8, 2, d, dt, seed=4))
