@@ -37,6 +37,13 @@
 // added to; value rows past the end are cleared in shared memory; and a row whose
 // result is not finite, in an item with a value that is not finite and that the row
 // does not see, is computed again without it.
+//
+// Measured: a prompt of 8191 tokens, 32 heads of 128: 343 us, 1.60 PFLOP/s, the tensor
+// cores active in 69% of the cycles.  A pair of tiles took 2671 cycles, its products
+// need 2048; the likely bound is shared memory's bandwidth under Q K^T and TMA
+// (calculated, not counted).  Two contexts of 100000 to 131000 keys, 5 tokens each: 152
+// us, 6.2 TB/s: device memory.  Without turns of the two MMA warps the streams fell into
+// step: 451 us against 356 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -807,7 +814,8 @@ __device__ __forceinline__ int64_t row_offset(const AttnParams& p, const Item& i
 // times a weight of zero is not zero.  Where there is such a value that the row
 // does not see, its result is computed again, key by key, with the weights that it had
 // (m, l); else it stands.  A warp takes a row at a time: a lane takes a key's
-// score, then some columns of all 32 keys' values.  Slow (0.1 us a key and 32 rows) and rare.
+// score, then some columns of all 32 keys' values.  Slow and rare: 8191 tokens, 32 heads
+// with one such value at key 127 take 7.6 ms, at key 8000 146 ms, and 0.35 ms without.
 template <int kD, bool kF16, bool kPaged>
 __device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, int s, uint32_t rows, float m, float l, int col0,
                                          int col1, uint16_t* out, float* part) {
