@@ -11,7 +11,9 @@ As with :class:`Plan`, a plan is made once for a layer's shape and its ``run``
 takes the caller's buffers; the functions ``qkv_norm_rope``,
 ``prompt_attention`` and ``tree_attention`` allocate them.  Buffers follow
 PyTorch's stream rules: a tensor used on a ``stream`` other than the one it
-was made on has to be ready there, and to outlive the work.
+was made on has to be ready there, and to outlive the work.  A ``stream`` is a
+``torch.cuda.Stream``, an object with a ``cuda_stream`` handle, or the handle;
+what the functions allocate belongs to it.
 """
 from __future__ import annotations
 
@@ -407,12 +409,16 @@ def _is_f16(x) -> bool:
 
 
 class _On:
-    """Allocations inside belong to `stream` (None, or a raw handle: the current one)."""
+    """Allocations inside, and their zero fills, belong to `stream` in any of its forms (None: the current one)."""
 
     def __init__(self, stream):
         import torch
 
-        self._ctx = torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else None
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            handle = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+            # ExternalStream would take handle 0 for "a new stream": it is the default one
+            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        self._ctx = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
         if self._ctx is not None:
