@@ -350,6 +350,27 @@ def _check_operands(xs, y, rhs_transpose: bool):
     return m, k, n
 
 
+class _On:
+    """Allocations inside, and their zero fills, belong to `stream` in any of its forms (None: the current one)."""
+
+    def __init__(self, stream):
+        import torch
+
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            handle = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+            # ExternalStream would take handle 0 for "a new stream": it is the default one
+            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        self._ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
 _plan_cache: Dict[tuple, Plan] = {}
 
 
@@ -357,7 +378,8 @@ def all_gather_matmul(xs, y, my_id: int = 0, rhs_transpose: bool = False, out=No
                       out_f32: bool = False, workspace=None, stream=None, return_gathered: bool = False):
     """all-gather(xs, axis=0) @ y on one GPU; returns O [P*m, n] in the input
     dtype (bf16 or fp16) or float32.  With return_gathered it returns
-    (O, concat(xs)): the fused kernel stores the gathered rows as it loads them."""
+    (O, concat(xs)): the fused kernel stores the gathered rows as it loads them.
+    What it allocates belongs to ``stream``, a torch.cuda.Stream or a handle."""
     import torch
 
     m, k, n = _check_operands(xs, y, rhs_transpose)
@@ -367,14 +389,16 @@ def all_gather_matmul(xs, y, my_id: int = 0, rhs_transpose: bool = False, out=No
     if plan is None:
         plan = Plan(len(xs), m, k, n, rhs_transpose, out_f32, f16)
         _plan_cache[key] = plan
-    if out is None:
-        out = torch.empty((plan.M, n), dtype=torch.float32 if out_f32 else xs[0].dtype, device=y.device)
-    if workspace is None:
-        workspace = plan.new_workspace(unfused, device=y.device)
+    if return_gathered and unfused:
+        raise ValueError("return_gathered uses the fused path")
+    with _On(stream):
+        if out is None:
+            out = torch.empty((plan.M, n), dtype=torch.float32 if out_f32 else xs[0].dtype, device=y.device)
+        if workspace is None:
+            workspace = plan.new_workspace(unfused, device=y.device)
+        if return_gathered:
+            xcat = torch.empty((plan.M, k), dtype=xs[0].dtype, device=y.device)
     if return_gathered:
-        if unfused:
-            raise ValueError("return_gathered uses the fused path")
-        xcat = torch.empty((plan.M, k), dtype=xs[0].dtype, device=y.device)
         plan.run_gather(xs, y, out, xcat, my_id, workspace, stream)
         return out, xcat
     (plan.run_unfused if unfused else plan.run)(xs, y, out, my_id, workspace, stream)

@@ -21,7 +21,7 @@ import ctypes
 import struct
 from typing import Dict, List, Optional, Sequence
 
-from . import AGMM_BF16, AGMM_F16, _check, load_library
+from . import AGMM_BF16, AGMM_F16, _check, _On, load_library
 
 ATTENTION_SYMBOLS = [
     "agmm_norm_rope_plan", "agmm_norm_rope_run", "agmm_norm_rope_destroy",
@@ -406,27 +406,6 @@ def _is_f16(x) -> bool:
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("inputs must be bfloat16 or float16")
     return x.dtype == torch.float16
-
-
-class _On:
-    """Allocations inside, and their zero fills, belong to `stream` in any of its forms (None: the current one)."""
-
-    def __init__(self, stream):
-        import torch
-
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            handle = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
-            # ExternalStream would take handle 0 for "a new stream": it is the default one
-            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-        self._ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
 
 
 def qkv_norm_rope(qkv, q_weight, k_weight, positions, q_heads: int, kv_heads: int, k_cache=None, v_cache=None, slots=None,
