@@ -4,11 +4,17 @@
 //   out_i = sum_j softmax_j(scale * q_i . k_j) v_j   over the keys j that row i sees
 //
 // in one pass over the keys: S = Q K^T for a tile of 128 rows and 128 keys, p =
-// 2^(c s - c m) with a reference m for each row, O += P V, l += sum p, and O /
+// 2^(c s - c m + w) with a reference m for each row, O += P V, l += sum p, and O /
 // l at the end.  m is the running maximum, but it follows only when it has grown by
-// more than 2^8 (the weights stay exact to their own rounding up to there, in
-// 16 bits as in 32), so the rescaling of O, a round trip through tensor
+// more than 2^8, so the rescaling of O, a round trip through tensor
 // memory, is rare after the first keys.
+//
+// P is an operand of the tensor cores: the weights are rounded to the 16-bit type, and l
+// sums them as they are rounded.  In bf16 that is a relative 2^-9 whatever their
+// size, and w = 0.  fp16 ends at 65504 and begins at 2^-24, so w = 7: the largest weight
+// is 2^(8 + 7), a weight keeps all its bits down to 2^-21 of the reference's, and is lost
+// below 2^-32 of it (2^-25 with w = 0, which lost up to 0.39 % of the mass of one key
+// and 131072 faint ones).  The factor 2^w is in O as in l and cancels.
 //
 // One persistent CTA per SM.  Two "streams" of 128 query rows each, so that
 // the tensor cores work on one while the other's weights are computed:
@@ -59,7 +65,7 @@ namespace {
 
 constexpr int kItemSlots = 2;
 constexpr int kDrawAhead = 3;  // key tiles still to be loaded when the next item is asked for
-constexpr float kMaxGrowth = 8.0f;  // log2 of how far the weights may grow past 1
+constexpr float kMaxGrowth = 8.0f;  // log2 of how far the weights may grow past the reference's
 
 template <int kD>
 struct Layout {
@@ -733,6 +739,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
+// What is added to c s for the exponent of a weight.  A row that has seen nothing has no reference.
+template <bool kF16>
+__device__ __forceinline__ float weight_shift(float m, float c) {
+  return (m == -INFINITY ? 0.0f : -m * c) + (kF16 ? 7.0f : 0.0f);
+}
+
 template <bool kF16>
 __device__ __forceinline__ float value16(uint16_t b) {
   if constexpr (kF16)
@@ -845,7 +857,7 @@ __device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, in
     }
     if (!__any_sync(0xffffffffu, found)) continue;
     const float row_m = __shfl_sync(0xffffffffu, m, from), row_l = __shfl_sync(0xffffffffu, l, from);
-    const float shift = row_m == -INFINITY ? 0.0f : -row_m * p->scale_log2;
+    const float shift = weight_shift<kF16>(row_m, p->scale_log2);
     const int head = it->head + s * (it->alternate ? 0 : it->head_step) +
                      (p->pack == 1 ? 0 : (threadIdx.x & 96) + from - (row.token - it->tok[s]) * p->pack);
     const uint16_t* const q = p->q + (int64_t)(it->q0 + row.token) * p->q_ts + head * p->q_hs;
@@ -1113,7 +1125,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
         for (;;) {
           load_scores(t_s, v);
           sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
-          weights<kF16>(v[0], v[1], c, m == -INFINITY ? 0.0f : -m * c, pk, sum);
+          weights<kF16>(v[0], v[1], c, weight_shift<kF16>(m, c), pk, sum);
           const float top = row_max(v);
           const bool grows = (top - m) * c > kMaxGrowth;  // also from -inf to anything
           if (!__any_sync(0xffffffffu, grows)) break;
@@ -1127,7 +1139,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars.p_ready(s, 0));
-        weights<kF16>(v[2], v[3], c, m == -INFINITY ? 0.0f : -m * c, pk, sum);
+        weights<kF16>(v[2], v[3], c, weight_shift<kF16>(m, c), pk, sum);
         ptx::tmem_st_32x32b_x32(t_s + 32, pk);
         ptx::tmem_st_wait();
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -1221,7 +1233,8 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           packed[e] = pack2<kF16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-          top = __vmaxu2(top, packed[e] & 0x7fff7fffu);
+          // in bf16, whose range is float32's: the sums of a part may be past fp16's and finite
+          top = __vmaxu2(top, (kF16 ? pack2<false>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])) : packed[e]) & 0x7fff7fffu);
         }
         if (whole)
           store_rows(packed, lane, rows_there, out + col);
@@ -1229,8 +1242,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
           store_rows(o, lane, rows_there, part + col);
       }
       // (a weight sum that is NaN makes the row NaN, as it should be)
-      constexpr uint32_t kInf2 = kF16 ? 0x7c007c00u : 0x7f807f80u;
-      const uint32_t bad = __ballot_sync(0xffffffffu, own.there && l == l && __vcmpgeu2(top, kInf2) != 0);
+      const uint32_t bad = __ballot_sync(0xffffffffu, own.there && l == l && __vcmpgeu2(top, 0x7f807f80u) != 0);
       if (bad) {
         __syncwarp();  // the other lanes' stores come first
         repair_rows<kD, kF16, kPaged>(&p, &it, s, bad, m, l, col0, col1, out, part);

@@ -5,7 +5,10 @@
  *
  * Types: every matrix is bf16 (AGMM_BF16) or fp16 (AGMM_F16), fixed by the
  * plan; sums, softmax statistics and norms are held in float32 and rounded
- * once, to the nearest, at the output.
+ * once, to the nearest, at the output.  The weights of a softmax are rounded to
+ * that type too, as an operand of the tensor cores, and summed as they are
+ * rounded; in fp16 as numbers 2^7 times as large, so that a weight of 2^-21 of
+ * its row's largest has all its bits, and one of 2^-32 still counts.
  *
  * Strides count elements; the innermost (head_dim) stride is 1.  Data
  * pointers are 16-byte aligned and strides are multiples of 8 elements
