@@ -51,6 +51,8 @@ _NORM_ROPE_ARGS = struct.Struct("=23q")
 _PROMPT_ARGS = struct.Struct("=18q")
 _TREE_ARGS = struct.Struct("=22q")
 
+MAX_NODES = 1024  # what agmm_tree_plan takes
+
 _bound = None
 
 
@@ -445,18 +447,33 @@ def prompt_attention(q, k, v, starts, kv_starts=None, scale: Optional[float] = N
     return out
 
 
-def tree_attention(q, k_cache, v_cache, page_table, context_lens, node_starts, mask=None, max_nodes: int = 1,
+def tree_attention(q, k_cache, v_cache, page_table, context_lens, node_starts, mask=None, max_nodes: Optional[int] = None,
                    scale: Optional[float] = None, out=None, workspace=None, stream=None):
     """Attention of drafted tokens over a paged cache; returns [tokens,
-    q_heads, head_dim] (TreePlan).  max_nodes: the most drafted tokens of a
-    sequence."""
+    q_heads, head_dim] (TreePlan).
+
+    max_nodes: the most drafted tokens of a sequence, 1 for the ordinary decode
+    step.  It is not known on the host; without it room is made for all of q's
+    tokens in one sequence (1024 of them at most), and a workspace as large is
+    zeroed: give it where the time of a call counts.  Rows past it are zero in an
+    output that is made here, as it is the plan that bounds them."""
     import torch
 
+    tokens, sequences = q.shape[0], page_table.shape[0]
+    if max_nodes is None:
+        # a power of two: few plans for all numbers of tokens
+        max_nodes = min(MAX_NODES, 1 << max(0, tokens - 1).bit_length())
+        if mask is not None and mask.dim() == 2 and mask.shape[1] < (max_nodes + 63) // 64:
+            with _On(stream):  # words that are not there have no bit set
+                mask = torch.nn.functional.pad(mask, (0, (max_nodes + 63) // 64 - mask.shape[1]))
+    elif tokens > sequences * int(max_nodes):
+        raise ValueError(f"{tokens} drafted tokens of {sequences} sequences: some have more than max_nodes = {max_nodes}")
     plan = _cached(TreePlan, q.shape[1], k_cache.shape[2], q.shape[2], page_size=k_cache.shape[1], max_nodes=int(max_nodes),
                    scale=scale, f16=_is_f16(q))
     with _On(stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            # zeros where a sequence could have rows past the bound
+            out = (torch.zeros if tokens > plan.max_nodes else torch.empty)(q.shape, dtype=q.dtype, device=q.device)
         if workspace is None:
             workspace = plan.new_workspace()
     plan.run(q, k_cache, v_cache, page_table, context_lens, node_starts, out, workspace, mask=mask, stream=stream)
