@@ -146,11 +146,13 @@ __device__ __forceinline__ Sequence sequence_of(const AttnParams& p, int s) {
   x.q0 = (int)a;
   x.q_len = (int)(b - a);
   if constexpr (kPaged) {
-    x.q_len = min(x.q_len, p.max_nodes);
     const int64_t most = p.table_pages << p.page_shift;
     const int64_t ctx = max(__ldg(p.context_lens + s), 0);
     x.kv_row = 0;
-    x.kv_len = (int)min(ctx + x.q_len, most);
+    // nodes past max_nodes are not computed, but a mask may let those before them see them
+    const int nodes = min(x.q_len, p.max_nodes);
+    x.kv_len = (int)min(ctx + (p.mask ? x.q_len : nodes), most);
+    x.q_len = nodes;
     x.off = (int)min(ctx, most);
   } else {
     const int64_t c = min(max((int64_t)__ldg(p.kv_starts + s), (int64_t)0), p.kv_tokens);

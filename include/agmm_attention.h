@@ -138,7 +138,8 @@ void agmm_prompt_destroy(agmm_prompt_t plan);
  * whole context and the nodes j whose bit is set: bit j % 64 of word j / 64 of
  * its mask row; without a mask it sees the nodes up to itself.  One node
  * without a mask is the ordinary decode step.  A node that sees nothing is
- * zero.  max_nodes bounds a sequence's nodes: nodes past it are not computed.
+ * zero.  max_nodes bounds a sequence's nodes: nodes past it are not computed, but
+ * a mask may let others see them.
  */
 typedef struct {
   int q_heads, kv_heads; /* q_heads a multiple of kv_heads, at most 128 heads to a group */
