@@ -78,7 +78,7 @@ struct Layout {
   // control block
   static constexpr uint32_t kBars = kCtl;
   static constexpr uint32_t kItems = kCtl + 384;                // kItemSlots x 96 bytes
-  static constexpr uint32_t kFlags = kItems + kItemSlots * 96;  // abort, TMEM base, non-finite flag
+  static constexpr uint32_t kFlags = kItems + kItemSlots * 96;  // abort, TMEM base, pulse
   static constexpr uint32_t kStats = kFlags + 16;               // [2 streams][128 rows][2] float
   static constexpr size_t kBytes = kStats + 2 * 128 * 2 * 4;
   static_assert(kBytes <= 232448, "more shared memory than a CTA can have");
@@ -832,10 +832,11 @@ __device__ __forceinline__ int64_t row_offset(const AttnParams& p, const Item& i
 // with one such value at key 127 take 2.1 ms, at key 8000 57 ms, and 0.35 ms without.
 // Loads are 4 to 16 bytes, in the order that the sums need (2 bytes at a time: 7.6 and
 // 146 ms).  Unrolled by 8 it takes 48 ms, but prompts without such a value, which never
-// come here, 348 us instead of 341.
+// come here, 348 us instead of 341.  Other warps may wait for this one longer than a wait
+// lasts (2 s are reached at about 280 thousand keys): it shows them that it goes on.
 template <int kD, bool kF16, bool kPaged>
-__device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, int s, uint32_t rows, float m, float l, int col0,
-                                         int col1, uint16_t* out, float* part) {
+__device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, const Waiter* wait, int s, uint32_t rows, float m,
+                                         float l, int col0, int col1, uint16_t* out, float* part) {
   constexpr int kN = kD / 32;
   const int lane = threadIdx.x & 31;
   const int begin = it->kv_tile * kKeys, end = min(it->kv_len, (it->kv_tile + it->tiles) * kKeys);
@@ -844,6 +845,7 @@ __device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, in
     const int from = __ffs(rows) - 1;
     const Row row = row_of<kPaged>(*p, *it, s, (threadIdx.x & 96) + from);
     bool found = false;
+    wait->beat();
 #pragma unroll 1
     for (int place = max(it->masked_from / kKeys * kKeys, begin) + lane; place < end; place += 32) {
       if (seen32(*it, row, p->mask_words, place) & 1u) continue;
@@ -868,6 +870,8 @@ __device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, in
     for (int e = 0; e < kN; ++e) o[e] = 0.0f;
 #pragma unroll 1
     for (int place0 = begin; place0 < end; place0 += 32) {
+      if (__any_sync(0xffffffffu, *wait->abort != 0)) return;
+      wait->beat();
       float w = 0.0f;
       int64_t v_at = -1;
       if (place0 + lane < end && (seen32(*it, row, p->mask_words, place0 + lane) & 1u)) {
@@ -1247,7 +1251,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, const Bars& bars, c
       const uint32_t bad = __ballot_sync(0xffffffffu, own.there && l == l && __vcmpgeu2(top, 0x7f807f80u) != 0);
       if (bad) {
         __syncwarp();  // the other lanes' stores come first
-        repair_rows<kD, kF16, kPaged>(&p, &it, s, bad, m, l, col0, col1, out, part);
+        repair_rows<kD, kF16, kPaged>(&p, &it, &wait, s, bad, m, l, col0, col1, out, part);
       }
       if (!whole && own.there && col0 == 0) {
         float* const ml =
@@ -1285,7 +1289,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
   }
   const Bars bars{smem + L::kBars, L::kStages};
   Item* const slots = reinterpret_cast<Item*>(base + L::kItems);
-  int* const flags = reinterpret_cast<int*>(base + L::kFlags);  // [0] abort, [1] TMEM base
+  int* const flags = reinterpret_cast<int*>(base + L::kFlags);  // [0] abort, [1] TMEM base, [2] pulse
   float* const stats = reinterpret_cast<float*>(base + L::kStats);
 
   if (warp == 9) {
@@ -1293,7 +1297,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) agmm_attention(const __grid_c
     ptx::tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    flags[0] = 0;
+    flags[0] = flags[2] = 0;
     for (int i = 0; i < L::kStages; ++i) {
       ptx::mbar_init(bars.full(i), 1);
       ptx::mbar_init(bars.empty(i), 2);  // both MMA warps

@@ -120,20 +120,25 @@ __device__ __forceinline__ void add_halves(float& acc0, float& acc1, uint32_t w)
 // Bounded waits.  A wait that runs out raises the CTA's abort flag and records
 // AGMM_ERR_TIMEOUT (5) in the status words; every other wait of the CTA then
 // ends too, and all roles leave their loops.
+//
+// Work whose length grows with the problem while other warps wait for it (rows that
+// are computed again) leaves the time of its last step in the pulse: a wait runs out
+// when it has lasted for its limit and no step came in as long a time.  That work ends
+// by itself, and when the flag is raised.
 struct Waiter {
-  volatile int* abort;
+  volatile int* abort;  // [0] the flag, [2] the pulse: cycles / 1024, odd; 0: no step yet
   uint64_t limit;
   int* status;
   int role;
 
-  // A converged warp waits; every lane gets the same answer.
-  __device__ __forceinline__ bool retry(uint32_t bar, uint32_t parity, int where) const {
-    const uint64_t t0 = ptx::clock_cycles();
-    for (;;) {
-      if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000))) return true;
-      if (__any_sync(0xffffffffu, *abort != 0)) return false;
-      if (__any_sync(0xffffffffu, ptx::clock_cycles() - t0 > limit)) break;
-    }
+  // Whether a wait that has lasted for its limit is given up; raises the flag.  A call of
+  // its own: the softmax warps' key loop has to stay short (inlined, 256 became 279 us and 371
+  // became 381 us for a piece of a prompt and a long one).
+  __device__ __noinline__ bool expired(int where) const {
+    const int last = abort[2];
+    // the pulse may be one ahead of the clock
+    const uint32_t since = (uint32_t)(ptx::clock_cycles() >> 10) + 1u - (uint32_t)last;
+    if (__any_sync(0xffffffffu, last != 0 && since <= (uint32_t)(limit >> 10) + 2u)) return false;
     *abort = 1;
     if ((threadIdx.x & 31) == 0 && atomicCAS(status, 0, 5) == 0) {
       status[1] = role;
@@ -141,7 +146,17 @@ struct Waiter {
       status[3] = (int)blockIdx.x;
     }
     __syncwarp();
-    return false;
+    return true;
+  }
+
+  // A converged warp waits; every lane gets the same answer.
+  __device__ __forceinline__ bool retry(uint32_t bar, uint32_t parity, int where) const {
+    const uint64_t t0 = ptx::clock_cycles();
+    for (;;) {
+      if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000))) return true;
+      if (__any_sync(0xffffffffu, *abort != 0)) return false;
+      if (__any_sync(0xffffffffu, ptx::clock_cycles() - t0 > limit) && expired(where)) return false;
+    }
   }
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int where) const {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
@@ -153,6 +168,10 @@ struct Waiter {
   __device__ __forceinline__ bool compact(uint32_t bar, uint32_t parity, int where) const {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     return retry_call(bar, parity, where);
+  }
+  // A converged warp has done a step of such work.
+  __device__ __forceinline__ void beat() const {
+    abort[2] = (int)(ptx::clock_cycles() >> 10) | 1;
   }
   // Waits for work in flight, whatever the abort flag says.
   __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const {
