@@ -162,7 +162,8 @@ class _AttentionPlan:
         return workspace.data_ptr()
 
     def query_status(self, workspace, stream=None) -> int:
-        """Synchronize and return (and clear) the device status; raises on error."""
+        """Synchronize and return (and clear) the device status; raises on error.
+        The workspace can be used again after that."""
         st = self._lib.agmm_query_status(None, workspace.data_ptr(), self._stream(stream))
         _check(st)
         return st

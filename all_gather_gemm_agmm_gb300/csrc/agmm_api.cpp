@@ -984,7 +984,10 @@ agmm_status_t agmm_query_status(agmm_plan_t plan, void* workspace, void* stream)
   if ((e = cudaMemcpy(words, workspace, sizeof words, cudaMemcpyDeviceToHost)) != cudaSuccess)
     return fail_cuda(e, "status read");
   if (words[0] == 0) return AGMM_OK;
-  if ((e = cudaMemset(workspace, 0, sizeof words)) != cudaSuccess) return fail_cuda(e, "status clear");
+  // the whole head of the workspace, with the counters that stand beside the words; on
+  // the stream, and waited for: the next run may be on any other
+  if ((e = cudaMemsetAsync(workspace, 0, kStatusBytes, s)) != cudaSuccess) return fail_cuda(e, "status clear");
+  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return fail_cuda(e, "status clear");
   static const char* roles[] = {"?", "producer", "mma", "epilogue", "drain", "store"};
   const char* role = (words[1] >= 1 && words[1] <= 5) ? roles[words[1]] : roles[0];
   return fail(words[0] == AGMM_ERR_TIMEOUT ? AGMM_ERR_TIMEOUT : AGMM_ERR_CUDA,

@@ -39,8 +39,9 @@ constexpr int kRows = 128;        // query rows of a tile (MMA M, TMEM lanes)
 constexpr int kKeys = 128;        // keys of a tile
 constexpr int kAttnThreads = 384;  // 2 x 4 softmax warps, then producer, MMA and scheduler warps and an idle one
 
-// Workspace: status words and the counter that prompts draw from, then a join
-// record per CTA and the partial results of split work.
+// Workspace: status words and the counter that prompts draw from, which a run that gave
+// up leaves somewhere and agmm_query_status zeroes with the words; then a join record
+// per CTA and the partial results of split work, which every run writes before it reads.
 constexpr size_t kAttnStatusBytes = 256;
 constexpr size_t kCounterOffset = 128;
 constexpr int kJoinInts = 8;  // 1 (or 0: no join); first tile's token, rows, head; last CTA; second tile's token, rows, head

@@ -286,7 +286,7 @@ agmm_status_t agmm_run_host(agmm_plan_t plan, const void* const* x_host, const v
 
 /*
  * Synchronize `stream`, read the device status words in `workspace` and
- * clear them.  Returns AGMM_OK, AGMM_ERR_TIMEOUT if a kernel gave up on a
+ * clear them: where they report an error, the workspace's first 256 bytes.  Returns AGMM_OK, AGMM_ERR_TIMEOUT if a kernel gave up on a
  * wait since the last query, or AGMM_ERR_CUDA if the stream reports an error.
  */
 agmm_status_t agmm_query_status(agmm_plan_t plan, void* workspace, void* stream);

@@ -22,9 +22,9 @@
  * used by several host threads at once.  A workspace is zero-filled before
  * its first use, and runs that overlap on the device need one each; its status
  * words are read with agmm_query_status(NULL, workspace, stream), which
- * reports a device-side wait that ran out (the results are then not valid, and
- * the workspace is zero-filled again before its next use).  A call with nothing to do (no
- * tokens) returns AGMM_OK and launches nothing.
+ * reports a device-side wait that ran out: the results since the last query are
+ * then not valid, and the query leaves the workspace ready for its next use.  A
+ * call with nothing to do (no tokens) returns AGMM_OK and launches nothing.
  *
  * Values in device memory (starts, lengths, page numbers, slots) are not read
  * by the host.  The kernels bound them: starts are clamped to the tokens there
