@@ -55,6 +55,10 @@ constexpr int kMinPromptTiles = 4;
 // 341 us drawn, 418 us cut.
 constexpr int kDrawnItems = 2;
 
+// Most rows, and most places of a sequence: the kernels count both in 32 bits, and
+// go past an end by a tile of keys, two of rows, or a tree's nodes.
+constexpr int64_t kMostPlaces = INT_MAX - 4096;
+
 agmm_status_t fail(agmm_status_t s, const char* fmt, ...) {
   char text[256];
   va_list ap;
@@ -392,8 +396,8 @@ size_t agmm_prompt_workspace_bytes(agmm_prompt_t plan) { return plan ? workspace
 
 agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, void* stream) {
   if (!plan || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
-  AGMM_TRY(check_range("tokens", a->tokens, 0, INT_MAX));
-  AGMM_TRY(check_range("kv_tokens", a->kv_tokens, 0, INT_MAX));
+  AGMM_TRY(check_range("tokens", a->tokens, 0, kMostPlaces));
+  AGMM_TRY(check_range("kv_tokens", a->kv_tokens, 0, kMostPlaces));
   AGMM_TRY(check_range("sequences", a->sequences, 0, 1 << 20));
   if (a->tokens == 0 || a->sequences == 0) return AGMM_OK;
   AGMM_TRY(check_operand("q", a->q, a->q_token_stride, a->q_head_stride));
@@ -482,7 +486,7 @@ size_t agmm_tree_workspace_bytes(agmm_tree_t plan) { return plan ? workspace_byt
 
 agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* stream) {
   if (!plan || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
-  AGMM_TRY(check_range("tokens", a->tokens, 0, INT_MAX));
+  AGMM_TRY(check_range("tokens", a->tokens, 0, kMostPlaces));
   AGMM_TRY(check_range("sequences", a->sequences, 0, 1 << 20));
   if (a->tokens == 0 || a->sequences == 0) return AGMM_OK;
   AGMM_TRY(check_operand("q", a->q, a->q_token_stride, a->q_head_stride));
@@ -490,7 +494,7 @@ agmm_status_t agmm_tree_run(agmm_tree_t plan, const agmm_tree_args_t* a, void* s
   AGMM_TRY(check_operand("k_cache", a->k_cache, a->cache_token_stride, a->cache_head_stride));
   AGMM_TRY(check_operand("v_cache", a->v_cache, a->cache_page_stride, a->cache_head_stride));
   AGMM_TRY(check_range("pages", a->pages, 1, INT_MAX));
-  AGMM_TRY(check_range("table_pages", a->table_pages, 1, INT_MAX / plan->page_size));
+  AGMM_TRY(check_range("table_pages", a->table_pages, 1, kMostPlaces / plan->page_size));
   AGMM_TRY(check_range("table_stride", a->table_stride, 0, (int64_t)1 << 38));
   AGMM_TRY(check_pointer("page_table", a->page_table, 4));
   AGMM_TRY(check_pointer("context_lens", a->context_lens, 4));

@@ -110,7 +110,7 @@ typedef struct {
 } agmm_prompt_desc_t;
 
 typedef struct {
-  int64_t tokens, kv_tokens, sequences;
+  int64_t tokens, kv_tokens, sequences; /* up to 2^31 - 4097 rows, 2^20 sequences */
   const void* q;             /* [tokens, q_heads, head_dim]     */
   int64_t q_token_stride, q_head_stride;
   const void* k;             /* [kv_tokens, kv_heads, head_dim] */
@@ -160,7 +160,7 @@ typedef struct {
   const void* v_cache;          /* the same shape and strides               */
   int64_t pages, cache_page_stride, cache_token_stride, cache_head_stride;
   const int32_t* page_table;    /* [sequences, table_pages]                 */
-  int64_t table_pages;          /* pages a sequence can have                */
+  int64_t table_pages;          /* pages a sequence can have, up to 2^31 - 4097 places */
   int64_t table_stride;         /* entries from one sequence to the next    */
   const int32_t* context_lens;  /* [sequences]                              */
   const int32_t* node_starts;   /* [sequences + 1], not falling             */
