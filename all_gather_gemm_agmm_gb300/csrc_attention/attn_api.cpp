@@ -411,7 +411,7 @@ agmm_status_t agmm_prompt_run(agmm_prompt_t plan, const agmm_prompt_args_t* a, v
   AGMM_TRY(check_pointer("workspace", a->workspace, 16));
   // row-tile pairs there can be
   const int64_t pairs = a->tokens / (2 * kRows) + (a->sequences < a->tokens ? a->sequences : a->tokens);
-  if (pairs * plan->q_heads >= INT_MAX / 2)
+  if (pairs * plan->q_heads >= kMostItems)
     return fail(AGMM_ERR_UNSUPPORTED, "too many rows for one run: %lld tokens of %d heads", (long long)a->tokens, plan->q_heads);
   AGMM_TRY(check_plan_device(plan->device));
   AttnParams p = {};

@@ -293,15 +293,21 @@ struct Draw {
   __device__ __forceinline__ int level_items() const { return pairs * p.q_heads + singles * (p.q_heads / 2); }
   __device__ __forceinline__ void init() {
     lane = threadIdx.x & 31;
-    int most = 0, sum = 0;
+    int most = 0;
+    int64_t sum = 0;
 #pragma unroll 1
     for (int s = lane; s < p.sequences; s += 32) {
       bool single;
       const int n = sets_of(s, single);
       most = max(most, n);
-      sum += n * p.q_heads - (single ? p.q_heads - p.q_heads / 2 : 0);
+      sum += (int64_t)n * p.q_heads - (single ? p.q_heads - p.q_heads / 2 : 0);
     }
-    items = __reduce_add_sync(0xffffffffu, sum);
+    // The host bounds the items of starts that do not fall.  Starts that fall can stand for
+    // more rows than there are, and for more items than can be counted: none is done then.
+    const int64_t total = ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(sum >> 16 & 0x3ffffff)) << 16) +
+                          __reduce_add_sync(0xffffffffu, (unsigned)(sum & 0xffff));
+    const bool countable = !__any_sync(0xffffffffu, sum >> 42) && total < kMostItems;
+    items = countable ? (int)total : 0;
     level = __reduce_max_sync(0xffffffffu, most);
     base = pairs = singles = 0;
     next = (int)blockIdx.x - (int)gridDim.x;  // the first item is this CTA's number

@@ -37,6 +37,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, bool f16, cu
 
 constexpr int kRows = 128;        // query rows of a tile (MMA M, TMEM lanes)
 constexpr int kKeys = 128;        // keys of a tile
+constexpr int kMostItems = 1 << 30;  // of a run of prompts
 constexpr int kAttnThreads = 384;  // 2 x 4 softmax warps, then producer, MMA and scheduler warps and an idle one
 
 // Workspace: status words and the counter that prompts draw from, which a run that gave

@@ -28,8 +28,10 @@
  *
  * Values in device memory (starts, lengths, page numbers, slots) are not read
  * by the host.  The kernels bound them: starts are clamped to the tokens there
- * are, lengths to what the page table covers, a page number outside the cache
- * reads zeros, and a slot outside the cache is not written.
+ * are (where they fall, a sequence is empty; when they stand for 2^30 tiles of
+ * work or more so, prompts are not worked on), lengths to what the page table
+ * covers, a page number outside the cache reads zeros, and a slot outside the
+ * cache is not written.
  */
 #ifndef AGMM_ATTENTION_H_
 #define AGMM_ATTENTION_H_
