@@ -49,10 +49,12 @@ namespace {
 // round trip through device memory, 256 rows in float32.
 constexpr int kMinPromptTiles = 4;
 // From this many items for each CTA on, prompts draw whole items; fewer are cut along
-// the keys.  Measured: 1.5 items (two pieces of 1024 and 700 tokens behind 8000 to
-// 15000 keys, 32 heads) 332 us drawn, 239 us cut; 4.1 items (prompts of 17 to 4001
-// tokens, 16 heads) 87 us drawn, 118 us cut; 6.7 items (one of 8191 tokens, 32 heads)
-// 341 us drawn, 418 us cut.
+// the keys.  Measured, each pair in one build: 1.5 items (two pieces of 1024 and 700 tokens
+// behind 8000 to 15000 keys, 32 heads) 332 us drawn, 239 us cut; 4.1 items (prompts of 17
+// to 4001 tokens, 16 heads) 87 us drawn, 118 us cut; 6.7 items (one of 8191 tokens, 32
+// heads) 341 us drawn, 418 us cut.  Between 1.5 and 4.1 nothing was measured.  The
+// rule goes by the most items that the rows can make, not by those they make, and not
+// by their keys, which the host does not know.
 constexpr int kDrawnItems = 2;
 
 // Most rows, and most places of a sequence: the kernels count both in 32 bits, and

@@ -44,12 +44,13 @@
 // result is not finite, in an item with a value that is not finite and that the row
 // does not see, is computed again without it.
 //
-// Measured: a prompt of 8191 tokens, 32 heads of 128: 343 us, 1.60 PFLOP/s, the tensor
-// cores active in 69% of the cycles.  A pair of tiles took 2671 cycles, its products
+// Measured: a prompt of 8191 tokens, 32 heads of 128: 369 us back to back under the power
+// cap, 1.49 PFLOP/s (341 to 378 us over boxes and builds); the tensor cores were active in 69%
+// of the cycles of one launch.  A pair of tiles took 2671 cycles, its products
 // need 2048; the likely bound is shared memory's bandwidth under Q K^T and TMA
-// (calculated, not counted).  Two contexts of 100000 to 131000 keys, 5 tokens each: 152
+// (calculated, not counted).  Two contexts of 100000 to 131000 keys, 5 tokens each: 153
 // us, 6.2 TB/s: device memory.  Without turns of the two MMA warps the streams fell into
-// step: 451 us against 356 us.
+// step: 451 us against 356 us, in one build.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -172,8 +173,8 @@ __device__ __forceinline__ int key_tiles(const AttnParams& p, const Sequence& x,
 // The work is laid out in a line: sequences, in each its sets of row tiles (one
 // or two tiles), for each the heads, for each item its key tiles.  In front of
 // its tiles an item has kItemCost places for what it takes besides them (32 decode
-// steps over 150 to 8100 keys: 61.4 us with 1 place, 55.9 with 2, 53.6 with 4, 55.6 with
-// 6).  The line is cut into a part for every CTA, equal but for cuts that would leave
+// steps over 150 to 8100 keys, in one build: 61.4 us with 1 place, 55.9 with 2, 53.6 with 4,
+// 55.6 with 6; 56.3 us now, with 4).  The line is cut into a part for every CTA, equal but for cuts that would leave
 // less than p.min_tiles of an item on one side: those move to the item's edge.
 constexpr int kItemCost = 4;
 
@@ -270,10 +271,11 @@ struct Line {
 };
 
 // Prompts with many items for each CTA: whole items, drawn one at a time from a
-// counter, those of the last row set of their sequence first (they see the most
-// keys), and of one such level the sets of two tiles first, then by sequence, then
-// by head.  No result makes a round trip through memory, and what the line's cost
-// model misses evens out.
+// counter, those of the last row set of their sequence first (of one sequence they see
+// the most keys), and of one such level the sets of two tiles first, then by sequence,
+// then by head.  No result makes a round trip through memory, and what the line's cost
+// model misses evens out.  Keys before the queries are not looked at: a short piece behind a
+// long prefix is drawn among the last, and its items are one CTA's each.
 struct Draw {
   const AttnParams& p;
   int lane;
@@ -835,11 +837,11 @@ __device__ __forceinline__ int64_t row_offset(const AttnParams& p, const Item& i
 // does not see, its result is computed again, key by key, with the weights that it had
 // (m, l); else it stands.  A warp takes a row at a time: a lane takes a key's
 // score, then some columns of all 32 keys' values.  Slow and rare: 8191 tokens, 32 heads
-// with one such value at key 127 take 2.1 ms, at key 8000 57 ms, and 0.35 ms without.
+// with one such value at key 127 take 2.1 ms, at key 8000 54 ms, and 0.35 ms without.
 // Loads are 4 to 16 bytes, in the order that the sums need (2 bytes at a time: 7.6 and
-// 146 ms).  Unrolled by 8 it takes 48 ms, but prompts without such a value, which never
+// 146 ms).  Unrolled by 8 it took 48 ms (57 in that build), but prompts without such a value, which never
 // come here, 348 us instead of 341.  Other warps may wait for this one longer than a wait
-// lasts (2 s are reached at about 280 thousand keys): it shows them that it goes on.
+// lasts (2 s are reached at about 300 thousand keys): it shows them that it goes on.
 template <int kD, bool kF16, bool kPaged>
 __device__ __noinline__ void repair_rows(const AttnParams* p, const Item* it, const Waiter* wait, int s, uint32_t rows, float m,
                                          float l, int col0, int col1, uint16_t* out, float* part) {

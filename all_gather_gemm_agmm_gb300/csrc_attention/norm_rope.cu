@@ -16,8 +16,8 @@
 // does not grow with the position (a float32 product is off by up to
 // position * 2^-24 radians).
 //
-// Measured: 16384 tokens of 80 heads of 128: 127 us, 5.5 TB/s.  Blocks of 256 threads: 142
-// us; of 512: 226 us; of 64: 137 us at best.
+// Measured: 16384 tokens of 80 heads of 128: 129 us, 5.5 TB/s.  In one build: 127 us; blocks
+// of 256 threads 142 us; of 512: 226 us; of 64: 137 us at best.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -101,7 +101,7 @@ void agmm_norm_rope_destroy(agmm_norm_rope_t plan);
  * 128-row tile sees, or that lies outside the sequence, is never used, whatever
  * it holds; a non-finite value in a row that some rows see reaches those only.
  * (The others of its tile are then computed again one by one, in time that grows
- * with their keys: 57 ms for 8000.  That is not a wait that runs out.)
+ * with their keys: 54 ms for 8000.  That is not a wait that runs out.)
  */
 typedef struct {
   int q_heads, kv_heads; /* q_heads a multiple of kv_heads */
