@@ -358,8 +358,9 @@ class _On:
 
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             handle = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
-            # ExternalStream would take handle 0 for "a new stream": it is the default one
-            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+            # 0 and 1 (cudaStreamLegacy) are PyTorch's default stream; ExternalStream makes
+            # another one of 0, and takes an odd handle for a number of its own
+            stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
         self._ctx = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):

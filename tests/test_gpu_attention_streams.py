@@ -107,3 +107,20 @@ def test_the_default_stream_by_its_handle(agmm, name):
         got = call(stream=0)
     torch.cuda.synchronize()
     assert _same(got, want)
+
+
+@pytest.mark.parametrize("handle", [1, 2], ids=["legacy", "per-thread"])
+@pytest.mark.parametrize("name", ["rope", "prompt", "tree"])
+def test_the_special_handles(agmm, name, handle):
+    """cudaStreamLegacy and cudaStreamPerThread, while the current stream is another one and busy."""
+    call = _calls(agmm)[name]
+    want = call()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        _dirty()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)
+        got = call(stream=handle)
+    torch.cuda.synchronize()
+    assert _same(got, want)
