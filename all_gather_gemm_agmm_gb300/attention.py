@@ -461,6 +461,7 @@ def tree_attention(q, k_cache, v_cache, page_table, context_lens, node_starts, m
     import torch
 
     tokens, sequences = q.shape[0], page_table.shape[0]
+    bound = max_nodes
     if max_nodes is None:
         # a power of two: few plans for all numbers of tokens
         max_nodes = min(MAX_NODES, 1 << max(0, tokens - 1).bit_length())
@@ -477,5 +478,8 @@ def tree_attention(q, k_cache, v_cache, page_table, context_lens, node_starts, m
             out = (torch.zeros if tokens > plan.max_nodes else torch.empty)(q.shape, dtype=q.dtype, device=q.device)
         if workspace is None:
             workspace = plan.new_workspace()
+        elif bound is None and workspace.numel() * workspace.element_size() < plan.workspace_bytes():
+            raise ValueError(f"without max_nodes, room is made for {plan.max_nodes} drafted tokens to a sequence, which needs a "
+                             f"workspace of {plan.workspace_bytes()} bytes: give the max_nodes that this one was made for")
     plan.run(q, k_cache, v_cache, page_table, context_lens, node_starts, out, workspace, mask=mask, stream=stream)
     return out

@@ -70,3 +70,15 @@ def test_more_tokens_than_the_given_bound_allows(agmm):
     check(got[:3], want[:3], bound[:3])
     check(got[5:], want[5:], bound[5:])
     assert bool((got[3:5] == 0).all())
+
+
+def test_a_workspace_for_fewer_nodes(agmm):
+    """A plan's workspace goes with the plan's bound; without the bound the function says so."""
+    p = Problem([40] * 32, [1] * 32, 8, 2, 64, 16, torch.bfloat16, seed=7)
+    want, bound = p.ref(_chain(p), 0.125)
+    ws = agmm.TreePlan(8, 2, 64, page_size=16, max_nodes=1).new_workspace()
+    check(_call(agmm, p, max_nodes=1, workspace=ws), want, bound)
+    with pytest.raises(ValueError, match="max_nodes"):
+        _call(agmm, p, workspace=ws)
+    ws = agmm.TreePlan(8, 2, 64, page_size=16, max_nodes=32).new_workspace()
+    check(_call(agmm, p, workspace=ws), want, bound)
