@@ -408,3 +408,5 @@ def all_gather_matmul(xs, y, my_id: int = 0, rhs_transpose: bool = False, out=No
 
 from .attention import (NormRopePlan, PromptPlan, TreePlan, prompt_attention, qkv_norm_rope,  # noqa: E402,F401
                         rotary_axes, tree_attention, tree_mask)
+from .feedforward import (GatedPlan, LayerNormPlan, LinearPlan, gated_matmul, gated_matmul_backward,  # noqa: E402,F401
+                          layer_norm, layer_norm_backward, linear_matmul, linear_matmul_backward)

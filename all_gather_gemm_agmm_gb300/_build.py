@@ -1,7 +1,8 @@
 """Build the sm_103a shared library ``libagmm.so`` in-tree with nvcc.
 
 The translation units (kernel variants in three groups, selection and launch,
-C ABI, allocation-free entry point; the attention operators' kernels and C ABI)
+C ABI, allocation-free entry point; the attention and the feed-forward operators'
+kernels and C ABI)
 compile in parallel to objects under
 ``_build/`` and link, with the CUDA runtime linked statically, into
 ``all_gather_gemm_agmm_gb300/libagmm.so``.  No cmake, one ``-gencode``.
@@ -18,12 +19,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 CSRC_ATTENTION = os.path.join(PKG, "csrc_attention")
+CSRC_FEEDFORWARD = os.path.join(PKG, "csrc_feedforward")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libagmm.so")
 SOURCES = ["agmm_select_rows_a1.cu", "agmm_select_rows_a2.cu", "agmm_select_swap.cu", "agmm_kernels.cu",
            "agmm_api.cpp", "agmm_noalloc.cu"]
 ATTENTION_SOURCES = ["norm_rope.cu", "attn_prompt.cu", "attn_tree.cu", "attn_launch.cu", "attn_api.cpp"]
+FEEDFORWARD_SOURCES = ["ff_rows_plain.cu", "ff_rows_gated.cu", "ff_rows_linear.cu", "ff_swap_plain.cu", "ff_swap_gated.cu",
+                       "ff_swap_linear.cu", "ff_launch.cu", "ff_pointwise.cu", "layer_norm.cu", "ff_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,7 +39,7 @@ def _nvcc() -> str:
 
 
 def _deps():
-    files = [os.path.join(d, f) for d in (CSRC, CSRC_ATTENTION, INCLUDE) for f in os.listdir(d)]
+    files = [os.path.join(d, f) for d in (CSRC, CSRC_ATTENTION, CSRC_FEEDFORWARD, INCLUDE) for f in os.listdir(d)]
     files.append(os.path.abspath(__file__))
     return files
 
@@ -52,7 +56,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
-    common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-I", CSRC_ATTENTION]
+    common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-I", CSRC_ATTENTION, "-I", CSRC_FEEDFORWARD]
     if ptxas_info:
         common += ["-Xptxas", "-v"]
 
@@ -69,6 +73,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj
 
     sources = [os.path.join(CSRC, f) for f in SOURCES] + [os.path.join(CSRC_ATTENTION, f) for f in ATTENTION_SOURCES]
+    sources += [os.path.join(CSRC_FEEDFORWARD, f) for f in FEEDFORWARD_SOURCES]
     with ThreadPoolExecutor(max_workers=len(sources)) as ex:
         objs = list(ex.map(compile_one, sources))
     tmp = LIB + f".tmp{os.getpid()}"

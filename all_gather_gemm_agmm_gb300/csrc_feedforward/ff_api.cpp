@@ -1,0 +1,767 @@
+// ff_api.cpp -- the C ABI of include/agmm_feedforward.h: argument checks, plans,
+// tile schedules and launches of the feed-forward operators.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <mutex>
+#include <new>
+
+#include <cudaTypedefs.h>
+
+#include "agmm_feedforward.h"
+#include "ff_params.h"
+
+namespace agmm {
+agmm_status_t set_last_error(agmm_status_t status, const char* message);
+}
+
+using namespace agmm;
+using namespace agmm::ff;
+
+struct ProductPlan {
+  int64_t k, n;
+  int act;
+  bool transpose, f16;  // weights stored [n, k]; fp16
+  int device, sms;
+  int pairs, singles;   // CTA pairs, and CTAs, that run at once
+  uint64_t wait_limit_cycles;
+  int test_drop;
+};
+struct agmm_gated_s : ProductPlan {};
+struct agmm_linear_s : ProductPlan {};
+struct agmm_layer_norm_s {
+  int columns, device, sms;
+  float eps;
+  bool f16;
+};
+
+namespace {
+
+// A cluster's share of cut tiles is at least this many k blocks (of 64 values): the parts
+// make a round trip through L2, 128 KiB of each CTA of a row tile, and those of a swapped
+// tile in proportion to its tokens.
+constexpr int kMinRowBlocks = 8;
+constexpr int kMinSwapBlocks = 4;
+// Row tiles (pairs of them) that sweep the columns together.
+constexpr int kGroupM = 8;
+constexpr int64_t kMostRows = INT_MAX - 1024;  // coordinates of tiles behind the last row fit 32 bits
+constexpr int64_t kMostTiles = 1 << 30;
+constexpr int64_t kMostWidth = 1 << 20;
+
+agmm_status_t fail(agmm_status_t s, const char* fmt, ...) {
+  char text[256];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(text, sizeof text, fmt, ap);
+  va_end(ap);
+  return set_last_error(s, text);
+}
+
+#define AGMM_TRY(expr)                        \
+  do {                                        \
+    const agmm_status_t st_ = (expr);         \
+    if (st_ != AGMM_OK) return st_;           \
+  } while (0)
+
+agmm_status_t check_cuda(cudaError_t e, const char* what) {
+  return e == cudaSuccess ? AGMM_OK : fail(AGMM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+agmm_status_t check_device(int* device, int* sms) {
+  int major = 0, minor = 0;
+  cudaError_t e = cudaGetDevice(device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device);
+  AGMM_TRY(check_cuda(e, "device query"));
+  if (major != 10 || minor != 3)
+    return fail(AGMM_ERR_UNSUPPORTED, "this library is built for sm_103a only; device is sm_%d%d", major, minor);
+  return AGMM_OK;
+}
+
+agmm_status_t check_plan_device(int device) {
+  int now = -1;
+  AGMM_TRY(check_cuda(cudaGetDevice(&now), "cudaGetDevice"));
+  if (now != device) return fail(AGMM_ERR_INVALID_ARG, "the plan belongs to device %d, the current device is %d", device, now);
+  return AGMM_OK;
+}
+
+agmm_status_t check_width(const char* name, int64_t v, int64_t most) {
+  if (v < 8 || v > most || v % 8)
+    return fail(AGMM_ERR_INVALID_ARG, "%s must be a multiple of 8 in [8, %lld]: %lld", name, (long long)most, (long long)v);
+  return AGMM_OK;
+}
+
+agmm_status_t check_dtype(int dtype) {
+  if (dtype != AGMM_BF16 && dtype != AGMM_F16)
+    return fail(AGMM_ERR_INVALID_ARG, "dtype must be AGMM_BF16 or AGMM_F16: %d", dtype);
+  return AGMM_OK;
+}
+
+agmm_status_t check_pointer(const char* name, const void* p, size_t align) {
+  if (!p) return fail(AGMM_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) % align) return fail(AGMM_ERR_ALIGNMENT, "%s is not %zu-byte aligned", name, align);
+  return AGMM_OK;
+}
+
+// A matrix: there, 16-byte aligned, its rows whole and a multiple of 16 bytes apart.
+// One row has no stride to speak of.
+agmm_status_t check_matrix(const char* name, const void* p, int64_t* stride, int64_t rows, int64_t cols) {
+  AGMM_TRY(check_pointer(name, p, 16));
+  if (rows <= 1) {
+    *stride = cols;
+    return AGMM_OK;
+  }
+  if (*stride < cols || *stride >= (int64_t)1 << 36)
+    return fail(AGMM_ERR_INVALID_ARG, "%s: the row stride (%lld) must be at least the row's %lld values", name, (long long)*stride,
+                (long long)cols);
+  if (*stride % 8) return fail(AGMM_ERR_ALIGNMENT, "%s: the row stride (%lld) must be a multiple of 8", name, (long long)*stride);
+  return AGMM_OK;
+}
+
+// The device's peak clock.  Asked once per device: the driver takes most of a
+// millisecond to answer.
+int peak_clock_khz(int device) {
+  static std::atomic<int> known[64];
+  const bool cached = device >= 0 && device < 64;
+  int khz = cached ? known[device].load(std::memory_order_relaxed) : 0;
+  if (khz > 0) return khz;
+  if (cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, device) != cudaSuccess || khz <= 0) {
+    (void)cudaGetLastError();
+    khz = 2100000;  // above the part's 2.07 GHz peak
+  }
+  if (cached) known[device].store(khz, std::memory_order_relaxed);
+  return khz;
+}
+
+// ------------------------------------------------------------------ workspace
+// status words, counters of cut tiles | partial results.  Fewer than two tiles to a cluster
+// are cut, with a counter for each CTA's epilogue warps.
+constexpr int kMostSms = (AGMM_FEEDFORWARD_HEAD_BYTES - kStatusBytes) / (2 * kEpiWarps * (int)sizeof(int));
+size_t partial_bytes(const ProductPlan* pl) { return (size_t)pl->sms * kSlots * kSlotBytes; }
+size_t workspace_bytes(const ProductPlan* pl) { return AGMM_FEEDFORWARD_HEAD_BYTES + partial_bytes(pl); }
+
+// -------------------------------------------------------------- tensor maps
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// {inner, rows, segments} of 16-bit values; boxes of 64 x box_rows, 128-byte swizzled,
+// zeros outside: what lies behind a segment's last row is not its neighbour's.
+agmm_status_t encode(CUtensorMap* map, const char* name, const void* ptr, int64_t inner, int64_t rows, int64_t segments, int64_t stride,
+                     int box_rows, bool f16) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(AGMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)segments};
+  const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, (cuuint64_t)(segments > 1 ? rows * stride : stride) * 2};
+  const cuuint32_t box[3] = {kTileK, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
+  const CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
+                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(AGMM_ERR_CUDA, "tensor map of %s: cuTensorMapEncodeTiled gave %d", name, (int)r);
+  return AGMM_OK;
+}
+
+// A matrix as an operand that is contracted along its rows' values (K-major), or along
+// its rows (MN-major).
+struct Matrix {
+  const char* name;
+  const void* ptr;
+  int64_t inner, rows, segments, stride;
+};
+
+agmm_status_t encode_operand(CUtensorMap* map, const Matrix& m, bool mn_major, int box_rows, bool f16) {
+  return encode(map, m.name, m.ptr, m.inner, m.rows, m.segments, m.stride, mn_major ? 64 : box_rows, f16);
+}
+
+// ---------------------------------------------------------------- schedules
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Whole tiles go round the clusters.  Those of a last wave that fills less than two thirds
+// of them are cut along k, with the wave before it, evenly over the clusters, as far as
+// every share is worth its parts' round trip.
+void make_schedule(GemmParams* p, int clusters, int min_blocks) {
+  const int T = p->num_tiles, C = clusters, rem = T % C;
+  p->dp_tiles = T;
+  p->sk_clusters = 1;
+  if (rem == 0 || 3 * rem >= 2 * C) return;
+  const int shared = T < C ? T : C + rem;
+  const int64_t units = (int64_t)shared * p->k_blocks;
+  const int64_t parts = std::min<int64_t>(C, units / min_blocks);
+  // a share of a tile or more, where tiles are fewer: nothing to gain
+  if (parts <= std::min(shared, C - 1)) return;
+  p->dp_tiles = T - shared;
+  p->sk_clusters = (int)parts;
+}
+
+// How the tokens' rows lie in tiles: boxes of rows that never leave their shard.
+void chunk_rows(GemmParams* p, int shards, int64_t rows, int box) {
+  p->shards = shards;
+  p->shard_rows = rows;
+  p->box = box;
+  p->shard_chunks = (int)ceil_div(rows, box);
+  p->chunks = p->shard_chunks * shards;
+}
+
+// Row tiles of several shards: the box that makes the fewest tiles, the largest of those.
+int row_box(int shards, int64_t rows) {
+  int best = 128;
+  if (shards == 1) return best;
+  int64_t fewest = INT64_MAX;
+  for (int box = 128; box >= 8; box /= 2) {
+    const int64_t tiles = ceil_div(ceil_div(rows, box) * shards, 128 / box);
+    if (tiles < fewest) {
+      fewest = tiles;
+      best = box;
+    }
+  }
+  return best;
+}
+
+// Swapped tiles hold all tokens: their box, or 0 where they are too many.
+int swap_box(int shards, int64_t rows) {
+  if (rows > kMaxSwapRows) return 0;
+  const int box = (int)ceil_div(rows, 8) * 8;
+  return box * shards <= kMaxSwapRows ? box : 0;
+}
+
+void common_params(const ProductPlan* pl, GemmParams* p, void* workspace) {
+  char* const ws = static_cast<char*>(workspace);
+  p->status = reinterpret_cast<int*>(ws);
+  p->counters = reinterpret_cast<int*>(ws + kStatusBytes);
+  p->partial = reinterpret_cast<float*>(ws + AGMM_FEEDFORWARD_HEAD_BYTES);
+  p->wait_limit_cycles = pl->wait_limit_cycles;
+  p->test_drop = pl->test_drop;
+  p->f16 = pl->f16;
+  p->problems = 1;
+  p->seg_blocks = p->k_blocks = 1;
+}
+
+agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, int64_t m_tiles, int64_t n_tiles, cudaStream_t stream) {
+  if (m_tiles * n_tiles * p->problems > kMostTiles) return fail(AGMM_ERR_UNSUPPORTED, "more than 2^30 tiles of results");
+  p->m_tiles = (int)m_tiles;
+  p->n_tiles = (int)n_tiles;
+  p->tiles_per_problem = p->m_tiles * p->n_tiles;
+  p->num_tiles = p->tiles_per_problem * p->problems;
+  p->group_m = kGroupM;
+  p->stages = kRowStages;
+  p->tmem_cols = 512;
+  make_schedule(p, pl->pairs, kMinRowBlocks);
+  const int clusters = p->dp_tiles == p->num_tiles ? std::min(p->num_tiles, pl->pairs) : pl->pairs;
+  const size_t smem = 1024 + (size_t)kRowStages * 2 * kTileBytes + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
+  return check_cuda(launch_gemm(rows_gemm(epi, pl->f16), *p, clusters, 2, smem, stream), "product launch");
+}
+
+agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t features, cudaStream_t stream) {
+  p->m_tiles = (int)ceil_div(features, kTileM);
+  p->n_tiles = 1;
+  p->tiles_per_problem = p->num_tiles = p->m_tiles;
+  p->group_m = 1;
+  p->mma_n = (int)ceil_div(p->chunks * p->box, 16) * 16;
+  const int accs = epi == kEpiGated ? 2 : 1;
+  const size_t stage = (size_t)accs * kTileBytes + (size_t)p->mma_n * 128;
+  p->stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - 1024 - kCtlBytes) / stage);
+  p->tmem_cols = 32;
+  while ((int)p->tmem_cols < 2 * accs * p->mma_n) p->tmem_cols *= 2;
+  make_schedule(p, pl->singles, kMinSwapBlocks);
+  const int clusters = p->dp_tiles == p->num_tiles ? std::min(p->num_tiles, pl->singles) : pl->singles;
+  return check_cuda(launch_gemm(swap_gemm(epi, pl->f16), *p, clusters, 1, 1024 + p->stages * stage + kCtlBytes, stream),
+                    "product launch");
+}
+
+// X Wi for one weight or two (gated), with an epilogue.
+agmm_status_t forward(const ProductPlan* pl, GemmParams* p, int epi, int shards, int64_t rows, const void* const* x, int64_t x_stride,
+                      const void* const* w, int64_t w_stride, cudaStream_t stream) {
+  const int weights = epi == kEpiGated ? 2 : 1;
+  const int swap = swap_box(shards, rows);
+  const int box = swap ? swap : row_box(shards, rows);
+  chunk_rows(p, shards, rows, box);
+  p->cols = pl->n;
+  p->k_blocks = p->seg_blocks = (int)ceil_div(pl->k, kTileK);
+  OperandParams &xo = swap ? p->b : p->a, &wo = swap ? p->a : p->b;
+  CUtensorMap *xm = swap ? p->b_map : p->a_map, *wm = swap ? p->a_map : p->b_map;
+  xo.maps = shards;
+  xo.by_shard = 1;
+  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], {"x", x[s], pl->k, rows, 1, x_stride}, false, box, pl->f16));
+  wo.maps = weights;
+  wo.mn_major = !pl->transpose;
+  for (int i = 0; i < weights; ++i) {
+    const Matrix m = pl->transpose ? Matrix{"a weight", w[i], pl->k, pl->n, 1, w_stride} : Matrix{"a weight", w[i], pl->n, pl->k, 1, w_stride};
+    AGMM_TRY(encode_operand(&wm[i], m, wo.mn_major, kTileM, pl->f16));
+  }
+  if (swap) return run_swap(pl, p, epi, pl->n, stream);
+  if (epi == kEpiGated) {
+    wo.by_rank = 1;
+    p->b_tile_step = kTileN / 2;
+  } else {
+    p->b_tile_step = kTileN;
+    p->b_half_step = kTileN / 2;
+  }
+  return run_rows(pl, p, epi, ceil_div((int64_t)p->chunks * box, 2 * kTileM), ceil_div(pl->n, p->b_tile_step), stream);
+}
+
+// dx = sum over the weights of d_i Wi^T
+agmm_status_t input_grad(const ProductPlan* pl, GemmParams* p, int weights, int64_t rows, const void* const* d, int64_t d_stride,
+                         const void* const* w, int64_t w_stride, void* dx, int64_t dx_stride, cudaStream_t stream) {
+  const int swap = swap_box(1, rows);
+  chunk_rows(p, 1, rows, swap ? swap : kTileM);
+  p->out[0] = dx;
+  p->ldo = dx_stride;
+  p->cols = pl->k;
+  p->seg_blocks = (int)ceil_div(pl->n, kTileK);
+  p->k_blocks = weights * p->seg_blocks;
+  OperandParams &to = swap ? p->b : p->a, &wo = swap ? p->a : p->b;
+  CUtensorMap *tm = swap ? p->b_map : p->a_map, *wm = swap ? p->a_map : p->b_map;
+  to.maps = wo.maps = weights;
+  to.by_segment = wo.by_segment = 1;
+  wo.mn_major = pl->transpose;
+  for (int i = 0; i < weights; ++i) {
+    AGMM_TRY(encode_operand(&tm[i], {"a gradient", d[i], pl->n, rows, 1, d_stride}, false, p->box, pl->f16));
+    const Matrix m = pl->transpose ? Matrix{"a weight", w[i], pl->k, pl->n, 1, w_stride} : Matrix{"a weight", w[i], pl->n, pl->k, 1, w_stride};
+    AGMM_TRY(encode_operand(&wm[i], m, wo.mn_major, kTileM, pl->f16));
+  }
+  if (swap) return run_swap(pl, p, kEpiPlain, pl->k, stream);
+  p->b_tile_step = kTileN;
+  p->b_half_step = kTileN / 2;
+  return run_rows(pl, p, kEpiPlain, ceil_div(rows, 2 * kTileM), ceil_div(pl->k, kTileN), stream);
+}
+
+// dWi = X^T d_i, stored like the weight; the tokens of each shard are a segment of the sum.
+agmm_status_t weight_grad(const ProductPlan* pl, GemmParams* p, int weights, int shards, int64_t rows, const void* const* x,
+                          int64_t x_stride, const void* const* d, int64_t d_stride, void* const* dw, int64_t dw_stride, bool f32,
+                          cudaStream_t stream) {
+  const int64_t out_rows = pl->transpose ? pl->n : pl->k, out_cols = pl->transpose ? pl->k : pl->n;
+  chunk_rows(p, 1, out_rows, kTileM);
+  p->problems = weights;
+  for (int i = 0; i < weights; ++i) p->out[i] = dw[i];
+  p->ldo = dw_stride;
+  p->out_f32 = f32;
+  p->cols = out_cols;
+  p->seg_blocks = (int)ceil_div(rows, kTileK);
+  if ((int64_t)p->seg_blocks * shards > INT_MAX) return fail(AGMM_ERR_UNSUPPORTED, "too many rows");
+  p->k_blocks = p->seg_blocks * shards;
+  OperandParams &xo = pl->transpose ? p->b : p->a, &go = pl->transpose ? p->a : p->b;
+  CUtensorMap *xm = pl->transpose ? p->b_map : p->a_map, *gm = pl->transpose ? p->a_map : p->b_map;
+  xo.maps = shards;
+  go.maps = weights;
+  xo.mn_major = go.mn_major = 1;
+  xo.by_segment = 1;
+  go.by_problem = 1;
+  go.z_segment = 1;
+  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], {"x", x[s], pl->k, rows, 1, x_stride}, true, 0, pl->f16));
+  for (int i = 0; i < weights; ++i) AGMM_TRY(encode_operand(&gm[i], {"a gradient", d[i], pl->n, rows, shards, d_stride}, true, 0, pl->f16));
+  p->b_tile_step = kTileN;
+  p->b_half_step = kTileN / 2;
+  return run_rows(pl, p, kEpiPlain, ceil_div(out_rows, 2 * kTileM), ceil_div(out_cols, kTileN), stream);
+}
+
+agmm_status_t zero_rows(const char* name, void* p, int64_t stride, int64_t rows, int64_t cols, bool f32, cudaStream_t stream) {
+  const size_t size = f32 ? 4 : 2;
+  return check_cuda(cudaMemset2DAsync(p, (size_t)stride * size, 0, (size_t)cols * size, (size_t)rows, stream), name);
+}
+
+// ---------------------------------------------------------------------- plans
+agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int transpose, int dtype) {
+  pl->k = k;
+  pl->n = n;
+  pl->act = act;
+  pl->transpose = transpose != 0;
+  pl->f16 = dtype == AGMM_F16;
+  const int khz = peak_clock_khz(pl->device);
+  const char* ms = std::getenv("AGMM_WAIT_LIMIT_MS");
+  const int limit = ms && *ms ? std::atoi(ms) : 0;
+  pl->wait_limit_cycles = (uint64_t)(limit > 0 ? limit : 2000) * (uint64_t)khz;
+  const char* drop = std::getenv("AGMM_TEST_DROP_ARRIVE");
+  pl->test_drop = drop && std::atoi(drop) != 0;
+  if (pl->sms > kMostSms) return fail(AGMM_ERR_UNSUPPORTED, "more than %d SMs", kMostSms);
+  pl->singles = pl->sms;
+  pl->pairs = pl->sms / 2;
+  for (int epi = kEpiPlain; epi <= kEpiLinear; ++epi) {
+    int pairs = 0, singles = 0;
+    AGMM_TRY(check_cuda(prepare_gemm(rows_gemm(epi, pl->f16), 2, &pairs), "kernel attributes"));
+    AGMM_TRY(check_cuda(prepare_gemm(swap_gemm(epi, pl->f16), 1, &singles), "kernel attributes"));
+    pl->pairs = std::min(pl->pairs, pairs);
+    pl->singles = std::min(pl->singles, singles);
+  }
+  if (pl->pairs < 1 || pl->singles < 1) return fail(AGMM_ERR_UNSUPPORTED, "the kernels do not fit this device");
+  return AGMM_OK;
+}
+
+template <class Plan>
+agmm_status_t product_plan(int64_t k, int64_t n, int act, bool none_ok, int transpose, int dtype, Plan** out) {
+  AGMM_TRY(check_width("k", k, kMostWidth));
+  AGMM_TRY(check_width("n", n, kMostWidth));
+  AGMM_TRY(check_dtype(dtype));
+  if (act < (none_ok ? kActNone : kActRelu) || act > kActGeluTanh) return fail(AGMM_ERR_INVALID_ARG, "unknown activation: %d", act);
+  if (transpose != 0 && transpose != 1) return fail(AGMM_ERR_INVALID_ARG, "rhs_transpose must be 0 or 1: %d", transpose);
+  int device = 0, sms = 0;
+  AGMM_TRY(check_device(&device, &sms));
+  Plan* pl = new (std::nothrow) Plan();
+  if (!pl) return fail(AGMM_ERR_NOMEM, "plan allocation");
+  pl->device = device;
+  pl->sms = sms;
+  const agmm_status_t st = fill_plan(pl, k, n, act, transpose, dtype);
+  if (st != AGMM_OK) {
+    delete pl;
+    return st;
+  }
+  *out = pl;
+  return AGMM_OK;
+}
+
+agmm_status_t check_tokens(int64_t shards, int64_t rows) {
+  if (shards < 1 || shards > kMaxShards) return fail(AGMM_ERR_INVALID_ARG, "shards must be in [1, 8]: %lld", (long long)shards);
+  if (rows < 0 || rows > kMostRows / shards)
+    return fail(AGMM_ERR_INVALID_ARG, "shards * rows must be in [0, 2^31 - 1024]: %lld * %lld", (long long)shards, (long long)rows);
+  return AGMM_OK;
+}
+
+agmm_status_t check_x(const void* const* x, int64_t shards, int64_t* stride, int64_t rows, int64_t k) {
+  for (int s = 0; s < shards; ++s) AGMM_TRY(check_matrix("x", x[s], stride, rows, k));
+  return AGMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ----------------------------------------------------------------- layer_norm
+agmm_status_t agmm_layer_norm_plan(const agmm_layer_norm_desc_t* d, agmm_layer_norm_t* out) {
+  if (!out) return fail(AGMM_ERR_INVALID_ARG, "out_plan is NULL");
+  *out = nullptr;
+  if (!d) return fail(AGMM_ERR_INVALID_ARG, "desc is NULL");
+  AGMM_TRY(check_width("columns", d->columns, kMaxNormColumns));
+  AGMM_TRY(check_dtype(d->dtype));
+  if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) return fail(AGMM_ERR_INVALID_ARG, "eps must be finite and not negative");
+  int device = 0, sms = 0;
+  AGMM_TRY(check_device(&device, &sms));
+  agmm_layer_norm_s* pl = new (std::nothrow) agmm_layer_norm_s();
+  if (!pl) return fail(AGMM_ERR_NOMEM, "plan allocation");
+  pl->columns = d->columns;
+  pl->eps = d->eps;
+  pl->f16 = d->dtype == AGMM_F16;
+  pl->device = device;
+  pl->sms = sms;
+  *out = pl;
+  return AGMM_OK;
+}
+
+void agmm_layer_norm_destroy(agmm_layer_norm_t plan) { delete plan; }
+
+size_t agmm_layer_norm_workspace_bytes(agmm_layer_norm_t pl) {
+  if (!pl) return 0;
+  return AGMM_FEEDFORWARD_HEAD_BYTES + (size_t)norm_grad_blocks(INT_MAX, pl->columns, pl->sms) * 2 * pl->columns * sizeof(float);
+}
+
+agmm_status_t agmm_layer_norm_run(agmm_layer_norm_t pl, const agmm_layer_norm_args_t* a, void* stream) {
+  if (!pl || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
+  if (a->rows < 0 || a->rows > INT_MAX) return fail(AGMM_ERR_INVALID_ARG, "rows must be in [0, 2^31 - 1]: %lld", (long long)a->rows);
+  if (a->rows == 0) return AGMM_OK;
+  NormParams p = {};
+  p.ldx = a->x_stride;
+  p.ldo = a->out_stride;
+  AGMM_TRY(check_matrix("x", a->x, &p.ldx, a->rows, pl->columns));
+  AGMM_TRY(check_matrix("out", a->out, &p.ldo, a->rows, pl->columns));
+  if (a->weight) AGMM_TRY(check_pointer("weight", a->weight, 16));
+  if (a->bias) AGMM_TRY(check_pointer("bias", a->bias, 16));
+  if (a->mean) AGMM_TRY(check_pointer("mean", a->mean, 4));
+  if (a->rstd) AGMM_TRY(check_pointer("rstd", a->rstd, 4));
+  AGMM_TRY(check_plan_device(pl->device));
+  p.rows = a->rows;
+  p.cols = pl->columns;
+  p.eps = pl->eps;
+  p.x = static_cast<const uint16_t*>(a->x);
+  p.weight = static_cast<const uint16_t*>(a->weight);
+  p.bias = static_cast<const uint16_t*>(a->bias);
+  p.out = static_cast<uint16_t*>(a->out);
+  p.mean = a->mean;
+  p.rstd = a->rstd;
+  return check_cuda(launch_norm(p, pl->f16, static_cast<cudaStream_t>(stream)), "layer_norm launch");
+}
+
+agmm_status_t agmm_layer_norm_backward(agmm_layer_norm_t pl, const agmm_layer_norm_grad_args_t* a, void* stream) {
+  if (!pl || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
+  if (a->rows < 0 || a->rows > INT_MAX) return fail(AGMM_ERR_INVALID_ARG, "rows must be in [0, 2^31 - 1]: %lld", (long long)a->rows);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool sums = a->d_weight || a->d_bias;
+  if (a->d_weight) AGMM_TRY(check_pointer("d_weight", a->d_weight, 16));
+  if (a->d_bias) AGMM_TRY(check_pointer("d_bias", a->d_bias, 16));
+  if (a->rows == 0) {
+    if (sums) AGMM_TRY(check_plan_device(pl->device));
+    if (a->d_weight) AGMM_TRY(zero_rows("d_weight", a->d_weight, pl->columns, 1, pl->columns, a->f32_grads != 0, s));
+    if (a->d_bias) AGMM_TRY(zero_rows("d_bias", a->d_bias, pl->columns, 1, pl->columns, a->f32_grads != 0, s));
+    return AGMM_OK;
+  }
+  if (!a->dx && !sums) return AGMM_OK;
+  NormGradParams p = {};
+  p.ld_out = a->d_out_stride;
+  p.ldx = a->x_stride;
+  p.ld_add = a->add_stride;
+  p.ld_dx = a->dx_stride;
+  AGMM_TRY(check_matrix("d_out", a->d_out, &p.ld_out, a->rows, pl->columns));
+  AGMM_TRY(check_matrix("x", a->x, &p.ldx, a->rows, pl->columns));
+  AGMM_TRY(check_pointer("mean", a->mean, 4));
+  AGMM_TRY(check_pointer("rstd", a->rstd, 4));
+  if (a->weight) AGMM_TRY(check_pointer("weight", a->weight, 16));
+  if (a->add && !a->dx) return fail(AGMM_ERR_INVALID_ARG, "add is given without dx");
+  if (a->add) AGMM_TRY(check_matrix("add", a->add, &p.ld_add, a->rows, pl->columns));
+  if (a->dx) AGMM_TRY(check_matrix("dx", a->dx, &p.ld_dx, a->rows, pl->columns));
+  if (sums) AGMM_TRY(check_pointer("workspace", a->workspace, 256));
+  AGMM_TRY(check_plan_device(pl->device));
+  p.rows = a->rows;
+  p.cols = pl->columns;
+  p.d_out = static_cast<const uint16_t*>(a->d_out);
+  p.x = static_cast<const uint16_t*>(a->x);
+  p.weight = static_cast<const uint16_t*>(a->weight);
+  p.add = static_cast<const uint16_t*>(a->add);
+  p.mean = a->mean;
+  p.rstd = a->rstd;
+  p.dx = static_cast<uint16_t*>(a->dx);
+  p.part = sums ? reinterpret_cast<float*>(static_cast<char*>(a->workspace) + AGMM_FEEDFORWARD_HEAD_BYTES) : nullptr;
+  const int blocks = norm_grad_blocks(a->rows, pl->columns, pl->sms);
+  AGMM_TRY(check_cuda(launch_norm_grad(p, pl->f16, blocks, s), "layer_norm backward launch"));
+  if (!sums) return AGMM_OK;
+  SumPartsParams q = {};
+  q.part = p.part;
+  q.parts = blocks;
+  q.sums = 2;
+  q.cols = pl->columns;
+  q.out[0] = a->d_weight;
+  q.out[1] = a->d_bias;
+  q.out_f32 = a->f32_grads != 0;
+  return check_cuda(launch_sum_parts(q, pl->f16, s), "layer_norm sums launch");
+}
+
+// ---------------------------------------------------------------------- gated
+agmm_status_t agmm_gated_plan(const agmm_gated_desc_t* d, agmm_gated_t* out) {
+  if (!out) return fail(AGMM_ERR_INVALID_ARG, "out_plan is NULL");
+  *out = nullptr;
+  if (!d) return fail(AGMM_ERR_INVALID_ARG, "desc is NULL");
+  return product_plan(d->k, d->n, d->activation, false, d->rhs_transpose, d->dtype, out);
+}
+
+void agmm_gated_destroy(agmm_gated_t plan) { delete plan; }
+
+size_t agmm_gated_workspace_bytes(agmm_gated_t pl) { return pl ? workspace_bytes(pl) : 0; }
+
+agmm_status_t agmm_gated_run(agmm_gated_t pl, const agmm_gated_args_t* a, void* stream) {
+  if (!pl || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
+  AGMM_TRY(check_tokens(a->shards, a->rows));
+  if (a->rows == 0) return AGMM_OK;
+  const int64_t tokens = a->shards * a->rows, w_rows = pl->transpose ? pl->n : pl->k, w_cols = pl->transpose ? pl->k : pl->n;
+  int64_t x_stride = a->x_stride, w_stride = a->w_stride, out_stride = a->out_stride, saved_stride = a->saved_stride;
+  AGMM_TRY(check_x(a->x, a->shards, &x_stride, a->rows, pl->k));
+  AGMM_TRY(check_matrix("w_gate", a->w_gate, &w_stride, w_rows, w_cols));
+  AGMM_TRY(check_matrix("w_up", a->w_up, &w_stride, w_rows, w_cols));
+  AGMM_TRY(check_matrix("out", a->out, &out_stride, tokens, pl->n));
+  if (!a->gate != !a->up) return fail(AGMM_ERR_INVALID_ARG, "gate and up are given together or not at all");
+  if (a->gate) {
+    AGMM_TRY(check_matrix("gate", a->gate, &saved_stride, tokens, pl->n));
+    AGMM_TRY(check_matrix("up", a->up, &saved_stride, tokens, pl->n));
+  }
+  AGMM_TRY(check_pointer("workspace", a->workspace, 256));
+  AGMM_TRY(check_plan_device(pl->device));
+  GemmParams p = {};
+  common_params(pl, &p, a->workspace);
+  p.out[0] = a->out;
+  p.ldo = out_stride;
+  p.saved[0] = a->gate;
+  p.saved[1] = a->up;
+  p.lds = saved_stride;
+  p.act = pl->act;
+  const void* const w[2] = {a->w_gate, a->w_up};
+  return forward(pl, &p, kEpiGated, (int)a->shards, a->rows, a->x, x_stride, w, w_stride, static_cast<cudaStream_t>(stream));
+}
+
+agmm_status_t agmm_gated_backward(agmm_gated_t pl, const agmm_gated_grad_args_t* a, void* stream) {
+  if (!pl || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
+  AGMM_TRY(check_tokens(a->shards, a->rows));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t tokens = a->shards * a->rows, w_rows = pl->transpose ? pl->n : pl->k, w_cols = pl->transpose ? pl->k : pl->n;
+  int64_t x_stride = a->x_stride, w_stride = a->w_stride, out_stride = a->d_out_stride, saved_stride = a->saved_stride,
+          d_stride = a->d_stride, dx_stride = a->dx_stride, dw_stride = a->dw_stride;
+  if (!a->dw_gate != !a->dw_up) return fail(AGMM_ERR_INVALID_ARG, "dw_gate and dw_up are given together or not at all");
+  if (a->dw_gate) {
+    AGMM_TRY(check_matrix("dw_gate", a->dw_gate, &dw_stride, w_rows, w_cols));
+    AGMM_TRY(check_matrix("dw_up", a->dw_up, &dw_stride, w_rows, w_cols));
+  }
+  void* const dw[2] = {a->dw_gate, a->dw_up};
+  if (a->rows == 0) {
+    if (!a->dw_gate) return AGMM_OK;
+    AGMM_TRY(check_plan_device(pl->device));
+    AGMM_TRY(zero_rows("dw_gate", a->dw_gate, dw_stride, w_rows, w_cols, a->f32_grads != 0, s));
+    return zero_rows("dw_up", a->dw_up, dw_stride, w_rows, w_cols, a->f32_grads != 0, s);
+  }
+  AGMM_TRY(check_matrix("d_out", a->d_out, &out_stride, tokens, pl->n));
+  AGMM_TRY(check_matrix("gate", a->gate, &saved_stride, tokens, pl->n));
+  AGMM_TRY(check_matrix("up", a->up, &saved_stride, tokens, pl->n));
+  AGMM_TRY(check_matrix("d_gate", a->d_gate, &d_stride, tokens, pl->n));
+  AGMM_TRY(check_matrix("d_up", a->d_up, &d_stride, tokens, pl->n));
+  if (a->dx) {
+    AGMM_TRY(check_matrix("w_gate", a->w_gate, &w_stride, w_rows, w_cols));
+    AGMM_TRY(check_matrix("w_up", a->w_up, &w_stride, w_rows, w_cols));
+    AGMM_TRY(check_matrix("dx", a->dx, &dx_stride, tokens, pl->k));
+  }
+  if (a->dw_gate) AGMM_TRY(check_x(a->x, a->shards, &x_stride, a->rows, pl->k));
+  AGMM_TRY(check_pointer("workspace", a->workspace, 256));
+  AGMM_TRY(check_plan_device(pl->device));
+  GatedGradParams g = {};
+  g.rows = tokens;
+  g.cols = pl->n;
+  g.d_out = static_cast<const uint16_t*>(a->d_out);
+  g.gate = static_cast<const uint16_t*>(a->gate);
+  g.up = static_cast<const uint16_t*>(a->up);
+  g.d_gate = static_cast<uint16_t*>(a->d_gate);
+  g.d_up = static_cast<uint16_t*>(a->d_up);
+  g.ld_out = out_stride;
+  g.ld_saved = saved_stride;
+  g.ld_grad = d_stride;
+  g.act = pl->act;
+  AGMM_TRY(check_cuda(launch_gated_grad(g, pl->f16, pl->sms, s), "gated backward launch"));
+  const void* const d[2] = {a->d_gate, a->d_up};
+  const void* const w[2] = {a->w_gate, a->w_up};
+  if (a->dx) {
+    GemmParams p = {};
+    common_params(pl, &p, a->workspace);
+    AGMM_TRY(input_grad(pl, &p, 2, tokens, d, d_stride, w, w_stride, a->dx, dx_stride, s));
+  }
+  if (a->dw_gate) {
+    GemmParams p = {};
+    common_params(pl, &p, a->workspace);
+    AGMM_TRY(weight_grad(pl, &p, 2, (int)a->shards, a->rows, a->x, x_stride, d, d_stride, dw, dw_stride, a->f32_grads != 0, s));
+  }
+  return AGMM_OK;
+}
+
+// --------------------------------------------------------------------- linear
+agmm_status_t agmm_linear_plan(const agmm_linear_desc_t* d, agmm_linear_t* out) {
+  if (!out) return fail(AGMM_ERR_INVALID_ARG, "out_plan is NULL");
+  *out = nullptr;
+  if (!d) return fail(AGMM_ERR_INVALID_ARG, "desc is NULL");
+  return product_plan(d->k, d->n, d->activation, true, d->rhs_transpose, d->dtype, out);
+}
+
+void agmm_linear_destroy(agmm_linear_t plan) { delete plan; }
+
+size_t agmm_linear_workspace_bytes(agmm_linear_t pl) { return pl ? workspace_bytes(pl) : 0; }
+
+agmm_status_t agmm_linear_run(agmm_linear_t pl, const agmm_linear_args_t* a, void* stream) {
+  if (!pl || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
+  AGMM_TRY(check_tokens(a->shards, a->rows));
+  if (a->rows == 0) return AGMM_OK;
+  const int64_t tokens = a->shards * a->rows, w_rows = pl->transpose ? pl->n : pl->k, w_cols = pl->transpose ? pl->k : pl->n;
+  int64_t x_stride = a->x_stride, w_stride = a->w_stride, out_stride = a->out_stride, res_stride = a->residual_stride,
+          pre_stride = a->pre_stride;
+  AGMM_TRY(check_x(a->x, a->shards, &x_stride, a->rows, pl->k));
+  AGMM_TRY(check_matrix("w", a->w, &w_stride, w_rows, w_cols));
+  if (a->bias) AGMM_TRY(check_pointer("bias", a->bias, 16));
+  if (a->residual) AGMM_TRY(check_matrix("residual", a->residual, &res_stride, tokens, pl->n));
+  AGMM_TRY(check_matrix("out", a->out, &out_stride, tokens, pl->n));
+  if (a->pre) AGMM_TRY(check_matrix("pre", a->pre, &pre_stride, tokens, pl->n));
+  AGMM_TRY(check_pointer("workspace", a->workspace, 256));
+  AGMM_TRY(check_plan_device(pl->device));
+  GemmParams p = {};
+  common_params(pl, &p, a->workspace);
+  p.out[0] = a->out;
+  p.ldo = out_stride;
+  p.saved[0] = a->pre;
+  p.lds = pre_stride;
+  p.bias = a->bias;
+  p.residual = a->residual;
+  p.ldr = res_stride;
+  p.act = pl->act;
+  return forward(pl, &p, kEpiLinear, (int)a->shards, a->rows, a->x, x_stride, &a->w, w_stride, static_cast<cudaStream_t>(stream));
+}
+
+agmm_status_t agmm_linear_backward(agmm_linear_t pl, const agmm_linear_grad_args_t* a, void* stream) {
+  if (!pl || !a) return fail(AGMM_ERR_INVALID_ARG, "plan or args is NULL");
+  AGMM_TRY(check_tokens(a->shards, a->rows));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t tokens = a->shards * a->rows, w_rows = pl->transpose ? pl->n : pl->k, w_cols = pl->transpose ? pl->k : pl->n;
+  int64_t x_stride = a->x_stride, w_stride = a->w_stride, out_stride = a->d_out_stride, pre_stride = a->pre_stride,
+          d_stride = a->d_pre_stride, dx_stride = a->dx_stride, dw_stride = a->dw_stride;
+  const bool f32 = a->f32_grads != 0;
+  if (a->dw) AGMM_TRY(check_matrix("dw", a->dw, &dw_stride, w_rows, w_cols));
+  if (a->d_bias) AGMM_TRY(check_pointer("d_bias", a->d_bias, 16));
+  if (a->rows == 0) {
+    if (a->dw || a->d_bias) AGMM_TRY(check_plan_device(pl->device));
+    if (a->dw) AGMM_TRY(zero_rows("dw", a->dw, dw_stride, w_rows, w_cols, f32, s));
+    if (a->d_bias) AGMM_TRY(zero_rows("d_bias", a->d_bias, pl->n, 1, pl->n, f32, s));
+    return AGMM_OK;
+  }
+  const bool acts = pl->act != kActNone;
+  AGMM_TRY(check_matrix("d_out", a->d_out, &out_stride, tokens, pl->n));
+  if (acts) {
+    AGMM_TRY(check_matrix("pre", a->pre, &pre_stride, tokens, pl->n));
+    AGMM_TRY(check_matrix("d_pre", a->d_pre, &d_stride, tokens, pl->n));
+  } else if (a->pre || a->d_pre) {
+    return fail(AGMM_ERR_INVALID_ARG, "pre and d_pre belong to an activation, and the plan has none");
+  }
+  if (a->dx) {
+    AGMM_TRY(check_matrix("w", a->w, &w_stride, w_rows, w_cols));
+    AGMM_TRY(check_matrix("dx", a->dx, &dx_stride, tokens, pl->k));
+  }
+  if (a->dw) AGMM_TRY(check_x(a->x, a->shards, &x_stride, a->rows, pl->k));
+  AGMM_TRY(check_pointer("workspace", a->workspace, 256));
+  AGMM_TRY(check_plan_device(pl->device));
+  if (acts || a->d_bias) {
+    GemmParams where = {};
+    common_params(pl, &where, a->workspace);
+    ActGradParams g = {};
+    g.rows = tokens;
+    g.cols = pl->n;
+    g.d_out = static_cast<const uint16_t*>(a->d_out);
+    g.pre = static_cast<const uint16_t*>(a->pre);
+    g.d_pre = static_cast<uint16_t*>(a->d_pre);
+    g.ld_out = out_stride;
+    g.ld_pre = pre_stride;
+    g.ld_grad = d_stride;
+    g.act = pl->act;
+    g.part = a->d_bias ? where.partial : nullptr;
+    g.row_blocks = act_grad_row_blocks(tokens, pl->n, pl->sms);
+    const int64_t room = (int64_t)(partial_bytes(pl) / ((size_t)pl->n * sizeof(float)));
+    if (a->d_bias) g.row_blocks = (int)std::min<int64_t>(g.row_blocks, room);
+    AGMM_TRY(check_cuda(launch_act_grad(g, pl->f16, s), "linear backward launch"));
+    if (a->d_bias) {
+      SumPartsParams q = {};
+      q.part = g.part;
+      q.parts = g.row_blocks;
+      q.sums = 1;
+      q.cols = pl->n;
+      q.out[0] = a->d_bias;
+      q.out_f32 = f32;
+      AGMM_TRY(check_cuda(launch_sum_parts(q, pl->f16, s), "linear backward sums launch"));
+    }
+  }
+  const void* const d = acts ? a->d_pre : a->d_out;
+  if (!acts) d_stride = out_stride;
+  if (a->dx) {
+    GemmParams p = {};
+    common_params(pl, &p, a->workspace);
+    AGMM_TRY(input_grad(pl, &p, 1, tokens, &d, d_stride, &a->w, w_stride, a->dx, dx_stride, s));
+  }
+  if (a->dw) {
+    GemmParams p = {};
+    common_params(pl, &p, a->workspace);
+    AGMM_TRY(weight_grad(pl, &p, 1, (int)a->shards, a->rows, a->x, x_stride, &d, d_stride, &a->dw, dw_stride, f32, s));
+  }
+  return AGMM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,833 @@
+// ff_gemm.cuh -- the matrix products of the feed-forward operators: a persistent
+// warp-specialised tcgen05 kernel with the operators' epilogues.
+//
+//   gated   out = act(X Wg) * (X Wu)         both products' tiles in one accumulator
+//   linear  out = act(X W + bias) + residual
+//   plain   the products of the backward passes (gradients of X and of the weights)
+//
+// Warp 0 loads operand tiles by TMA, warp 1 issues the MMAs (float32 accumulators in
+// tensor memory, two of them, so that a tile's epilogue runs beside the next tile's
+// products), warps 2-9 are the epilogue.  Either operand may be stored along k or
+// along its own rows or columns (the weights come in both layouts, and the gradients
+// of the weights sum over tokens): that is a matter of the tensor maps' boxes and two
+// bits of the MMA's descriptor, chosen at run time.
+//
+//   row tiles      a CTA pair multiplies 256 rows by 256 columns (cta_group::2), each
+//                  CTA holding its own rows and half of the columns' operand.  Gated:
+//                  the leader's half is 128 columns of the gate's weight, the
+//                  follower's the same columns of the other, so both products of an
+//                  output value land in one thread.
+//                  Bound: the tensor cores.
+//   swapped tiles  for up to 128 tokens: 128 columns of the weights are the MMA's rows
+//                  and all tokens its columns, so that each thread of the epilogue has
+//                  one column of the weights and only the tokens that there are.
+//                  Bound: the weights' bytes.
+//
+// Work: cluster c takes whole tiles in turn; tiles of a ragged last wave (and the wave
+// before it) are cut along k evenly over the clusters.  Every warp of a cut tile's
+// epilogue leaves its float32 partial results in the workspace and counts its k blocks;
+// the warp that completes the count adds all parts in the order of k and goes on to the
+// results.  Nobody waits for another CTA, and the sum does not depend on who is last.
+//
+// Every mbarrier wait is bounded; one that runs out records AGMM_ERR_TIMEOUT in the
+// status words, all roles leave their loops, wait (bounded) for their own work in
+// flight, and the CTA frees its tensor memory and returns.
+#pragma once
+
+#include <type_traits>
+
+#include "ff_math.cuh"
+#include "ptx_sm103.cuh"
+
+namespace agmm {
+namespace ff {
+namespace {
+
+constexpr int kStatusTimeout = 5;  // AGMM_ERR_TIMEOUT
+enum Role : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleDrain = 4 };
+
+// Control block: full[], empty[], acc_full[2], acc_empty[2], drain; then the abort flag,
+// the TMEM address and the swapped tiles' table of output rows.
+__device__ __forceinline__ uint32_t bar_full(uint32_t ctl, int s) { return ctl + 8u * s; }
+__device__ __forceinline__ uint32_t bar_empty(uint32_t ctl, int s) { return ctl + 8u * (kMaxStages + s); }
+__device__ __forceinline__ uint32_t bar_acc_full(uint32_t ctl, int a) { return ctl + 8u * (2 * kMaxStages + a); }
+__device__ __forceinline__ uint32_t bar_acc_empty(uint32_t ctl, int a) { return ctl + 8u * (2 * kMaxStages + 2 + a); }
+__device__ __forceinline__ uint32_t bar_drain(uint32_t ctl) { return ctl + 8u * (2 * kMaxStages + 4); }
+constexpr int kAbortOffset = 8 * (2 * kMaxStages + 6);
+constexpr int kTmemOffset = kAbortOffset + 8;
+constexpr int kTableOffset = 256;  // int[kMaxSwapRows]
+static_assert(kTmemOffset + 4 <= kTableOffset && kTableOffset + 4 * kMaxSwapRows <= kCtlBytes, "control block");
+
+enum WaitResult : int { kWaitOk = 1, kWaitTimeout = 0, kWaitAborted = -1 };
+constexpr uint32_t kSleepHintNs = 20000;
+
+template <bool kClusterScope>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  if constexpr (kClusterScope)
+    return ptx::mbar_try_wait_cluster(bar, parity);
+  else
+    return ptx::mbar_try_wait(bar, parity);
+}
+
+template <bool kClusterScope = false>
+__device__ __forceinline__ int wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  if (try_wait<kClusterScope>(bar, parity)) return kWaitOk;
+  const uint64_t t0 = ptx::clock_cycles();
+  for (;;) {
+    bool done;
+    if constexpr (kClusterScope)
+      done = ptx::mbar_try_wait_cluster_sleep(bar, parity, kSleepHintNs);
+    else
+      done = ptx::mbar_try_wait_sleep(bar, parity, kSleepHintNs);
+    if (done) return kWaitOk;
+    if (*abort) return kWaitAborted;
+    if (ptx::clock_cycles() - t0 > limit) return kWaitTimeout;
+  }
+}
+
+// Waits for work in flight whatever the abort flag says.
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, uint64_t limit) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::clock_cycles();
+  for (;;) {
+    if (ptx::mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (ptx::clock_cycles() - t0 > limit) return false;
+  }
+}
+
+__device__ __noinline__ void record_failure(const GemmParams& p, volatile int* abort, int result, int role, int stage, int tile) {
+  *abort = 1;
+  if (result == kWaitTimeout && atomicCAS(p.status, 0, kStatusTimeout) == 0) {
+    p.status[1] = role;
+    p.status[2] = stage;
+    p.status[3] = tile;
+  }
+}
+
+// A cluster's share of the work, one segment after another: its even share of the cut
+// tiles' k blocks first, so that the parts are there early, then its whole tiles.
+struct Segment {
+  int tile, problem, mt, nt;
+  int kb0, kb1;
+  bool whole;
+};
+
+__device__ __forceinline__ int64_t first_unit(const GemmParams& p, int cluster) {
+  return (int64_t)(p.num_tiles - p.dp_tiles) * p.k_blocks * cluster / p.sk_clusters;
+}
+
+struct SegmentIter {
+  int64_t u, hi;
+  int next_dp, clusters;
+
+  __device__ __forceinline__ void init(const GemmParams& p, int cluster, int nclusters) {
+    clusters = nclusters;
+    next_dp = cluster;
+    u = hi = 0;
+    if (cluster < p.sk_clusters) {
+      u = first_unit(p, cluster);
+      hi = first_unit(p, cluster + 1);
+    }
+  }
+
+  __device__ __forceinline__ bool next(const GemmParams& p, Segment& s) {
+    if (u < hi) {
+      const int t = (int)(u / p.k_blocks);
+      s.tile = p.dp_tiles + t;
+      s.kb0 = (int)(u - (int64_t)t * p.k_blocks);
+      s.kb1 = (int)min((int64_t)p.k_blocks, s.kb0 + (hi - u));
+      u += s.kb1 - s.kb0;
+    } else if (next_dp < p.dp_tiles) {
+      s.tile = next_dp;
+      s.kb0 = 0;
+      s.kb1 = p.k_blocks;
+      next_dp += clusters;
+    } else {
+      return false;
+    }
+    s.whole = s.kb0 == 0 && s.kb1 == p.k_blocks;
+    s.problem = s.tile / p.tiles_per_problem;
+    // bands of group_m row tiles sweep the columns together: their rows stay in L2
+    const int t = s.tile - s.problem * p.tiles_per_problem;
+    const int per_group = p.group_m * p.n_tiles;
+    const int group = t / per_group, first = group * p.group_m;
+    const int in_group = min(p.m_tiles - first, p.group_m), r = t - group * per_group;
+    s.mt = first + r % in_group;
+    s.nt = r / in_group;
+    return true;
+  }
+};
+
+// Where the parts of a cut tile lie: clusters [first, last], the tile's k in their order.
+struct Parts {
+  int first, last;
+};
+__device__ __forceinline__ Parts find_parts(const GemmParams& p, int tile) {
+  const int64_t units = (int64_t)(p.num_tiles - p.dp_tiles) * p.k_blocks;
+  const int64_t u0 = (int64_t)(tile - p.dp_tiles) * p.k_blocks, u1 = u0 + p.k_blocks - 1;
+  // the last c with floor(units c / clusters) <= u
+  Parts r;
+  r.first = (int)(((u0 + 1) * p.sk_clusters + units - 1) / units) - 1;
+  r.last = (int)(((u1 + 1) * p.sk_clusters + units - 1) / units) - 1;
+  return r;
+}
+
+// One warp's part of a tile that cluster `c` holds: its first tile's lies in slot 0.
+__device__ __forceinline__ float4* part_slot(const GemmParams& p, int c, int ctas, int rank, int tile, int ewarp) {
+  const int first_tile = p.dp_tiles + (int)(first_unit(p, c) / p.k_blocks);
+  const size_t slot = ((size_t)c * ctas + rank) * kSlots + (tile == first_tile ? 0 : 1);
+  return reinterpret_cast<float4*>(reinterpret_cast<char*>(p.partial) + slot * kSlotBytes + (size_t)ewarp * (kSlotBytes / kEpiWarps));
+}
+
+// Counts this warp's k blocks of a cut tile, after its part was stored; true for the
+// warp that completes the tile.
+__device__ __forceinline__ bool complete_tile(const GemmParams& p, int* counter, int blocks, int lane) {
+  __threadfence();
+  __syncwarp();
+  int last = 0;
+  if (lane == 0) {
+    last = atomicAdd(counter, blocks) + blocks == p.k_blocks;
+    if (last) *counter = 0;  // ready for the next run
+  }
+  last = __shfl_sync(0xffffffffu, last, 0);
+  __threadfence();
+  __syncwarp();
+  return last != 0;
+}
+
+// kCount values of this lane from column `col` on (of this warp's kWarpCols columns, in the order in
+// which they are stored), summed over the parts.
+template <int kCount>
+__device__ __forceinline__ void sum_parts(const GemmParams& p, const Parts& parts, int ctas, int rank, int tile, int ewarp, int col,
+                                          int lane, uint32_t (&v)[kCount]) {
+  constexpr int kQuads = kCount / 4;
+  constexpr int kDepth = kQuads >= 8 ? 1 : 8;  // parts whose loads are in flight together
+  float sum[kCount];
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+  for (int c0 = parts.first; c0 <= parts.last; c0 += kDepth) {
+    float4 x[kDepth][kQuads];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (c0 + d <= parts.last) {
+        const float4* const src = part_slot(p, c0 + d, ctas, rank, tile, ewarp) + (size_t)(col / 4) * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) x[d][i] = __ldcg(src + i * 32);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) x[d][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        sum[4 * i] += x[d][i].x;
+        sum[4 * i + 1] += x[d][i].y;
+        sum[4 * i + 2] += x[d][i].z;
+        sum[4 * i + 3] += x[d][i].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) v[i] = __float_as_uint(sum[i]);
+}
+
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+template <int kCount>
+__device__ __forceinline__ void store_part(float4* slot, int col, int lane, const uint32_t (&v)[kCount]) {
+#pragma unroll
+  for (int i = 0; i < kCount / 4; ++i)
+    __stcg(slot + (size_t)(col / 4 + i) * 32 + lane,
+           make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                       __uint_as_float(v[4 * i + 3])));
+}
+
+// A warp's staging buffer: 32 rows of 128 bytes, 16-byte pieces swizzled by the row, so
+// that both a lane's own row and four whole rows at a time are free of bank conflicts.
+__device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
+  return reinterpret_cast<uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+}
+
+// Writes a staged 32 x 128-byte block: row r of it to row out_row (of lane r; < 0: none) of
+// `out`, 8 lanes to a row.
+__device__ __forceinline__ void write_staged(uint8_t* stage, void* out, int64_t row_bytes, int64_t col_bytes, int64_t end_bytes,
+                                             int64_t out_row, int lane) {
+  __syncwarp();
+  const int piece = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + (lane >> 3);
+    const int64_t at = __shfl_sync(0xffffffffu, out_row, row);
+    const uint4 v = *staged(stage, row, piece);
+    if (at >= 0 && col_bytes + 16 * piece < end_bytes)
+      *reinterpret_cast<uint4*>(static_cast<char*>(out) + at * row_bytes + col_bytes + 16 * piece) = v;
+  }
+  __syncwarp();
+}
+
+// The same block's rows of `in`, into the staging buffer.
+__device__ __forceinline__ void load_rows(uint4 (&v)[8], const void* in, int64_t row_bytes, int64_t col_bytes, int64_t end_bytes,
+                                          int64_t out_row, int lane) {
+  const int piece = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t at = __shfl_sync(0xffffffffu, out_row, 4 * i + (lane >> 3));
+    v[i] = make_uint4(0, 0, 0, 0);
+    // not through the read-only path: the residual may be the output
+    if (at >= 0 && col_bytes + 16 * piece < end_bytes)
+      v[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(in) + at * row_bytes + col_bytes + 16 * piece);
+  }
+}
+
+template <bool kF16>
+__device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack2<kF16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
+
+// A lane's 64 packed values, as its row of the staging buffer.
+__device__ __forceinline__ void stage_half(uint8_t* stage, int lane, int half, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *staged(stage, lane, half * 4 + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+template <bool kSwap, int kEpi, bool kF16>
+__global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constant__ GemmParams p) {
+  constexpr bool kPair = !kSwap;
+  constexpr int kCtas = kPair ? 2 : 1;
+  constexpr int kAccs = kSwap && kEpi == kEpiGated ? 2 : 1;  // swapped tiles: products of a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const int S = p.stages;
+  constexpr uint32_t a_slot = (uint32_t)kAccs * kTileBytes;
+  const uint32_t b_slot = kSwap ? (uint32_t)p.mma_n * 128u : (uint32_t)kTileBytes;
+  const uint32_t a0 = base, b0 = base + (uint32_t)S * a_slot;
+  const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results
+  const uint32_t ctl = out0 + (kSwap ? 0u : (uint32_t)(kEpiWarps * kStageOutBytes));
+  uint8_t* const ctl_ptr = base_ptr + (ctl - base);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kAbortOffset);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctl_ptr + kTmemOffset);
+  int* const row_table = reinterpret_cast<int*>(ctl_ptr + kTableOffset);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = p.wait_limit_cycles;
+  const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
+  const int cluster = (int)blockIdx.x / kCtas, clusters = (int)gridDim.x / kCtas;
+
+  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+  if (warp == 0) {
+    if (lane < S) {
+      ptx::mbar_init(bar_full(ctl, lane), kCtas);  // a pair: both producers count on the leader's
+      ptx::mbar_init(bar_empty(ctl, lane), 1);
+    } else if (lane < S + 2) {
+      ptx::mbar_init(bar_acc_full(ctl, lane - S), 1);
+      ptx::mbar_init(bar_acc_empty(ctl, lane - S), kEpiWarps * kCtas);
+    } else if (lane == S + 2) {
+      ptx::mbar_init(bar_drain(ctl), 1);
+    }
+    if (lane < p.a.maps) ptx::prefetch_tensormap(&p.a_map[lane]);
+    if (lane < p.b.maps) ptx::prefetch_tensormap(&p.b_map[lane]);
+    if (lane == 0) *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (kSwap && warp >= 2) {
+    // the output row of each token column
+    const int c = (warp - 2) * 32 + lane;
+    if (c < p.mma_n) {
+      const int chunk = c / p.box, r = c - chunk * p.box;
+      const int shard = chunk / p.shard_chunks;
+      const int64_t row = (int64_t)(chunk - shard * p.shard_chunks) * p.box + r;
+      row_table[c] = chunk < p.chunks && row < p.shard_rows ? (int)(shard * p.shard_rows + row) : -1;
+    }
+  }
+  if (warp == 1) {
+    if constexpr (kPair) {
+      ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), p.tmem_cols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(ptx::smem_addr(tmem_slot), p.tmem_cols);
+      ptx::tmem_relinquish();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (kPair) {
+    // both CTAs' barriers are there before either's loads and MMAs signal them
+    ptx::cluster_arrive_relaxed();
+    ptx::cluster_wait();
+  }
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  ptx::griddep_wait();  // no access to global memory before this
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    const bool leader = ptx::elect_one();
+    const bool to_leader = kPair && rank == 1;
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true, dropped = false;
+    SegmentIter iter;
+    iter.init(p, cluster, clusters);
+    Segment sg;
+    const uint32_t bytes = a_slot + (kSwap ? (uint32_t)(p.chunks * p.box) * 128u : (uint32_t)kTileBytes);
+    auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+      if (to_leader)
+        ptx::tma_load_3d_pair(dst, map, bar, c0, c1, c2);
+      else
+        ptx::tma_load_3d(dst, map, bar, c0, c1, c2);
+    };
+    while (ok && iter.next(p, sg)) {
+      int seg = sg.kb0 / p.seg_blocks, ko = (sg.kb0 - seg * p.seg_blocks) * kTileK;
+      const int seg_end = p.seg_blocks * kTileK;
+      const int row_tile = kPair ? sg.mt * 2 + rank : sg.mt;
+      const int b_row = sg.nt * p.b_tile_step + rank * p.b_half_step;
+      // row tiles whose rows lie along k: the chunks of this tile (the first in registers)
+      const int per_tile = kTileM / (kSwap ? kTileM : p.box);
+      bool empty_ready = false;
+      for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
+        if (!empty_ready) {
+          int res = wait_phase(bar_empty(ctl, stage), phase ^ 1u, abort_flag, limit);
+          res = __shfl_sync(0xffffffffu, res, 0);
+          if (res != kWaitOk) {
+            if (leader) record_failure(p, abort_flag, res, kRoleProducer, stage, sg.tile);
+            ok = false;
+            break;
+          }
+        }
+        const int next_stage = stage + 1 == S ? 0 : stage + 1;
+        const uint32_t next_phase = stage + 1 == S ? phase ^ 1u : phase;
+        empty_ready = kb + 1 < sg.kb1 && ptx::mbar_test_wait(bar_empty(ctl, next_stage), next_phase ^ 1u);
+        const uint32_t full = to_leader ? ptx::map_shared_rank(bar_full(ctl, stage), 0) : bar_full(ctl, stage);
+        const bool drop = p.test_drop && !dropped;
+        dropped = true;
+        if (!drop && !to_leader) {
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        }
+        if (!drop && leader) {
+          if (to_leader)
+            ptx::mbar_arrive_expect_tx_remote(full, bytes);
+          else
+            ptx::mbar_arrive_expect_tx(full, bytes);
+          const uint32_t a_dst = a0 + (uint32_t)stage * a_slot, b_dst = b0 + (uint32_t)stage * b_slot;
+          const int a_z = seg * p.a.z_segment, b_z = seg * p.b.z_segment;
+          const CUtensorMap* const a_map = &p.a_map[sg.problem * p.a.by_problem + seg * p.a.by_segment];
+          const CUtensorMap* const b_map = &p.b_map[sg.problem * p.b.by_problem + seg * p.b.by_segment + rank * p.b.by_rank];
+          // A: rows of this CTA (swapped tiles: columns of the weights)
+          if (p.a.mn_major) {
+#pragma unroll
+            for (int t = 0; t < kAccs; ++t)
+#pragma unroll
+              for (int i = 0; i < kTileM / 64; ++i)
+                load(a_dst + (uint32_t)t * kTileBytes + (uint32_t)i * 8192u, a_map + t, full, row_tile * kTileM + 64 * i, ko, a_z);
+          } else if constexpr (kSwap) {
+#pragma unroll
+            for (int t = 0; t < kAccs; ++t) load(a_dst + (uint32_t)t * kTileBytes, a_map + t, full, ko, row_tile * kTileM, a_z);
+          } else {
+            for (int j = 0; j < per_tile; ++j) {
+              // a chunk behind the last lies outside its map: zeros
+              const int chunk = row_tile * per_tile + j;
+              const int shard = min(chunk / p.shard_chunks, p.shards - 1);
+              load(a_dst + (uint32_t)(j * p.box) * 128u, a_map + shard * p.a.by_shard, full, ko,
+                   (chunk - shard * p.shard_chunks) * p.box, a_z);
+            }
+          }
+          // B
+          if constexpr (kSwap) {
+            for (int j = 0; j < p.chunks; ++j) {
+              const int shard = j / p.shard_chunks;
+              load(b_dst + (uint32_t)(j * p.box) * 128u, b_map + shard * p.b.by_shard, full, ko, (j - shard * p.shard_chunks) * p.box, b_z);
+            }
+          } else if (p.b.mn_major) {
+#pragma unroll
+            for (int i = 0; i < kTileM / 64; ++i) load(b_dst + (uint32_t)i * 8192u, b_map, full, b_row + 64 * i, ko, b_z);
+          } else {
+            load(b_dst, b_map, full, ko, b_row, b_z);
+          }
+        }
+        ko += kTileK;
+        if (ko == seg_end) {
+          ko = 0;
+          ++seg;
+        }
+        stage = next_stage;
+        phase = next_phase;
+      }
+    }
+    // only after an abort can a load be unconsumed
+    if (leader)
+      for (int s = 0; s < S; ++s)
+        if ((armed >> s) & 1u)
+          if (!wait_drain(bar_full(ctl, s), (armed_parity >> s) & 1u, limit))
+            record_failure(p, abort_flag, kWaitTimeout, kRoleDrain, s, -1);
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      const bool issuer = ptx::elect_one();
+      const int n = kSwap ? p.mma_n : kTileN;
+      const uint32_t idesc = ptx::idesc_f16kind_f32(kPair ? 2 * kTileM : kTileM, n, p.a.mn_major != 0, p.b.mn_major != 0, kF16);
+      // a k step of 16 values: 32 bytes inside the swizzle row, or 16 rows of 128 bytes
+      const uint64_t a_step = p.a.mn_major ? 2048u / 16u : 32u / 16u, b_step = p.b.mn_major ? 2048u / 16u : 32u / 16u;
+      const uint32_t a_lbo = p.a.mn_major ? 8192u : 16u, b_lbo = p.b.mn_major ? 8192u : 16u;
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      SegmentIter iter;
+      iter.init(p, cluster, clusters);
+      Segment sg;
+      for (; ok && iter.next(p, sg); ++it) {
+        const int acc = it & 1;
+        int res = wait_phase<kPair>(bar_acc_empty(ctl, acc), (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, limit);
+        res = __shfl_sync(0xffffffffu, res, 0);
+        if (res != kWaitOk) {
+          if (issuer) record_failure(p, abort_flag, res, kRoleMma, -1, sg.tile);
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * kAccs * n);
+        bool full_ready = false;
+        for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
+          if (!full_ready) {
+            res = wait_phase(bar_full(ctl, stage), phase, abort_flag, limit);
+            res = __shfl_sync(0xffffffffu, res, 0);
+            if (res != kWaitOk) {
+              if (issuer) record_failure(p, abort_flag, res, kRoleMma, stage, sg.tile);
+              ok = false;
+              break;
+            }
+          }
+          ptx::tc_fence_after();
+          const int next_stage = stage + 1 == S ? 0 : stage + 1;
+          const uint32_t next_phase = stage + 1 == S ? phase ^ 1u : phase;
+          full_ready = kb + 1 < sg.kb1 && ptx::mbar_test_wait(bar_full(ctl, next_stage), next_phase);
+          const uint64_t b_desc = ptx::smem_desc_sw128(b0 + (uint32_t)stage * b_slot, b_lbo, 1024u);
+          if (issuer) {
+#pragma unroll
+            for (int t = 0; t < kAccs; ++t) {
+              const uint64_t a_desc = ptx::smem_desc_sw128(a0 + (uint32_t)stage * a_slot + (uint32_t)t * kTileBytes, a_lbo, 1024u);
+#pragma unroll
+              for (int kk = 0; kk < kTileK / 16; ++kk) {
+                const uint32_t accumulate = kb > sg.kb0 || kk > 0 ? 1u : 0u;
+                if constexpr (kPair)
+                  ptx::mma_bf16_pair(d, a_desc + a_step * (uint64_t)kk, b_desc + b_step * (uint64_t)kk, idesc, accumulate);
+                else
+                  ptx::mma_bf16(d + (uint32_t)(t * n), a_desc + a_step * (uint64_t)kk, b_desc + b_step * (uint64_t)kk, idesc, accumulate);
+              }
+            }
+            if constexpr (kPair)
+              ptx::mma_commit_pair(bar_empty(ctl, stage), 3);
+            else
+              ptx::mma_commit(bar_empty(ctl, stage));
+          }
+          stage = next_stage;
+          phase = next_phase;
+        }
+        if (!ok) break;
+        if (issuer) {
+          if constexpr (kPair)
+            ptx::mma_commit_pair(bar_acc_full(ctl, acc), 3);
+          else
+            ptx::mma_commit(bar_acc_full(ctl, acc));
+        }
+      }
+      if (issuer) {
+        if constexpr (kPair)
+          ptx::mma_commit_pair(bar_drain(ctl), 3);
+        else
+          ptx::mma_commit(bar_drain(ctl));
+        if (!wait_drain(bar_drain(ctl), 0, limit)) record_failure(p, abort_flag, kWaitTimeout, kRoleDrain, -1, -1);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3, ewarp = warp - 2, half = ewarp >> 2;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
+    uint8_t* const stage_out = base_ptr + (out0 - base) + ewarp * kStageOutBytes;
+    SegmentIter iter;
+    iter.init(p, cluster, clusters);
+    Segment sg;
+    for (int it = 0; iter.next(p, sg); ++it) {
+      const int acc = it & 1;
+      int res = kWaitOk;
+      if (lane == 0) res = wait_phase(bar_acc_full(ctl, acc), (uint32_t)(it >> 1) & 1u, abort_flag, limit);
+      res = __shfl_sync(0xffffffffu, res, 0);
+      if (res != kWaitOk) {
+        if (lane == 0) record_failure(p, abort_flag, res, kRoleEpilogue, acc, sg.tile);
+        break;
+      }
+      ptx::tc_fence_after();
+      // the accumulator may be refilled (a pair's leader refills both CTAs')
+      auto release = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair && rank == 1)
+            ptx::mbar_arrive_remote(ptx::map_shared_rank(bar_acc_empty(ctl, acc), 0));
+          else
+            ptx::mbar_arrive(bar_acc_empty(ctl, acc));
+        }
+      };
+      int* const counter =
+          sg.whole ? nullptr : p.counters + ((size_t)(sg.tile - p.dp_tiles) * kCtas + rank) * kEpiWarps + ewarp;
+
+      if constexpr (kSwap) {
+        // This lane's column of the weights, and this warp's half of the tokens.
+        const int n = p.mma_n, c0 = half * (n / 2);
+        const uint32_t t0 = lane_base + (uint32_t)(acc * kAccs * n + c0);
+        int live = 0;  // columns up to the last that holds a token
+        for (int c = 0; c < n / 2; c += 32) {
+          const unsigned there = __ballot_sync(0xffffffffu, c + lane < n / 2 && row_table[c0 + c + lane] >= 0);
+          if (there) live = c + 32 - __clz(there);
+        }
+        Parts parts = {0, 0};
+        if (!sg.whole) {
+          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile, ewarp);
+#pragma unroll 1
+          for (int c = 0; c < live; c += 8) {
+            uint32_t v[kAccs][8];
+#pragma unroll
+            for (int t = 0; t < kAccs; ++t) tmem_ld_x8(t0 + (uint32_t)(t * n + c), v[t]);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int t = 0; t < kAccs; ++t) store_part<8>(slot, t * (n / 2) + c, lane, v[t]);
+          }
+          release();
+          if (live == 0 || !complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
+          parts = find_parts(p, sg.tile);
+        }
+        const int64_t f = (int64_t)sg.mt * kTileM + q * 32 + lane;  // the column
+        const bool there = f < p.cols;
+        float bias = 0.0f;
+        if constexpr (kEpi == kEpiLinear)
+          if (p.bias && there) bias = unpack1<kF16>(static_cast<const uint16_t*>(p.bias)[f]);
+#pragma unroll 1
+        for (int c = 0; c < live; c += 8) {
+          uint32_t v[kAccs][8];
+          uint16_t res16[8];
+          if constexpr (kEpi == kEpiLinear) {
+            if (p.residual) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int row = row_table[c0 + c + i];
+                res16[i] = row >= 0 && there ? static_cast<const uint16_t*>(p.residual)[row * p.ldr + f] : (uint16_t)0;
+              }
+            }
+          }
+          if (sg.whole) {
+#pragma unroll
+            for (int t = 0; t < kAccs; ++t) tmem_ld_x8(t0 + (uint32_t)(t * n + c), v[t]);
+            ptx::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int t = 0; t < kAccs; ++t)
+              sum_parts<8>(p, parts, kCtas, rank, sg.tile, ewarp, t * (n / 2) + c, lane, v[t]);
+          }
+          with_activation(p.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = row_table[c0 + c + i];
+              if (row < 0 || !there) continue;
+              float x = __uint_as_float(v[0][i]);
+              if constexpr (kEpi == kEpiGated) {
+                const float y = __uint_as_float(v[kAccs - 1][i]);
+                if (p.saved[0]) {
+                  static_cast<uint16_t*>(p.saved[0])[row * p.lds + f] = pack1<kF16>(x);
+                  static_cast<uint16_t*>(p.saved[1])[row * p.lds + f] = pack1<kF16>(y);
+                }
+                x = activate<act.value>(x) * y;
+              } else if constexpr (kEpi == kEpiLinear) {
+                x += bias;
+                if (p.saved[0]) static_cast<uint16_t*>(p.saved[0])[row * p.lds + f] = pack1<kF16>(x);
+                x = activate<act.value>(x);
+                if (p.residual) x += unpack1<kF16>(res16[i]);
+              }
+              if (kEpi == kEpiPlain && p.out_f32)
+                static_cast<float*>(p.out[sg.problem])[row * p.ldo + f] = x;
+              else
+                static_cast<uint16_t*>(p.out[sg.problem])[row * p.ldo + f] = pack1<kF16>(x);
+            }
+          });
+        }
+        if (sg.whole) release();
+      } else {
+        // This lane's row, and this warp's half of the columns.
+        const int trow = (sg.mt * 2 + rank) * kTileM + q * 32 + lane;
+        const int chunk = trow / p.box, shard = chunk / p.shard_chunks;
+        const int in_shard = trow - shard * p.shard_chunks * p.box;
+        const int64_t out_row = shard < p.shards && in_shard < p.shard_rows ? shard * p.shard_rows + in_shard : -1;
+        const uint32_t t0 = lane_base + (uint32_t)(acc * kTileN);
+        // gated: 64 columns of each product (the second's 128 columns on); else 128 columns
+        constexpr int kOtherAcc = 128;
+        const int first_col = kEpi == kEpiGated ? half * 64 : half * 128;
+        Parts parts = {0, 0};
+        if (!sg.whole) {
+          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile, ewarp);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t v[32];
+            // gated: this warp's columns of the first product, then of the second
+            const int col = kEpi == kEpiGated ? (c < 64 ? first_col + c : kOtherAcc + first_col + c - 64) : first_col + c;
+            ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)col, v);
+            ptx::tmem_ld_wait();
+            store_part<32>(slot, c, lane, v);
+          }
+          release();
+          if (!complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
+          parts = find_parts(p, sg.tile);
+        }
+        if constexpr (kEpi == kEpiGated) {
+          const int64_t col = (int64_t)sg.nt * 128 + first_col;
+          uint32_t g16[2][16], u16[2][16], o16[2][16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t g[32], u[32];
+            if (sg.whole) {
+              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + 32 * h), g);
+              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(kOtherAcc + first_col + 32 * h), u);
+              ptx::tmem_ld_wait();
+              if (h == 1) release();
+            } else {
+              sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, 32 * h, lane, g);
+              sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, 64 + 32 * h, lane, u);
+            }
+            if (p.saved[0]) {
+              pack32<kF16>(g, g16[h]);
+              pack32<kF16>(u, u16[h]);
+            }
+            with_activation(p.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                g[i] = __float_as_uint(activate<act.value>(__uint_as_float(g[i])) * __uint_as_float(u[i]));
+            });
+            pack32<kF16>(g, o16[h]);
+          }
+          stage_half(stage_out, lane, 0, o16[0]);
+          stage_half(stage_out, lane, 1, o16[1]);
+          write_staged(stage_out, p.out[0], p.ldo * 2, col * 2, p.cols * 2, out_row, lane);
+          if (p.saved[0]) {
+            stage_half(stage_out, lane, 0, g16[0]);
+            stage_half(stage_out, lane, 1, g16[1]);
+            write_staged(stage_out, p.saved[0], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
+            stage_half(stage_out, lane, 0, u16[0]);
+            stage_half(stage_out, lane, 1, u16[1]);
+            write_staged(stage_out, p.saved[1], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
+          }
+        } else {
+          const int64_t tile_col = (int64_t)sg.nt * kTileN + first_col;
+          if (kEpi == kEpiPlain && p.out_f32) {
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t v[32];
+              if (sg.whole) {
+                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), v);
+                ptx::tmem_ld_wait();
+                if (c == 96) release();
+              } else {
+                sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, c, lane, v);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) *staged(stage_out, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              write_staged(stage_out, p.out[sg.problem], p.ldo * 4, (tile_col + c) * 4, p.cols * 4, out_row, lane);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              const int64_t col = tile_col + c;
+              uint32_t z16[2][16], o16[2][16];
+              uint4 res16[8];
+              bool has_residual = false, has_saved = false;
+              if constexpr (kEpi == kEpiLinear) {
+                has_residual = p.residual != nullptr;
+                has_saved = p.saved[0] != nullptr;
+                if (has_residual) {
+                  load_rows(res16, p.residual, p.ldr * 2, col * 2, p.cols * 2, out_row, lane);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) *staged(stage_out, 4 * i + (lane >> 3), lane & 7) = res16[i];
+                  __syncwarp();
+                }
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                if (sg.whole) {
+                  ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c + 32 * h), v);
+                  ptx::tmem_ld_wait();
+                  if (c == 64 && h == 1) release();
+                } else {
+                  sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, c + 32 * h, lane, v);
+                }
+                if constexpr (kEpi == kEpiLinear) {
+                  if (p.bias) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      if (col + 32 * h + 8 * i < p.cols) {
+                        float b[8];
+                        unpack8<kF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col + 32 * h + 8 * i)), b);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[8 * i + e] = __float_as_uint(__uint_as_float(v[8 * i + e]) + b[e]);
+                      }
+                    }
+                  }
+                  if (has_saved) pack32<kF16>(v, z16[h]);
+                  with_activation(p.act, [&](auto act) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(activate<act.value>(__uint_as_float(v[i])));
+                  });
+                  if (has_residual) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      float r[8];
+                      unpack8<kF16>(*staged(stage_out, lane, h * 4 + i), r);
+#pragma unroll
+                      for (int e = 0; e < 8; ++e) v[8 * i + e] = __float_as_uint(__uint_as_float(v[8 * i + e]) + r[e]);
+                    }
+                  }
+                }
+                pack32<kF16>(v, o16[h]);
+              }
+              stage_half(stage_out, lane, 0, o16[0]);
+              stage_half(stage_out, lane, 1, o16[1]);
+              write_staged(stage_out, p.out[sg.problem], p.ldo * 2, col * 2, p.cols * 2, out_row, lane);
+              if (has_saved) {
+                stage_half(stage_out, lane, 0, z16[0]);
+                stage_half(stage_out, lane, 1, z16[1]);
+                write_staged(stage_out, p.saved[0], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  if constexpr (kPair) {
+    // the leader's MMAs read the follower's shared memory, and its commits arrive there
+    __syncwarp();
+    ptx::cluster_sync_all();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    if constexpr (kPair)
+      ptx::tmem_dealloc_pair(tmem_base, p.tmem_cols);
+    else
+      ptx::tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+}  // namespace
+}  // namespace ff
+}  // namespace agmm

@@ -1,0 +1,46 @@
+// ff_launch.cu -- launches of the feed-forward products' kernel.
+#include "ff_params.h"
+
+namespace agmm {
+namespace ff {
+
+GemmFn rows_gemm(int epi, bool f16) { return epi == kEpiGated ? rows_gated(f16) : epi == kEpiLinear ? rows_linear(f16) : rows_plain(f16); }
+GemmFn swap_gemm(int epi, bool f16) { return epi == kEpiGated ? swap_gated(f16) : epi == kEpiLinear ? swap_linear(f16) : swap_plain(f16); }
+
+cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters) {
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(clusters, fn, &cfg);
+}
+
+cudaError_t launch_gemm(GemmFn fn, const GemmParams& p, int clusters, int cluster, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  // The prologue may overlap the previous kernel's tail; the kernel waits
+  // (griddepcontrol.wait) before its first access to global memory.
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+}  // namespace ff
+}  // namespace agmm

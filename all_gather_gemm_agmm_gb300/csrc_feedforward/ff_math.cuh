@@ -1,0 +1,114 @@
+// ff_math.cuh -- 16-bit packing and the activations with their derivatives.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ff_params.h"
+
+namespace agmm {
+namespace ff {
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kF16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <bool kF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (kF16)
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint16_t pack1(float x) {
+  return (uint16_t)(pack2<kF16>(x, 0.0f) & 0xffffu);
+}
+
+template <bool kF16>
+__device__ __forceinline__ float unpack1(uint16_t w) {
+  return unpack2<kF16>((uint32_t)w).x;
+}
+
+template <bool kF16>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<kF16>(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack2<kF16>(x[0], x[1]), pack2<kF16>(x[2], x[3]), pack2<kF16>(x[4], x[5]), pack2<kF16>(x[6], x[7]));
+}
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTanhScale2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kTanhCube = 0.044715f;
+
+// 1 / (1 + e^-z).  A z so low that e^-z is infinite gives 0.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// z Phi(z) by the complementary error function: no cancellation where Phi is small.
+// The tanh form of it, 0.5 z (1 + tanh(v)), is z sigmoid(2 v) for the same reason.
+template <int kAct>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (kAct == kActRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays one
+  if constexpr (kAct == kActSilu) return z * sigmoid(z);
+  if constexpr (kAct == kActGelu) return 0.5f * z * erfcf(-kSqrtHalf * z);
+  if constexpr (kAct == kActGeluTanh) return z * sigmoid(kTanhScale2 * (z + kTanhCube * z * z * z));
+  return z;
+}
+
+// The activation and its derivative.  The bounds on z are where the second term of the
+// derivative has long been 0 in float32: beyond them its factors would be infinity and 0.
+template <int kAct>
+__device__ __forceinline__ void activate_with_slope(float z, float& a, float& slope) {
+  a = z;
+  slope = 1.0f;
+  if constexpr (kAct == kActRelu) {
+    a = z < 0.0f ? 0.0f : z;
+    slope = z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  } else if constexpr (kAct == kActSilu) {
+    const float s = sigmoid(z), b = fminf(fmaxf(z, -200.0f), 200.0f);
+    a = z * s;
+    slope = s * (1.0f + b * (1.0f - s));
+  } else if constexpr (kAct == kActGelu) {
+    const float phi = 0.5f * erfcf(-kSqrtHalf * z), b = fminf(fmaxf(z, -20.0f), 20.0f);
+    a = z * phi;
+    slope = phi + b * (kInvSqrt2Pi * __expf(-0.5f * b * b));
+  } else if constexpr (kAct == kActGeluTanh) {
+    const float b = fminf(fmaxf(z, -20.0f), 20.0f);
+    const float s = sigmoid(kTanhScale2 * (z + kTanhCube * z * z * z));
+    a = z * s;
+    slope = s + b * s * (1.0f - s) * (kTanhScale2 * (1.0f + 3.0f * kTanhCube * b * b));
+  }
+}
+
+// Calls f with the activation as a compile-time constant.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>()); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>()); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>()); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>()); break;
+    default: f(std::integral_constant<int, kActNone>()); break;
+  }
+}
+
+}  // namespace ff
+}  // namespace agmm

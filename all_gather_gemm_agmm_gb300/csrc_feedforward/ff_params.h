@@ -1,0 +1,162 @@
+// ff_params.h -- parameter blocks shared by the host code (ff_api.cpp) and the
+// kernels of the feed-forward operators.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace agmm {
+namespace ff {
+
+constexpr int kMaxShards = 8;
+constexpr int kThreads = 320;     // warp 0: TMA producer, warp 1: MMA issuer, warps 2-9: epilogue
+constexpr int kEpiWarps = 8;
+constexpr int kTileM = 128;       // rows of the A operand of one CTA = TMEM lanes
+constexpr int kTileN = 256;       // row tiles: columns of a CTA pair's tile
+constexpr int kTileK = 64;        // one 128-byte swizzle row of 16-bit values
+constexpr int kTileBytes = kTileM * kTileK * 2;  // 16 KiB
+constexpr int kMaxStages = 12;
+constexpr int kRowStages = 6;     // 6 x 32 KiB of operands beside 32 KiB of staged results
+constexpr int kMaxSwapRows = 128; // swapped tiles: token columns of a tile
+constexpr int kStageOutBytes = 4096;  // row tiles: one warp's staged 32 rows x 128 bytes
+constexpr int kCtlBytes = 1024;
+constexpr size_t kMaxSmem = 232448;   // 227 KiB
+constexpr int kStatusBytes = 256;     // status words at the start of the workspace
+constexpr size_t kSlotBytes = (size_t)kTileM * kTileN * sizeof(float);  // one CTA's float32 partial results
+constexpr int kSlots = 2;             // of each CTA: the first and the last tile of its share
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+enum Epi : int { kEpiPlain = 0, kEpiGated = 1, kEpiLinear = 2 };
+
+// One operand's tensor maps, all {inner, rows, segments}, boxes of 64 inner values.
+// The map of a load: problem * by_problem + segment * by_segment + shard * by_shard
+// (+ CTA rank * by_rank); its last coordinate: segment * z_segment.
+struct OperandParams {
+  int maps;      // how many there are
+  int mn_major;  // the inner dimension runs along the tile, not along k
+  int by_problem, by_segment, by_shard, by_rank, z_segment;
+};
+
+struct __align__(128) GemmParams {
+  CUtensorMap a_map[kMaxShards];
+  CUtensorMap b_map[kMaxShards];
+  OperandParams a, b;
+  // Row tiles: pair tiles of 256 x 256 (gated: 256 x 128 of each product).
+  // Swapped tiles: 128 columns of the weights, all tokens.
+  int problems;            // products that share one launch (gradients of two weights)
+  int tiles_per_problem, m_tiles, n_tiles, num_tiles, group_m;
+  int b_tile_step;         // row tiles: B rows from one tile to the next
+  int b_half_step;         // row tiles: ... and from the leader's half to the follower's
+  int k_blocks;            // of all segments
+  int seg_blocks;          // of one segment
+  int dp_tiles;            // tiles [0, dp_tiles) are worked on whole
+  int sk_clusters;         // the k blocks of the others are dealt evenly to this many clusters
+  // Tokens (row tiles: the rows of A; swapped tiles: the rows of B) in chunks of
+  // box rows that lie in one shard.
+  int shards, box, shard_chunks;  // shard_chunks: chunks of a shard
+  int chunks;                     // of all shards
+  int64_t shard_rows;
+  int mma_n;               // swapped tiles: token columns, a multiple of 16
+  int stages;
+  uint32_t tmem_cols;
+  // results
+  void* out[2];            // by problem
+  int64_t ldo;
+  int out_f32;             // plain products: float32 results
+  int64_t cols;            // columns of the results
+  void* saved[2];          // gated: the two products; linear: the sum before the activation
+  int64_t lds;
+  const void* bias;
+  const void* residual;
+  int64_t ldr;
+  int act;
+  int f16;
+  // workspace
+  int* status;
+  int* counters;           // [shared tiles][CTAs of a cluster][kEpiWarps], zero between runs
+  float* partial;          // [CTAs][kSlots][kSlotBytes]
+  uint64_t wait_limit_cycles;
+  int test_drop;           // test hook: the first arrival of a producer is dropped
+};
+
+using GemmFn = void (*)(GemmParams);
+// swapped tiles, result, fp16
+GemmFn rows_gemm(int epi, bool f16);
+GemmFn swap_gemm(int epi, bool f16);
+GemmFn rows_plain(bool f16);
+GemmFn rows_gated(bool f16);
+GemmFn rows_linear(bool f16);
+GemmFn swap_plain(bool f16);
+GemmFn swap_gated(bool f16);
+GemmFn swap_linear(bool f16);
+
+// Sets the shared-memory limit of a kernel and reports the clusters that fit.
+cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters);
+cudaError_t launch_gemm(GemmFn fn, const GemmParams& p, int clusters, int cluster, size_t smem, cudaStream_t stream);
+
+// --------------------------------------------------------------- pointwise
+// d_gate = d_out * up * act'(gate), d_up = d_out * act(gate)
+struct GatedGradParams {
+  int64_t rows, cols;
+  const uint16_t *d_out, *gate, *up;
+  uint16_t *d_gate, *d_up;
+  int64_t ld_out, ld_saved, ld_grad;
+  int act;
+};
+cudaError_t launch_gated_grad(const GatedGradParams& p, bool f16, int sms, cudaStream_t stream);
+
+// d_pre = d_out * act'(pre) (pre NULL: no activation, nothing is written), and the sums of
+// its columns, in parts of [blocks][cols].
+struct ActGradParams {
+  int64_t rows, cols;
+  const uint16_t *d_out, *pre;
+  uint16_t* d_pre;
+  int64_t ld_out, ld_pre, ld_grad;
+  int act;
+  float* part;  // NULL: no sums
+  int row_blocks;
+};
+int act_grad_row_blocks(int64_t rows, int64_t cols, int sms);
+cudaError_t launch_act_grad(const ActGradParams& p, bool f16, cudaStream_t stream);
+
+// out[c] = sum over parts of part[i][c], for one or two sums of `cols` columns
+struct SumPartsParams {
+  const float* part;  // [parts][sums][cols]
+  int parts, sums;
+  int64_t cols;
+  void* out[2];       // NULL: not wanted
+  int out_f32;
+};
+cudaError_t launch_sum_parts(const SumPartsParams& p, bool f16, cudaStream_t stream);
+
+// -------------------------------------------------------------- layer norm
+constexpr int kMaxNormColumns = 16384;
+struct NormParams {
+  int64_t rows;
+  int cols;
+  float eps;
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t *weight, *bias;
+  uint16_t* out;
+  int64_t ldo;
+  float *mean, *rstd;
+};
+cudaError_t launch_norm(const NormParams& p, bool f16, cudaStream_t stream);
+
+struct NormGradParams {
+  int64_t rows;
+  int cols;
+  const uint16_t *d_out, *x, *weight, *add;
+  int64_t ld_out, ldx, ld_add;
+  const float *mean, *rstd;
+  uint16_t* dx;
+  int64_t ld_dx;
+  float* part;  // [blocks][2][cols]: the sums of d_out * xhat and of d_out; NULL: not wanted
+};
+int norm_grad_blocks(int64_t rows, int cols, int sms);
+cudaError_t launch_norm_grad(const NormGradParams& p, bool f16, int blocks, cudaStream_t stream);
+
+}  // namespace ff
+}  // namespace agmm

@@ -1,0 +1,211 @@
+// ff_pointwise.cu -- the elementwise steps of the feed-forward operators' backward
+// passes, and the sums over tokens.
+//
+//   gated   d_gate = d_out * up * act'(gate),  d_up = d_out * act(gate)
+//   linear  d_pre = d_out * act'(pre),  d_bias = sum over tokens of d_pre
+//
+// The results are rounded to the operands' 16-bit type: the tensor cores multiply them next.
+// Bound: device memory.  A thread keeps its 8 columns and walks down the rows, so that
+// sums of columns stay in its registers; the blocks' sums are added in a fixed order.
+#include "ff_math.cuh"
+#include "ptx_sm103.cuh"
+
+namespace agmm {
+namespace ff {
+namespace {
+
+template <bool kF16, int kAct>
+__device__ __forceinline__ void gated_grad_piece(const uint4& d, const uint4& g, const uint4& u, uint4& dg, uint4& du) {
+  float dv[8], gv[8], uv[8];
+  unpack8<kF16>(d, dv);
+  unpack8<kF16>(g, gv);
+  unpack8<kF16>(u, uv);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a, slope;
+    activate_with_slope<kAct>(gv[i], a, slope);
+    gv[i] = dv[i] * uv[i] * slope;
+    uv[i] = dv[i] * a;
+  }
+  dg = pack8<kF16>(gv);
+  du = pack8<kF16>(uv);
+}
+
+constexpr int kUnroll = 2;  // rows whose loads are in flight together
+
+template <bool kF16>
+__global__ void __launch_bounds__(256) agmm_gated_grad(const __grid_constant__ GatedGradParams p) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (col >= p.cols) return;
+  with_activation(p.act, [&](auto act) {
+    const int64_t step = gridDim.y;
+    for (int64_t r = blockIdx.y; r < p.rows; r += step * kUnroll) {
+      uint4 d[kUnroll], g[kUnroll], u[kUnroll];
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int64_t row = r + i * step;
+        if (row < p.rows) {
+          // plain loads: d_gate and d_up may lie over gate and up
+          d[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + col);
+          g[i] = *reinterpret_cast<const uint4*>(p.gate + row * p.ld_saved + col);
+          u[i] = *reinterpret_cast<const uint4*>(p.up + row * p.ld_saved + col);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int64_t row = r + i * step;
+        if (row < p.rows) {
+          uint4 dg, du;
+          gated_grad_piece<kF16, act.value>(d[i], g[i], u[i], dg, du);
+          *reinterpret_cast<uint4*>(p.d_gate + row * p.ld_grad + col) = dg;
+          *reinterpret_cast<uint4*>(p.d_up + row * p.ld_grad + col) = du;
+        }
+      }
+    }
+  });
+}
+
+template <bool kF16>
+__global__ void __launch_bounds__(256) agmm_act_grad(const __grid_constant__ ActGradParams p) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (col >= p.cols) return;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  with_activation(p.act, [&](auto act) {
+    const int64_t step = gridDim.y;
+    for (int64_t r = blockIdx.y; r < p.rows; r += step * kUnroll) {
+      uint4 d[kUnroll], z[kUnroll];
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int64_t row = r + i * step;
+        if (row < p.rows) {
+          d[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + col);
+          if constexpr (act.value != kActNone) z[i] = *reinterpret_cast<const uint4*>(p.pre + row * p.ld_pre + col);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int64_t row = r + i * step;
+        if (row < p.rows) {
+          float dv[8];
+          unpack8<kF16>(d[i], dv);
+          if constexpr (act.value != kActNone) {
+            float zv[8];
+            unpack8<kF16>(z[i], zv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float a, slope;
+              activate_with_slope<act.value>(zv[e], a, slope);
+              dv[e] *= slope;
+            }
+            *reinterpret_cast<uint4*>(p.d_pre + row * p.ld_grad + col) = pack8<kF16>(dv);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += dv[e];
+        }
+      }
+    }
+  });
+  if (p.part) {
+    float4* const dst = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.y * p.cols + col);
+    dst[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    dst[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  }
+}
+
+// 32 columns to a block, their parts dealt to its 16 warps.
+constexpr int kSumWarps = 16;
+
+template <bool kF16>
+__global__ void __launch_bounds__(kSumWarps * 32) agmm_sum_parts(const __grid_constant__ SumPartsParams p) {
+  __shared__ float s[kSumWarps][32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (p.out[blockIdx.y] == nullptr) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + lane;
+  float sum = 0.0f;
+  if (col < p.cols) {
+    const float* const src = p.part + (int64_t)blockIdx.y * p.cols + col;
+    const int64_t stride = (int64_t)p.sums * p.cols;
+#pragma unroll 8
+    for (int i = warp; i < p.parts; i += kSumWarps) sum += __ldcg(src + i * stride);
+  }
+  s[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && col < p.cols) {
+#pragma unroll
+    for (int i = 1; i < kSumWarps; ++i) sum += s[i][lane];
+    if (p.out_f32)
+      static_cast<float*>(p.out[blockIdx.y])[col] = sum;
+    else
+      static_cast<uint16_t*>(p.out[blockIdx.y])[col] = pack1<kF16>(sum);
+  }
+}
+
+template <class P>
+cudaError_t launch(void (*fn)(P), const P& p, dim3 grid, int threads, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+// Threads of a block: the fewest idle ones beside the last columns.
+int threads_for(int64_t pieces) {
+  const int64_t blocks = (pieces + 255) / 256;
+  return (int)(((pieces + blocks - 1) / blocks + 31) / 32 * 32);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_grad(const GatedGradParams& p, bool f16, int sms, cudaStream_t stream) {
+  const int64_t pieces = p.cols / 8;
+  const int threads = threads_for(pieces);
+  const int64_t x = (pieces + threads - 1) / threads;
+  // enough blocks for 2048 threads on every SM twice over, and no more rows than there are
+  int64_t y = (int64_t)sms * 2 * (2048 / threads) / x;
+  y = y < 1 ? 1 : y;
+  const int64_t most = (p.rows + kUnroll - 1) / kUnroll;
+  if (y > most) y = most;
+  if (y > 65535) y = 65535;
+  const dim3 grid((unsigned)x, (unsigned)y);
+  return launch(f16 ? &agmm_gated_grad<true> : &agmm_gated_grad<false>, p, grid, threads, stream);
+}
+
+int act_grad_row_blocks(int64_t rows, int64_t cols, int sms) {
+  const int64_t pieces = cols / 8;
+  const int threads = threads_for(pieces);
+  const int64_t x = (pieces + threads - 1) / threads;
+  int64_t y = (int64_t)sms * (2048 / threads) / x;
+  y = y < 1 ? 1 : y;
+  const int64_t most = (rows + kUnroll - 1) / kUnroll;
+  if (y > most) y = most;
+  return (int)(y > 1024 ? 1024 : y);
+}
+
+cudaError_t launch_act_grad(const ActGradParams& p, bool f16, cudaStream_t stream) {
+  const int64_t pieces = p.cols / 8;
+  const int threads = threads_for(pieces);
+  const dim3 grid((unsigned)((pieces + threads - 1) / threads), (unsigned)p.row_blocks);
+  return launch(f16 ? &agmm_act_grad<true> : &agmm_act_grad<false>, p, grid, threads, stream);
+}
+
+cudaError_t launch_sum_parts(const SumPartsParams& p, bool f16, cudaStream_t stream) {
+  const dim3 grid((unsigned)((p.cols + 31) / 32), (unsigned)p.sums);
+  return launch(f16 ? &agmm_sum_parts<true> : &agmm_sum_parts<false>, p, grid, kSumWarps * 32, stream);
+}
+
+}  // namespace ff
+}  // namespace agmm

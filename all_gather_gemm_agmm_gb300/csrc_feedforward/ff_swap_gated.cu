@@ -1,0 +1,10 @@
+// ff_swap_gated.cu -- instantiations of the feed-forward products' kernel.
+#include "ff_gemm.cuh"
+
+namespace agmm {
+namespace ff {
+GemmFn swap_gated(bool f16) {
+  return f16 ? &agmm_ff_gemm<true, kEpiGated, true> : &agmm_ff_gemm<true, kEpiGated, false>;
+}
+}  // namespace ff
+}  // namespace agmm
