@@ -162,32 +162,31 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// {inner, rows, segments} of 16-bit values; boxes of 64 x box_rows, 128-byte swizzled,
-// zeros outside: what lies behind a segment's last row is not its neighbour's.
-agmm_status_t encode(CUtensorMap* map, const char* name, const void* ptr, int64_t inner, int64_t rows, int64_t segments, int64_t stride,
-                     int box_rows, bool f16) {
-  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return fail(AGMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)segments};
-  const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, (cuuint64_t)(segments > 1 ? rows * stride : stride) * 2};
-  const cuuint32_t box[3] = {kTileK, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
-  const CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
-                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(AGMM_ERR_CUDA, "tensor map of %s: cuTensorMapEncodeTiled gave %d", name, (int)r);
-  return AGMM_OK;
-}
-
-// A matrix as an operand that is contracted along its rows' values (K-major), or along
-// its rows (MN-major).
+// A matrix of 16-bit values: rows of `inner` values, `stride` apart, in segments.
 struct Matrix {
   const char* name;
   const void* ptr;
   int64_t inner, rows, segments, stride;
 };
 
-agmm_status_t encode_operand(CUtensorMap* map, const Matrix& m, bool mn_major, int box_rows, bool f16) {
-  return encode(map, m.name, m.ptr, m.inner, m.rows, m.segments, m.stride, mn_major ? 64 : box_rows, f16);
+// A matrix as an operand that is contracted along its rows' values (K-major, boxes of
+// box_rows), or along its rows (MN-major).  128-byte swizzled, zeros outside: what lies
+// behind a segment's last row is not its neighbour's.
+agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m, bool mn_major, int box_rows, bool f16) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(AGMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  o->mn_major = mn_major;
+  o->blocked = mn_major && m.inner % 64 == 0;
+  const cuuint64_t inner = (cuuint64_t)m.inner, rows = (cuuint64_t)m.rows, step = (cuuint64_t)m.stride * 2;
+  const cuuint64_t blocks = o->blocked ? inner / 64 : 1;
+  const cuuint64_t dims[4] = {inner / blocks, rows, blocks, (cuuint64_t)m.segments};
+  const cuuint64_t strides[3] = {step, o->blocked ? 128 : step, (m.segments > 1 ? rows : 1) * step};
+  const cuuint32_t box[4] = {kTileK, (cuuint32_t)(mn_major ? 64 : box_rows), (cuuint32_t)(o->blocked ? 2 : 1), 1}, one[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mn_major ? 4 : 2,
+                         const_cast<void*>(m.ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(AGMM_ERR_CUDA, "tensor map of %s: cuTensorMapEncodeTiled gave %d", m.name, (int)r);
+  return AGMM_OK;
 }
 
 // ---------------------------------------------------------------- schedules
@@ -199,15 +198,17 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 void make_schedule(GemmParams* p, int clusters, int min_blocks) {
   const int T = p->num_tiles, C = clusters, rem = T % C;
   p->dp_tiles = T;
-  p->sk_clusters = 1;
+  p->sk_clusters = 0;
   if (rem == 0 || 3 * rem >= 2 * C) return;
   const int shared = T < C ? T : C + rem;
   const int64_t units = (int64_t)shared * p->k_blocks;
   const int64_t parts = std::min<int64_t>(C, units / min_blocks);
   // a share of a tile or more, where tiles are fewer: nothing to gain
-  if (parts <= std::min(shared, C - 1)) return;
+  if (parts <= std::min(shared, C - 1) || units > INT_MAX) return;
   p->dp_tiles = T - shared;
   p->sk_clusters = (int)parts;
+  p->sk_share = (int)(units / parts);
+  p->sk_extra = (int)(units % parts);
 }
 
 // How the tokens' rows lie in tiles: boxes of rows that never leave their shard.
@@ -298,12 +299,11 @@ agmm_status_t forward(const ProductPlan* pl, GemmParams* p, int epi, int shards,
   CUtensorMap *xm = swap ? p->b_map : p->a_map, *wm = swap ? p->a_map : p->b_map;
   xo.maps = shards;
   xo.by_shard = 1;
-  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], {"x", x[s], pl->k, rows, 1, x_stride}, false, box, pl->f16));
+  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], &xo, {"x", x[s], pl->k, rows, 1, x_stride}, false, box, pl->f16));
   wo.maps = weights;
-  wo.mn_major = !pl->transpose;
   for (int i = 0; i < weights; ++i) {
     const Matrix m = pl->transpose ? Matrix{"a weight", w[i], pl->k, pl->n, 1, w_stride} : Matrix{"a weight", w[i], pl->n, pl->k, 1, w_stride};
-    AGMM_TRY(encode_operand(&wm[i], m, wo.mn_major, kTileM, pl->f16));
+    AGMM_TRY(encode_operand(&wm[i], &wo, m, !pl->transpose, kTileM, pl->f16));
   }
   if (swap) return run_swap(pl, p, epi, pl->n, stream);
   if (epi == kEpiGated) {
@@ -330,11 +330,10 @@ agmm_status_t input_grad(const ProductPlan* pl, GemmParams* p, int weights, int6
   CUtensorMap *tm = swap ? p->b_map : p->a_map, *wm = swap ? p->a_map : p->b_map;
   to.maps = wo.maps = weights;
   to.by_segment = wo.by_segment = 1;
-  wo.mn_major = pl->transpose;
   for (int i = 0; i < weights; ++i) {
-    AGMM_TRY(encode_operand(&tm[i], {"a gradient", d[i], pl->n, rows, 1, d_stride}, false, p->box, pl->f16));
+    AGMM_TRY(encode_operand(&tm[i], &to, {"a gradient", d[i], pl->n, rows, 1, d_stride}, false, p->box, pl->f16));
     const Matrix m = pl->transpose ? Matrix{"a weight", w[i], pl->k, pl->n, 1, w_stride} : Matrix{"a weight", w[i], pl->n, pl->k, 1, w_stride};
-    AGMM_TRY(encode_operand(&wm[i], m, wo.mn_major, kTileM, pl->f16));
+    AGMM_TRY(encode_operand(&wm[i], &wo, m, pl->transpose, kTileM, pl->f16));
   }
   if (swap) return run_swap(pl, p, kEpiPlain, pl->k, stream);
   p->b_tile_step = kTileN;
@@ -360,12 +359,11 @@ agmm_status_t weight_grad(const ProductPlan* pl, GemmParams* p, int weights, int
   CUtensorMap *xm = pl->transpose ? p->b_map : p->a_map, *gm = pl->transpose ? p->a_map : p->b_map;
   xo.maps = shards;
   go.maps = weights;
-  xo.mn_major = go.mn_major = 1;
   xo.by_segment = 1;
   go.by_problem = 1;
   go.z_segment = 1;
-  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], {"x", x[s], pl->k, rows, 1, x_stride}, true, 0, pl->f16));
-  for (int i = 0; i < weights; ++i) AGMM_TRY(encode_operand(&gm[i], {"a gradient", d[i], pl->n, rows, shards, d_stride}, true, 0, pl->f16));
+  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], &xo, {"x", x[s], pl->k, rows, 1, x_stride}, true, 0, pl->f16));
+  for (int i = 0; i < weights; ++i) AGMM_TRY(encode_operand(&gm[i], &go, {"a gradient", d[i], pl->n, rows, shards, d_stride}, true, 0, pl->f16));
   p->b_tile_step = kTileN;
   p->b_half_step = kTileN / 2;
   return run_rows(pl, p, kEpiPlain, ceil_div(out_rows, 2 * kTileM), ceil_div(out_cols, kTileN), stream);
@@ -492,7 +490,7 @@ agmm_status_t agmm_layer_norm_run(agmm_layer_norm_t pl, const agmm_layer_norm_ar
   p.out = static_cast<uint16_t*>(a->out);
   p.mean = a->mean;
   p.rstd = a->rstd;
-  return check_cuda(launch_norm(p, pl->f16, static_cast<cudaStream_t>(stream)), "layer_norm launch");
+  return check_cuda(launch_norm(p, pl->f16, pl->sms, static_cast<cudaStream_t>(stream)), "layer_norm launch");
 }
 
 agmm_status_t agmm_layer_norm_backward(agmm_layer_norm_t pl, const agmm_layer_norm_grad_args_t* a, void* stream) {

@@ -112,13 +112,12 @@ struct Segment {
   bool whole;
 };
 
-__device__ __forceinline__ int64_t first_unit(const GemmParams& p, int cluster) {
-  return (int64_t)(p.num_tiles - p.dp_tiles) * p.k_blocks * cluster / p.sk_clusters;
+__device__ __forceinline__ int first_unit(const GemmParams& p, int cluster) {
+  return cluster * p.sk_share + min(cluster, p.sk_extra);
 }
 
 struct SegmentIter {
-  int64_t u, hi;
-  int next_dp, clusters;
+  int u, hi, next_dp, clusters;
 
   __device__ __forceinline__ void init(const GemmParams& p, int cluster, int nclusters) {
     clusters = nclusters;
@@ -132,10 +131,10 @@ struct SegmentIter {
 
   __device__ __forceinline__ bool next(const GemmParams& p, Segment& s) {
     if (u < hi) {
-      const int t = (int)(u / p.k_blocks);
+      const int t = u / p.k_blocks;
       s.tile = p.dp_tiles + t;
-      s.kb0 = (int)(u - (int64_t)t * p.k_blocks);
-      s.kb1 = (int)min((int64_t)p.k_blocks, s.kb0 + (hi - u));
+      s.kb0 = u - t * p.k_blocks;
+      s.kb1 = min(p.k_blocks, s.kb0 + (hi - u));
       u += s.kb1 - s.kb0;
     } else if (next_dp < p.dp_tiles) {
       s.tile = next_dp;
@@ -146,37 +145,40 @@ struct SegmentIter {
       return false;
     }
     s.whole = s.kb0 == 0 && s.kb1 == p.k_blocks;
-    s.problem = s.tile / p.tiles_per_problem;
+    s.problem = s.tile >= p.tiles_per_problem;
     // bands of group_m row tiles sweep the columns together: their rows stay in L2
     const int t = s.tile - s.problem * p.tiles_per_problem;
     const int per_group = p.group_m * p.n_tiles;
     const int group = t / per_group, first = group * p.group_m;
     const int in_group = min(p.m_tiles - first, p.group_m), r = t - group * per_group;
-    s.mt = first + r % in_group;
     s.nt = r / in_group;
+    s.mt = first + r - s.nt * in_group;
     return true;
   }
 };
 
 // Where the parts of a cut tile lie: clusters [first, last], the tile's k in their order.
+// Each has its first tile's part in slot 0: this tile's, but for a first cluster that began before it.
 struct Parts {
-  int first, last;
+  int first, last, first_slot;
 };
+__device__ __forceinline__ int cluster_of(const GemmParams& p, int unit) {
+  const int longer = p.sk_extra * (p.sk_share + 1);  // the units of the first sk_extra clusters
+  return unit < longer ? unit / (p.sk_share + 1) : p.sk_extra + (unit - longer) / p.sk_share;
+}
 __device__ __forceinline__ Parts find_parts(const GemmParams& p, int tile) {
-  const int64_t units = (int64_t)(p.num_tiles - p.dp_tiles) * p.k_blocks;
-  const int64_t u0 = (int64_t)(tile - p.dp_tiles) * p.k_blocks, u1 = u0 + p.k_blocks - 1;
-  // the last c with floor(units c / clusters) <= u
+  const int u0 = (tile - p.dp_tiles) * p.k_blocks;
   Parts r;
-  r.first = (int)(((u0 + 1) * p.sk_clusters + units - 1) / units) - 1;
-  r.last = (int)(((u1 + 1) * p.sk_clusters + units - 1) / units) - 1;
+  r.first = cluster_of(p, u0);
+  r.last = cluster_of(p, u0 + p.k_blocks - 1);
+  r.first_slot = first_unit(p, r.first) < u0 ? 1 : 0;
   return r;
 }
 
-// One warp's part of a tile that cluster `c` holds: its first tile's lies in slot 0.
-__device__ __forceinline__ float4* part_slot(const GemmParams& p, int c, int ctas, int rank, int tile, int ewarp) {
-  const int first_tile = p.dp_tiles + (int)(first_unit(p, c) / p.k_blocks);
-  const size_t slot = ((size_t)c * ctas + rank) * kSlots + (tile == first_tile ? 0 : 1);
-  return reinterpret_cast<float4*>(reinterpret_cast<char*>(p.partial) + slot * kSlotBytes + (size_t)ewarp * (kSlotBytes / kEpiWarps));
+// A warp's part of a cut tile.
+__device__ __forceinline__ float4* part_slot(const GemmParams& p, int c, int ctas, int rank, int slot, int ewarp) {
+  return reinterpret_cast<float4*>(reinterpret_cast<char*>(p.partial) + (((size_t)c * ctas + rank) * kSlots + slot) * kSlotBytes +
+                                   (size_t)ewarp * (kSlotBytes / kEpiWarps));
 }
 
 // Counts this warp's k blocks of a cut tile, after its part was stored; true for the
@@ -198,7 +200,7 @@ __device__ __forceinline__ bool complete_tile(const GemmParams& p, int* counter,
 // kCount values of this lane from column `col` on (of this warp's kWarpCols columns, in the order in
 // which they are stored), summed over the parts.
 template <int kCount>
-__device__ __forceinline__ void sum_parts(const GemmParams& p, const Parts& parts, int ctas, int rank, int tile, int ewarp, int col,
+__device__ __forceinline__ void sum_parts(const GemmParams& p, const Parts& parts, int ctas, int rank, int ewarp, int col,
                                           int lane, uint32_t (&v)[kCount]) {
   constexpr int kQuads = kCount / 4;
   constexpr int kDepth = kQuads >= 8 ? 1 : 8;  // parts whose loads are in flight together
@@ -211,7 +213,7 @@ __device__ __forceinline__ void sum_parts(const GemmParams& p, const Parts& part
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       if (c0 + d <= parts.last) {
-        const float4* const src = part_slot(p, c0 + d, ctas, rank, tile, ewarp) + (size_t)(col / 4) * 32 + lane;
+        const float4* const src = part_slot(p, c0 + d, ctas, rank, c0 + d == parts.first ? parts.first_slot : 0, ewarp) + (size_t)(col / 4) * 32 + lane;
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) x[d][i] = __ldcg(src + i * 32);
       } else {
@@ -239,6 +241,61 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr)
                : "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// How an operand's tile is copied: rows of 64 values of k each in one box, or (chunks) by the
+// other lanes; or MN-major, 128 values of 64 rows of k as two blocks of 64 x 64, in one box
+// where the map has the blocks as a dimension.
+enum LayoutKind : int { kLayoutRows = 0, kLayoutChunks = 1, kLayoutBlocks = 2, kLayoutTwoBoxes = 3 };
+template <int kLayout>
+using Layout = std::integral_constant<int, kLayout>;
+
+template <bool kPair>
+__device__ __forceinline__ void load_rows_of(uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row) {
+  if constexpr (kPair)
+    ptx::tma_load_2d_pair(dst, map, bar, k, row);
+  else
+    ptx::tma_load_2d(dst, map, bar, k, row);
+}
+
+template <bool kPair, int kLayout>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row, int z) {
+  if constexpr (kLayout == kLayoutRows) {
+    load_rows_of<kPair>(dst, map, bar, k, row);
+  } else if constexpr (kLayout == kLayoutBlocks) {
+    tma_load_4d<kPair>(dst, map, bar, 0, k, row >> 6, z);
+  } else if constexpr (kLayout == kLayoutTwoBoxes) {
+    tma_load_4d<kPair>(dst, map, bar, row, k, 0, z);
+    tma_load_4d<kPair>(dst + 8192u, map, bar, row + 64, k, 0, z);
+  }
+}
+
+template <class F>
+__device__ __forceinline__ void with_layout(int mn_major, int blocked, bool chunks, F&& f) {
+  if (!mn_major) {
+    if (chunks)
+      f(Layout<kLayoutChunks>());
+    else
+      f(Layout<kLayoutRows>());
+  } else if (blocked) {
+    f(Layout<kLayoutBlocks>());
+  } else {
+    f(Layout<kLayoutTwoBoxes>());
+  }
 }
 
 template <int kCount>
@@ -372,97 +429,106 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
+    // One elected lane of the converged warp issues the copies.  What a copy needs is worked out
+    // once for a tile and a segment of k, and the operands' layouts are compiled in: with both
+    // inside the loop over k, the issue took 750 cycles a k block, and the MMAs take 512.
     const bool leader = ptx::elect_one();
-    const bool to_leader = kPair && rank == 1;
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
-    bool ok = true, dropped = false;
+    bool ok = true, dropped = p.test_drop == 0;
     SegmentIter iter;
     iter.init(p, cluster, clusters);
     Segment sg;
+    const int per_tile = kSwap ? p.chunks : kTileM / p.box;  // chunks of the tokens: at most 16
     const uint32_t bytes = a_slot + (kSwap ? (uint32_t)(p.chunks * p.box) * 128u : (uint32_t)kTileBytes);
-    auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
-      if (to_leader)
-        ptx::tma_load_3d_pair(dst, map, bar, c0, c1, c2);
-      else
-        ptx::tma_load_3d(dst, map, bar, c0, c1, c2);
-    };
-    while (ok && iter.next(p, sg)) {
-      int seg = sg.kb0 / p.seg_blocks, ko = (sg.kb0 - seg * p.seg_blocks) * kTileK;
-      const int seg_end = p.seg_blocks * kTileK;
-      const int row_tile = kPair ? sg.mt * 2 + rank : sg.mt;
-      const int b_row = sg.nt * p.b_tile_step + rank * p.b_half_step;
-      // row tiles whose rows lie along k: the chunks of this tile (the first in registers)
-      const int per_tile = kTileM / (kSwap ? kTileM : p.box);
+    const uint32_t full0 = kPair ? ptx::map_shared_rank(bar_full(ctl, 0), 0) : bar_full(ctl, 0);
+    // The loads of k blocks [kb0, kb1) of one segment, from value ko of it on.
+    auto produce = [&](auto a_layout, auto b_layout, int kb0, int kb1, int ko, const CUtensorMap* a_map, int a_row, int a_z,
+                       const CUtensorMap* b_map, int b_row, int b_z, const CUtensorMap* lane_map, int lane_row) {
+      constexpr int kA = a_layout.value, kB = b_layout.value;
+      constexpr bool kChunks = kA == kLayoutChunks || kB == kLayoutChunks;
       bool empty_ready = false;
-      for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
+#pragma unroll 1
+      for (int kb = kb0; kb < kb1; ++kb, ko += kTileK) {
         if (!empty_ready) {
           int res = wait_phase(bar_empty(ctl, stage), phase ^ 1u, abort_flag, limit);
           res = __shfl_sync(0xffffffffu, res, 0);
           if (res != kWaitOk) {
             if (leader) record_failure(p, abort_flag, res, kRoleProducer, stage, sg.tile);
             ok = false;
-            break;
+            return;
           }
         }
         const int next_stage = stage + 1 == S ? 0 : stage + 1;
         const uint32_t next_phase = stage + 1 == S ? phase ^ 1u : phase;
-        empty_ready = kb + 1 < sg.kb1 && ptx::mbar_test_wait(bar_empty(ctl, next_stage), next_phase ^ 1u);
-        const uint32_t full = to_leader ? ptx::map_shared_rank(bar_full(ctl, stage), 0) : bar_full(ctl, stage);
-        const bool drop = p.test_drop && !dropped;
-        dropped = true;
-        if (!drop && !to_leader) {
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-        }
-        if (!drop && leader) {
-          if (to_leader)
-            ptx::mbar_arrive_expect_tx_remote(full, bytes);
-          else
-            ptx::mbar_arrive_expect_tx(full, bytes);
+        empty_ready = kb + 1 < kb1 && ptx::mbar_test_wait(bar_empty(ctl, next_stage), next_phase ^ 1u);
+        if (dropped) {
+          if (rank == 0) {
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          }
+          const uint32_t full = full0 + 8u * stage;
           const uint32_t a_dst = a0 + (uint32_t)stage * a_slot, b_dst = b0 + (uint32_t)stage * b_slot;
-          const int a_z = seg * p.a.z_segment, b_z = seg * p.b.z_segment;
-          const CUtensorMap* const a_map = &p.a_map[sg.problem * p.a.by_problem + seg * p.a.by_segment];
-          const CUtensorMap* const b_map = &p.b_map[sg.problem * p.b.by_problem + seg * p.b.by_segment + rank * p.b.by_rank];
-          // A: rows of this CTA (swapped tiles: columns of the weights)
-          if (p.a.mn_major) {
+          if (leader) {
+            if (kPair && rank == 1)
+              ptx::mbar_arrive_expect_tx_remote(full, bytes);
+            else
+              ptx::mbar_arrive_expect_tx(bar_full(ctl, stage), bytes);
+          }
+          if constexpr (kChunks) {
+            __syncwarp();
+            if (lane < per_tile) load_rows_of<kPair>((kSwap ? b_dst : a_dst) + (uint32_t)(lane * p.box) * 128u, lane_map, full, ko, lane_row);
+          }
+          if (leader) {
 #pragma unroll
             for (int t = 0; t < kAccs; ++t)
-#pragma unroll
-              for (int i = 0; i < kTileM / 64; ++i)
-                load(a_dst + (uint32_t)t * kTileBytes + (uint32_t)i * 8192u, a_map + t, full, row_tile * kTileM + 64 * i, ko, a_z);
-          } else if constexpr (kSwap) {
-#pragma unroll
-            for (int t = 0; t < kAccs; ++t) load(a_dst + (uint32_t)t * kTileBytes, a_map + t, full, ko, row_tile * kTileM, a_z);
-          } else {
-            for (int j = 0; j < per_tile; ++j) {
-              // a chunk behind the last lies outside its map: zeros
-              const int chunk = row_tile * per_tile + j;
-              const int shard = min(chunk / p.shard_chunks, p.shards - 1);
-              load(a_dst + (uint32_t)(j * p.box) * 128u, a_map + shard * p.a.by_shard, full, ko,
-                   (chunk - shard * p.shard_chunks) * p.box, a_z);
-            }
+              load_operand<kPair, kA>(a_dst + (uint32_t)t * kTileBytes, a_map + t, full, ko, a_row, a_z);
+            load_operand<kPair, kB>(b_dst, b_map, full, ko, b_row, b_z);
           }
-          // B
-          if constexpr (kSwap) {
-            for (int j = 0; j < p.chunks; ++j) {
-              const int shard = j / p.shard_chunks;
-              load(b_dst + (uint32_t)(j * p.box) * 128u, b_map + shard * p.b.by_shard, full, ko, (j - shard * p.shard_chunks) * p.box, b_z);
-            }
-          } else if (p.b.mn_major) {
-#pragma unroll
-            for (int i = 0; i < kTileM / 64; ++i) load(b_dst + (uint32_t)i * 8192u, b_map, full, b_row + 64 * i, ko, b_z);
-          } else {
-            load(b_dst, b_map, full, ko, b_row, b_z);
-          }
+          if constexpr (kChunks) __syncwarp();
         }
-        ko += kTileK;
-        if (ko == seg_end) {
-          ko = 0;
-          ++seg;
-        }
+        dropped = true;
         stage = next_stage;
         phase = next_phase;
+      }
+    };
+    while (ok && iter.next(p, sg)) {
+      const int row_tile = kPair ? sg.mt * 2 + rank : sg.mt;
+      // Chunks of the tokens in a stage.  One to a stage is the elected lane's, with operands
+      // that are uniform over the warp; else lane j has chunk j's map and row.  A chunk behind
+      // the last lies outside its map: zeros.
+      const int chunk0 = kSwap ? 0 : row_tile * per_tile;
+      const int shard0 = min(chunk0 / p.shard_chunks, p.shards - 1);
+      const int row0 = (chunk0 - shard0 * p.shard_chunks) * p.box;
+      const int chunk = chunk0 + lane, shard = min(chunk / p.shard_chunks, p.shards - 1);
+      const int lane_row = (chunk - shard * p.shard_chunks) * p.box;
+      const int b_row = kSwap ? row0 : sg.nt * p.b_tile_step + rank * p.b_half_step;
+      const int a_row = kSwap || p.a.mn_major ? row_tile * kTileM : row0;
+      int seg = sg.kb0 / p.seg_blocks;
+      for (int kb = sg.kb0; ok && kb < sg.kb1; ++seg) {
+        const int end = min(sg.kb1, (seg + 1) * p.seg_blocks);
+        const int ko = (kb - seg * p.seg_blocks) * kTileK, a_z = seg * p.a.z_segment, b_z = seg * p.b.z_segment;
+        const CUtensorMap* a_map = p.a_map + sg.problem * p.a.by_problem + seg * p.a.by_segment;
+        const CUtensorMap* b_map = p.b_map + sg.problem * p.b.by_problem + seg * p.b.by_segment + rank * p.b.by_rank;
+        const CUtensorMap* const lane_map = kSwap ? b_map + shard * p.b.by_shard : a_map + shard * p.a.by_shard;
+        if (kSwap)
+          b_map += shard0 * p.b.by_shard;
+        else
+          a_map += shard0 * p.a.by_shard;
+        with_layout(p.a.mn_major, p.a.blocked, !kSwap && per_tile > 1, [&](auto a_layout) {
+          // swapped tiles: the tokens' rows lie along k
+          if constexpr (kSwap) {
+            if (per_tile > 1)
+              produce(a_layout, Layout<kLayoutChunks>(), kb, end, ko, a_map, a_row, a_z, b_map, b_row, b_z, lane_map, lane_row);
+            else
+              produce(a_layout, Layout<kLayoutRows>(), kb, end, ko, a_map, a_row, a_z, b_map, b_row, b_z, lane_map, lane_row);
+          } else {
+            with_layout(p.b.mn_major, p.b.blocked, false, [&](auto b_layout) {
+              produce(a_layout, b_layout, kb, end, ko, a_map, a_row, a_z, b_map, b_row, b_z, lane_map, lane_row);
+            });
+          }
+        });
+        kb = end;
       }
     }
     // only after an abort can a load be unconsumed
@@ -558,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     uint8_t* const stage_out = base_ptr + (out0 - base) + ewarp * kStageOutBytes;
     SegmentIter iter;
     iter.init(p, cluster, clusters);
+    const int first_cut = p.dp_tiles + iter.u / p.k_blocks;  // the tile whose part lies in slot 0
     Segment sg;
     for (int it = 0; iter.next(p, sg); ++it) {
       const int acc = it & 1;
@@ -592,9 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           const unsigned there = __ballot_sync(0xffffffffu, c + lane < n / 2 && row_table[c0 + c + lane] >= 0);
           if (there) live = c + 32 - __clz(there);
         }
-        Parts parts = {0, 0};
+        Parts parts = {0, 0, 0};
         if (!sg.whole) {
-          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile, ewarp);
+          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile == first_cut ? 0 : 1, ewarp);
 #pragma unroll 1
           for (int c = 0; c < live; c += 8) {
             uint32_t v[kAccs][8];
@@ -633,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           } else {
 #pragma unroll
             for (int t = 0; t < kAccs; ++t)
-              sum_parts<8>(p, parts, kCtas, rank, sg.tile, ewarp, t * (n / 2) + c, lane, v[t]);
+              sum_parts<8>(p, parts, kCtas, rank, ewarp, t * (n / 2) + c, lane, v[t]);
           }
           with_activation(p.act, [&](auto act) {
 #pragma unroll
@@ -672,9 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         // gated: 64 columns of each product (the second's 128 columns on); else 128 columns
         constexpr int kOtherAcc = 128;
         const int first_col = kEpi == kEpiGated ? half * 64 : half * 128;
-        Parts parts = {0, 0};
+        Parts parts = {0, 0, 0};
         if (!sg.whole) {
-          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile, ewarp);
+          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile == first_cut ? 0 : 1, ewarp);
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
             uint32_t v[32];
@@ -700,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               ptx::tmem_ld_wait();
               if (h == 1) release();
             } else {
-              sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, 32 * h, lane, g);
-              sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, 64 + 32 * h, lane, u);
+              sum_parts<32>(p, parts, kCtas, rank, ewarp, 32 * h, lane, g);
+              sum_parts<32>(p, parts, kCtas, rank, ewarp, 64 + 32 * h, lane, u);
             }
             if (p.saved[0]) {
               pack32<kF16>(g, g16[h]);
@@ -736,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                 ptx::tmem_ld_wait();
                 if (c == 96) release();
               } else {
-                sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, c, lane, v);
+                sum_parts<32>(p, parts, kCtas, rank, ewarp, c, lane, v);
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i) *staged(stage_out, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -767,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                   ptx::tmem_ld_wait();
                   if (c == 64 && h == 1) release();
                 } else {
-                  sum_parts<32>(p, parts, kCtas, rank, sg.tile, ewarp, c + 32 * h, lane, v);
+                  sum_parts<32>(p, parts, kCtas, rank, ewarp, c + 32 * h, lane, v);
                 }
                 if constexpr (kEpi == kEpiLinear) {
                   if (p.bias) {

@@ -54,21 +54,55 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack2<kF16>(x[0], x[1]), pack2<kF16>(x[2], x[3]), pack2<kF16>(x[4], x[5]), pack2<kF16>(x[6], x[7]));
 }
 
-constexpr float kSqrtHalf = 0.70710678118654752f;
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
 
 // 1 / (1 + e^-z).  A z so low that e^-z is infinite gives 0.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.0f + exp2_approx(-kLog2e * z)); }
 
-// z Phi(z) by the complementary error function: no cancellation where Phi is small.
-// The tanh form of it, 0.5 z (1 + tanh(v)), is z sigmoid(2 v) for the same reason.
+// The normal distribution Phi(z), and e^(-z^2 / 2).  For z <= 0
+//     Phi(z) = t 2^(P(t) - z^2 log2(e) / 2),   t = 1 / (1 + 0.35 |z|),
+// with P fitted to log2(Phi e^(z^2/2) / t) at Chebyshev nodes of |z| <= 13.5, where it is off by
+// 1e-6: no cancellation where Phi is small, one reciprocal and one exponential.  In float32
+// Phi is off by 2^-18.5 of itself up to |z| = 8, by the exponent's rounding.  (erfcf took 193 us
+// for 4096 tokens, k 2560, n 5120, where the product alone takes a third.)
+__device__ __forceinline__ float normal(float z, float& gauss) {
+  const float x = fabsf(z), t = rcp_approx(fmaf(0.35f, x, 1.0f)), e = x * x * (-0.5f * kLog2e);
+  float p = -0.27522552f;
+  p = fmaf(p, t, 1.1202697f);
+  p = fmaf(p, t, -1.5381097f);
+  p = fmaf(p, t, 0.60237956f);
+  p = fmaf(p, t, -0.09033469f);
+  p = fmaf(p, t, 0.5817873f);
+  p = fmaf(p, t, 1.4394445f);
+  p = fmaf(p, t, -2.840212f);
+  gauss = exp2_approx(e);
+  const float low = t * exp2_approx(p + e);
+  return z > 0.0f ? 1.0f - low : low;
+}
+
+// The tanh form of z Phi(z), 0.5 z (1 + tanh(v)), is z sigmoid(2 v): nothing cancels.
 template <int kAct>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (kAct == kActRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays one
   if constexpr (kAct == kActSilu) return z * sigmoid(z);
-  if constexpr (kAct == kActGelu) return 0.5f * z * erfcf(-kSqrtHalf * z);
+  if constexpr (kAct == kActGelu) {
+    float gauss;
+    return z * normal(z, gauss);
+  }
   if constexpr (kAct == kActGeluTanh) return z * sigmoid(kTanhScale2 * (z + kTanhCube * z * z * z));
   return z;
 }
@@ -87,9 +121,10 @@ __device__ __forceinline__ void activate_with_slope(float z, float& a, float& sl
     a = z * s;
     slope = s * (1.0f + b * (1.0f - s));
   } else if constexpr (kAct == kActGelu) {
-    const float phi = 0.5f * erfcf(-kSqrtHalf * z), b = fminf(fmaxf(z, -20.0f), 20.0f);
+    float gauss;
+    const float phi = normal(z, gauss), b = fminf(fmaxf(z, -20.0f), 20.0f);
     a = z * phi;
-    slope = phi + b * (kInvSqrt2Pi * __expf(-0.5f * b * b));
+    slope = phi + b * (kInvSqrt2Pi * gauss);
   } else if constexpr (kAct == kActGeluTanh) {
     const float b = fminf(fmaxf(z, -20.0f), 20.0f);
     const float s = sigmoid(kTanhScale2 * (z + kTanhCube * z * z * z));

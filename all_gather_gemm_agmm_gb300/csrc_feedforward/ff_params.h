@@ -29,12 +29,15 @@ constexpr int kSlots = 2;             // of each CTA: the first and the last til
 enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 enum Epi : int { kEpiPlain = 0, kEpiGated = 1, kEpiLinear = 2 };
 
-// One operand's tensor maps, all {inner, rows, segments}, boxes of 64 inner values.
-// The map of a load: problem * by_problem + segment * by_segment + shard * by_shard
-// (+ CTA rank * by_rank); its last coordinate: segment * z_segment.
+// One operand's tensor maps, boxes of 64 values along the rows.  K-major: {k, rows}.
+// MN-major: {64, k, blocks of 64 values, segments} where the rows are whole blocks, so that one
+// box brings two of them, else {values, k, 1, segments}.  The map of a load: problem *
+// by_problem + segment * by_segment + shard * by_shard (+ CTA rank * by_rank); its last
+// coordinate, if MN-major: segment * z_segment.
 struct OperandParams {
   int maps;      // how many there are
-  int mn_major;  // the inner dimension runs along the tile, not along k
+  int mn_major;  // rows run along the tile, not along k
+  int blocked;   // ... and are whole blocks
   int by_problem, by_segment, by_shard, by_rank, z_segment;
 };
 
@@ -51,7 +54,8 @@ struct __align__(128) GemmParams {
   int k_blocks;            // of all segments
   int seg_blocks;          // of one segment
   int dp_tiles;            // tiles [0, dp_tiles) are worked on whole
-  int sk_clusters;         // the k blocks of the others are dealt evenly to this many clusters
+  int sk_clusters;         // the k blocks of the others are dealt evenly to this many clusters:
+  int sk_share, sk_extra;  // sk_share to each, and one more to the first sk_extra
   // Tokens (row tiles: the rows of A; swapped tiles: the rows of B) in chunks of
   // box rows that lie in one shard.
   int shards, box, shard_chunks;  // shard_chunks: chunks of a shard
@@ -142,8 +146,9 @@ struct NormParams {
   uint16_t* out;
   int64_t ldo;
   float *mean, *rstd;
+  int stages;  // rows in flight, where they stream
 };
-cudaError_t launch_norm(const NormParams& p, bool f16, cudaStream_t stream);
+cudaError_t launch_norm(const NormParams& p, bool f16, int sms, cudaStream_t stream);
 
 struct NormGradParams {
   int64_t rows;
@@ -154,6 +159,7 @@ struct NormGradParams {
   uint16_t* dx;
   int64_t ld_dx;
   float* part;  // [blocks][2][cols]: the sums of d_out * xhat and of d_out; NULL: not wanted
+  int stages;   // rows in flight, where they stream
 };
 int norm_grad_blocks(int64_t rows, int cols, int sms);
 cudaError_t launch_norm_grad(const NormGradParams& p, bool f16, int blocks, cudaStream_t stream);
