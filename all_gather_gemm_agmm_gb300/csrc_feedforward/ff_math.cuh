@@ -65,6 +65,60 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// Two float32 values in one 64-bit register pair, for the packed instructions.
+using Two = uint64_t;
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ Two both(float x) { return two(x, x); }
+__device__ __forceinline__ float2 halves(Two x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(Two x) {
+  const float2 v = halves(x);
+  return v.x + v.y;
+}
+
+// 8 values of 16 bits as four pairs, and back.
+template <bool kF16>
+__device__ __forceinline__ void widen(const uint4& u, Two (&x)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<kF16>(w[i]);
+    x[i] = two(f.x, f.y);
+  }
+}
+template <bool kF16>
+__device__ __forceinline__ uint4 narrow(const Two (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = halves(x[i]);
+    w[i] = pack2<kF16>(f.x, f.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)

@@ -146,7 +146,6 @@ struct NormParams {
   uint16_t* out;
   int64_t ldo;
   float *mean, *rstd;
-  int stages;  // rows in flight, where they stream
 };
 cudaError_t launch_norm(const NormParams& p, bool f16, int sms, cudaStream_t stream);
 

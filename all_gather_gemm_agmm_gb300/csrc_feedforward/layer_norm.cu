@@ -23,26 +23,73 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The sum over a team: a warp, or the whole block (`s` has room for a value of each warp).
+// The sum over the block, whose warps meet in `s`; it may be written again behind another barrier.
+__device__ __forceinline__ float block_sum(float v, float* s) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? s[threadIdx.x & 31] : 0.0f);
+}
+
+// The sum over a team: a warp, or the block.
 template <bool kWarpRow>
 __device__ __forceinline__ float team_sum(float v, float* s) {
-  v = warp_sum(v);
-  if constexpr (!kWarpRow) {
-    const int warps = blockDim.x >> 5;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = (int)(threadIdx.x & 31) < warps ? s[threadIdx.x & 31] : 0.0f;
-    v = warp_sum(v);
-  }
-  return v;
+  return kWarpRow ? warp_sum(v) : block_sum(v, s);
+}
+
+// Eight ones: a weight that is not there.
+template <bool kF16>
+__device__ __forceinline__ uint4 ones() {
+  constexpr uint32_t w = kF16 ? 0x3c003c00u : 0x3f803f80u;
+  return make_uint4(w, w, w, w);
+}
+
+// x * rstd * w + b of a piece
+template <bool kF16>
+__device__ __forceinline__ uint4 scaled(const Two (&x)[4], float rstd, const uint4& w16, const uint4& b16) {
+  Two w[4], b[4], y[4];
+  widen<kF16>(w16, w);
+  widen<kF16>(b16, b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = fma2(mul2(x[e], both(rstd)), w[e], b[e]);
+  return narrow<kF16>(y);
+}
+
+// A piece of the backward pass: xhat, and g = d * w.
+struct GradPiece {
+  Two x[4], g[4];
+};
+template <bool kF16>
+__device__ __forceinline__ GradPiece grad_piece(const uint4& x16, const uint4& d16, float mean, float rstd) {
+  GradPiece q;
+  widen<kF16>(x16, q.x);
+  widen<kF16>(d16, q.g);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q.x[e] = mul2(add2(q.x[e], both(-mean)), both(rstd));
+  return q;
+}
+template <bool kF16>
+__device__ __forceinline__ void weigh(GradPiece& q, const uint4& w16) {
+  Two w[4];
+  widen<kF16>(w16, w);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q.g[e] = mul2(q.g[e], w[e]);
+}
+// rstd * (g - mg - xhat * mgx) + add
+template <bool kF16>
+__device__ __forceinline__ uint4 input_grad(const GradPiece& q, float rstd, float mg, float mgx, const uint4& a16) {
+  Two a[4], y[4];
+  widen<kF16>(a16, a);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = fma2(fma2(q.x[e], both(-mgx), add2(q.g[e], both(-mg))), both(rstd), a[e]);
+  return narrow<kF16>(y);
 }
 
 constexpr int kWarpRowWarps = 4;
 
 template <bool kF16, bool kWarpRow, int kPieces>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : 512) agmm_layer_norm(const __grid_constant__ NormParams p) {
-  __shared__ float s[32];
+__global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : kPieces == 1 ? 1024 : 512) agmm_layer_norm(const __grid_constant__ NormParams p) {
+  __shared__ float s[2][32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int team = kWarpRow ? 32 : blockDim.x;
@@ -50,35 +97,35 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : 512) agmm_laye
   const int64_t row = kWarpRow ? (int64_t)blockIdx.x * kWarpRowWarps + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= p.rows) return;
   uint4 in[kPieces];
-  float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = (t + i * team) * 8;
     if (c < p.cols) in[i] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + c);
   }
-  float x[kPieces][8];
+  Two x[kPieces][4], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     if ((t + i * team) * 8 < p.cols) {
-      unpack8<kF16>(in[i], x[i]);
+      widen<kF16>(in[i], x[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += x[i][e];
+      for (int e = 0; e < 4; ++e) sum = add2(sum, x[i][e]);
     }
   }
   const float inv = 1.0f / (float)p.cols;
-  const float mean = team_sum<kWarpRow>(sum, s) * inv;
-  float squares = 0.0f;
+  const float mean = team_sum<kWarpRow>(sum2(sum), s[0]) * inv;
+  const Two minus = both(-mean);
+  Two squares = 0;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     if ((t + i * team) * 8 < p.cols) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[i][e] -= mean;
-        squares += x[i][e] * x[i][e];
+      for (int e = 0; e < 4; ++e) {
+        x[i][e] = add2(x[i][e], minus);
+        squares = fma2(x[i][e], x[i][e], squares);
       }
     }
   }
-  const float rstd = rsqrtf(team_sum<kWarpRow>(squares, s) * inv + p.eps);
+  const float rstd = rsqrtf(team_sum<kWarpRow>(sum2(squares), s[1]) * inv + p.eps);
   if (t == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
@@ -87,16 +134,9 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : 512) agmm_laye
   for (int i = 0; i < kPieces; ++i) {
     const int c = (t + i * team) * 8;
     if (c < p.cols) {
-      float w[8], b[8];
-      if (p.weight) unpack8<kF16>(__ldg(reinterpret_cast<const uint4*>(p.weight + c)), w);
-      if (p.bias) unpack8<kF16>(__ldg(reinterpret_cast<const uint4*>(p.bias + c)), b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[i][e] *= rstd;
-        if (p.weight) x[i][e] *= w[e];
-        if (p.bias) x[i][e] += b[e];
-      }
-      *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8<kF16>(x[i]);
+      const uint4 w = p.weight ? __ldg(reinterpret_cast<const uint4*>(p.weight + c)) : ones<kF16>();
+      const uint4 b = p.bias ? __ldg(reinterpret_cast<const uint4*>(p.bias + c)) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = scaled<kF16>(x[i], rstd, w, b);
     }
   }
 }
@@ -124,83 +164,6 @@ __device__ __forceinline__ void copy_wait(int left) {
 constexpr int kMostStages = 8;
 constexpr int kSumBytes = 512;  // the warps' sums, at the start of shared memory
 
-template <bool kF16, int kPieces>
-__global__ void __launch_bounds__(512, kPieces > 2 ? 1 : 2) agmm_layer_norm_stream(const __grid_constant__ NormParams p) {
-  extern __shared__ __align__(16) uint8_t shared[];
-  float* const s = reinterpret_cast<float*>(shared);
-  uint4* const ring = reinterpret_cast<uint4*>(shared + kSumBytes);
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int t = threadIdx.x, team = blockDim.x, stages = p.stages;
-  const int64_t step = gridDim.x;
-  auto fetch = [&](int64_t row, int stage) {
-    if (row < p.rows) {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int c = (t + i * team) * 8;
-        if (c < p.cols) copy_async(ring + (stage * kPieces + i) * team + t, p.x + row * p.ldx + c);
-      }
-    }
-    copy_commit();
-  };
-  uint4 w16[kPieces], b16[kPieces];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int c = (t + i * team) * 8;
-    if (p.weight && c < p.cols) w16[i] = __ldg(reinterpret_cast<const uint4*>(p.weight + c));
-    if (p.bias && c < p.cols) b16[i] = __ldg(reinterpret_cast<const uint4*>(p.bias + c));
-  }
-  for (int k = 0; k < stages - 1; ++k) fetch(blockIdx.x + k * step, k);
-  const float inv = 1.0f / (float)p.cols;
-  int stage = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += step) {
-    fetch(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
-    copy_wait(stages - 1);
-    float x[kPieces][8], sum = 0.0f, squares = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if ((t + i * team) * 8 < p.cols) {
-        unpack8<kF16>(ring[(stage * kPieces + i) * team + t], x[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += x[i][e];
-      }
-    }
-    const float mean = team_sum<false>(sum, s) * inv;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if ((t + i * team) * 8 < p.cols) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[i][e] -= mean;
-          squares += x[i][e] * x[i][e];
-        }
-      }
-    }
-    const float rstd = rsqrtf(team_sum<false>(squares, s + 32) * inv + p.eps);
-    if (t == 0) {
-      if (p.mean) p.mean[row] = mean;
-      if (p.rstd) p.rstd[row] = rstd;
-    }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int c = (t + i * team) * 8;
-      if (c < p.cols) {
-        float w[8], b[8];
-        if (p.weight) unpack8<kF16>(w16[i], w);
-        if (p.bias) unpack8<kF16>(b16[i], b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[i][e] *= rstd;
-          if (p.weight) x[i][e] *= w[e];
-          if (p.bias) x[i][e] += b[e];
-        }
-        *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8<kF16>(x[i]);
-      }
-    }
-    stage = stage + 1 == stages ? 0 : stage + 1;
-  }
-}
-
 // Short rows: a warp to a row.
 template <bool kF16, int kPieces>
 __global__ void __launch_bounds__(32 * kWarpRowWarps) agmm_layer_norm_grad_short(const __grid_constant__ NormGradParams p) {
@@ -211,14 +174,14 @@ __global__ void __launch_bounds__(32 * kWarpRowWarps) agmm_layer_norm_grad_short
   const int t = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = (int64_t)gridDim.x * kWarpRowWarps;
   const float inv = 1.0f / (float)p.cols;
-  float dw[kPieces][8], db[kPieces][8];
+  Two dw[kPieces][4], db[kPieces][4];
   uint4 w16[kPieces];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = (t + i * 32) * 8;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
-    if (p.weight && c < p.cols) w16[i] = __ldg(reinterpret_cast<const uint4*>(p.weight + c));
+    for (int e = 0; e < 4; ++e) dw[i][e] = db[i][e] = 0;
+    w16[i] = p.weight && c < p.cols ? __ldg(reinterpret_cast<const uint4*>(p.weight + c)) : ones<kF16>();
   }
 #pragma unroll 1
   for (int64_t row = (int64_t)blockIdx.x * kWarpRowWarps + warp; row < p.rows; row += step) {
@@ -226,6 +189,7 @@ __global__ void __launch_bounds__(32 * kWarpRowWarps) agmm_layer_norm_grad_short
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (t + i * 32) * 8;
+      a16[i] = make_uint4(0, 0, 0, 0);
       if (c < p.cols) {
         x16[i] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + c);
         d16[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + c);
@@ -233,41 +197,31 @@ __global__ void __launch_bounds__(32 * kWarpRowWarps) agmm_layer_norm_grad_short
       }
     }
     const float mean = __ldg(p.mean + row), r = __ldg(p.rstd + row);
-    float x[kPieces][8], g[kPieces][8];
-    float sum_g = 0.0f, sum_gx = 0.0f;
+    GradPiece q[kPieces];
+    Two sum_g = 0, sum_gx = 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       if ((t + i * 32) * 8 < p.cols) {
-        float w[8];
-        unpack8<kF16>(x16[i], x[i]);
-        unpack8<kF16>(d16[i], g[i]);
-        if (p.weight) unpack8<kF16>(w16[i], w);
+        q[i] = grad_piece<kF16>(x16[i], d16[i], mean, r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[i][e] = (x[i][e] - mean) * r;
-          dw[i][e] += g[i][e] * x[i][e];
-          db[i][e] += g[i][e];
-          if (p.weight) g[i][e] *= w[e];
-          sum_g += g[i][e];
-          sum_gx += g[i][e] * x[i][e];
+        for (int e = 0; e < 4; ++e) {
+          dw[i][e] = fma2(q[i].g[e], q[i].x[e], dw[i][e]);
+          db[i][e] = add2(db[i][e], q[i].g[e]);
+        }
+        weigh<kF16>(q[i], w16[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum_g = add2(sum_g, q[i].g[e]);
+          sum_gx = fma2(q[i].g[e], q[i].x[e], sum_gx);
         }
       }
     }
     if (p.dx) {
-      const float mg = warp_sum(sum_g) * inv, mgx = warp_sum(sum_gx) * inv;
+      const float mg = warp_sum(sum2(sum_g)) * inv, mgx = warp_sum(sum2(sum_gx)) * inv;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (t + i * 32) * 8;
-        if (c < p.cols) {
-          float a[8];
-          if (p.add) unpack8<kF16>(a16[i], a);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            g[i][e] = r * (g[i][e] - mg - x[i][e] * mgx);
-            if (p.add) g[i][e] += a[e];
-          }
-          *reinterpret_cast<uint4*>(p.dx + row * p.ld_dx + c) = pack8<kF16>(g[i]);
-        }
+        if (c < p.cols) *reinterpret_cast<uint4*>(p.dx + row * p.ld_dx + c) = input_grad<kF16>(q[i], r, mg, mgx, a16[i]);
       }
     }
   }
@@ -280,9 +234,9 @@ __global__ void __launch_bounds__(32 * kWarpRowWarps) agmm_layer_norm_grad_short
     const int c = (t + i * 32) * 8;
     if (c < p.cols) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        mine[c + e] = dw[i][e];
-        mine[p.cols + c + e] = db[i][e];
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<Two*>(mine + c + 2 * e) = dw[i][e];
+        *reinterpret_cast<Two*>(mine + p.cols + c + 2 * e) = db[i][e];
       }
     }
   }
@@ -295,8 +249,9 @@ __global__ void __launch_bounds__(32 * kWarpRowWarps) agmm_layer_norm_grad_short
   }
 }
 
-// Other rows: a block to a row, the rows streaming through shared memory.
-template <bool kF16, int kPieces>
+// Other rows: a block to kRows rows, the rows streaming through shared memory.  Two rows to a
+// turn: their sums meet in one barrier, and the latency of one row's sums hides behind the other.
+template <bool kF16, int kPieces, int kRows>
 __global__ void __launch_bounds__(512, 1) agmm_layer_norm_grad(const __grid_constant__ NormGradParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   uint4* const ring = reinterpret_cast<uint4*>(shared + kSumBytes);
@@ -304,91 +259,115 @@ __global__ void __launch_bounds__(512, 1) agmm_layer_norm_grad(const __grid_cons
   ptx::griddep_wait();
   const int t = threadIdx.x, warp = threadIdx.x >> 5, team = blockDim.x, stages = p.stages;
   const int inputs = p.add ? 3 : 2;
-  const int64_t step = gridDim.x;
+  const int64_t grid = gridDim.x, step = kRows * grid;
   const float inv = 1.0f / (float)p.cols;
-  auto slot = [&](int stage, int input, int i) { return ring + ((stage * inputs + input) * kPieces + i) * team + t; };
-  auto fetch = [&](int64_t row, int stage) {
-    if (row < p.rows) {
+  auto slot = [&](int stage, int k, int input, int i) { return ring + (((stage * kRows + k) * inputs + input) * kPieces + i) * team + t; };
+  auto fetch = [&](int64_t first, int stage) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int c = (t + i * team) * 8;
-        if (c < p.cols) {
-          copy_async(slot(stage, 0, i), p.x + row * p.ldx + c);
-          copy_async(slot(stage, 1, i), p.d_out + row * p.ld_out + c);
-          if (p.add) copy_async(slot(stage, 2, i), p.add + row * p.ld_add + c);
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t row = first + k * grid;
+      if (row < p.rows) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int c = (t + i * team) * 8;
+          if (c < p.cols) {
+            copy_async(slot(stage, k, 0, i), p.x + row * p.ldx + c);
+            copy_async(slot(stage, k, 1, i), p.d_out + row * p.ld_out + c);
+            if (p.add) copy_async(slot(stage, k, 2, i), p.add + row * p.ld_add + c);
+          }
         }
       }
     }
     copy_commit();
   };
-  float dw[kPieces][8], db[kPieces][8];
+  Two dw[kPieces][4], db[kPieces][4];
   uint4 w16[kPieces];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = (t + i * team) * 8;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
-    if (p.weight && c < p.cols) w16[i] = __ldg(reinterpret_cast<const uint4*>(p.weight + c));
+    for (int e = 0; e < 4; ++e) dw[i][e] = db[i][e] = 0;
+    w16[i] = p.weight && c < p.cols ? __ldg(reinterpret_cast<const uint4*>(p.weight + c)) : ones<kF16>();
   }
   for (int k = 0; k < stages - 1; ++k) fetch(blockIdx.x + k * step, k);
-  float next_mean = __ldg(p.mean + blockIdx.x), next_rstd = __ldg(p.rstd + blockIdx.x);
+  float next_mean[kRows], next_rstd[kRows];
+  auto fetch_stats = [&](int64_t first) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t row = first + k * grid;
+      next_mean[k] = row < p.rows ? __ldg(p.mean + row) : 0.0f;
+      next_rstd[k] = row < p.rows ? __ldg(p.rstd + row) : 0.0f;
+    }
+  };
+  fetch_stats(blockIdx.x);
   int stage = 0, turn = 0;
 #pragma unroll 1
-  for (int64_t row = blockIdx.x; row < p.rows; row += step) {
-    fetch(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
-    const float mean = next_mean, r = next_rstd;
-    if (row + step < p.rows) {
-      next_mean = __ldg(p.mean + row + step);
-      next_rstd = __ldg(p.rstd + row + step);
+  for (int64_t first = blockIdx.x; first < p.rows; first += step) {
+    fetch(first + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    float mean[kRows], r[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      mean[k] = next_mean[k];
+      r[k] = next_rstd[k];
     }
+    fetch_stats(first + step);
     copy_wait(stages - 1);
-    float sum_g = 0.0f, sum_gx = 0.0f;
+    Two sum_g[kRows], sum_gx[kRows];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if ((t + i * team) * 8 < p.cols) {
-        float x[8], g[8], w[8];
-        unpack8<kF16>(*slot(stage, 0, i), x);
-        unpack8<kF16>(*slot(stage, 1, i), g);
-        if (p.weight) unpack8<kF16>(w16[i], w);
+    for (int k = 0; k < kRows; ++k) {
+      sum_g[k] = sum_gx[k] = 0;
+      if (first + k * grid < p.rows) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = (x[e] - mean) * r;
-          dw[i][e] += g[e] * x[e];
-          db[i][e] += g[e];
-          if (p.weight) g[e] *= w[e];
-          sum_g += g[e];
-          sum_gx += g[e] * x[e];
+        for (int i = 0; i < kPieces; ++i) {
+          if ((t + i * team) * 8 < p.cols) {
+            GradPiece q = grad_piece<kF16>(*slot(stage, k, 0, i), *slot(stage, k, 1, i), mean[k], r[k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              dw[i][e] = fma2(q.g[e], q.x[e], dw[i][e]);
+              db[i][e] = add2(db[i][e], q.g[e]);
+            }
+            weigh<kF16>(q, w16[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sum_g[k] = add2(sum_g[k], q.g[e]);
+              sum_gx[k] = fma2(q.g[e], q.x[e], sum_gx[k]);
+            }
+          }
         }
       }
     }
     if (p.dx) {
-      // two sets of sums in turn: one barrier a row
+      // two sets of sums in turn: one barrier
       float2* const s = reinterpret_cast<float2*>(shared) + 32 * turn;
       turn ^= 1;
-      sum_g = warp_sum(sum_g);
-      sum_gx = warp_sum(sum_gx);
-      if ((t & 31) == 0) s[warp] = make_float2(sum_g, sum_gx);
+      float2 v[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) v[k] = make_float2(warp_sum(sum2(sum_g[k])), warp_sum(sum2(sum_gx[k])));
+      if ((t & 31) == 0) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) s[k * 16 + warp] = v[k];
+      }
       __syncthreads();
-      const float2 v = (t & 31) < (int)(blockDim.x >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f);
-      const float mg = warp_sum(v.x) * inv, mgx = warp_sum(v.y) * inv;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int c = (t + i * team) * 8;
-        if (c < p.cols) {
-          // read again rather than held: registers
-          float x[8], g[8], w[8], a[8];
-          unpack8<kF16>(*slot(stage, 0, i), x);
-          unpack8<kF16>(*slot(stage, 1, i), g);
-          if (p.weight) unpack8<kF16>(w16[i], w);
-          if (p.add) unpack8<kF16>(*slot(stage, 2, i), a);
+      for (int k = 0; k < kRows; ++k) {
+        v[k] = (t & 31) < (int)(blockDim.x >> 5) ? s[k * 16 + (t & 31)] : make_float2(0.0f, 0.0f);
+        v[k] = make_float2(warp_sum(v[k].x) * inv, warp_sum(v[k].y) * inv);
+      }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] = (x[e] - mean) * r;
-            if (p.weight) g[e] *= w[e];
-            g[e] = r * (g[e] - mg - x[e] * mgx);
-            if (p.add) g[e] += a[e];
+      for (int k = 0; k < kRows; ++k) {
+        const int64_t row = first + k * grid;
+        if (row < p.rows) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int c = (t + i * team) * 8;
+            if (c < p.cols) {
+              // read again rather than held: registers
+              GradPiece q = grad_piece<kF16>(*slot(stage, k, 0, i), *slot(stage, k, 1, i), mean[k], r[k]);
+              weigh<kF16>(q, w16[i]);
+              const uint4 a16 = p.add ? *slot(stage, k, 2, i) : make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(p.dx + row * p.ld_dx + c) = input_grad<kF16>(q, r[k], v[k].x, v[k].y, a16);
+            }
           }
-          *reinterpret_cast<uint4*>(p.dx + row * p.ld_dx + c) = pack8<kF16>(g);
         }
       }
     }
@@ -401,9 +380,9 @@ __global__ void __launch_bounds__(512, 1) agmm_layer_norm_grad(const __grid_cons
     const int c = (t + i * team) * 8;
     if (c < p.cols) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        *reinterpret_cast<float4*>(part + c + e) = make_float4(dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]);
-        *reinterpret_cast<float4*>(part + p.cols + c + e) = make_float4(db[i][e], db[i][e + 1], db[i][e + 2], db[i][e + 3]);
+      for (int e = 0; e < 4; e += 2) {
+        *reinterpret_cast<ulonglong2*>(part + c + 2 * e) = make_ulonglong2(dw[i][e], dw[i][e + 1]);
+        *reinterpret_cast<ulonglong2*>(part + p.cols + c + 2 * e) = make_ulonglong2(db[i][e], db[i][e + 1]);
       }
     }
   }
@@ -428,24 +407,28 @@ constexpr int kWarpRowPieces = 128;  // rows of up to 1024 values are one warp's
 
 int round_warp(int threads) { return (threads + 31) / 32 * 32; }
 
-// Blocks that stream: two or four pieces to a thread, at most 512 threads.
-int stream_pieces(int pieces) { return pieces <= 1024 ? 2 : 4; }
-int stream_threads(int pieces) { return round_warp((pieces + stream_pieces(pieces) - 1) / stream_pieces(pieces)); }
-
-// Blocks of an SM, by their threads: 1024 threads at least (512 for the widest rows), and the
-// rows that each has in flight.
-int stream_blocks(int pieces, int most_threads) {
-  const int blocks = most_threads / stream_threads(pieces);
-  return blocks < 1 ? 1 : blocks > 8 ? 8 : blocks;
-}
-int stream_stages(int pieces, int blocks, int inputs) {
-  const int bytes = stream_threads(pieces) * stream_pieces(pieces) * 16 * inputs;
-  const int stages = ((int)kMaxSmem / blocks - 1024 - kSumBytes) / bytes;
-  return stages > kMostStages ? kMostStages : stages;
+// Blocks that stream: two pieces to a thread and two rows to a turn, for the widest rows four
+// and one; 512 threads to an SM (their registers); and the turns' rows that each has in flight.
+struct Stream {
+  int pieces, rows, threads, blocks, stages;
+  size_t smem;
+};
+Stream stream_of(int cols, int inputs) {
+  Stream s;
+  const int pieces = cols / 8;
+  s.pieces = pieces <= 1024 ? 2 : 4;
+  s.rows = pieces <= 1024 ? 2 : 1;
+  s.threads = round_warp((pieces + s.pieces - 1) / s.pieces);
+  s.blocks = 512 / s.threads;
+  const size_t turn = (size_t)s.threads * s.pieces * 16 * inputs * s.rows;
+  const size_t stages = (kMaxSmem / s.blocks - 1024 - kSumBytes) / turn;
+  s.stages = (int)(stages > kMostStages ? kMostStages : stages);
+  s.smem = kSumBytes + s.stages * turn;
+  return s;
 }
 
 template <bool kF16>
-cudaError_t launch_norm_t(NormParams p, int sms, cudaStream_t stream) {
+cudaError_t launch_norm_t(const NormParams& p, int sms, cudaStream_t stream) {
   const int pieces = p.cols / 8;
   if (pieces <= kWarpRowPieces) {
     const unsigned blocks = (unsigned)((p.rows + kWarpRowWarps - 1) / kWarpRowWarps);
@@ -454,17 +437,8 @@ cudaError_t launch_norm_t(NormParams p, int sms, cudaStream_t stream) {
                                             : &agmm_layer_norm<kF16, true, 4>;
     return launch(fn, p, blocks, 32 * kWarpRowWarps, 0, stream);
   }
-  const int per_sm = stream_blocks(pieces, pieces <= 1024 ? 1024 : 512);
-  if (p.rows > (int64_t)sms * per_sm) {
-    p.stages = stream_stages(pieces, per_sm, 1);
-    const int threads = stream_threads(pieces);
-    const size_t smem = kSumBytes + (size_t)p.stages * threads * stream_pieces(pieces) * 16;
-    void (*fn)(NormParams) = pieces <= 1024 ? &agmm_layer_norm_stream<kF16, 2> : &agmm_layer_norm_stream<kF16, 4>;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
-    if (e != cudaSuccess) return e;
-    return launch(fn, p, (unsigned)(sms * per_sm), threads, smem, stream);
-  }
-  if (pieces <= 512) return launch(&agmm_layer_norm<kF16, false, 1>, p, (unsigned)p.rows, round_warp(pieces), 0, stream);
+  if (p.rows <= 2 * sms && pieces <= 1024)
+    return launch(&agmm_layer_norm<kF16, false, 1>, p, (unsigned)p.rows, round_warp(pieces), 0, stream);
   return launch(&agmm_layer_norm<kF16, false, 4>, p, (unsigned)p.rows, round_warp((pieces + 3) / 4), 0, stream);
 }
 
@@ -477,13 +451,12 @@ cudaError_t launch_norm_grad_t(NormGradParams p, int blocks, cudaStream_t stream
                                                 : &agmm_layer_norm_grad_short<kF16, 4>;
     return launch(fn, p, (unsigned)blocks, 32 * kWarpRowWarps, (size_t)kWarpRowWarps * 2 * p.cols * sizeof(float), stream);
   }
-  const int threads = stream_threads(pieces), inputs = p.add ? 3 : 2;
-  p.stages = stream_stages(pieces, stream_blocks(pieces, 512), inputs);
-  const size_t smem = kSumBytes + (size_t)p.stages * threads * stream_pieces(pieces) * 16 * inputs;
-  void (*fn)(NormGradParams) = pieces <= 1024 ? &agmm_layer_norm_grad<kF16, 2> : &agmm_layer_norm_grad<kF16, 4>;
+  const Stream st = stream_of(p.cols, p.add ? 3 : 2);
+  p.stages = st.stages;
+  void (*fn)(NormGradParams) = st.pieces == 2 ? &agmm_layer_norm_grad<kF16, 2, 2> : &agmm_layer_norm_grad<kF16, 4, 1>;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
-  return launch(fn, p, (unsigned)blocks, threads, smem, stream);
+  return launch(fn, p, (unsigned)blocks, st.threads, st.smem, stream);
 }
 
 }  // namespace
@@ -496,7 +469,7 @@ int norm_grad_blocks(int64_t rows, int cols, int sms) {
   const int pieces = cols / 8;
   const int64_t teams = pieces <= kWarpRowPieces ? kWarpRowWarps : 1;
   const int64_t most = (rows + teams - 1) / teams;
-  const int64_t want = (int64_t)sms * (pieces <= kWarpRowPieces ? 8 : stream_blocks(pieces, 512));
+  const int64_t want = (int64_t)sms * (pieces <= kWarpRowPieces ? 8 : stream_of(cols, 3).blocks);
   return (int)(most < want ? most : want);
 }
 
