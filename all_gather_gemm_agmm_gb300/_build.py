@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libagmm.so")
 SOURCES = ["agmm_select_rows_a1.cu", "agmm_select_rows_a2.cu", "agmm_select_swap.cu", "agmm_kernels.cu",
            "agmm_api.cpp", "agmm_noalloc.cu"]
 ATTENTION_SOURCES = ["norm_rope.cu", "attn_prompt.cu", "attn_tree.cu", "attn_launch.cu", "attn_api.cpp"]
-FEEDFORWARD_SOURCES = ["ff_rows_plain.cu", "ff_rows_gated.cu", "ff_rows_linear.cu", "ff_swap_plain.cu", "ff_swap_gated.cu",
+FEEDFORWARD_SOURCES = ["ff_wide_plain.cu", "ff_wide_gated.cu", "ff_wide_linear.cu", "ff_narrow_plain.cu",
+                       "ff_narrow_gated.cu", "ff_narrow_linear.cu", "ff_swap_plain.cu", "ff_swap_gated.cu",
                        "ff_swap_linear.cu", "ff_launch.cu", "ff_pointwise.cu", "layer_norm.cu", "ff_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -31,6 +31,7 @@ struct ProductPlan {
   bool transpose, f16;  // weights stored [n, k]; fp16
   int device, sms;
   int pairs, singles;   // CTA pairs, and CTAs, that run at once
+  int path, bn, cut;    // overrides for tests and experiments; -1: by the rules
   uint64_t wait_limit_cycles;
   int test_drop;
 };
@@ -44,11 +45,6 @@ struct agmm_layer_norm_s {
 
 namespace {
 
-// A cluster's share of cut tiles is at least this many k blocks (of 64 values): the parts
-// make a round trip through L2, 128 KiB of each CTA of a row tile, and those of a swapped
-// tile in proportion to its tokens.
-constexpr int kMinRowBlocks = 8;
-constexpr int kMinSwapBlocks = 4;
 // Row tiles (pairs of them) that sweep the columns together.
 constexpr int kGroupM = 8;
 constexpr int64_t kMostRows = INT_MAX - 1024;  // coordinates of tiles behind the last row fit 32 bits
@@ -169,10 +165,10 @@ struct Matrix {
   int64_t inner, rows, segments, stride;
 };
 
-// A matrix as an operand that is contracted along its rows' values (K-major, boxes of
-// box_rows), or along its rows (MN-major).  128-byte swizzled, zeros outside: what lies
+// A matrix as an operand that is contracted along its rows' values (K-major), or along its rows
+// (MN-major); a tile has tile_rows of its rows or values.  128-byte swizzled, zeros outside: what lies
 // behind a segment's last row is not its neighbour's.
-agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m, bool mn_major, int box_rows, bool f16) {
+agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m, bool mn_major, int tile_rows, bool f16) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return fail(AGMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   o->mn_major = mn_major;
@@ -181,7 +177,8 @@ agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m
   const cuuint64_t blocks = o->blocked ? inner / 64 : 1;
   const cuuint64_t dims[4] = {inner / blocks, rows, blocks, (cuuint64_t)m.segments};
   const cuuint64_t strides[3] = {step, o->blocked ? 128 : step, (m.segments > 1 ? rows : 1) * step};
-  const cuuint32_t box[4] = {kTileK, (cuuint32_t)(mn_major ? 64 : box_rows), (cuuint32_t)(o->blocked ? 2 : 1), 1}, one[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {kTileK, (cuuint32_t)(mn_major ? 64 : tile_rows),
+                             (cuuint32_t)(o->blocked ? tile_rows / 64 : 1), 1}, one[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mn_major ? 4 : 2,
                          const_cast<void*>(m.ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -192,23 +189,33 @@ agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m
 // ---------------------------------------------------------------- schedules
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Whole tiles go round the clusters.  Those of a last wave that fills less than two thirds
-// of them are cut along k, with the wave before it, evenly over the clusters, as far as
-// every share is worth its parts' round trip.
-void make_schedule(GemmParams* p, int clusters, int min_blocks) {
-  const int T = p->num_tiles, C = clusters, rem = T % C;
-  p->dp_tiles = T;
-  p->sk_clusters = 0;
-  if (rem == 0 || 3 * rem >= 2 * C) return;
-  const int shared = T < C ? T : C + rem;
+// The time that a schedule takes, in cycles, as far as it differs from others: clusters that each
+// work through `blocks` k blocks.  Constants as measured (the design doc has the table).
+constexpr double kWideBlock = 512, kNarrowBlock = 280;  // a k block of a row tile's main loop
+constexpr double kWideCut = 14000, kNarrowCut = 9000;   // the parts' round trip through L2
+constexpr double kSwapCut = 7600;
+constexpr double kSwapByte = 0.0141;                    // swapped tiles: a byte, at what one CTA keeps in flight
+constexpr double kMemoryByte = 2.84e-4;                 // ... and for each CTA that shares the device's memory
+
+// Whole tiles go round the clusters; or those of a ragged last wave, with the wave before it, are
+// cut along k evenly over the clusters.
+int cut_tiles(int tiles, int clusters) { return tiles < clusters ? tiles : tiles % clusters ? clusters + tiles % clusters : 0; }
+
+void make_schedule(GemmParams* p, int clusters, bool cut) {
+  const int shared = cut ? cut_tiles(p->num_tiles, clusters) : 0;
   const int64_t units = (int64_t)shared * p->k_blocks;
-  const int64_t parts = std::min<int64_t>(C, units / min_blocks);
-  // a share of a tile or more, where tiles are fewer: nothing to gain
-  if (parts <= std::min(shared, C - 1) || units > INT_MAX) return;
-  p->dp_tiles = T - shared;
+  const int64_t parts = std::min<int64_t>(clusters, units);
+  p->dp_tiles = p->num_tiles - shared;
   p->sk_clusters = (int)parts;
-  p->sk_share = (int)(units / parts);
-  p->sk_extra = (int)(units % parts);
+  if (parts) {
+    p->sk_share = (int)(units / parts);
+    p->sk_extra = (int)(units % parts);
+  }
+}
+
+bool can_cut(int64_t tiles, int k_blocks, int clusters) {
+  const int64_t shared = cut_tiles((int)tiles, clusters);
+  return shared > 0 && k_blocks > 1 && shared * k_blocks <= INT_MAX;
 }
 
 // How the tokens' rows lie in tiles: boxes of rows that never leave their shard.
@@ -254,19 +261,48 @@ void common_params(const ProductPlan* pl, GemmParams* p, void* workspace) {
   p->seg_blocks = p->k_blocks = 1;
 }
 
-agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, int64_t m_tiles, int64_t n_tiles, cudaStream_t stream) {
+// Row tiles: their width, and whether some are cut, by the shortest estimate.
+struct RowChoice {
+  int bn;
+  bool cut;
+};
+RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int k_blocks, int problems, bool gated) {
+  RowChoice best = {kWideN, false};
+  double least = 1e300;
+  for (int bn = kWideN; bn >= kNarrowN; bn -= kWideN - kNarrowN) {
+    if (pl->bn >= 0 && pl->bn != bn) continue;
+    const int64_t tiles = m_tiles * ceil_div(cols, gated ? bn / 2 : bn) * problems;
+    if (tiles > kMostTiles) continue;
+    const double block = bn == kWideN ? kWideBlock : kNarrowBlock;
+    const bool can = can_cut(tiles, k_blocks, pl->pairs);
+    for (int cut = 0; cut <= (can ? 1 : 0); ++cut) {
+      if (pl->cut >= 0 && pl->cut != cut && can) continue;
+      const double time = cut ? (double)tiles * k_blocks / pl->pairs * block + (bn == kWideN ? kWideCut : kNarrowCut)
+                              : (double)ceil_div(tiles, pl->pairs) * k_blocks * block;
+      if (time < least) {
+        least = time;
+        best = {bn, cut != 0};
+      }
+    }
+  }
+  return best;
+}
+
+agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice choice, int64_t m_tiles, cudaStream_t stream) {
+  const int64_t n_tiles = ceil_div(p->cols, p->b_tile_step);
   if (m_tiles * n_tiles * p->problems > kMostTiles) return fail(AGMM_ERR_UNSUPPORTED, "more than 2^30 tiles of results");
   p->m_tiles = (int)m_tiles;
   p->n_tiles = (int)n_tiles;
   p->tiles_per_problem = p->m_tiles * p->n_tiles;
   p->num_tiles = p->tiles_per_problem * p->problems;
   p->group_m = kGroupM;
-  p->stages = kRowStages;
-  p->tmem_cols = 512;
-  make_schedule(p, pl->pairs, kMinRowBlocks);
-  const int clusters = p->dp_tiles == p->num_tiles ? std::min(p->num_tiles, pl->pairs) : pl->pairs;
-  const size_t smem = 1024 + (size_t)kRowStages * 2 * kTileBytes + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
-  return check_cuda(launch_gemm(rows_gemm(epi, pl->f16), *p, clusters, 2, smem, stream), "product launch");
+  const bool wide = choice.bn == kWideN;
+  p->stages = wide ? kWideStages : kNarrowStages;
+  p->tmem_cols = 2 * choice.bn;
+  make_schedule(p, pl->pairs, choice.cut);
+  const int clusters = std::min(pl->pairs, std::max(p->dp_tiles, p->sk_clusters));
+  const size_t smem = 1024 + (size_t)p->stages * (kTileBytes + choice.bn * kTileK) + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
+  return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16), *p, clusters, 2, smem, stream), "product launch");
 }
 
 agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t features, cudaStream_t stream) {
@@ -280,9 +316,18 @@ agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t fe
   p->stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - 1024 - kCtlBytes) / stage);
   p->tmem_cols = 32;
   while ((int)p->tmem_cols < 2 * accs * p->mma_n) p->tmem_cols *= 2;
-  make_schedule(p, pl->singles, kMinSwapBlocks);
-  const int clusters = p->dp_tiles == p->num_tiles ? std::min(p->num_tiles, pl->singles) : pl->singles;
-  return check_cuda(launch_gemm(swap_gemm(epi, pl->f16), *p, clusters, 1, 1024 + p->stages * stage + kCtlBytes, stream),
+  const int C = pl->singles, T = p->num_tiles;
+  bool cut = can_cut(T, p->k_blocks, C);
+  if (cut && pl->cut >= 0) {
+    cut = pl->cut != 0;
+  } else if (cut) {
+    const double bytes = (double)stage * p->k_blocks;
+    const auto wave = [&](int ctas) { return ctas ? bytes * std::max(kSwapByte, kMemoryByte * ctas) : 0.0; };
+    cut = wave(C) * T / C + kSwapCut < wave(C) * (T / C) + wave(T % C);
+  }
+  make_schedule(p, C, cut);
+  const int clusters = std::min(C, std::max(p->dp_tiles, p->sk_clusters));
+  return check_cuda(launch_gemm(select_gemm(0, epi, pl->f16), *p, clusters, 1, 1024 + p->stages * stage + kCtlBytes, stream),
                     "product launch");
 }
 
@@ -290,11 +335,14 @@ agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t fe
 agmm_status_t forward(const ProductPlan* pl, GemmParams* p, int epi, int shards, int64_t rows, const void* const* x, int64_t x_stride,
                       const void* const* w, int64_t w_stride, cudaStream_t stream) {
   const int weights = epi == kEpiGated ? 2 : 1;
-  const int swap = swap_box(shards, rows);
+  const int swap = pl->path == 0 ? 0 : swap_box(shards, rows);
   const int box = swap ? swap : row_box(shards, rows);
   chunk_rows(p, shards, rows, box);
   p->cols = pl->n;
   p->k_blocks = p->seg_blocks = (int)ceil_div(pl->k, kTileK);
+  const int64_t m_tiles = ceil_div((int64_t)p->chunks * box, 2 * kTileM);
+  const RowChoice choice = choose_rows(pl, m_tiles, pl->n, p->k_blocks, 1, epi == kEpiGated);
+  const int w_rows = swap ? kTileM : choice.bn / 2;  // rows of a weight in a tile
   OperandParams &xo = swap ? p->b : p->a, &wo = swap ? p->a : p->b;
   CUtensorMap *xm = swap ? p->b_map : p->a_map, *wm = swap ? p->a_map : p->b_map;
   xo.maps = shards;
@@ -303,29 +351,32 @@ agmm_status_t forward(const ProductPlan* pl, GemmParams* p, int epi, int shards,
   wo.maps = weights;
   for (int i = 0; i < weights; ++i) {
     const Matrix m = pl->transpose ? Matrix{"a weight", w[i], pl->k, pl->n, 1, w_stride} : Matrix{"a weight", w[i], pl->n, pl->k, 1, w_stride};
-    AGMM_TRY(encode_operand(&wm[i], &wo, m, !pl->transpose, kTileM, pl->f16));
+    AGMM_TRY(encode_operand(&wm[i], &wo, m, !pl->transpose, w_rows, pl->f16));
   }
   if (swap) return run_swap(pl, p, epi, pl->n, stream);
   if (epi == kEpiGated) {
     wo.by_rank = 1;
-    p->b_tile_step = kTileN / 2;
+    p->b_tile_step = choice.bn / 2;
   } else {
-    p->b_tile_step = kTileN;
-    p->b_half_step = kTileN / 2;
+    p->b_tile_step = choice.bn;
+    p->b_half_step = choice.bn / 2;
   }
-  return run_rows(pl, p, epi, ceil_div((int64_t)p->chunks * box, 2 * kTileM), ceil_div(pl->n, p->b_tile_step), stream);
+  return run_rows(pl, p, epi, choice, m_tiles, stream);
 }
 
 // dx = sum over the weights of d_i Wi^T
 agmm_status_t input_grad(const ProductPlan* pl, GemmParams* p, int weights, int64_t rows, const void* const* d, int64_t d_stride,
                          const void* const* w, int64_t w_stride, void* dx, int64_t dx_stride, cudaStream_t stream) {
-  const int swap = swap_box(1, rows);
+  const int swap = pl->path == 0 ? 0 : swap_box(1, rows);
   chunk_rows(p, 1, rows, swap ? swap : kTileM);
   p->out[0] = dx;
   p->ldo = dx_stride;
   p->cols = pl->k;
   p->seg_blocks = (int)ceil_div(pl->n, kTileK);
   p->k_blocks = weights * p->seg_blocks;
+  const int64_t m_tiles = ceil_div(rows, 2 * kTileM);
+  const RowChoice choice = choose_rows(pl, m_tiles, pl->k, p->k_blocks, 1, false);
+  const int w_rows = swap ? kTileM : choice.bn / 2;
   OperandParams &to = swap ? p->b : p->a, &wo = swap ? p->a : p->b;
   CUtensorMap *tm = swap ? p->b_map : p->a_map, *wm = swap ? p->a_map : p->b_map;
   to.maps = wo.maps = weights;
@@ -333,12 +384,12 @@ agmm_status_t input_grad(const ProductPlan* pl, GemmParams* p, int weights, int6
   for (int i = 0; i < weights; ++i) {
     AGMM_TRY(encode_operand(&tm[i], &to, {"a gradient", d[i], pl->n, rows, 1, d_stride}, false, p->box, pl->f16));
     const Matrix m = pl->transpose ? Matrix{"a weight", w[i], pl->k, pl->n, 1, w_stride} : Matrix{"a weight", w[i], pl->n, pl->k, 1, w_stride};
-    AGMM_TRY(encode_operand(&wm[i], &wo, m, pl->transpose, kTileM, pl->f16));
+    AGMM_TRY(encode_operand(&wm[i], &wo, m, pl->transpose, w_rows, pl->f16));
   }
   if (swap) return run_swap(pl, p, kEpiPlain, pl->k, stream);
-  p->b_tile_step = kTileN;
-  p->b_half_step = kTileN / 2;
-  return run_rows(pl, p, kEpiPlain, ceil_div(rows, 2 * kTileM), ceil_div(pl->k, kTileN), stream);
+  p->b_tile_step = choice.bn;
+  p->b_half_step = choice.bn / 2;
+  return run_rows(pl, p, kEpiPlain, choice, m_tiles, stream);
 }
 
 // dWi = X^T d_i, stored like the weight; the tokens of each shard are a segment of the sum.
@@ -355,6 +406,9 @@ agmm_status_t weight_grad(const ProductPlan* pl, GemmParams* p, int weights, int
   p->seg_blocks = (int)ceil_div(rows, kTileK);
   if ((int64_t)p->seg_blocks * shards > INT_MAX) return fail(AGMM_ERR_UNSUPPORTED, "too many rows");
   p->k_blocks = p->seg_blocks * shards;
+  const int64_t m_tiles = ceil_div(out_rows, 2 * kTileM);
+  const RowChoice choice = choose_rows(pl, m_tiles, out_cols, p->k_blocks, weights, false);
+  const int x_rows = pl->transpose ? choice.bn / 2 : kTileM, g_rows = pl->transpose ? kTileM : choice.bn / 2;
   OperandParams &xo = pl->transpose ? p->b : p->a, &go = pl->transpose ? p->a : p->b;
   CUtensorMap *xm = pl->transpose ? p->b_map : p->a_map, *gm = pl->transpose ? p->a_map : p->b_map;
   xo.maps = shards;
@@ -362,11 +416,11 @@ agmm_status_t weight_grad(const ProductPlan* pl, GemmParams* p, int weights, int
   xo.by_segment = 1;
   go.by_problem = 1;
   go.z_segment = 1;
-  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], &xo, {"x", x[s], pl->k, rows, 1, x_stride}, true, 0, pl->f16));
-  for (int i = 0; i < weights; ++i) AGMM_TRY(encode_operand(&gm[i], &go, {"a gradient", d[i], pl->n, rows, shards, d_stride}, true, 0, pl->f16));
-  p->b_tile_step = kTileN;
-  p->b_half_step = kTileN / 2;
-  return run_rows(pl, p, kEpiPlain, ceil_div(out_rows, 2 * kTileM), ceil_div(out_cols, kTileN), stream);
+  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], &xo, {"x", x[s], pl->k, rows, 1, x_stride}, true, x_rows, pl->f16));
+  for (int i = 0; i < weights; ++i) AGMM_TRY(encode_operand(&gm[i], &go, {"a gradient", d[i], pl->n, rows, shards, d_stride}, true, g_rows, pl->f16));
+  p->b_tile_step = choice.bn;
+  p->b_half_step = choice.bn / 2;
+  return run_rows(pl, p, kEpiPlain, choice, m_tiles, stream);
 }
 
 agmm_status_t zero_rows(const char* name, void* p, int64_t stride, int64_t rows, int64_t cols, bool f32, cudaStream_t stream) {
@@ -375,6 +429,14 @@ agmm_status_t zero_rows(const char* name, void* p, int64_t stride, int64_t rows,
 }
 
 // ---------------------------------------------------------------------- plans
+// An environment override for tests and experiments, as agmm_plan reads them; -1: none in [lo, hi].
+int env_int(const char* name, int lo, int hi) {
+  const char* v = std::getenv(name);
+  if (!v || !*v) return -1;
+  const int i = std::atoi(v);
+  return i >= lo && i <= hi ? i : -1;
+}
+
 agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int transpose, int dtype) {
   pl->k = k;
   pl->n = n;
@@ -388,14 +450,19 @@ agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int tran
   const char* drop = std::getenv("AGMM_TEST_DROP_ARRIVE");
   pl->test_drop = drop && std::atoi(drop) != 0;
   if (pl->sms > kMostSms) return fail(AGMM_ERR_UNSUPPORTED, "more than %d SMs", kMostSms);
+  pl->path = env_int("AGMM_PATH", 0, 1);
+  pl->bn = env_int("AGMM_BN", kNarrowN, kWideN);
+  if (pl->bn != kNarrowN && pl->bn != kWideN) pl->bn = -1;
+  pl->cut = env_int("AGMM_STREAMK", 0, 1);
   pl->singles = pl->sms;
   pl->pairs = pl->sms / 2;
   for (int epi = kEpiPlain; epi <= kEpiLinear; ++epi) {
-    int pairs = 0, singles = 0;
-    AGMM_TRY(check_cuda(prepare_gemm(rows_gemm(epi, pl->f16), 2, &pairs), "kernel attributes"));
-    AGMM_TRY(check_cuda(prepare_gemm(swap_gemm(epi, pl->f16), 1, &singles), "kernel attributes"));
-    pl->pairs = std::min(pl->pairs, pairs);
-    pl->singles = std::min(pl->singles, singles);
+    for (int bn : {0, kNarrowN, kWideN}) {
+      int clusters = 0;
+      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(bn, epi, pl->f16), bn ? 2 : 1, &clusters), "kernel attributes"));
+      int& fit = bn ? pl->pairs : pl->singles;
+      fit = std::min(fit, clusters);
+    }
   }
   if (pl->pairs < 1 || pl->singles < 1) return fail(AGMM_ERR_UNSUPPORTED, "the kernels do not fit this device");
   return AGMM_OK;

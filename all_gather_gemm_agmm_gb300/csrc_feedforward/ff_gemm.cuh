@@ -12,11 +12,11 @@
 // of the weights sum over tokens): that is a matter of the tensor maps' boxes and two
 // bits of the MMA's descriptor, chosen at run time.
 //
-//   row tiles      a CTA pair multiplies 256 rows by 256 columns (cta_group::2), each
-//                  CTA holding its own rows and half of the columns' operand.  Gated:
-//                  the leader's half is 128 columns of the gate's weight, the
-//                  follower's the same columns of the other, so both products of an
-//                  output value land in one thread.
+//   row tiles      a CTA pair multiplies 256 rows by 256 columns (cta_group::2), or by
+//                  128 where that makes better use of the CTAs, each CTA holding its
+//                  own rows and half of the columns' operand.  Gated: the leader's half
+//                  is columns of the gate's weight, the follower's the same columns of
+//                  the other, so both products of an output value land in one thread.
 //                  Bound: the tensor cores.
 //   swapped tiles  for up to 128 tokens: 128 columns of the weights are the MMA's rows
 //                  and all tokens its columns, so that each thread of the epilogue has
@@ -197,43 +197,51 @@ __device__ __forceinline__ bool complete_tile(const GemmParams& p, int* counter,
   return last != 0;
 }
 
-// kCount values of this lane from column `col` on (of this warp's kWarpCols columns, in the order in
-// which they are stored), summed over the parts.
-template <int kCount>
-__device__ __forceinline__ void sum_parts(const GemmParams& p, const Parts& parts, int ctas, int rank, int ewarp, int col,
-                                          int lane, uint32_t (&v)[kCount]) {
+// kCount values of this lane from column `col` on (of its warp's columns, in the order in which
+// they are stored), of kArrays arrays `stride` columns apart, summed over the parts; the loads of
+// kDepth parts are in flight together.
+template <int kArrays, int kCount, int kDepth>
+__device__ __forceinline__ void sum_parts(const GemmParams& p, const Parts& parts, int ctas, int rank, int ewarp, int col, int stride,
+                                          int lane, uint32_t (&v)[kArrays][kCount]) {
   constexpr int kQuads = kCount / 4;
-  constexpr int kDepth = kQuads >= 8 ? 1 : 8;  // parts whose loads are in flight together
-  float sum[kCount];
+  float4 sum[kArrays][kQuads];
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) sum[i] = 0.0f;
+  for (int t = 0; t < kArrays; ++t)
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) sum[t][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
   for (int c0 = parts.first; c0 <= parts.last; c0 += kDepth) {
-    float4 x[kDepth][kQuads];
+    float4 x[kDepth][kArrays][kQuads];
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      if (c0 + d <= parts.last) {
-        const float4* const src = part_slot(p, c0 + d, ctas, rank, c0 + d == parts.first ? parts.first_slot : 0, ewarp) + (size_t)(col / 4) * 32 + lane;
+      const float4* const src = part_slot(p, c0 + d, ctas, rank, c0 + d == parts.first ? parts.first_slot : 0, ewarp) + lane;
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) x[d][i] = __ldcg(src + i * 32);
-      } else {
+      for (int t = 0; t < kArrays; ++t)
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) x[d][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
+        for (int i = 0; i < kQuads; ++i)
+          x[d][t][i] = c0 + d <= parts.last ? __ldcg(src + ((col + t * stride) / 4 + i) * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
+    for (int d = 0; d < kDepth; ++d)
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        sum[4 * i] += x[d][i].x;
-        sum[4 * i + 1] += x[d][i].y;
-        sum[4 * i + 2] += x[d][i].z;
-        sum[4 * i + 3] += x[d][i].w;
-      }
-    }
+      for (int t = 0; t < kArrays; ++t)
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          sum[t][i].x += x[d][t][i].x;
+          sum[t][i].y += x[d][t][i].y;
+          sum[t][i].z += x[d][t][i].z;
+          sum[t][i].w += x[d][t][i].w;
+        }
   }
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) v[i] = __float_as_uint(sum[i]);
+  for (int t = 0; t < kArrays; ++t)
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      v[t][4 * i] = __float_as_uint(sum[t][i].x);
+      v[t][4 * i + 1] = __float_as_uint(sum[t][i].y);
+      v[t][4 * i + 2] = __float_as_uint(sum[t][i].z);
+      v[t][4 * i + 3] = __float_as_uint(sum[t][i].w);
+    }
 }
 
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -258,8 +266,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint3
 }
 
 // How an operand's tile is copied: rows of 64 values of k each in one box, or (chunks) by the
-// other lanes; or MN-major, 128 values of 64 rows of k as two blocks of 64 x 64, in one box
-// where the map has the blocks as a dimension.
+// other lanes; or MN-major, 128 (or 64) values of 64 rows of k as blocks of 64 x 64, in one
+// box where the map has the blocks as a dimension.
 enum LayoutKind : int { kLayoutRows = 0, kLayoutChunks = 1, kLayoutBlocks = 2, kLayoutTwoBoxes = 3 };
 template <int kLayout>
 using Layout = std::integral_constant<int, kLayout>;
@@ -272,7 +280,7 @@ __device__ __forceinline__ void load_rows_of(uint32_t dst, const CUtensorMap* ma
     ptx::tma_load_2d(dst, map, bar, k, row);
 }
 
-template <bool kPair, int kLayout>
+template <bool kPair, int kLayout, int kRows>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row, int z) {
   if constexpr (kLayout == kLayoutRows) {
     load_rows_of<kPair>(dst, map, bar, k, row);
@@ -280,7 +288,7 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
     tma_load_4d<kPair>(dst, map, bar, 0, k, row >> 6, z);
   } else if constexpr (kLayout == kLayoutTwoBoxes) {
     tma_load_4d<kPair>(dst, map, bar, row, k, 0, z);
-    tma_load_4d<kPair>(dst + 8192u, map, bar, row + 64, k, 0, z);
+    if constexpr (kRows > 64) tma_load_4d<kPair>(dst + 8192u, map, bar, row + 64, k, 0, z);
   }
 }
 
@@ -313,15 +321,16 @@ __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
   return reinterpret_cast<uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
-// Writes a staged 32 x 128-byte block: row r of it to row out_row (of lane r; < 0: none) of
-// `out`, 8 lanes to a row.
+// Writes a staged block of 32 rows of kPieces 16-byte pieces: row r of it to row out_row (of lane
+// r; < 0: none) of `out`, kPieces lanes to a row.
+template <int kPieces>
 __device__ __forceinline__ void write_staged(uint8_t* stage, void* out, int64_t row_bytes, int64_t col_bytes, int64_t end_bytes,
                                              int64_t out_row, int lane) {
   __syncwarp();
-  const int piece = lane & 7;
+  const int piece = lane % kPieces;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3);
+  for (int i = 0; i < kPieces; ++i) {
+    const int row = (32 / kPieces) * i + lane / kPieces;
     const int64_t at = __shfl_sync(0xffffffffu, out_row, row);
     const uint4 v = *staged(stage, row, piece);
     if (at >= 0 && col_bytes + 16 * piece < end_bytes)
@@ -356,9 +365,39 @@ __device__ __forceinline__ void stage_half(uint8_t* stage, int lane, int half, c
   for (int i = 0; i < 4; ++i) *staged(stage, lane, half * 4 + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-template <bool kSwap, int kEpi, bool kF16>
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+
+// Swapped tiles: the weights of the first `blocks` k blocks of a segment.
+template <int kAccs>
+__device__ __forceinline__ void prefetch_weights(const GemmParams& p, const Segment& sg, int row, int blocks) {
+  const int end = min(sg.kb1, sg.kb0 + blocks);
+  for (int kb = sg.kb0; kb < end; ++kb) {
+    const int seg = kb / p.seg_blocks, ko = (kb - seg * p.seg_blocks) * kTileK;
+    for (int t = 0; t < kAccs; ++t) {
+      const CUtensorMap* const map = p.a_map + seg * p.a.by_segment + t;
+      if (!p.a.mn_major) {
+        prefetch_2d(map, ko, row);
+      } else if (p.a.blocked) {
+        prefetch_4d(map, 0, ko, row >> 6, 0);
+      } else {
+        prefetch_4d(map, row, ko, 0, 0);
+        prefetch_4d(map, row + 64, ko, 0, 0);
+      }
+    }
+  }
+}
+
+// kBN: columns of a row tile (0: swapped tiles).
+template <int kBN, int kEpi, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constant__ GemmParams p) {
-  constexpr bool kPair = !kSwap;
+  constexpr bool kSwap = kBN == 0, kPair = !kSwap;
+  constexpr int kHalf = kBN / 2;  // columns of the accumulator that a warp of the epilogue has
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kAccs = kSwap && kEpi == kEpiGated ? 2 : 1;  // swapped tiles: products of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -367,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
   uint8_t* const base_ptr = smem_raw + (base - raw);
   const int S = p.stages;
   constexpr uint32_t a_slot = (uint32_t)kAccs * kTileBytes;
-  const uint32_t b_slot = kSwap ? (uint32_t)p.mma_n * 128u : (uint32_t)kTileBytes;
+  const uint32_t b_slot = (uint32_t)(kSwap ? p.mma_n : kHalf) * 128u;
   const uint32_t a0 = base, b0 = base + (uint32_t)S * a_slot;
   const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results
   const uint32_t ctl = out0 + (kSwap ? 0u : (uint32_t)(kEpiWarps * kStageOutBytes));
@@ -425,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
   }
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  ptx::griddep_wait();  // no access to global memory before this
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -440,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     iter.init(p, cluster, clusters);
     Segment sg;
     const int per_tile = kSwap ? p.chunks : kTileM / p.box;  // chunks of the tokens: at most 16
-    const uint32_t bytes = a_slot + (kSwap ? (uint32_t)(p.chunks * p.box) * 128u : (uint32_t)kTileBytes);
+    const uint32_t bytes = a_slot + (uint32_t)(kSwap ? p.chunks * p.box : kHalf) * 128u;
     const uint32_t full0 = kPair ? ptx::map_shared_rank(bar_full(ctl, 0), 0) : bar_full(ctl, 0);
     // The loads of k blocks [kb0, kb1) of one segment, from value ko of it on.
     auto produce = [&](auto a_layout, auto b_layout, int kb0, int kb1, int ko, const CUtensorMap* a_map, int a_row, int a_z,
@@ -482,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           if (leader) {
 #pragma unroll
             for (int t = 0; t < kAccs; ++t)
-              load_operand<kPair, kA>(a_dst + (uint32_t)t * kTileBytes, a_map + t, full, ko, a_row, a_z);
-            load_operand<kPair, kB>(b_dst, b_map, full, ko, b_row, b_z);
+              load_operand<kPair, kA, kTileM>(a_dst + (uint32_t)t * kTileBytes, a_map + t, full, ko, a_row, a_z);
+            load_operand<kPair, kB, kHalf>(b_dst, b_map, full, ko, b_row, b_z);
           }
           if constexpr (kChunks) __syncwarp();
         }
@@ -492,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         phase = next_phase;
       }
     };
+    bool begun = false;
     while (ok && iter.next(p, sg)) {
       const int row_tile = kPair ? sg.mt * 2 + rank : sg.mt;
       // Chunks of the tokens in a stage.  One to a stage is the elected lane's, with operands
@@ -505,6 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       const int b_row = kSwap ? row0 : sg.nt * p.b_tile_step + rank * p.b_half_step;
       const int a_row = kSwap || p.a.mn_major ? row_tile * kTileM : row0;
       int seg = sg.kb0 / p.seg_blocks;
+      if (!begun) {
+        // The first stages' weights, into L2 while the kernel before this one ends: only a hint,
+        // so it does not matter whether that one writes them.
+        if (kSwap && leader) prefetch_weights<kAccs>(p, sg, row_tile * kTileM, S);
+        ptx::griddep_wait();  // no access to global memory before this, in any role
+        begun = true;
+      }
       for (int kb = sg.kb0; ok && kb < sg.kb1; ++seg) {
         const int end = min(sg.kb1, (seg + 1) * p.seg_blocks);
         const int ko = (kb - seg * p.seg_blocks) * kTileK, a_z = seg * p.a.z_segment, b_z = seg * p.b.z_segment;
@@ -542,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     // -------------------------------------------------------------- MMA issuer
     if (rank == 0) {
       const bool issuer = ptx::elect_one();
-      const int n = kSwap ? p.mma_n : kTileN;
+      const int n = kSwap ? p.mma_n : kBN;
       const uint32_t idesc = ptx::idesc_f16kind_f32(kPair ? 2 * kTileM : kTileM, n, p.a.mn_major != 0, p.b.mn_major != 0, kF16);
       // a k step of 16 values: 32 bytes inside the swizzle row, or 16 rows of 128 bytes
       const uint64_t a_step = p.a.mn_major ? 2048u / 16u : 32u / 16u, b_step = p.b.mn_major ? 2048u / 16u : 32u / 16u;
@@ -626,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     iter.init(p, cluster, clusters);
     const int first_cut = p.dp_tiles + iter.u / p.k_blocks;  // the tile whose part lies in slot 0
     Segment sg;
+    ptx::griddep_wait();
     for (int it = 0; iter.next(p, sg); ++it) {
       const int acc = it & 1;
       int res = kWaitOk;
@@ -680,32 +727,40 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         float bias = 0.0f;
         if constexpr (kEpi == kEpiLinear)
           if (p.bias && there) bias = unpack1<kF16>(static_cast<const uint16_t*>(p.bias)[f]);
+        constexpr int kGroup = kAccs == 1 ? 16 : 8;  // tokens at a time
 #pragma unroll 1
-        for (int c = 0; c < live; c += 8) {
-          uint32_t v[kAccs][8];
-          uint16_t res16[8];
+        for (int c = 0; c < live; c += kGroup) {
+          uint32_t v[kAccs][kGroup];
+          uint16_t res16[kGroup];
           if constexpr (kEpi == kEpiLinear) {
             if (p.residual) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int row = row_table[c0 + c + i];
+              for (int i = 0; i < kGroup; ++i) {
+                const int row = c + i < live ? row_table[c0 + c + i] : -1;
                 res16[i] = row >= 0 && there ? static_cast<const uint16_t*>(p.residual)[row * p.ldr + f] : (uint16_t)0;
               }
             }
           }
           if (sg.whole) {
 #pragma unroll
-            for (int t = 0; t < kAccs; ++t) tmem_ld_x8(t0 + (uint32_t)(t * n + c), v[t]);
-            ptx::tmem_ld_wait();
-          } else {
+            for (int t = 0; t < kAccs; ++t) {
 #pragma unroll
-            for (int t = 0; t < kAccs; ++t)
-              sum_parts<8>(p, parts, kCtas, rank, ewarp, t * (n / 2) + c, lane, v[t]);
+              for (int g = 0; g < kGroup; g += 8) {
+                uint32_t x[8];
+                // (a half of 8 columns has no second group)
+                if (c + g < n / 2) tmem_ld_x8(t0 + (uint32_t)(t * n + c + g), x);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[t][g + i] = x[i];
+              }
+            }
+          } else {
+            sum_parts<kAccs, kGroup, 4>(p, parts, kCtas, rank, ewarp, c, n / 2, lane, v);
           }
           with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = row_table[c0 + c + i];
+            for (int i = 0; i < kGroup; ++i) {
+              const int row = c + i < live ? row_table[c0 + c + i] : -1;
               if (row < 0 || !there) continue;
               float x = __uint_as_float(v[0][i]);
               if constexpr (kEpi == kEpiGated) {
@@ -735,18 +790,17 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         const int chunk = trow / p.box, shard = chunk / p.shard_chunks;
         const int in_shard = trow - shard * p.shard_chunks * p.box;
         const int64_t out_row = shard < p.shards && in_shard < p.shard_rows ? shard * p.shard_rows + in_shard : -1;
-        const uint32_t t0 = lane_base + (uint32_t)(acc * kTileN);
-        // gated: 64 columns of each product (the second's 128 columns on); else 128 columns
-        constexpr int kOtherAcc = 128;
-        const int first_col = kEpi == kEpiGated ? half * 64 : half * 128;
+        const uint32_t t0 = lane_base + (uint32_t)(acc * kBN);
+        // gated: as many columns of each product, the second's a half of the accumulator on
+        const int first_col = kEpi == kEpiGated ? half * (kHalf / 2) : half * kHalf;
         Parts parts = {0, 0, 0};
         if (!sg.whole) {
           float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile == first_cut ? 0 : 1, ewarp);
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < kHalf; c += 32) {
             uint32_t v[32];
             // gated: this warp's columns of the first product, then of the second
-            const int col = kEpi == kEpiGated ? (c < 64 ? first_col + c : kOtherAcc + first_col + c - 64) : first_col + c;
+            const int col = kEpi == kEpiGated && c >= kHalf / 2 ? kHalf + first_col + c - kHalf / 2 : first_col + c;
             ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)col, v);
             ptx::tmem_ld_wait();
             store_part<32>(slot, c, lane, v);
@@ -756,70 +810,70 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           parts = find_parts(p, sg.tile);
         }
         if constexpr (kEpi == kEpiGated) {
-          const int64_t col = (int64_t)sg.nt * 128 + first_col;
-          uint32_t g16[2][16], u16[2][16], o16[2][16];
+          constexpr int kBlocks = kHalf / 64;  // of 32 columns of results
+          const int64_t col = (int64_t)sg.nt * kHalf + first_col;
+          uint32_t g16[kBlocks][16], u16[kBlocks][16], o16[kBlocks][16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t g[32], u[32];
+          for (int h = 0; h < kBlocks; ++h) {
+            uint32_t v[2][32];
             if (sg.whole) {
-              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + 32 * h), g);
-              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(kOtherAcc + first_col + 32 * h), u);
+              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + 32 * h), v[0]);
+              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(kHalf + first_col + 32 * h), v[1]);
               ptx::tmem_ld_wait();
-              if (h == 1) release();
+              if (h == kBlocks - 1) release();
             } else {
-              sum_parts<32>(p, parts, kCtas, rank, ewarp, 32 * h, lane, g);
-              sum_parts<32>(p, parts, kCtas, rank, ewarp, 64 + 32 * h, lane, u);
+              sum_parts<2, 32, 1>(p, parts, kCtas, rank, ewarp, 32 * h, kHalf / 2, lane, v);
             }
             if (p.saved[0]) {
-              pack32<kF16>(g, g16[h]);
-              pack32<kF16>(u, u16[h]);
+              pack32<kF16>(v[0], g16[h]);
+              pack32<kF16>(v[1], u16[h]);
             }
             with_activation(p.act, [&](auto act) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                g[i] = __float_as_uint(activate<act.value>(__uint_as_float(g[i])) * __uint_as_float(u[i]));
+                v[0][i] = __float_as_uint(activate<act.value>(__uint_as_float(v[0][i])) * __uint_as_float(v[1][i]));
             });
-            pack32<kF16>(g, o16[h]);
+            pack32<kF16>(v[0], o16[h]);
           }
-          stage_half(stage_out, lane, 0, o16[0]);
-          stage_half(stage_out, lane, 1, o16[1]);
-          write_staged(stage_out, p.out[0], p.ldo * 2, col * 2, p.cols * 2, out_row, lane);
+          auto write = [&](uint32_t (&w)[kBlocks][16], void* out, int64_t ld) {
+#pragma unroll
+            for (int h = 0; h < kBlocks; ++h) stage_half(stage_out, lane, h, w[h]);
+            write_staged<4 * kBlocks>(stage_out, out, ld * 2, col * 2, p.cols * 2, out_row, lane);
+          };
+          write(o16, p.out[0], p.ldo);
           if (p.saved[0]) {
-            stage_half(stage_out, lane, 0, g16[0]);
-            stage_half(stage_out, lane, 1, g16[1]);
-            write_staged(stage_out, p.saved[0], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
-            stage_half(stage_out, lane, 0, u16[0]);
-            stage_half(stage_out, lane, 1, u16[1]);
-            write_staged(stage_out, p.saved[1], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
+            write(g16, p.saved[0], p.lds);
+            write(u16, p.saved[1], p.lds);
           }
         } else {
-          const int64_t tile_col = (int64_t)sg.nt * kTileN + first_col;
+          const int64_t tile_col = (int64_t)sg.nt * kBN + first_col;
           if (kEpi == kEpiPlain && p.out_f32) {
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t v[32];
+            for (int c = 0; c < kHalf; c += 32) {
+              uint32_t v[1][32];
               if (sg.whole) {
-                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), v);
+                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), v[0]);
                 ptx::tmem_ld_wait();
-                if (c == 96) release();
+                if (c + 32 == kHalf) release();
               } else {
-                sum_parts<32>(p, parts, kCtas, rank, ewarp, c, lane, v);
+                sum_parts<1, 32, 2>(p, parts, kCtas, rank, ewarp, c, 0, lane, v);
               }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) *staged(stage_out, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-              write_staged(stage_out, p.out[sg.problem], p.ldo * 4, (tile_col + c) * 4, p.cols * 4, out_row, lane);
+              for (int i = 0; i < 8; ++i)
+                *staged(stage_out, lane, i) = make_uint4(v[0][4 * i], v[0][4 * i + 1], v[0][4 * i + 2], v[0][4 * i + 3]);
+              write_staged<8>(stage_out, p.out[sg.problem], p.ldo * 4, (tile_col + c) * 4, p.cols * 4, out_row, lane);
             }
           } else {
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 64) {
+            for (int c = 0; c < kHalf; c += 64) {
               const int64_t col = tile_col + c;
               uint32_t z16[2][16], o16[2][16];
-              uint4 res16[8];
               bool has_residual = false, has_saved = false;
               if constexpr (kEpi == kEpiLinear) {
                 has_residual = p.residual != nullptr;
                 has_saved = p.saved[0] != nullptr;
                 if (has_residual) {
+                  uint4 res16[8];
                   load_rows(res16, p.residual, p.ldr * 2, col * 2, p.cols * 2, out_row, lane);
 #pragma unroll
                   for (int i = 0; i < 8; ++i) *staged(stage_out, 4 * i + (lane >> 3), lane & 7) = res16[i];
@@ -828,13 +882,14 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                uint32_t v[32];
+                uint32_t w[1][32];
+                uint32_t(&v)[32] = w[0];
                 if (sg.whole) {
                   ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c + 32 * h), v);
                   ptx::tmem_ld_wait();
-                  if (c == 64 && h == 1) release();
+                  if (c + 64 == kHalf && h == 1) release();
                 } else {
-                  sum_parts<32>(p, parts, kCtas, rank, ewarp, c + 32 * h, lane, v);
+                  sum_parts<1, 32, 1>(p, parts, kCtas, rank, ewarp, c + 32 * h, 0, lane, w);
                 }
                 if constexpr (kEpi == kEpiLinear) {
                   if (p.bias) {
@@ -867,11 +922,11 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               }
               stage_half(stage_out, lane, 0, o16[0]);
               stage_half(stage_out, lane, 1, o16[1]);
-              write_staged(stage_out, p.out[sg.problem], p.ldo * 2, col * 2, p.cols * 2, out_row, lane);
+              write_staged<8>(stage_out, p.out[sg.problem], p.ldo * 2, col * 2, p.cols * 2, out_row, lane);
               if (has_saved) {
                 stage_half(stage_out, lane, 0, z16[0]);
                 stage_half(stage_out, lane, 1, z16[1]);
-                write_staged(stage_out, p.saved[0], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
+                write_staged<8>(stage_out, p.saved[0], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
               }
             }
           }

@@ -4,8 +4,11 @@
 namespace agmm {
 namespace ff {
 
-GemmFn rows_gemm(int epi, bool f16) { return epi == kEpiGated ? rows_gated(f16) : epi == kEpiLinear ? rows_linear(f16) : rows_plain(f16); }
-GemmFn swap_gemm(int epi, bool f16) { return epi == kEpiGated ? swap_gated(f16) : epi == kEpiLinear ? swap_linear(f16) : swap_plain(f16); }
+GemmFn select_gemm(int bn, int epi, bool f16) {
+  if (bn == kWideN) return epi == kEpiGated ? wide_gated(f16) : epi == kEpiLinear ? wide_linear(f16) : wide_plain(f16);
+  if (bn == kNarrowN) return epi == kEpiGated ? narrow_gated(f16) : epi == kEpiLinear ? narrow_linear(f16) : narrow_plain(f16);
+  return epi == kEpiGated ? swap_gated(f16) : epi == kEpiLinear ? swap_linear(f16) : swap_plain(f16);
+}
 
 cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);

@@ -1,0 +1,8 @@
+// ff_narrow_gated.cu -- instantiations of the feed-forward products' kernel.
+#include "ff_gemm.cuh"
+
+namespace agmm {
+namespace ff {
+GemmFn narrow_gated(bool f16) { return f16 ? &agmm_ff_gemm<kNarrowN, kEpiGated, true> : &agmm_ff_gemm<kNarrowN, kEpiGated, false>; }
+}  // namespace ff
+}  // namespace agmm

@@ -13,17 +13,17 @@ constexpr int kMaxShards = 8;
 constexpr int kThreads = 320;     // warp 0: TMA producer, warp 1: MMA issuer, warps 2-9: epilogue
 constexpr int kEpiWarps = 8;
 constexpr int kTileM = 128;       // rows of the A operand of one CTA = TMEM lanes
-constexpr int kTileN = 256;       // row tiles: columns of a CTA pair's tile
+constexpr int kWideN = 256, kNarrowN = 128;  // row tiles: columns of a CTA pair's tile
 constexpr int kTileK = 64;        // one 128-byte swizzle row of 16-bit values
 constexpr int kTileBytes = kTileM * kTileK * 2;  // 16 KiB
 constexpr int kMaxStages = 12;
-constexpr int kRowStages = 6;     // 6 x 32 KiB of operands beside 32 KiB of staged results
+constexpr int kWideStages = 6, kNarrowStages = 8;  // 192 KiB of operands beside 32 KiB of staged results
 constexpr int kMaxSwapRows = 128; // swapped tiles: token columns of a tile
 constexpr int kStageOutBytes = 4096;  // row tiles: one warp's staged 32 rows x 128 bytes
 constexpr int kCtlBytes = 1024;
 constexpr size_t kMaxSmem = 232448;   // 227 KiB
 constexpr int kStatusBytes = 256;     // status words at the start of the workspace
-constexpr size_t kSlotBytes = (size_t)kTileM * kTileN * sizeof(float);  // one CTA's float32 partial results
+constexpr size_t kSlotBytes = (size_t)kTileM * kWideN * sizeof(float);  // one CTA's float32 partial results
 constexpr int kSlots = 2;             // of each CTA: the first and the last tile of its share
 
 enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
@@ -45,7 +45,7 @@ struct __align__(128) GemmParams {
   CUtensorMap a_map[kMaxShards];
   CUtensorMap b_map[kMaxShards];
   OperandParams a, b;
-  // Row tiles: pair tiles of 256 x 256 (gated: 256 x 128 of each product).
+  // Row tiles: pair tiles of 256 x 256 or 128 (gated: half of them columns of each product).
   // Swapped tiles: 128 columns of the weights, all tokens.
   int problems;            // products that share one launch (gradients of two weights)
   int tiles_per_problem, m_tiles, n_tiles, num_tiles, group_m;
@@ -85,12 +85,14 @@ struct __align__(128) GemmParams {
 };
 
 using GemmFn = void (*)(GemmParams);
-// swapped tiles, result, fp16
-GemmFn rows_gemm(int epi, bool f16);
-GemmFn swap_gemm(int epi, bool f16);
-GemmFn rows_plain(bool f16);
-GemmFn rows_gated(bool f16);
-GemmFn rows_linear(bool f16);
+// bn: columns of row tiles (0: swapped tiles)
+GemmFn select_gemm(int bn, int epi, bool f16);
+GemmFn wide_plain(bool f16);
+GemmFn wide_gated(bool f16);
+GemmFn wide_linear(bool f16);
+GemmFn narrow_plain(bool f16);
+GemmFn narrow_gated(bool f16);
+GemmFn narrow_linear(bool f16);
 GemmFn swap_plain(bool f16);
 GemmFn swap_gated(bool f16);
 GemmFn swap_linear(bool f16);

@@ -3,8 +3,6 @@
 
 namespace agmm {
 namespace ff {
-GemmFn swap_gated(bool f16) {
-  return f16 ? &agmm_ff_gemm<true, kEpiGated, true> : &agmm_ff_gemm<true, kEpiGated, false>;
-}
+GemmFn swap_gated(bool f16) { return f16 ? &agmm_ff_gemm<0, kEpiGated, true> : &agmm_ff_gemm<0, kEpiGated, false>; }
 }  // namespace ff
 }  // namespace agmm

@@ -3,8 +3,6 @@
 
 namespace agmm {
 namespace ff {
-GemmFn swap_linear(bool f16) {
-  return f16 ? &agmm_ff_gemm<true, kEpiLinear, true> : &agmm_ff_gemm<true, kEpiLinear, false>;
-}
+GemmFn swap_linear(bool f16) { return f16 ? &agmm_ff_gemm<0, kEpiLinear, true> : &agmm_ff_gemm<0, kEpiLinear, false>; }
 }  // namespace ff
 }  // namespace agmm

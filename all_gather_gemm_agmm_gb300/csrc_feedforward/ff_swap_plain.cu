@@ -3,8 +3,6 @@
 
 namespace agmm {
 namespace ff {
-GemmFn swap_plain(bool f16) {
-  return f16 ? &agmm_ff_gemm<true, kEpiPlain, true> : &agmm_ff_gemm<true, kEpiPlain, false>;
-}
+GemmFn swap_plain(bool f16) { return f16 ? &agmm_ff_gemm<0, kEpiPlain, true> : &agmm_ff_gemm<0, kEpiPlain, false>; }
 }  // namespace ff
 }  // namespace agmm
