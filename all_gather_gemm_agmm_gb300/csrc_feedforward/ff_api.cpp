@@ -50,6 +50,7 @@ constexpr int kGroupM = 8;
 constexpr int64_t kMostRows = INT_MAX - 1024;  // coordinates of tiles behind the last row fit 32 bits
 constexpr int64_t kMostTiles = 1 << 30;
 constexpr int64_t kMostWidth = 1 << 20;
+constexpr int64_t kMostStride = 1 << 29;  // the bytes of a row fit 32 bits
 
 agmm_status_t fail(agmm_status_t s, const char* fmt, ...) {
   char text[256];
@@ -115,9 +116,9 @@ agmm_status_t check_matrix(const char* name, const void* p, int64_t* stride, int
     *stride = cols;
     return AGMM_OK;
   }
-  if (*stride < cols || *stride >= (int64_t)1 << 36)
-    return fail(AGMM_ERR_INVALID_ARG, "%s: the row stride (%lld) must be at least the row's %lld values", name, (long long)*stride,
-                (long long)cols);
+  if (*stride < cols || *stride > kMostStride)
+    return fail(AGMM_ERR_INVALID_ARG, "%s: the row stride (%lld) must be at least the row's %lld values, and at most 2^29", name,
+                (long long)*stride, (long long)cols);
   if (*stride % 8) return fail(AGMM_ERR_ALIGNMENT, "%s: the row stride (%lld) must be a multiple of 8", name, (long long)*stride);
   return AGMM_OK;
 }
@@ -191,11 +192,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The time that a schedule takes, in cycles, as far as it differs from others: clusters that each
 // work through `blocks` k blocks.  Constants as measured (the design doc has the table).
-constexpr double kWideBlock = 512, kNarrowBlock = 280;  // a k block of a row tile's main loop
-constexpr double kWideCut = 14000, kNarrowCut = 9000;   // the parts' round trip through L2
-constexpr double kSwapCut = 7600;
-constexpr double kSwapByte = 0.0141;                    // swapped tiles: a byte, at what one CTA keeps in flight
-constexpr double kMemoryByte = 2.84e-4;                 // ... and for each CTA that shares the device's memory
+constexpr double kWideBlock = 512, kNarrowBlock = 340;    // a k block of a row tile's main loop
+constexpr double kWideTile = 4000, kNarrowTile = 2500;    // its results, beside the next tile's main loop
+constexpr double kWideCut = 26000, kNarrowCut = 9000;     // the parts' round trip through L2
+constexpr double kSwapCut = 6500;
+constexpr double kSwapByte = 0.019;                       // swapped tiles: a byte, for one CTA alone
+constexpr double kMemoryByte = 2.84e-4;                   // ... and for each CTA that shares the device's memory
 
 // Whole tiles go round the clusters; or those of a ragged last wave, with the wave before it, are
 // cut along k evenly over the clusters.
@@ -273,12 +275,12 @@ RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int 
     if (pl->bn >= 0 && pl->bn != bn) continue;
     const int64_t tiles = m_tiles * ceil_div(cols, gated ? bn / 2 : bn) * problems;
     if (tiles > kMostTiles) continue;
-    const double block = bn == kWideN ? kWideBlock : kNarrowBlock;
+    const double block = bn == kWideN ? kWideBlock : kNarrowBlock, tile = bn == kWideN ? kWideTile : kNarrowTile;
     const bool can = can_cut(tiles, k_blocks, pl->pairs);
     for (int cut = 0; cut <= (can ? 1 : 0); ++cut) {
       if (pl->cut >= 0 && pl->cut != cut && can) continue;
       const double time = cut ? (double)tiles * k_blocks / pl->pairs * block + (bn == kWideN ? kWideCut : kNarrowCut)
-                              : (double)ceil_div(tiles, pl->pairs) * k_blocks * block;
+                              : (double)ceil_div(tiles, pl->pairs) * std::max(k_blocks * block, tile);
       if (time < least) {
         least = time;
         best = {bn, cut != 0};

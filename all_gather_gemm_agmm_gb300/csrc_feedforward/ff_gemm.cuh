@@ -18,7 +18,7 @@
 //                  is columns of the gate's weight, the follower's the same columns of
 //                  the other, so both products of an output value land in one thread.
 //                  Bound: the tensor cores.
-//   swapped tiles  for up to 128 tokens: 128 columns of the weights are the MMA's rows
+//   swapped tiles  for up to 64 tokens: 128 columns of the weights are the MMA's rows
 //                  and all tokens its columns, so that each thread of the epilogue has
 //                  one column of the weights and only the tokens that there are.
 //                  Bound: the weights' bytes.
@@ -55,8 +55,8 @@ __device__ __forceinline__ uint32_t bar_acc_empty(uint32_t ctl, int a) { return 
 __device__ __forceinline__ uint32_t bar_drain(uint32_t ctl) { return ctl + 8u * (2 * kMaxStages + 4); }
 constexpr int kAbortOffset = 8 * (2 * kMaxStages + 6);
 constexpr int kTmemOffset = kAbortOffset + 8;
-constexpr int kTableOffset = 256;  // int[kMaxSwapRows]
-static_assert(kTmemOffset + 4 <= kTableOffset && kTableOffset + 4 * kMaxSwapRows <= kCtlBytes, "control block");
+constexpr int kTableOffset = 256;  // int[kMaxSwapRows + 16]: groups of tokens may be read past the last
+static_assert(kTmemOffset + 4 <= kTableOffset && kTableOffset + 4 * (kMaxSwapRows + 16) <= kCtlBytes, "control block");
 
 enum WaitResult : int { kWaitOk = 1, kWaitTimeout = 0, kWaitAborted = -1 };
 constexpr uint32_t kSleepHintNs = 20000;
@@ -321,36 +321,43 @@ __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
   return reinterpret_cast<uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
-// Writes a staged block of 32 rows of kPieces 16-byte pieces: row r of it to row out_row (of lane
-// r; < 0: none) of `out`, kPieces lanes to a row.
+// The rows of the results that a lane reads and writes in a block of 32 rows of kPieces 16-byte
+// pieces, kPieces lanes to a row: of row `mine` of each lane (< 0: none).
 template <int kPieces>
-__device__ __forceinline__ void write_staged(uint8_t* stage, void* out, int64_t row_bytes, int64_t col_bytes, int64_t end_bytes,
-                                             int64_t out_row, int lane) {
-  __syncwarp();
-  const int piece = lane % kPieces;
+__device__ __forceinline__ void block_rows(int (&rows)[kPieces], int mine, int lane) {
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int row = (32 / kPieces) * i + lane / kPieces;
-    const int64_t at = __shfl_sync(0xffffffffu, out_row, row);
-    const uint4 v = *staged(stage, row, piece);
-    if (at >= 0 && col_bytes + 16 * piece < end_bytes)
-      *reinterpret_cast<uint4*>(static_cast<char*>(out) + at * row_bytes + col_bytes + 16 * piece) = v;
-  }
+  for (int i = 0; i < kPieces; ++i) rows[i] = __shfl_sync(0xffffffffu, mine, (32 / kPieces) * i + lane / kPieces);
+}
+
+__device__ __forceinline__ char* row_address(const void* base, int row, uint32_t row_bytes) {
+  return const_cast<char*>(static_cast<const char*>(base)) + (uint64_t)(uint32_t)row * row_bytes;
+}
+
+// Writes a staged block to its rows of `out` (of which `base` is this lane's piece of row 0).
+template <int kPieces>
+__device__ __forceinline__ void write_staged(uint8_t* stage, void* base, uint32_t row_bytes, const int (&rows)[kPieces], bool inside, int lane) {
+  __syncwarp();
+  uint4 v[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) v[i] = *staged(stage, (32 / kPieces) * i + lane / kPieces, lane % kPieces);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (rows[i] >= 0 && inside) *reinterpret_cast<uint4*>(row_address(base, rows[i], row_bytes)) = v[i];
   __syncwarp();
 }
 
 // The same block's rows of `in`, into the staging buffer.
-__device__ __forceinline__ void load_rows(uint4 (&v)[8], const void* in, int64_t row_bytes, int64_t col_bytes, int64_t end_bytes,
-                                          int64_t out_row, int lane) {
-  const int piece = lane & 7;
+__device__ __forceinline__ void stage_rows(uint8_t* stage, const void* base, uint32_t row_bytes, const int (&rows)[8], bool inside, int lane) {
+  uint4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t at = __shfl_sync(0xffffffffu, out_row, 4 * i + (lane >> 3));
     v[i] = make_uint4(0, 0, 0, 0);
     // not through the read-only path: the residual may be the output
-    if (at >= 0 && col_bytes + 16 * piece < end_bytes)
-      v[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(in) + at * row_bytes + col_bytes + 16 * piece);
+    if (rows[i] >= 0 && inside) v[i] = *reinterpret_cast<const uint4*>(row_address(base, rows[i], row_bytes));
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) *staged(stage, 4 * i + (lane >> 3), lane & 7) = v[i];
+  __syncwarp();
 }
 
 template <bool kF16>
@@ -728,17 +735,28 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         if constexpr (kEpi == kEpiLinear)
           if (p.bias && there) bias = unpack1<kF16>(static_cast<const uint16_t*>(p.bias)[f]);
         constexpr int kGroup = kAccs == 1 ? 16 : 8;  // tokens at a time
+        const uint32_t ld_out = (uint32_t)p.ldo * (kEpi == kEpiPlain && p.out_f32 ? 4u : 2u), ld_saved = (uint32_t)p.lds * 2u;
 #pragma unroll 1
         for (int c = 0; c < live; c += kGroup) {
           uint32_t v[kAccs][kGroup];
+          int row[kGroup];
+#pragma unroll
+          for (int i = 0; i < kGroup; i += 4) {
+            const int4 r = *reinterpret_cast<const int4*>(row_table + c0 + c + i);  // (a table of kMaxSwapRows + 16)
+            row[i] = r.x;
+            row[i + 1] = r.y;
+            row[i + 2] = r.z;
+            row[i + 3] = r.w;
+          }
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) row[i] = c + i < live && there ? row[i] : -1;
           uint16_t res16[kGroup];
           if constexpr (kEpi == kEpiLinear) {
             if (p.residual) {
+              const uint16_t* const base = static_cast<const uint16_t*>(p.residual) + f;
 #pragma unroll
-              for (int i = 0; i < kGroup; ++i) {
-                const int row = c + i < live ? row_table[c0 + c + i] : -1;
-                res16[i] = row >= 0 && there ? static_cast<const uint16_t*>(p.residual)[row * p.ldr + f] : (uint16_t)0;
-              }
+              for (int i = 0; i < kGroup; ++i)
+                res16[i] = row[i] >= 0 ? *reinterpret_cast<const uint16_t*>(row_address(base, row[i], (uint32_t)p.ldr * 2u)) : (uint16_t)0;
             }
           }
           if (sg.whole) {
@@ -746,42 +764,55 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             for (int t = 0; t < kAccs; ++t) {
 #pragma unroll
               for (int g = 0; g < kGroup; g += 8) {
-                uint32_t x[8];
                 // (a half of 8 columns has no second group)
+                uint32_t x[8];
                 if (c + g < n / 2) tmem_ld_x8(t0 + (uint32_t)(t * n + c + g), x);
-                ptx::tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[t][g + i] = x[i];
               }
             }
+            ptx::tmem_ld_wait();
           } else {
             sum_parts<kAccs, kGroup, 4>(p, parts, kCtas, rank, ewarp, c, n / 2, lane, v);
           }
+          // all values first, then the stores: no branches between them
+          uint32_t pre[kGroup];
           with_activation(p.act, [&](auto act) {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
-              const int row = c + i < live ? row_table[c0 + c + i] : -1;
-              if (row < 0 || !there) continue;
               float x = __uint_as_float(v[0][i]);
               if constexpr (kEpi == kEpiGated) {
-                const float y = __uint_as_float(v[kAccs - 1][i]);
-                if (p.saved[0]) {
-                  static_cast<uint16_t*>(p.saved[0])[row * p.lds + f] = pack1<kF16>(x);
-                  static_cast<uint16_t*>(p.saved[1])[row * p.lds + f] = pack1<kF16>(y);
-                }
-                x = activate<act.value>(x) * y;
+                x = activate<act.value>(x) * __uint_as_float(v[kAccs - 1][i]);
               } else if constexpr (kEpi == kEpiLinear) {
                 x += bias;
-                if (p.saved[0]) static_cast<uint16_t*>(p.saved[0])[row * p.lds + f] = pack1<kF16>(x);
+                pre[i] = __float_as_uint(x);
                 x = activate<act.value>(x);
                 if (p.residual) x += unpack1<kF16>(res16[i]);
               }
-              if (kEpi == kEpiPlain && p.out_f32)
-                static_cast<float*>(p.out[sg.problem])[row * p.ldo + f] = x;
-              else
-                static_cast<uint16_t*>(p.out[sg.problem])[row * p.ldo + f] = pack1<kF16>(x);
+              if constexpr (kEpi == kEpiGated) pre[i] = v[0][i];
+              v[0][i] = __float_as_uint(x);
             }
           });
+          auto store = [&](void* out, uint32_t ld, const uint32_t (&x)[kGroup]) {
+            uint16_t* const base = static_cast<uint16_t*>(out) + f;
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+              if (row[i] >= 0) *reinterpret_cast<uint16_t*>(row_address(base, row[i], ld)) = pack1<kF16>(__uint_as_float(x[i]));
+          };
+          if (kEpi == kEpiPlain && p.out_f32) {
+            float* const base = static_cast<float*>(p.out[sg.problem]) + f;
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+              if (row[i] >= 0) *reinterpret_cast<uint32_t*>(row_address(base, row[i], ld_out)) = v[0][i];
+          } else {
+            store(p.out[sg.problem], ld_out, v[0]);
+          }
+          if constexpr (kEpi != kEpiPlain) {
+            if (p.saved[0]) {
+              store(p.saved[0], ld_saved, pre);
+              if constexpr (kEpi == kEpiGated) store(p.saved[1], ld_saved, v[kAccs - 1]);
+            }
+          }
         }
         if (sg.whole) release();
       } else {
@@ -789,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         const int trow = (sg.mt * 2 + rank) * kTileM + q * 32 + lane;
         const int chunk = trow / p.box, shard = chunk / p.shard_chunks;
         const int in_shard = trow - shard * p.shard_chunks * p.box;
-        const int64_t out_row = shard < p.shards && in_shard < p.shard_rows ? shard * p.shard_rows + in_shard : -1;
+        const int out_row = shard < p.shards && in_shard < p.shard_rows ? (int)(shard * p.shard_rows) + in_shard : -1;
         const uint32_t t0 = lane_base + (uint32_t)(acc * kBN);
         // gated: as many columns of each product, the second's a half of the accumulator on
         const int first_col = kEpi == kEpiGated ? half * (kHalf / 2) : half * kHalf;
@@ -811,11 +842,15 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         }
         if constexpr (kEpi == kEpiGated) {
           constexpr int kBlocks = kHalf / 64;  // of 32 columns of results
-          const int64_t col = (int64_t)sg.nt * kHalf + first_col;
-          uint32_t g16[kBlocks][16], u16[kBlocks][16], o16[kBlocks][16];
+          constexpr int kPieces = 4 * kBlocks;
+          const int64_t col = (int64_t)sg.nt * kHalf + first_col + 8 * (lane % kPieces);  // of this lane's piece
+          const bool inside = col < p.cols;
+          int rows[kPieces];
+          block_rows(rows, out_row, lane);
+          uint32_t g16[kBlocks][16], u16[kBlocks][16];
 #pragma unroll
           for (int h = 0; h < kBlocks; ++h) {
-            uint32_t v[2][32];
+            uint32_t v[2][32], o16[16];
             if (sg.whole) {
               ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + 32 * h), v[0]);
               ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(kHalf + first_col + 32 * h), v[1]);
@@ -833,20 +868,22 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               for (int i = 0; i < 32; ++i)
                 v[0][i] = __float_as_uint(activate<act.value>(__uint_as_float(v[0][i])) * __uint_as_float(v[1][i]));
             });
-            pack32<kF16>(v[0], o16[h]);
+            pack32<kF16>(v[0], o16);
+            stage_half(stage_out, lane, h, o16);
           }
-          auto write = [&](uint32_t (&w)[kBlocks][16], void* out, int64_t ld) {
-#pragma unroll
-            for (int h = 0; h < kBlocks; ++h) stage_half(stage_out, lane, h, w[h]);
-            write_staged<4 * kBlocks>(stage_out, out, ld * 2, col * 2, p.cols * 2, out_row, lane);
-          };
-          write(o16, p.out[0], p.ldo);
+          write_staged<kPieces>(stage_out, static_cast<uint16_t*>(p.out[0]) + col, (uint32_t)p.ldo * 2u, rows, inside, lane);
           if (p.saved[0]) {
-            write(g16, p.saved[0], p.lds);
-            write(u16, p.saved[1], p.lds);
+#pragma unroll
+            for (int h = 0; h < kBlocks; ++h) stage_half(stage_out, lane, h, g16[h]);
+            write_staged<kPieces>(stage_out, static_cast<uint16_t*>(p.saved[0]) + col, (uint32_t)p.lds * 2u, rows, inside, lane);
+#pragma unroll
+            for (int h = 0; h < kBlocks; ++h) stage_half(stage_out, lane, h, u16[h]);
+            write_staged<kPieces>(stage_out, static_cast<uint16_t*>(p.saved[1]) + col, (uint32_t)p.lds * 2u, rows, inside, lane);
           }
         } else {
           const int64_t tile_col = (int64_t)sg.nt * kBN + first_col;
+          int rows[8];
+          block_rows(rows, out_row, lane);
           if (kEpi == kEpiPlain && p.out_f32) {
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
@@ -861,36 +898,35 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 *staged(stage_out, lane, i) = make_uint4(v[0][4 * i], v[0][4 * i + 1], v[0][4 * i + 2], v[0][4 * i + 3]);
-              write_staged<8>(stage_out, p.out[sg.problem], p.ldo * 4, (tile_col + c) * 4, p.cols * 4, out_row, lane);
+              const int64_t col = tile_col + c + 4 * (lane & 7);
+              write_staged<8>(stage_out, static_cast<float*>(p.out[sg.problem]) + col, (uint32_t)p.ldo * 4u, rows, col < p.cols, lane);
             }
           } else {
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 64) {
-              const int64_t col = tile_col + c;
-              uint32_t z16[2][16], o16[2][16];
+              const int64_t col = tile_col + c, at = col + 8 * (lane & 7);  // this lane's piece
+              const bool inside = at < p.cols;
+              uint32_t z16[2][16];
               bool has_residual = false, has_saved = false;
               if constexpr (kEpi == kEpiLinear) {
                 has_residual = p.residual != nullptr;
                 has_saved = p.saved[0] != nullptr;
-                if (has_residual) {
-                  uint4 res16[8];
-                  load_rows(res16, p.residual, p.ldr * 2, col * 2, p.cols * 2, out_row, lane);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) *staged(stage_out, 4 * i + (lane >> 3), lane & 7) = res16[i];
-                  __syncwarp();
-                }
+                if (has_residual)
+                  stage_rows(stage_out, static_cast<const uint16_t*>(p.residual) + at, (uint32_t)p.ldr * 2u, rows, inside, lane);
+              }
+              uint32_t w[2][1][32];
+              if (sg.whole) {
+                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), w[0][0]);
+                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c + 32), w[1][0]);
+                ptx::tmem_ld_wait();
+                if (c + 64 == kHalf) release();
+              } else {
+                sum_parts<1, 32, 1>(p, parts, kCtas, rank, ewarp, c, 0, lane, w[0]);
+                sum_parts<1, 32, 1>(p, parts, kCtas, rank, ewarp, c + 32, 0, lane, w[1]);
               }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                uint32_t w[1][32];
-                uint32_t(&v)[32] = w[0];
-                if (sg.whole) {
-                  ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c + 32 * h), v);
-                  ptx::tmem_ld_wait();
-                  if (c + 64 == kHalf && h == 1) release();
-                } else {
-                  sum_parts<1, 32, 1>(p, parts, kCtas, rank, ewarp, c + 32 * h, 0, lane, w);
-                }
+                uint32_t(&v)[32] = w[h][0];
                 if constexpr (kEpi == kEpiLinear) {
                   if (p.bias) {
 #pragma unroll
@@ -918,15 +954,15 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                     }
                   }
                 }
-                pack32<kF16>(v, o16[h]);
+                uint32_t o16[16];
+                pack32<kF16>(v, o16);
+                stage_half(stage_out, lane, h, o16);
               }
-              stage_half(stage_out, lane, 0, o16[0]);
-              stage_half(stage_out, lane, 1, o16[1]);
-              write_staged<8>(stage_out, p.out[sg.problem], p.ldo * 2, col * 2, p.cols * 2, out_row, lane);
+              write_staged<8>(stage_out, static_cast<uint16_t*>(p.out[sg.problem]) + at, (uint32_t)p.ldo * 2u, rows, inside, lane);
               if (has_saved) {
                 stage_half(stage_out, lane, 0, z16[0]);
                 stage_half(stage_out, lane, 1, z16[1]);
-                write_staged<8>(stage_out, p.saved[0], p.lds * 2, col * 2, p.cols * 2, out_row, lane);
+                write_staged<8>(stage_out, static_cast<uint16_t*>(p.saved[0]) + at, (uint32_t)p.lds * 2u, rows, inside, lane);
               }
             }
           }

@@ -18,7 +18,7 @@ constexpr int kTileK = 64;        // one 128-byte swizzle row of 16-bit values
 constexpr int kTileBytes = kTileM * kTileK * 2;  // 16 KiB
 constexpr int kMaxStages = 12;
 constexpr int kWideStages = 6, kNarrowStages = 8;  // 192 KiB of operands beside 32 KiB of staged results
-constexpr int kMaxSwapRows = 128; // swapped tiles: token columns of a tile
+constexpr int kMaxSwapRows = 64;  // swapped tiles: token columns of a tile, at most
 constexpr int kStageOutBytes = 4096;  // row tiles: one warp's staged 32 rows x 128 bytes
 constexpr int kCtlBytes = 1024;
 constexpr size_t kMaxSmem = 232448;   // 227 KiB

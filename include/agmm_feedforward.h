@@ -15,8 +15,8 @@
  * row for each token have shards * rows rows, in the order of the shards.  A
  * weight is stored [k, n], or [n, k] with rhs_transpose, and its gradient alike.
  *
- * Strides count elements from one row to the next; rows are contiguous and do
- * not overlap.  Pointers are 16-byte aligned, and strides, k, n and columns are
+ * Strides count elements from one row to the next, 2^29 at most; rows are
+ * contiguous and do not overlap.  Pointers are 16-byte aligned, and strides, k, n and columns are
  * multiples of 8, else AGMM_ERR_ALIGNMENT (k, n, columns: AGMM_ERR_INVALID_ARG).
  * An output must not overlap an input, but where it is said that it may.
  *
