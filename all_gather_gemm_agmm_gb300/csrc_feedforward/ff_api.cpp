@@ -518,6 +518,7 @@ agmm_status_t agmm_layer_norm_plan(const agmm_layer_norm_desc_t* d, agmm_layer_n
   if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) return fail(AGMM_ERR_INVALID_ARG, "eps must be finite and not negative");
   int device = 0, sms = 0;
   AGMM_TRY(check_device(&device, &sms));
+  AGMM_TRY(check_cuda(prepare_norm(d->dtype == AGMM_F16), "kernel attributes"));
   agmm_layer_norm_s* pl = new (std::nothrow) agmm_layer_norm_s();
   if (!pl) return fail(AGMM_ERR_NOMEM, "plan allocation");
   pl->columns = d->columns;

@@ -149,6 +149,7 @@ struct NormParams {
   int64_t ldo;
   float *mean, *rstd;
 };
+cudaError_t prepare_norm(bool f16);  // shared-memory limits, once for a plan
 cudaError_t launch_norm(const NormParams& p, bool f16, int sms, cudaStream_t stream);
 
 struct NormGradParams {

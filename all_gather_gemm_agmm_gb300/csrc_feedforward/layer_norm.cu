@@ -454,12 +454,19 @@ cudaError_t launch_norm_grad_t(NormGradParams p, int blocks, cudaStream_t stream
   const Stream st = stream_of(p.cols, p.add ? 3 : 2);
   p.stages = st.stages;
   void (*fn)(NormGradParams) = st.pieces == 2 ? &agmm_layer_norm_grad<kF16, 2, 2> : &agmm_layer_norm_grad<kF16, 4, 1>;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
-  if (e != cudaSuccess) return e;
   return launch(fn, p, (unsigned)blocks, st.threads, st.smem, stream);
 }
 
 }  // namespace
+
+cudaError_t prepare_norm(bool f16) {
+  for (void (*fn)(NormGradParams) : {f16 ? &agmm_layer_norm_grad<true, 2, 2> : &agmm_layer_norm_grad<false, 2, 2>,
+                                     f16 ? &agmm_layer_norm_grad<true, 4, 1> : &agmm_layer_norm_grad<false, 4, 1>}) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 cudaError_t launch_norm(const NormParams& p, bool f16, int sms, cudaStream_t stream) {
   return f16 ? launch_norm_t<true>(p, sms, stream) : launch_norm_t<false>(p, sms, stream);

@@ -109,20 +109,20 @@ class _FeedForwardPlan(_AttentionPlan):
                 workspace.view(-1).view(torch.uint8)[:HEAD_BYTES].zero_()
             raise
 
-    def _plain(self, name, x):
-        if x.requires_grad and self._grad_mode():
-            raise ValueError(f"{name} requires grad, and nothing is recorded here: call under torch.no_grad()")
-
     def _matrix(self, name, x, rows, cols, dtype=None):
         """(pointer, row stride) of a [rows, cols] tensor."""
-        shape = x.shape
-        if len(shape) != 2 or shape[0] != rows or shape[1] != cols or x.stride(1) != 1:
+        stride = x.stride()
+        if x.shape != (rows, cols) or stride[1] != 1:
             raise ValueError(f"{name} must be [{rows}, {cols}] with a contiguous last dimension, "
-                             f"got {tuple(shape)} with strides {x.stride()}")
-        if x.dtype != (dtype or self.dtype) or x.device != self.device:
+                             f"got {tuple(x.shape)} with strides {stride}")
+        self._check(name, x, dtype)
+        return x.data_ptr(), stride[0]
+
+    def _check(self, name, x, dtype):
+        if x.dtype is not (dtype or self.dtype) or x.get_device() != self._index:
             raise ValueError(f"{name} must be {dtype or self.dtype} on {self.device}, got {x.dtype} on {x.device}")
-        self._plain(name, x)
-        return x.data_ptr(), x.stride(0)
+        if x.requires_grad and self._grad_mode():
+            raise ValueError(f"{name} requires grad, and nothing is recorded here: call under torch.no_grad()")
 
     def _pair(self, names, xs, rows, cols, dtype=None):
         """(pointer, pointer, row stride) of two [rows, cols] tensors laid out alike."""
@@ -136,15 +136,19 @@ class _FeedForwardPlan(_AttentionPlan):
         """Pointer of a contiguous vector of `size` values; 0 for None."""
         if x is None:
             return 0
-        self._plain(name, x)
-        return self._vector(name, x, dtype or self.dtype, size)
+        if x.shape != (size,) or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous vector of {size}, got {tuple(x.shape)} with strides {x.stride()}")
+        self._check(name, x, dtype)
+        return x.data_ptr()
 
-    def _grad_type(self, **grads):
+    def _grad_type(self, a, b):
         """The type of the weights' gradients: the plan's, or float32 for all of them."""
-        types = {x.dtype for x in grads.values() if x is not None}
-        if not types <= {self.dtype} and types != {self._float32}:
-            raise ValueError(f"{', '.join(grads)} must all be {self.dtype} or all float32, got {sorted(map(str, types))}")
-        return self._float32 if types == {self._float32} else self.dtype
+        f32 = self._float32
+        if a is None:
+            return f32 if b is not None and b.dtype is f32 else self.dtype
+        if b is not None and (a.dtype is f32) != (b.dtype is f32):
+            raise ValueError(f"the gradients of the weights must all be {self.dtype} or all float32, got {a.dtype} and {b.dtype}")
+        return f32 if a.dtype is f32 else self.dtype
 
     def _call(self, f, args, stream):
         st = f(self._h, args, self._stream(stream))
@@ -182,7 +186,7 @@ class LayerNormPlan(_FeedForwardPlan):
         x_ptr, x_s = self._matrix("x", x, rows, c)
         a_ptr, a_s = (0, 0) if add is None else self._matrix("add", add, rows, c)
         dx_ptr, dx_s = (0, 0) if dx is None else self._matrix("dx", dx, rows, c)
-        grads = self._grad_type(d_weight=d_weight, d_bias=d_bias)
+        grads = self._grad_type(d_weight, d_bias)
         if workspace is None and d_weight is None and d_bias is None:
             ws = 0
         else:
@@ -255,7 +259,7 @@ class GatedPlan(_ProductPlan):
         g, u, s_s = self._pair(("gate", "up"), (gate, up), tokens, self.n)
         dg, du, d_s = self._pair(("d_gate", "d_up"), (d_gate, d_up), tokens, self.n)
         dx_ptr, dx_s = (0, 0) if dx is None else self._matrix("dx", dx, tokens, self.k)
-        grads = self._grad_type(dw_gate=dw_gate, dw_up=dw_up)
+        grads = self._grad_type(dw_gate, dw_up)
         dwg = dwu = dw_s = 0
         if dw_gate is not None or dw_up is not None:
             if dw_gate is None or dw_up is None:
@@ -303,7 +307,7 @@ class LinearPlan(_ProductPlan):
         p_ptr, p_s = (0, 0) if pre is None else self._matrix("pre", pre, tokens, self.n)
         d_ptr, d_s = (0, 0) if d_pre is None else self._matrix("d_pre", d_pre, tokens, self.n)
         dx_ptr, dx_s = (0, 0) if dx is None else self._matrix("dx", dx, tokens, self.k)
-        grads = self._grad_type(dw=dw, d_bias=d_bias)
+        grads = self._grad_type(dw, d_bias)
         dw_ptr, dw_s = (0, 0) if dw is None else self._matrix("dw", dw, *self._weight_shape, grads)
         args = _LINEAR_GRAD_ARGS.pack(shards, rows, *xp, x_s, w_ptr, w_s, o_ptr, o_s, p_ptr, p_s, d_ptr, d_s, dx_ptr, dx_s, dw_ptr,
                                       dw_s, self._values("d_bias", d_bias, self.n, grads), grads is self._float32,
