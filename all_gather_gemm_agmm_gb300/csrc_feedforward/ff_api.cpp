@@ -30,8 +30,9 @@ struct ProductPlan {
   int act;
   bool transpose, f16;  // weights stored [n, k]; fp16
   int device, sms;
-  int pairs, singles;   // CTA pairs, and CTAs, that run at once
-  int path, bn, cut;    // overrides for tests and experiments; -1: by the rules
+  int pairs;                  // CTA pairs that run at once
+  int clusters[kMaxSplit + 1];  // clusters of that many CTAs that do
+  int path, bn, cut, split;   // overrides for tests and experiments; -1: by the rules
   uint64_t wait_limit_cycles;
   int test_drop;
 };
@@ -195,9 +196,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr double kWideBlock = 512, kNarrowBlock = 340;    // a k block of a row tile's main loop
 constexpr double kWideTile = 4000, kNarrowTile = 2500;    // its results, beside the next tile's main loop
 constexpr double kWideCut = 26000, kNarrowCut = 9000;     // the parts' round trip through L2
-constexpr double kSwapCut = 6500;
 constexpr double kSwapByte = 0.019;                       // swapped tiles: a byte, for one CTA alone
 constexpr double kMemoryByte = 2.84e-4;                   // ... and for each CTA that shares the device's memory
+constexpr double kSplitTile = 1500;                       // ... the parts' way through distributed shared memory
 
 // Whole tiles go round the clusters; or those of a ragged last wave, with the wave before it, are
 // cut along k evenly over the clusters.
@@ -313,24 +314,30 @@ agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t fe
   p->tiles_per_problem = p->num_tiles = p->m_tiles;
   p->group_m = 1;
   p->mma_n = (int)ceil_div(p->chunks * p->box, 16) * 16;
-  const int accs = epi == kEpiGated ? 2 : 1;
+  const int accs = epi == kEpiGated ? 2 : 1, tiles = p->num_tiles, groups = (int)ceil_div(p->chunks * p->box, 8);
   const size_t stage = (size_t)accs * kTileBytes + (size_t)p->mma_n * 128;
-  p->stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - 1024 - kCtlBytes) / stage);
+  // The CTAs of a cluster share a tile's k where that is estimated to be shorter.
+  p->split = 1;
+  double least = 1e300;
+  for (int split = 1; split <= kMaxSplit; ++split) {
+    if (split > 1 && (split > p->k_blocks || tiles > pl->clusters[split])) break;
+    if (pl->split >= 1 && split != std::min(pl->split, p->k_blocks)) continue;
+    const int ctas = std::min(tiles * split, pl->clusters[1]);
+    const double time = (double)p->k_blocks / split * stage * std::max(kSwapByte, kMemoryByte * ctas) + (split > 1 ? kSplitTile : 0);
+    if (time < 1.02 * least) {  // of two alike the one with more copies in flight
+      least = time;
+      p->split = split;
+    }
+  }
+  p->recv_slots = (int)ceil_div(groups, p->split);
+  p->recv_bytes = p->split > 1 ? (uint32_t)(p->split * p->recv_slots * accs * kTileM * 8 * sizeof(float)) : 0;
+  p->stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - 1024 - kCtlBytes - p->recv_bytes) / stage);
   p->tmem_cols = 32;
   while ((int)p->tmem_cols < 2 * accs * p->mma_n) p->tmem_cols *= 2;
-  const int C = pl->singles, T = p->num_tiles;
-  bool cut = can_cut(T, p->k_blocks, C);
-  if (cut && pl->cut >= 0) {
-    cut = pl->cut != 0;
-  } else if (cut) {
-    const double bytes = (double)stage * p->k_blocks;
-    const auto wave = [&](int ctas) { return ctas ? bytes * std::max(kSwapByte, kMemoryByte * ctas) : 0.0; };
-    cut = wave(C) * T / C + kSwapCut < wave(C) * (T / C) + wave(T % C);
-  }
-  make_schedule(p, C, cut);
-  const int clusters = std::min(C, std::max(p->dp_tiles, p->sk_clusters));
-  return check_cuda(launch_gemm(select_gemm(0, epi, pl->f16), *p, clusters, 1, 1024 + p->stages * stage + kCtlBytes, stream),
-                    "product launch");
+  make_schedule(p, pl->clusters[1], false);
+  const int clusters = p->split > 1 ? tiles : std::min(pl->clusters[1], tiles);
+  const size_t smem = 1024 + p->stages * stage + p->recv_bytes + kCtlBytes;
+  return check_cuda(launch_gemm(select_gemm(0, epi, pl->f16), *p, clusters, p->split, smem, stream), "product launch");
 }
 
 // X Wi for one weight or two (gated), with an epilogue.
@@ -456,17 +463,21 @@ agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int tran
   pl->bn = env_int("AGMM_BN", kNarrowN, kWideN);
   if (pl->bn != kNarrowN && pl->bn != kWideN) pl->bn = -1;
   pl->cut = env_int("AGMM_STREAMK", 0, 1);
-  pl->singles = pl->sms;
+  pl->split = env_int("AGMM_SPLITK", 1, kMaxSplit);
   pl->pairs = pl->sms / 2;
+  for (int split = 1; split <= kMaxSplit; ++split) pl->clusters[split] = pl->sms / split;
   for (int epi = kEpiPlain; epi <= kEpiLinear; ++epi) {
-    for (int bn : {0, kNarrowN, kWideN}) {
-      int clusters = 0;
-      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(bn, epi, pl->f16), bn ? 2 : 1, &clusters), "kernel attributes"));
-      int& fit = bn ? pl->pairs : pl->singles;
-      fit = std::min(fit, clusters);
+    int fit = 0;
+    for (int bn : {kNarrowN, kWideN}) {
+      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(bn, epi, pl->f16), 2, &fit), "kernel attributes"));
+      pl->pairs = std::min(pl->pairs, fit);
+    }
+    for (int split = 1; split <= kMaxSplit; ++split) {
+      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(0, epi, pl->f16), split, &fit), "kernel attributes"));
+      pl->clusters[split] = std::min(pl->clusters[split], fit);
     }
   }
-  if (pl->pairs < 1 || pl->singles < 1) return fail(AGMM_ERR_UNSUPPORTED, "the kernels do not fit this device");
+  if (pl->pairs < 1 || pl->clusters[1] < 1) return fail(AGMM_ERR_UNSUPPORTED, "the kernels do not fit this device");
   return AGMM_OK;
 }
 

@@ -23,11 +23,12 @@
 //                  one column of the weights and only the tokens that there are.
 //                  Bound: the weights' bytes.
 //
-// Work: cluster c takes whole tiles in turn; tiles of a ragged last wave (and the wave
-// before it) are cut along k evenly over the clusters.  Every warp of a cut tile's
-// epilogue leaves its float32 partial results in the workspace and counts its k blocks;
-// the warp that completes the count adds all parts in the order of k and goes on to the
-// results.  Nobody waits for another CTA, and the sum does not depend on who is last.
+// Work: cluster c takes whole tiles in turn.  Where few tiles leave SMs idle, k is shared:
+// swapped tiles by the CTAs of a cluster, whose parts meet in distributed shared memory; row
+// tiles (those of a ragged last wave and the wave before it) evenly over the clusters.  Every
+// warp of a cut row tile's epilogue leaves its float32 partial results in the workspace and
+// counts its k blocks; the warp that completes the count adds all parts and goes on to the
+// results.  Nobody waits for another cluster, and parts are added in the order of k.
 //
 // Every mbarrier wait is bounded; one that runs out records AGMM_ERR_TIMEOUT in the
 // status words, all roles leave their loops, wait (bounded) for their own work in
@@ -117,11 +118,13 @@ __device__ __forceinline__ int first_unit(const GemmParams& p, int cluster) {
 }
 
 struct SegmentIter {
-  int u, hi, next_dp, clusters;
+  int u, hi, next_dp, clusters, rank, split;
 
-  __device__ __forceinline__ void init(const GemmParams& p, int cluster, int nclusters) {
+  __device__ __forceinline__ void init(const GemmParams& p, int cluster, int nclusters, int cta_rank, int splits) {
     clusters = nclusters;
     next_dp = cluster;
+    rank = cta_rank;
+    split = splits;
     u = hi = 0;
     if (cluster < p.sk_clusters) {
       u = first_unit(p, cluster);
@@ -138,8 +141,8 @@ struct SegmentIter {
       u += s.kb1 - s.kb0;
     } else if (next_dp < p.dp_tiles) {
       s.tile = next_dp;
-      s.kb0 = 0;
-      s.kb1 = p.k_blocks;
+      s.kb0 = split > 1 ? p.k_blocks * rank / split : 0;
+      s.kb1 = split > 1 ? p.k_blocks * (rank + 1) / split : p.k_blocks;
       next_dp += clusters;
     } else {
       return false;
@@ -306,6 +309,11 @@ __device__ __forceinline__ void with_layout(int mn_major, int blocked, bool chun
   }
 }
 
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+constexpr uint32_t kPartBytes = kTileM * 8 * sizeof(float);  // swapped tiles: one product's part of 8 tokens
+
 template <int kCount>
 __device__ __forceinline__ void store_part(float4* slot, int col, int lane, const uint32_t (&v)[kCount]) {
 #pragma unroll
@@ -415,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
   constexpr uint32_t a_slot = (uint32_t)kAccs * kTileBytes;
   const uint32_t b_slot = (uint32_t)(kSwap ? p.mma_n : kHalf) * 128u;
   const uint32_t a0 = base, b0 = base + (uint32_t)S * a_slot;
-  const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results
-  const uint32_t ctl = out0 + (kSwap ? 0u : (uint32_t)(kEpiWarps * kStageOutBytes));
+  const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results; swapped tiles: other CTAs' parts
+  const uint32_t ctl = out0 + (kSwap ? p.recv_bytes : (uint32_t)(kEpiWarps * kStageOutBytes));
   uint8_t* const ctl_ptr = base_ptr + (ctl - base);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kAbortOffset);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctl_ptr + kTmemOffset);
@@ -424,8 +432,10 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = p.wait_limit_cycles;
-  const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
-  const int cluster = (int)blockIdx.x / kCtas, clusters = (int)gridDim.x / kCtas;
+  // swapped tiles: the CTAs of a cluster share a tile's k, or each is one of its own
+  const int split = kSwap ? p.split : 1;
+  const int rank = kPair ? (int)(blockIdx.x & 1) : (int)blockIdx.x % split;
+  const int cluster = (int)blockIdx.x / (kCtas * split), clusters = (int)gridDim.x / (kCtas * split);
 
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   if (warp == 0) {
@@ -468,6 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     // both CTAs' barriers are there before either's loads and MMAs signal them
     ptx::cluster_arrive_relaxed();
     ptx::cluster_wait();
+  } else if (split > 1) {
+    ptx::cluster_arrive_relaxed();  // matched before the first store to another CTA
   }
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true, dropped = p.test_drop == 0;
     SegmentIter iter;
-    iter.init(p, cluster, clusters);
+    iter.init(p, cluster, clusters, rank, split);
     Segment sg;
     const int per_tile = kSwap ? p.chunks : kTileM / p.box;  // chunks of the tokens: at most 16
     const uint32_t bytes = a_slot + (uint32_t)(kSwap ? p.chunks * p.box : kHalf) * 128u;
@@ -508,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         const uint32_t next_phase = stage + 1 == S ? phase ^ 1u : phase;
         empty_ready = kb + 1 < kb1 && ptx::mbar_test_wait(bar_empty(ctl, next_stage), next_phase ^ 1u);
         if (dropped) {
-          if (rank == 0) {
+          if (!kPair || rank == 0) {
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           }
@@ -591,9 +603,13 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           if (!wait_drain(bar_full(ctl, s), (armed_parity >> s) & 1u, limit))
             record_failure(p, abort_flag, kWaitTimeout, kRoleDrain, s, -1);
     __syncwarp();
+    if (kSwap && split > 1) {
+      ptx::cluster_wait();
+      ptx::cluster_sync_all();
+    }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
-    if (rank == 0) {
+    if (!kPair || rank == 0) {
       const bool issuer = ptx::elect_one();
       const int n = kSwap ? p.mma_n : kBN;
       const uint32_t idesc = ptx::idesc_f16kind_f32(kPair ? 2 * kTileM : kTileM, n, p.a.mn_major != 0, p.b.mn_major != 0, kF16);
@@ -604,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       uint32_t phase = 0;
       bool ok = true;
       SegmentIter iter;
-      iter.init(p, cluster, clusters);
+      iter.init(p, cluster, clusters, rank, split);
       Segment sg;
       for (; ok && iter.next(p, sg); ++it) {
         const int acc = it & 1;
@@ -670,16 +686,71 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       }
       __syncwarp();
     }
+    if (kSwap && split > 1) {
+      ptx::cluster_wait();
+      ptx::cluster_sync_all();
+    }
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, ewarp = warp - 2, half = ewarp >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
     uint8_t* const stage_out = base_ptr + (out0 - base) + ewarp * kStageOutBytes;
     SegmentIter iter;
-    iter.init(p, cluster, clusters);
+    iter.init(p, cluster, clusters, rank, split);
     const int first_cut = p.dp_tiles + iter.u / p.k_blocks;  // the tile whose part lies in slot 0
     Segment sg;
     ptx::griddep_wait();
+    if (kSwap && split > 1) ptx::cluster_wait();  // every CTA of the cluster is there
+    // Swapped tiles: the results of 8 tokens, columns [c, c + 8), of this lane's column of the weights.
+    auto finish = [&](uint32_t (&v)[kAccs][8], int c) {
+      const int64_t f = (int64_t)sg.mt * kTileM + q * 32 + lane;
+      const bool there = f < p.cols;
+      int row[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const int4 r = *reinterpret_cast<const int4*>(row_table + c + i);
+        row[i] = there ? r.x : -1;
+        row[i + 1] = there ? r.y : -1;
+        row[i + 2] = there ? r.z : -1;
+        row[i + 3] = there ? r.w : -1;
+      }
+      float bias = 0.0f;
+      uint16_t res16[8];
+      if constexpr (kEpi == kEpiLinear) {
+        if (p.bias && there) bias = unpack1<kF16>(static_cast<const uint16_t*>(p.bias)[f]);
+        if (p.residual) {
+          const uint16_t* const base = static_cast<const uint16_t*>(p.residual) + f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            res16[i] = row[i] >= 0 ? *reinterpret_cast<const uint16_t*>(row_address(base, row[i], (uint32_t)p.ldr * 2u)) : (uint16_t)0;
+        }
+      }
+      // all values first, then the stores: no branches between them
+      uint32_t pre[8];
+      with_activation(p.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x = __uint_as_float(v[0][i]);
+          if constexpr (kEpi == kEpiLinear) x += bias;
+          pre[i] = __float_as_uint(x);
+          if constexpr (kEpi == kEpiGated) x = activate<act.value>(x) * __uint_as_float(v[kAccs - 1][i]);
+          if constexpr (kEpi == kEpiLinear) {
+            x = activate<act.value>(x);
+            if (p.residual) x += unpack1<kF16>(res16[i]);
+          }
+          v[0][i] = __float_as_uint(x);
+        }
+      });
+      auto store = [&](void* out, uint32_t ld, const uint32_t (&x)[8]) {
+        uint16_t* const base = static_cast<uint16_t*>(out) + f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (row[i] >= 0) *reinterpret_cast<uint16_t*>(row_address(base, row[i], ld)) = pack1<kF16>(__uint_as_float(x[i]));
+      };
+      if (kEpi == kEpiGated && p.saved[0]) store(p.saved[1], (uint32_t)p.lds * 2u, v[kAccs - 1]);
+      store(p.out[0], (uint32_t)p.ldo * 2u, v[0]);
+      if (kEpi != kEpiPlain && p.saved[0]) store(p.saved[0], (uint32_t)p.lds * 2u, pre);
+    };
     for (int it = 0; iter.next(p, sg); ++it) {
       const int acc = it & 1;
       int res = kWaitOk;
@@ -705,116 +776,29 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           sg.whole ? nullptr : p.counters + ((size_t)(sg.tile - p.dp_tiles) * kCtas + rank) * kEpiWarps + ewarp;
 
       if constexpr (kSwap) {
-        // This lane's column of the weights, and this warp's half of the tokens.
-        const int n = p.mma_n, c0 = half * (n / 2);
-        const uint32_t t0 = lane_base + (uint32_t)(acc * kAccs * n + c0);
-        int live = 0;  // columns up to the last that holds a token
-        for (int c = 0; c < n / 2; c += 32) {
-          const unsigned there = __ballot_sync(0xffffffffu, c + lane < n / 2 && row_table[c0 + c + lane] >= 0);
-          if (there) live = c + 32 - __clz(there);
-        }
-        Parts parts = {0, 0, 0};
-        if (!sg.whole) {
-          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile == first_cut ? 0 : 1, ewarp);
-#pragma unroll 1
-          for (int c = 0; c < live; c += 8) {
-            uint32_t v[kAccs][8];
+        // This lane's column of the weights, and this warp's half of the tokens, 8 at a time.
+        const int n = p.mma_n, end = min((half + 1) * (n / 2), p.chunks * p.box);
+        const uint32_t t0 = lane_base + (uint32_t)(acc * kAccs * n);
+        for (int c = half * (n / 2); c < end; c += 8) {
+          uint32_t v[kAccs][8];
 #pragma unroll
-            for (int t = 0; t < kAccs; ++t) tmem_ld_x8(t0 + (uint32_t)(t * n + c), v[t]);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int t = 0; t < kAccs; ++t) store_part<8>(slot, t * (n / 2) + c, lane, v[t]);
-          }
-          release();
-          if (live == 0 || !complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
-          parts = find_parts(p, sg.tile);
-        }
-        const int64_t f = (int64_t)sg.mt * kTileM + q * 32 + lane;  // the column
-        const bool there = f < p.cols;
-        float bias = 0.0f;
-        if constexpr (kEpi == kEpiLinear)
-          if (p.bias && there) bias = unpack1<kF16>(static_cast<const uint16_t*>(p.bias)[f]);
-        constexpr int kGroup = kAccs == 1 ? 16 : 8;  // tokens at a time
-        const uint32_t ld_out = (uint32_t)p.ldo * (kEpi == kEpiPlain && p.out_f32 ? 4u : 2u), ld_saved = (uint32_t)p.lds * 2u;
-#pragma unroll 1
-        for (int c = 0; c < live; c += kGroup) {
-          uint32_t v[kAccs][kGroup];
-          int row[kGroup];
-#pragma unroll
-          for (int i = 0; i < kGroup; i += 4) {
-            const int4 r = *reinterpret_cast<const int4*>(row_table + c0 + c + i);  // (a table of kMaxSwapRows + 16)
-            row[i] = r.x;
-            row[i + 1] = r.y;
-            row[i + 2] = r.z;
-            row[i + 3] = r.w;
-          }
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i) row[i] = c + i < live && there ? row[i] : -1;
-          uint16_t res16[kGroup];
-          if constexpr (kEpi == kEpiLinear) {
-            if (p.residual) {
-              const uint16_t* const base = static_cast<const uint16_t*>(p.residual) + f;
-#pragma unroll
-              for (int i = 0; i < kGroup; ++i)
-                res16[i] = row[i] >= 0 ? *reinterpret_cast<const uint16_t*>(row_address(base, row[i], (uint32_t)p.ldr * 2u)) : (uint16_t)0;
-            }
-          }
-          if (sg.whole) {
+          for (int t = 0; t < kAccs; ++t) tmem_ld_x8(t0 + (uint32_t)(t * n + c), v[t]);
+          ptx::tmem_ld_wait();
+          if (split == 1) {
+            finish(v, c);
+          } else {
+            // to the CTA that owns these tokens: group c / 8 is slot c / 8 / split of CTA c / 8 % split
+            const int slot = c / 8 / split;
+            const uint32_t at = ptx::map_shared_rank(out0, (uint32_t)(c / 8 - slot * split)) +
+                                (uint32_t)((rank * p.recv_slots + slot) * kAccs) * kPartBytes + (uint32_t)(q * 32 + lane) * 16u;
 #pragma unroll
             for (int t = 0; t < kAccs; ++t) {
-#pragma unroll
-              for (int g = 0; g < kGroup; g += 8) {
-                // (a half of 8 columns has no second group)
-                uint32_t x[8];
-                if (c + g < n / 2) tmem_ld_x8(t0 + (uint32_t)(t * n + c + g), x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[t][g + i] = x[i];
-              }
-            }
-            ptx::tmem_ld_wait();
-          } else {
-            sum_parts<kAccs, kGroup, 4>(p, parts, kCtas, rank, ewarp, c, n / 2, lane, v);
-          }
-          // all values first, then the stores: no branches between them
-          uint32_t pre[kGroup];
-          with_activation(p.act, [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i) {
-              float x = __uint_as_float(v[0][i]);
-              if constexpr (kEpi == kEpiGated) {
-                x = activate<act.value>(x) * __uint_as_float(v[kAccs - 1][i]);
-              } else if constexpr (kEpi == kEpiLinear) {
-                x += bias;
-                pre[i] = __float_as_uint(x);
-                x = activate<act.value>(x);
-                if (p.residual) x += unpack1<kF16>(res16[i]);
-              }
-              if constexpr (kEpi == kEpiGated) pre[i] = v[0][i];
-              v[0][i] = __float_as_uint(x);
-            }
-          });
-          auto store = [&](void* out, uint32_t ld, const uint32_t (&x)[kGroup]) {
-            uint16_t* const base = static_cast<uint16_t*>(out) + f;
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-              if (row[i] >= 0) *reinterpret_cast<uint16_t*>(row_address(base, row[i], ld)) = pack1<kF16>(__uint_as_float(x[i]));
-          };
-          if (kEpi == kEpiPlain && p.out_f32) {
-            float* const base = static_cast<float*>(p.out[sg.problem]) + f;
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-              if (row[i] >= 0) *reinterpret_cast<uint32_t*>(row_address(base, row[i], ld_out)) = v[0][i];
-          } else {
-            store(p.out[sg.problem], ld_out, v[0]);
-          }
-          if constexpr (kEpi != kEpiPlain) {
-            if (p.saved[0]) {
-              store(p.saved[0], ld_saved, pre);
-              if constexpr (kEpi == kEpiGated) store(p.saved[1], ld_saved, v[kAccs - 1]);
+              st_cluster_v4(at + (uint32_t)t * kPartBytes, v[t][0], v[t][1], v[t][2], v[t][3]);
+              st_cluster_v4(at + (uint32_t)t * kPartBytes + kPartBytes / 2, v[t][4], v[t][5], v[t][6], v[t][7]);
             }
           }
         }
-        if (sg.whole) release();
+        release();
       } else {
         // This lane's row, and this warp's half of the columns.
         const int trow = (sg.mt * 2 + rank) * kTileM + q * 32 + lane;
@@ -967,6 +951,40 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             }
           }
         }
+      }
+    }
+    if (kSwap && split > 1) {
+      // The parts are all there: the owner adds them in the order of k.
+      __syncwarp();
+      ptx::cluster_sync_all();
+      const uint4* const recv = reinterpret_cast<const uint4*>(base_ptr + (out0 - base)) + q * 32 + lane;
+      const int groups = (p.chunks * p.box + 7) / 8;
+      for (int slot = half; slot * split + rank < groups; slot += 2) {
+        float sum[kAccs][8];
+        uint32_t v[kAccs][8];
+#pragma unroll
+        for (int t = 0; t < kAccs; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[t][i] = 0.0f;
+#pragma unroll 2
+        for (int r = 0; r < split; ++r) {
+#pragma unroll
+          for (int t = 0; t < kAccs; ++t) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 x = recv[(((r * p.recv_slots + slot) * kAccs + t) * 2 + h) * kTileM];
+              sum[t][4 * h] += __uint_as_float(x.x);
+              sum[t][4 * h + 1] += __uint_as_float(x.y);
+              sum[t][4 * h + 2] += __uint_as_float(x.z);
+              sum[t][4 * h + 3] += __uint_as_float(x.w);
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kAccs; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[t][i] = __float_as_uint(sum[t][i]);
+        finish(v, (slot * split + rank) * 8);
       }
     }
   }
