@@ -300,11 +300,13 @@ agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice 
   p->num_tiles = p->tiles_per_problem * p->problems;
   p->group_m = kGroupM;
   const bool wide = choice.bn == kWideN;
-  p->stages = wide ? kWideStages : kNarrowStages;
+  const bool two = wide && p->residual;  // the residual of a tile is staged while its products are made
+  p->stages = two ? kResidualStages : wide ? kWideStages : kNarrowStages;
+  p->stage_out_bytes = two ? 2 * kStageOutBytes : kStageOutBytes;
   p->tmem_cols = 2 * choice.bn;
   make_schedule(p, pl->pairs, choice.cut);
   const int clusters = std::min(pl->pairs, std::max(p->dp_tiles, p->sk_clusters));
-  const size_t smem = 1024 + (size_t)p->stages * (kTileBytes + choice.bn * kTileK) + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
+  const size_t smem = 1024 + (size_t)p->stages * (kTileBytes + choice.bn * kTileK) + (size_t)kEpiWarps * p->stage_out_bytes + kCtlBytes;
   return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16), *p, clusters, 2, smem, stream), "product launch");
 }
 

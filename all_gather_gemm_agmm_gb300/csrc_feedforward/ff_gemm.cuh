@@ -354,18 +354,26 @@ __device__ __forceinline__ void write_staged(uint8_t* stage, void* base, uint32_
   __syncwarp();
 }
 
-// The same block's rows of `in`, into the staging buffer.
+// The same block's rows of `in`, into the staging buffer, asynchronously; zeros where there are none.
 __device__ __forceinline__ void stage_rows(uint8_t* stage, const void* base, uint32_t row_bytes, const int (&rows)[8], bool inside, int lane) {
-  uint4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v[i] = make_uint4(0, 0, 0, 0);
-    // not through the read-only path: the residual may be the output
-    if (rows[i] >= 0 && inside) v[i] = *reinterpret_cast<const uint4*>(row_address(base, rows[i], row_bytes));
+    const bool there = rows[i] >= 0 && inside;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(staged(stage, 4 * i + (lane >> 3), lane & 7))),
+                 "l"(there ? row_address(base, rows[i], row_bytes) : base), "r"(there ? 16 : 0)
+                 : "memory");
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) *staged(stage, 4 * i + (lane >> 3), lane & 7) = v[i];
-  __syncwarp();
+}
+
+template <int kCount>
+__device__ __forceinline__ Two pair_of(const uint32_t (&v)[kCount], int i) {
+  return two(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+}
+template <int kCount>
+__device__ __forceinline__ void set_pair(uint32_t (&v)[kCount], int i, Two x) {
+  const float2 f = halves(x);
+  v[i] = __float_as_uint(f.x);
+  v[i + 1] = __float_as_uint(f.y);
 }
 
 template <bool kF16>
@@ -424,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
   const uint32_t b_slot = (uint32_t)(kSwap ? p.mma_n : kHalf) * 128u;
   const uint32_t a0 = base, b0 = base + (uint32_t)S * a_slot;
   const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results; swapped tiles: other CTAs' parts
-  const uint32_t ctl = out0 + (kSwap ? p.recv_bytes : (uint32_t)(kEpiWarps * kStageOutBytes));
+  const uint32_t ctl = out0 + (kSwap ? p.recv_bytes : (uint32_t)kEpiWarps * p.stage_out_bytes);
   uint8_t* const ctl_ptr = base_ptr + (ctl - base);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kAbortOffset);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctl_ptr + kTmemOffset);
@@ -694,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, ewarp = warp - 2, half = ewarp >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
-    uint8_t* const stage_out = base_ptr + (out0 - base) + ewarp * kStageOutBytes;
+    uint8_t* const stage_out = base_ptr + (out0 - base) + (kSwap ? 0u : (uint32_t)ewarp * p.stage_out_bytes);
     SegmentIter iter;
     iter.init(p, cluster, clusters, rank, split);
     const int first_cut = p.dp_tiles + iter.u / p.k_blocks;  // the tile whose part lies in slot 0
@@ -729,16 +737,15 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       uint32_t pre[8];
       with_activation(p.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x = __uint_as_float(v[0][i]);
-          if constexpr (kEpi == kEpiLinear) x += bias;
-          pre[i] = __float_as_uint(x);
-          if constexpr (kEpi == kEpiGated) x = activate<act.value>(x) * __uint_as_float(v[kAccs - 1][i]);
-          if constexpr (kEpi == kEpiLinear) {
-            x = activate<act.value>(x);
-            if (p.residual) x += unpack1<kF16>(res16[i]);
-          }
-          v[0][i] = __float_as_uint(x);
+        for (int i = 0; i < 8; i += 2) {
+          Two x = pair_of(v[0], i);
+          if constexpr (kEpi == kEpiLinear) x = add2(x, both(bias));
+          set_pair(pre, i, x);
+          if constexpr (kEpi != kEpiPlain) x = activate<act.value>(x);
+          if constexpr (kEpi == kEpiGated) x = mul2(x, pair_of(v[kAccs - 1], i));
+          if constexpr (kEpi == kEpiLinear)
+            if (p.residual) x = add2(x, two(unpack1<kF16>(res16[i]), unpack1<kF16>(res16[i + 1])));
+          set_pair(v[0], i, x);
         }
       });
       auto store = [&](void* out, uint32_t ld, const uint32_t (&x)[8]) {
@@ -753,6 +760,30 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     };
     for (int it = 0; iter.next(p, sg); ++it) {
       const int acc = it & 1;
+      // Row tiles: this lane's row, those that it reads and writes, and this warp's half of the columns.
+      int out_row = -1, rows[8];
+      // gated: as many columns of each product, the second's a half of the accumulator on
+      const int first_col = kEpi == kEpiGated ? half * (kHalf / 2) : half * kHalf;
+      const int64_t tile_col = (int64_t)sg.nt * (kEpi == kEpiGated ? kHalf : kBN) + first_col;
+      auto fetch_residual = [&]() {
+        if constexpr (!kSwap && kEpi == kEpiLinear) {
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 64) {
+            const int64_t at = tile_col + c + 8 * (lane & 7);
+            stage_rows(stage_out + c / 64 * kStageOutBytes, static_cast<const uint16_t*>(p.residual) + (at < p.cols ? at : 0),
+                       (uint32_t)p.ldr * 2u, rows, at < p.cols, lane);
+          }
+        }
+      };
+      const bool has_residual = kEpi == kEpiLinear && p.residual != nullptr;
+      if constexpr (!kSwap) {
+        const int trow = (sg.mt * 2 + rank) * kTileM + q * 32 + lane;
+        const int chunk = trow / p.box, shard = chunk / p.shard_chunks;
+        const int in_shard = trow - shard * p.shard_chunks * p.box;
+        if (shard < p.shards && in_shard < p.shard_rows) out_row = (int)(shard * p.shard_rows) + in_shard;
+        block_rows(rows, out_row, lane);
+        if (has_residual && sg.whole) fetch_residual();  // while the products are made
+      }
       int res = kWaitOk;
       if (lane == 0) res = wait_phase(bar_acc_full(ctl, acc), (uint32_t)(it >> 1) & 1u, abort_flag, limit);
       res = __shfl_sync(0xffffffffu, res, 0);
@@ -800,14 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         }
         release();
       } else {
-        // This lane's row, and this warp's half of the columns.
-        const int trow = (sg.mt * 2 + rank) * kTileM + q * 32 + lane;
-        const int chunk = trow / p.box, shard = chunk / p.shard_chunks;
-        const int in_shard = trow - shard * p.shard_chunks * p.box;
-        const int out_row = shard < p.shards && in_shard < p.shard_rows ? (int)(shard * p.shard_rows) + in_shard : -1;
         const uint32_t t0 = lane_base + (uint32_t)(acc * kBN);
-        // gated: as many columns of each product, the second's a half of the accumulator on
-        const int first_col = kEpi == kEpiGated ? half * (kHalf / 2) : half * kHalf;
         Parts parts = {0, 0, 0};
         if (!sg.whole) {
           float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile == first_cut ? 0 : 1, ewarp);
@@ -823,11 +847,12 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           release();
           if (!complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
           parts = find_parts(p, sg.tile);
+          if (has_residual) fetch_residual();
         }
         if constexpr (kEpi == kEpiGated) {
           constexpr int kBlocks = kHalf / 64;  // of 32 columns of results
           constexpr int kPieces = 4 * kBlocks;
-          const int64_t col = (int64_t)sg.nt * kHalf + first_col + 8 * (lane % kPieces);  // of this lane's piece
+          const int64_t col = tile_col + 8 * (lane % kPieces);  // of this lane's piece
           const bool inside = col < p.cols;
           int rows[kPieces];
           block_rows(rows, out_row, lane);
@@ -849,8 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             }
             with_activation(p.act, [&](auto act) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                v[0][i] = __float_as_uint(activate<act.value>(__uint_as_float(v[0][i])) * __uint_as_float(v[1][i]));
+              for (int i = 0; i < 32; i += 2) set_pair(v[0], i, mul2(activate<act.value>(pair_of(v[0], i)), pair_of(v[1], i)));
             });
             pack32<kF16>(v[0], o16);
             stage_half(stage_out, lane, h, o16);
@@ -865,9 +889,10 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             write_staged<kPieces>(stage_out, static_cast<uint16_t*>(p.saved[1]) + col, (uint32_t)p.lds * 2u, rows, inside, lane);
           }
         } else {
-          const int64_t tile_col = (int64_t)sg.nt * kBN + first_col;
-          int rows[8];
-          block_rows(rows, out_row, lane);
+          if (has_residual) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+          }
           if (kEpi == kEpiPlain && p.out_f32) {
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
@@ -890,14 +915,9 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             for (int c = 0; c < kHalf; c += 64) {
               const int64_t col = tile_col + c, at = col + 8 * (lane & 7);  // this lane's piece
               const bool inside = at < p.cols;
+              uint8_t* const stage_c = stage_out + (has_residual ? c / 64 * kStageOutBytes : 0);
               uint32_t z16[2][16];
-              bool has_residual = false, has_saved = false;
-              if constexpr (kEpi == kEpiLinear) {
-                has_residual = p.residual != nullptr;
-                has_saved = p.saved[0] != nullptr;
-                if (has_residual)
-                  stage_rows(stage_out, static_cast<const uint16_t*>(p.residual) + at, (uint32_t)p.ldr * 2u, rows, inside, lane);
-              }
+              const bool has_saved = kEpi == kEpiLinear && p.saved[0] != nullptr;
               uint32_t w[2][1][32];
               if (sg.whole) {
                 ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), w[0][0]);
@@ -916,37 +936,37 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                       if (col + 32 * h + 8 * i < p.cols) {
-                        float b[8];
-                        unpack8<kF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col + 32 * h + 8 * i)), b);
+                        Two b[4];
+                        widen<kF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col + 32 * h + 8 * i)), b);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[8 * i + e] = __float_as_uint(__uint_as_float(v[8 * i + e]) + b[e]);
+                        for (int e = 0; e < 4; ++e) set_pair(v, 8 * i + 2 * e, add2(pair_of(v, 8 * i + 2 * e), b[e]));
                       }
                     }
                   }
                   if (has_saved) pack32<kF16>(v, z16[h]);
                   with_activation(p.act, [&](auto act) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(activate<act.value>(__uint_as_float(v[i])));
+                    for (int i = 0; i < 32; i += 2) set_pair(v, i, activate<act.value>(pair_of(v, i)));
                   });
                   if (has_residual) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                      float r[8];
-                      unpack8<kF16>(*staged(stage_out, lane, h * 4 + i), r);
+                      Two r[4];
+                      widen<kF16>(*staged(stage_c, lane, h * 4 + i), r);
 #pragma unroll
-                      for (int e = 0; e < 8; ++e) v[8 * i + e] = __float_as_uint(__uint_as_float(v[8 * i + e]) + r[e]);
+                      for (int e = 0; e < 4; ++e) set_pair(v, 8 * i + 2 * e, add2(pair_of(v, 8 * i + 2 * e), r[e]));
                     }
                   }
                 }
                 uint32_t o16[16];
                 pack32<kF16>(v, o16);
-                stage_half(stage_out, lane, h, o16);
+                stage_half(stage_c, lane, h, o16);
               }
-              write_staged<8>(stage_out, static_cast<uint16_t*>(p.out[sg.problem]) + at, (uint32_t)p.ldo * 2u, rows, inside, lane);
+              write_staged<8>(stage_c, static_cast<uint16_t*>(p.out[sg.problem]) + at, (uint32_t)p.ldo * 2u, rows, inside, lane);
               if (has_saved) {
-                stage_half(stage_out, lane, 0, z16[0]);
-                stage_half(stage_out, lane, 1, z16[1]);
-                write_staged<8>(stage_out, static_cast<uint16_t*>(p.saved[0]) + at, (uint32_t)p.lds * 2u, rows, inside, lane);
+                stage_half(stage_c, lane, 0, z16[0]);
+                stage_half(stage_c, lane, 1, z16[1]);
+                write_staged<8>(stage_c, static_cast<uint16_t*>(p.saved[0]) + at, (uint32_t)p.lds * 2u, rows, inside, lane);
               }
             }
           }

@@ -38,22 +38,6 @@ __device__ __forceinline__ float unpack1(uint16_t w) {
   return unpack2<kF16>((uint32_t)w).x;
 }
 
-template <bool kF16>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<kF16>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-
-template <bool kF16>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack2<kF16>(x[0], x[1]), pack2<kF16>(x[2], x[3]), pack2<kF16>(x[4], x[5]), pack2<kF16>(x[6], x[7]));
-}
-
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -124,66 +108,106 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
 
-// 1 / (1 + e^-z).  A z so low that e^-z is infinite gives 0.
-__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.0f + exp2_approx(-kLog2e * z)); }
-
-// The normal distribution Phi(z), and e^(-z^2 / 2).  For z <= 0
-//     Phi(z) = t 2^(P(t) - z^2 log2(e) / 2),   t = 1 / (1 + 0.35 |z|),
-// with P fitted to log2(Phi e^(z^2/2) / t) at Chebyshev nodes of |z| <= 13.5, where it is off by
-// 1e-6: no cancellation where Phi is small, one reciprocal and one exponential.  In float32
-// Phi is off by 2^-18.5 of itself up to |z| = 8, by the exponent's rounding.  (erfcf took 193 us
-// for 4096 tokens, k 2560, n 5120, where the product alone takes a third.)
-__device__ __forceinline__ float normal(float z, float& gauss) {
-  const float x = fabsf(z), t = rcp_approx(fmaf(0.35f, x, 1.0f)), e = x * x * (-0.5f * kLog2e);
-  float p = -0.27522552f;
-  p = fmaf(p, t, 1.1202697f);
-  p = fmaf(p, t, -1.5381097f);
-  p = fmaf(p, t, 0.60237956f);
-  p = fmaf(p, t, -0.09033469f);
-  p = fmaf(p, t, 0.5817873f);
-  p = fmaf(p, t, 1.4394445f);
-  p = fmaf(p, t, -2.840212f);
-  gauss = exp2_approx(e);
-  const float low = t * exp2_approx(p + e);
-  return z > 0.0f ? 1.0f - low : low;
+// Activations work on pairs, in packed arithmetic: the reciprocals and exponentials take turns
+// of the same unit, two to a value at most, and the rest is half as many instructions.
+__device__ __forceinline__ Two exp2_two(Two x) {
+  const float2 v = halves(x);
+  return two(exp2_approx(v.x), exp2_approx(v.y));
+}
+__device__ __forceinline__ Two rcp_two(Two x) {
+  const float2 v = halves(x);
+  return two(rcp_approx(v.x), rcp_approx(v.y));
+}
+// max(z, 0); a NaN stays one
+__device__ __forceinline__ float positive(float z) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(z));
+  return y;
+}
+__device__ __forceinline__ Two positive_two(Two z) {
+  const float2 v = halves(z);
+  return two(positive(v.x), positive(v.y));
+}
+__device__ __forceinline__ Two clamp_two(Two z, float most) {
+  const float2 v = halves(z);
+  return two(fminf(fmaxf(v.x, -most), most), fminf(fmaxf(v.y, -most), most));
 }
 
-// The tanh form of z Phi(z), 0.5 z (1 + tanh(v)), is z sigmoid(2 v): nothing cancels.
+// 1 / (1 + 2^x): of x = -z log2(e) the logistic function of z.  An infinite 2^x gives 0.
+__device__ __forceinline__ Two logistic_two(Two x) { return rcp_two(add2(both(1.0f), exp2_two(x))); }
+
+// Phi(-|z|), e^(-z^2 / 2) and x = min(|z|, 9), where Phi is the normal distribution:
+//     Phi(-x) = 2^(P(x) - z^2 log2(e) / 2)
+// with P fitted to log2(Phi(-x) e^(x^2/2)) at Chebyshev nodes of [0, 9], in u = 2 x / 9 - 1, where
+// it is off by 2e-6: one exponential and nothing that cancels.  In float32 Phi is off by 2^-17.5
+// of itself up to x = 9, by the exponent's rounding, and by 1e-19 beyond.
+__device__ __forceinline__ Two normal_tail(Two z, Two& x, Two& gauss) {
+  const float2 v = halves(z);
+  x = two(fminf(fabsf(v.x), 9.0f), fminf(fabsf(v.y), 9.0f));
+  const Two u = fma2(x, both(2.0f / 9.0f), both(-1.0f)), e = mul2(mul2(z, z), both(-0.5f * kLog2e));
+  Two p = both(0.0035879954f);
+  p = fma2(p, u, both(-0.0029788145f));
+  p = fma2(p, u, both(-0.011076425f));
+  p = fma2(p, u, both(0.019956289f));
+  p = fma2(p, u, both(-0.02364965f));
+  p = fma2(p, u, both(0.04836166f));
+  p = fma2(p, u, both(-0.096737415f));
+  p = fma2(p, u, both(0.171032f));
+  p = fma2(p, u, both(-0.30213198f));
+  p = fma2(p, u, both(0.56688064f));
+  p = fma2(p, u, both(-1.3264755f));
+  p = fma2(p, u, both(-3.559733f));
+  gauss = exp2_two(e);
+  return exp2_two(add2(p, e));
+}
+
+// -log2(e) times the argument 2 v of which gelu_tanh is the logistic function: 0.5 z (1 + tanh(v))
+// is z / (1 + e^(-2 v)), and nothing cancels.
+__device__ __forceinline__ Two tanh_exponent(Two z) {
+  return mul2(mul2(z, fma2(mul2(z, z), both(kTanhCube), both(1.0f))), both(-kLog2e * kTanhScale2));
+}
+
 template <int kAct>
-__device__ __forceinline__ float activate(float z) {
-  if constexpr (kAct == kActRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays one
-  if constexpr (kAct == kActSilu) return z * sigmoid(z);
+__device__ __forceinline__ Two activate(Two z) {
+  if constexpr (kAct == kActRelu) return positive_two(z);
+  if constexpr (kAct == kActSilu) return mul2(z, logistic_two(mul2(z, both(-kLog2e))));
   if constexpr (kAct == kActGelu) {
-    float gauss;
-    return z * normal(z, gauss);
+    // z Phi(z) = max(z, 0) - |z| Phi(-|z|); past 9 the second term is less than 2^-59
+    Two x, gauss;
+    const Two low = normal_tail(z, x, gauss);
+    return fma2(mul2(x, both(-1.0f)), low, positive_two(z));
   }
-  if constexpr (kAct == kActGeluTanh) return z * sigmoid(kTanhScale2 * (z + kTanhCube * z * z * z));
+  if constexpr (kAct == kActGeluTanh) return mul2(z, logistic_two(tanh_exponent(z)));
   return z;
 }
 
 // The activation and its derivative.  The bounds on z are where the second term of the
 // derivative has long been 0 in float32: beyond them its factors would be infinity and 0.
 template <int kAct>
-__device__ __forceinline__ void activate_with_slope(float z, float& a, float& slope) {
+__device__ __forceinline__ void activate_with_slope(Two z, Two& a, Two& slope) {
   a = z;
-  slope = 1.0f;
+  slope = both(1.0f);
   if constexpr (kAct == kActRelu) {
-    a = z < 0.0f ? 0.0f : z;
-    slope = z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    const float2 v = halves(z);
+    a = positive_two(z);
+    slope = two(v.x > 0.0f ? 1.0f : (v.x != v.x ? v.x : 0.0f), v.y > 0.0f ? 1.0f : (v.y != v.y ? v.y : 0.0f));
   } else if constexpr (kAct == kActSilu) {
-    const float s = sigmoid(z), b = fminf(fmaxf(z, -200.0f), 200.0f);
-    a = z * s;
-    slope = s * (1.0f + b * (1.0f - s));
+    const Two s = logistic_two(mul2(z, both(-kLog2e))), rest = fma2(s, both(-1.0f), both(1.0f));
+    a = mul2(z, s);
+    slope = mul2(s, fma2(clamp_two(z, 200.0f), rest, both(1.0f)));
   } else if constexpr (kAct == kActGelu) {
-    float gauss;
-    const float phi = normal(z, gauss), b = fminf(fmaxf(z, -20.0f), 20.0f);
-    a = z * phi;
-    slope = phi + b * (kInvSqrt2Pi * gauss);
+    Two x, gauss;
+    const Two low = normal_tail(z, x, gauss);
+    a = fma2(mul2(x, both(-1.0f)), low, positive_two(z));
+    // Phi(z) = 1/2 + sign(z) (1/2 - Phi(-|z|)); the low end without that difference
+    const float2 v = halves(z), l = halves(low);
+    const Two phi = two(v.x > 0.0f ? 1.0f - l.x : l.x, v.y > 0.0f ? 1.0f - l.y : l.y);
+    slope = fma2(clamp_two(z, 20.0f), mul2(gauss, both(kInvSqrt2Pi)), phi);
   } else if constexpr (kAct == kActGeluTanh) {
-    const float b = fminf(fmaxf(z, -20.0f), 20.0f);
-    const float s = sigmoid(kTanhScale2 * (z + kTanhCube * z * z * z));
-    a = z * s;
-    slope = s + b * s * (1.0f - s) * (kTanhScale2 * (1.0f + 3.0f * kTanhCube * b * b));
+    const Two b = clamp_two(z, 20.0f), s = logistic_two(tanh_exponent(z)), rest = fma2(s, both(-1.0f), both(1.0f));
+    a = mul2(z, s);
+    const Two dv = mul2(fma2(mul2(b, b), both(3.0f * kTanhCube), both(1.0f)), both(kTanhScale2));
+    slope = fma2(mul2(b, mul2(s, rest)), dv, s);
   }
 }
 

@@ -15,26 +15,26 @@ namespace ff {
 namespace {
 
 template <bool kF16, int kAct>
-__device__ __forceinline__ void gated_grad_piece(const uint4& d, const uint4& g, const uint4& u, uint4& dg, uint4& du) {
-  float dv[8], gv[8], uv[8];
-  unpack8<kF16>(d, dv);
-  unpack8<kF16>(g, gv);
-  unpack8<kF16>(u, uv);
+__device__ __forceinline__ void gated_grad_piece(const uint4& d16, const uint4& g16, const uint4& u16, uint4& dg, uint4& du) {
+  Two d[4], g[4], u[4];
+  widen<kF16>(d16, d);
+  widen<kF16>(g16, g);
+  widen<kF16>(u16, u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float a, slope;
-    activate_with_slope<kAct>(gv[i], a, slope);
-    gv[i] = dv[i] * uv[i] * slope;
-    uv[i] = dv[i] * a;
+  for (int i = 0; i < 4; ++i) {
+    Two a, slope;
+    activate_with_slope<kAct>(g[i], a, slope);
+    g[i] = mul2(mul2(d[i], u[i]), slope);
+    u[i] = mul2(d[i], a);
   }
-  dg = pack8<kF16>(gv);
-  du = pack8<kF16>(uv);
+  dg = narrow<kF16>(g);
+  du = narrow<kF16>(u);
 }
 
 constexpr int kUnroll = 2;  // rows whose loads are in flight together
 
 template <bool kF16>
-__global__ void __launch_bounds__(256) agmm_gated_grad(const __grid_constant__ GatedGradParams p) {
+__global__ void __launch_bounds__(256, 4) agmm_gated_grad(const __grid_constant__ GatedGradParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
@@ -68,14 +68,12 @@ __global__ void __launch_bounds__(256) agmm_gated_grad(const __grid_constant__ G
 }
 
 template <bool kF16>
-__global__ void __launch_bounds__(256) agmm_act_grad(const __grid_constant__ ActGradParams p) {
+__global__ void __launch_bounds__(256, 4) agmm_act_grad(const __grid_constant__ ActGradParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (col >= p.cols) return;
-  float sum[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  Two sum[4] = {0, 0, 0, 0};
   with_activation(p.act, [&](auto act) {
     const int64_t step = gridDim.y;
     for (int64_t r = blockIdx.y; r < p.rows; r += step * kUnroll) {
@@ -92,29 +90,29 @@ __global__ void __launch_bounds__(256) agmm_act_grad(const __grid_constant__ Act
       for (int i = 0; i < kUnroll; ++i) {
         const int64_t row = r + i * step;
         if (row < p.rows) {
-          float dv[8];
-          unpack8<kF16>(d[i], dv);
+          Two dv[4];
+          widen<kF16>(d[i], dv);
           if constexpr (act.value != kActNone) {
-            float zv[8];
-            unpack8<kF16>(z[i], zv);
+            Two zv[4];
+            widen<kF16>(z[i], zv);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float a, slope;
+            for (int e = 0; e < 4; ++e) {
+              Two a, slope;
               activate_with_slope<act.value>(zv[e], a, slope);
-              dv[e] *= slope;
+              dv[e] = mul2(dv[e], slope);
             }
-            *reinterpret_cast<uint4*>(p.d_pre + row * p.ld_grad + col) = pack8<kF16>(dv);
+            *reinterpret_cast<uint4*>(p.d_pre + row * p.ld_grad + col) = narrow<kF16>(dv);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] += dv[e];
+          for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], dv[e]);
         }
       }
     }
   });
   if (p.part) {
-    float4* const dst = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.y * p.cols + col);
-    dst[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-    dst[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+    ulonglong2* const dst = reinterpret_cast<ulonglong2*>(p.part + (int64_t)blockIdx.y * p.cols + col);
+    dst[0] = make_ulonglong2(sum[0], sum[1]);
+    dst[1] = make_ulonglong2(sum[2], sum[3]);
   }
 }
 
