@@ -264,6 +264,11 @@ void common_params(const ProductPlan* pl, GemmParams* p, void* workspace) {
   p->seg_blocks = p->k_blocks = 1;
 }
 
+// Cut tiles of full waves are worked on at different places of k, and no longer share what they
+// load while it is in L2: their operands have to fit there all together.  (8192 x 4096 by 14336
+// values, 352 MB of operands: 499 us whole, 562 us cut; 4096 x 2560 by 5120, 68 MB: 76 and 67 us.)
+constexpr int64_t kCutBytes = 80 << 20;
+
 // Row tiles: their width, and whether some are cut, by the shortest estimate.
 struct RowChoice {
   int bn;
@@ -277,7 +282,8 @@ RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int 
     const int64_t tiles = m_tiles * ceil_div(cols, gated ? bn / 2 : bn) * problems;
     if (tiles > kMostTiles) continue;
     const double block = bn == kWideN ? kWideBlock : kNarrowBlock, tile = bn == kWideN ? kWideTile : kNarrowTile;
-    const bool can = can_cut(tiles, k_blocks, pl->pairs);
+    const int64_t bytes = (m_tiles * 2 * kTileM + cols) * problems * k_blocks * kTileK * 2;
+    const bool can = can_cut(tiles, k_blocks, pl->pairs) && (tiles < pl->pairs || bytes <= kCutBytes);
     for (int cut = 0; cut <= (can ? 1 : 0); ++cut) {
       if (pl->cut >= 0 && pl->cut != cut && can) continue;
       const double time = cut ? (double)tiles * k_blocks / pl->pairs * block + (bn == kWideN ? kWideCut : kNarrowCut)
