@@ -265,9 +265,10 @@ void common_params(const ProductPlan* pl, GemmParams* p, void* workspace) {
 }
 
 // Cut tiles of full waves are worked on at different places of k, and no longer share what they
-// load while it is in L2: their operands have to fit there all together.  (8192 x 4096 by 14336
-// values, 352 MB of operands: 499 us whole, 562 us cut; 4096 x 2560 by 5120, 68 MB: 76 and 67 us.)
-constexpr int64_t kCutBytes = 80 << 20;
+// load while it is in L2: their operands have to fit there, more or less.  (8192 x 4096 by 14336
+// values, 352 MB of operands: 499 us whole, 562 us cut; 2048 x 8192 by 7168, 147 MB: 139 and
+// 134 us; 4096 x 2560 by 5120, 68 MB: 76 and 67 us.)
+constexpr int64_t kCutBytes = 160 << 20;
 
 // Row tiles: their width, and whether some are cut, by the shortest estimate.
 struct RowChoice {
@@ -306,13 +307,11 @@ agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice 
   p->num_tiles = p->tiles_per_problem * p->problems;
   p->group_m = kGroupM;
   const bool wide = choice.bn == kWideN;
-  const bool two = wide && p->residual;  // the residual of a tile is staged while its products are made
-  p->stages = two ? kResidualStages : wide ? kWideStages : kNarrowStages;
-  p->stage_out_bytes = two ? 2 * kStageOutBytes : kStageOutBytes;
+  p->stages = wide ? kWideStages : kNarrowStages;
   p->tmem_cols = 2 * choice.bn;
   make_schedule(p, pl->pairs, choice.cut);
   const int clusters = std::min(pl->pairs, std::max(p->dp_tiles, p->sk_clusters));
-  const size_t smem = 1024 + (size_t)p->stages * (kTileBytes + choice.bn * kTileK) + (size_t)kEpiWarps * p->stage_out_bytes + kCtlBytes;
+  const size_t smem = 1024 + (size_t)p->stages * (kTileBytes + choice.bn * kTileK) + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
   return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16), *p, clusters, 2, smem, stream), "product launch");
 }
 

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
   const uint32_t b_slot = (uint32_t)(kSwap ? p.mma_n : kHalf) * 128u;
   const uint32_t a0 = base, b0 = base + (uint32_t)S * a_slot;
   const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results; swapped tiles: other CTAs' parts
-  const uint32_t ctl = out0 + (kSwap ? p.recv_bytes : (uint32_t)kEpiWarps * p.stage_out_bytes);
+  const uint32_t ctl = out0 + (kSwap ? p.recv_bytes : (uint32_t)(kEpiWarps * kStageOutBytes));
   uint8_t* const ctl_ptr = base_ptr + (ctl - base);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kAbortOffset);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctl_ptr + kTmemOffset);
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, ewarp = warp - 2, half = ewarp >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
-    uint8_t* const stage_out = base_ptr + (out0 - base) + (kSwap ? 0u : (uint32_t)ewarp * p.stage_out_bytes);
+    uint8_t* const stage_out = base_ptr + (out0 - base) + ewarp * kStageOutBytes;  // row tiles
     SegmentIter iter;
     iter.init(p, cluster, clusters, rank, split);
     const int first_cut = p.dp_tiles + iter.u / p.k_blocks;  // the tile whose part lies in slot 0
@@ -765,14 +765,11 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       // gated: as many columns of each product, the second's a half of the accumulator on
       const int first_col = kEpi == kEpiGated ? half * (kHalf / 2) : half * kHalf;
       const int64_t tile_col = (int64_t)sg.nt * (kEpi == kEpiGated ? kHalf : kBN) + first_col;
-      auto fetch_residual = [&]() {
+      // columns [c, c + 64) of this warp's half, into its staging buffer
+      auto fetch_residual = [&](int c) {
         if constexpr (!kSwap && kEpi == kEpiLinear) {
-#pragma unroll
-          for (int c = 0; c < kHalf; c += 64) {
-            const int64_t at = tile_col + c + 8 * (lane & 7);
-            stage_rows(stage_out + c / 64 * kStageOutBytes, static_cast<const uint16_t*>(p.residual) + (at < p.cols ? at : 0),
-                       (uint32_t)p.ldr * 2u, rows, at < p.cols, lane);
-          }
+          const int64_t at = tile_col + c + 8 * (lane & 7);
+          stage_rows(stage_out, static_cast<const uint16_t*>(p.residual) + (at < p.cols ? at : 0), (uint32_t)p.ldr * 2u, rows, at < p.cols, lane);
         }
       };
       const bool has_residual = kEpi == kEpiLinear && p.residual != nullptr;
@@ -782,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         const int in_shard = trow - shard * p.shard_chunks * p.box;
         if (shard < p.shards && in_shard < p.shard_rows) out_row = (int)(shard * p.shard_rows) + in_shard;
         block_rows(rows, out_row, lane);
-        if (has_residual && sg.whole) fetch_residual();  // while the products are made
+        if (has_residual && sg.whole) fetch_residual(0);  // while the products are made
       }
       int res = kWaitOk;
       if (lane == 0) res = wait_phase(bar_acc_full(ctl, acc), (uint32_t)(it >> 1) & 1u, abort_flag, limit);
@@ -847,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           release();
           if (!complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
           parts = find_parts(p, sg.tile);
-          if (has_residual) fetch_residual();
+          if (has_residual) fetch_residual(0);
         }
         if constexpr (kEpi == kEpiGated) {
           constexpr int kBlocks = kHalf / 64;  // of 32 columns of results
@@ -889,10 +886,6 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             write_staged<kPieces>(stage_out, static_cast<uint16_t*>(p.saved[1]) + col, (uint32_t)p.lds * 2u, rows, inside, lane);
           }
         } else {
-          if (has_residual) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-          }
           if (kEpi == kEpiPlain && p.out_f32) {
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
@@ -915,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             for (int c = 0; c < kHalf; c += 64) {
               const int64_t col = tile_col + c, at = col + 8 * (lane & 7);  // this lane's piece
               const bool inside = at < p.cols;
-              uint8_t* const stage_c = stage_out + (has_residual ? c / 64 * kStageOutBytes : 0);
+              if (has_residual && c > 0) fetch_residual(c);  // beside the loads and the activation below
               uint32_t z16[2][16];
               const bool has_saved = kEpi == kEpiLinear && p.saved[0] != nullptr;
               uint32_t w[2][1][32];
@@ -949,10 +942,14 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                     for (int i = 0; i < 32; i += 2) set_pair(v, i, activate<act.value>(pair_of(v, i)));
                   });
                   if (has_residual) {
+                    if (h == 0) {
+                      asm volatile("cp.async.wait_all;" ::: "memory");
+                      __syncwarp();
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                       Two r[4];
-                      widen<kF16>(*staged(stage_c, lane, h * 4 + i), r);
+                      widen<kF16>(*staged(stage_out, lane, h * 4 + i), r);
 #pragma unroll
                       for (int e = 0; e < 4; ++e) set_pair(v, 8 * i + 2 * e, add2(pair_of(v, 8 * i + 2 * e), r[e]));
                     }
@@ -960,13 +957,13 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                 }
                 uint32_t o16[16];
                 pack32<kF16>(v, o16);
-                stage_half(stage_c, lane, h, o16);
+                stage_half(stage_out, lane, h, o16);
               }
-              write_staged<8>(stage_c, static_cast<uint16_t*>(p.out[sg.problem]) + at, (uint32_t)p.ldo * 2u, rows, inside, lane);
+              write_staged<8>(stage_out, static_cast<uint16_t*>(p.out[sg.problem]) + at, (uint32_t)p.ldo * 2u, rows, inside, lane);
               if (has_saved) {
-                stage_half(stage_c, lane, 0, z16[0]);
-                stage_half(stage_c, lane, 1, z16[1]);
-                write_staged<8>(stage_c, static_cast<uint16_t*>(p.saved[0]) + at, (uint32_t)p.lds * 2u, rows, inside, lane);
+                stage_half(stage_out, lane, 0, z16[0]);
+                stage_half(stage_out, lane, 1, z16[1]);
+                write_staged<8>(stage_out, static_cast<uint16_t*>(p.saved[0]) + at, (uint32_t)p.lds * 2u, rows, inside, lane);
               }
             }
           }

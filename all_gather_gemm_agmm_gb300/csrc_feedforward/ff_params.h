@@ -18,10 +18,9 @@ constexpr int kTileK = 64;        // one 128-byte swizzle row of 16-bit values
 constexpr int kTileBytes = kTileM * kTileK * 2;  // 16 KiB
 constexpr int kMaxStages = 12;
 constexpr int kWideStages = 6, kNarrowStages = 8;  // 192 KiB of operands beside 32 KiB of staged results
-constexpr int kResidualStages = 5;  // wide tiles that stage a whole tile's residual, 64 KiB
 constexpr int kMaxSplit = 8;
 constexpr int kMaxSwapRows = 64;  // swapped tiles: token columns of a tile, at most
-constexpr int kStageOutBytes = 4096;  // row tiles: a staging buffer of a warp, 32 rows x 128 bytes
+constexpr int kStageOutBytes = 4096;  // row tiles: a warp's staging buffer, 32 rows x 128 bytes
 constexpr int kCtlBytes = 1024;
 constexpr size_t kMaxSmem = 232448;   // 227 KiB
 constexpr int kStatusBytes = 256;     // status words at the start of the workspace
@@ -68,7 +67,6 @@ struct __align__(128) GemmParams {
   int recv_slots;          // ... groups of 8 tokens that each of them owns
   uint32_t recv_bytes;     // ... and their parts, in its shared memory
   int stages;
-  uint32_t stage_out_bytes;  // row tiles: a warp's staging buffers, one or two
   uint32_t tmem_cols;
   // results
   void* out[2];            // by problem

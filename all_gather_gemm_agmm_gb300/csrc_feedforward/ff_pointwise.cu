@@ -31,7 +31,7 @@ __device__ __forceinline__ void gated_grad_piece(const uint4& d16, const uint4& 
   du = narrow<kF16>(u);
 }
 
-constexpr int kUnroll = 2;  // rows whose loads are in flight together
+constexpr int kUnroll = 2, kActUnroll = 4;  // rows whose loads are in flight together
 
 template <bool kF16>
 __global__ void __launch_bounds__(256, 4) agmm_gated_grad(const __grid_constant__ GatedGradParams p) {
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256, 4) agmm_gated_grad(const __grid_constant_
 }
 
 template <bool kF16>
-__global__ void __launch_bounds__(256, 4) agmm_act_grad(const __grid_constant__ ActGradParams p) {
+__global__ void __launch_bounds__(256, 3) agmm_act_grad(const __grid_constant__ ActGradParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
@@ -76,10 +76,10 @@ __global__ void __launch_bounds__(256, 4) agmm_act_grad(const __grid_constant__ 
   Two sum[4] = {0, 0, 0, 0};
   with_activation(p.act, [&](auto act) {
     const int64_t step = gridDim.y;
-    for (int64_t r = blockIdx.y; r < p.rows; r += step * kUnroll) {
-      uint4 d[kUnroll], z[kUnroll];
+    for (int64_t r = blockIdx.y; r < p.rows; r += step * kActUnroll) {
+      uint4 d[kActUnroll], z[kActUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
+      for (int i = 0; i < kActUnroll; ++i) {
         const int64_t row = r + i * step;
         if (row < p.rows) {
           d[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + col);
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256, 4) agmm_act_grad(const __grid_constant__ 
         }
       }
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
+      for (int i = 0; i < kActUnroll; ++i) {
         const int64_t row = r + i * step;
         if (row < p.rows) {
           Two dv[4];
