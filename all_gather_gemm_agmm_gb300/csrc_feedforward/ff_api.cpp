@@ -195,7 +195,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // work through `blocks` k blocks.  Constants as measured (the design doc has the table).
 constexpr double kWideBlock = 512, kNarrowBlock = 340;    // a k block of a row tile's main loop
 constexpr double kWideTile = 4000, kNarrowTile = 2500;    // its results, beside the next tile's main loop
-constexpr double kWideCut = 26000, kNarrowCut = 9000;     // the parts' round trip through L2
+constexpr double kWideCut = 16000, kNarrowCut = 6500;     // the parts' way to L2 and back
+constexpr double kWidePart = 3000, kNarrowPart = 1400;    // ... and each part that is added
 constexpr double kSwapByte = 0.019;                       // swapped tiles: a byte, for one CTA alone
 constexpr double kMemoryByte = 2.84e-4;                   // ... and for each CTA that shares the device's memory
 constexpr double kSplitTile = 1500;                       // ... the parts' way through distributed shared memory
@@ -204,15 +205,15 @@ constexpr double kSplitTile = 1500;                       // ... the parts' way 
 // cut along k evenly over the clusters.
 int cut_tiles(int tiles, int clusters) { return tiles < clusters ? tiles : tiles % clusters ? clusters + tiles % clusters : 0; }
 
-void make_schedule(GemmParams* p, int clusters, bool cut) {
-  const int shared = cut ? cut_tiles(p->num_tiles, clusters) : 0;
+// `parts`: clusters that share the cut tiles (0: none is cut).
+void make_schedule(GemmParams* p, int clusters, int parts) {
+  const int shared = parts ? cut_tiles(p->num_tiles, clusters) : 0;
   const int64_t units = (int64_t)shared * p->k_blocks;
-  const int64_t parts = std::min<int64_t>(clusters, units);
   p->dp_tiles = p->num_tiles - shared;
-  p->sk_clusters = (int)parts;
-  if (parts) {
-    p->sk_share = (int)(units / parts);
-    p->sk_extra = (int)(units % parts);
+  p->sk_clusters = (int)std::min<int64_t>(parts, units);
+  if (p->sk_clusters) {
+    p->sk_share = (int)(units / p->sk_clusters);
+    p->sk_extra = (int)(units % p->sk_clusters);
   }
 }
 
@@ -270,29 +271,38 @@ void common_params(const ProductPlan* pl, GemmParams* p, void* workspace) {
 // 134 us; 4096 x 2560 by 5120, 68 MB: 76 and 67 us.)
 constexpr int64_t kCutBytes = 160 << 20;
 
-// Row tiles: their width, and whether some are cut, by the shortest estimate.
+// Row tiles: their width, and the clusters that share cut ones (0: none is cut), by the shortest
+// estimate.
 struct RowChoice {
-  int bn;
-  bool cut;
+  int bn, parts;
 };
 RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int k_blocks, int problems, bool gated) {
-  RowChoice best = {kWideN, false};
+  RowChoice best = {kWideN, 0};
   double least = 1e300;
+  const int C = pl->pairs;
   for (int bn = kWideN; bn >= kNarrowN; bn -= kWideN - kNarrowN) {
     if (pl->bn >= 0 && pl->bn != bn) continue;
     const int64_t tiles = m_tiles * ceil_div(cols, gated ? bn / 2 : bn) * problems;
     if (tiles > kMostTiles) continue;
-    const double block = bn == kWideN ? kWideBlock : kNarrowBlock, tile = bn == kWideN ? kWideTile : kNarrowTile;
-    const int64_t bytes = (m_tiles * 2 * kTileM + cols) * problems * k_blocks * kTileK * 2;
-    const bool can = can_cut(tiles, k_blocks, pl->pairs) && (tiles < pl->pairs || bytes <= kCutBytes);
-    for (int cut = 0; cut <= (can ? 1 : 0); ++cut) {
-      if (pl->cut >= 0 && pl->cut != cut && can) continue;
-      const double time = cut ? (double)tiles * k_blocks / pl->pairs * block + (bn == kWideN ? kWideCut : kNarrowCut)
-                              : (double)ceil_div(tiles, pl->pairs) * std::max(k_blocks * block, tile);
+    const bool wide = bn == kWideN;
+    const double block = wide ? kWideBlock : kNarrowBlock, tile = wide ? kWideTile : kNarrowTile;
+    const double cut = wide ? kWideCut : kNarrowCut, part = wide ? kWidePart : kNarrowPart;
+    const auto offer = [&](double time, int parts) {
       if (time < least) {
         least = time;
-        best = {bn, cut != 0};
+        best = {bn, parts};
       }
+    };
+    const int64_t bytes = (m_tiles * 2 * kTileM + cols) * problems * k_blocks * kTileK * 2;
+    const bool can = can_cut(tiles, k_blocks, C) && (tiles < C || bytes <= kCutBytes) && pl->cut != 0;
+    if (!can || pl->cut != 1) offer((double)ceil_div(tiles, C) * std::max(k_blocks * block, tile), 0);
+    if (!can) continue;
+    if (tiles > C) {
+      offer(std::max(k_blocks * block, tile) * tiles / C + cut + 2 * part, C);
+    } else {
+      // every tile in `n` parts, or all clusters at work
+      for (int64_t n = 2; n * tiles <= C && n <= k_blocks; ++n) offer(ceil_div(k_blocks, n) * block + cut + n * part, (int)(n * tiles));
+      offer(k_blocks * block * tiles / C + cut + (double)(ceil_div(C, tiles) + 1) * part, C);
     }
   }
   return best;
@@ -309,7 +319,7 @@ agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice 
   const bool wide = choice.bn == kWideN;
   p->stages = wide ? kWideStages : kNarrowStages;
   p->tmem_cols = 2 * choice.bn;
-  make_schedule(p, pl->pairs, choice.cut);
+  make_schedule(p, pl->pairs, choice.parts);
   const int clusters = std::min(pl->pairs, std::max(p->dp_tiles, p->sk_clusters));
   const size_t smem = 1024 + (size_t)p->stages * (kTileBytes + choice.bn * kTileK) + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
   return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16), *p, clusters, 2, smem, stream), "product launch");
@@ -341,7 +351,7 @@ agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t fe
   p->stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - 1024 - kCtlBytes - p->recv_bytes) / stage);
   p->tmem_cols = 32;
   while ((int)p->tmem_cols < 2 * accs * p->mma_n) p->tmem_cols *= 2;
-  make_schedule(p, pl->clusters[1], false);
+  make_schedule(p, pl->clusters[1], 0);
   const int clusters = p->split > 1 ? tiles : std::min(pl->clusters[1], tiles);
   const size_t smem = 1024 + p->stages * stage + p->recv_bytes + kCtlBytes;
   return check_cuda(launch_gemm(select_gemm(0, epi, pl->f16), *p, clusters, p->split, smem, stream), "product launch");
