@@ -388,34 +388,6 @@ __device__ __forceinline__ void stage_half(uint8_t* stage, int lane, int half, c
   for (int i = 0; i < 4; ++i) *staged(stage, lane, half * 4 + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int c0, int c1) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1) : "memory");
-}
-__device__ __forceinline__ void prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
-
-// Swapped tiles: the weights of the first `blocks` k blocks of a segment.
-template <int kAccs>
-__device__ __forceinline__ void prefetch_weights(const GemmParams& p, const Segment& sg, int row, int blocks) {
-  const int end = min(sg.kb1, sg.kb0 + blocks);
-  for (int kb = sg.kb0; kb < end; ++kb) {
-    const int seg = kb / p.seg_blocks, ko = (kb - seg * p.seg_blocks) * kTileK;
-    for (int t = 0; t < kAccs; ++t) {
-      const CUtensorMap* const map = p.a_map + seg * p.a.by_segment + t;
-      if (!p.a.mn_major) {
-        prefetch_2d(map, ko, row);
-      } else if (p.a.blocked) {
-        prefetch_4d(map, 0, ko, row >> 6, 0);
-      } else {
-        prefetch_4d(map, row, ko, 0, 0);
-        prefetch_4d(map, row + 64, ko, 0, 0);
-      }
-    }
-  }
-}
-
 // kBN: columns of a row tile (0: swapped tiles).
 template <int kBN, int kEpi, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constant__ GemmParams p) {
@@ -557,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         phase = next_phase;
       }
     };
-    bool begun = false;
+    ptx::griddep_wait();  // no access to global memory before this, in any role
     while (ok && iter.next(p, sg)) {
       const int row_tile = kPair ? sg.mt * 2 + rank : sg.mt;
       // Chunks of the tokens in a stage.  One to a stage is the elected lane's, with operands
@@ -571,13 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       const int b_row = kSwap ? row0 : sg.nt * p.b_tile_step + rank * p.b_half_step;
       const int a_row = kSwap || p.a.mn_major ? row_tile * kTileM : row0;
       int seg = sg.kb0 / p.seg_blocks;
-      if (!begun) {
-        // The first stages' weights, into L2 while the kernel before this one ends: only a hint,
-        // so it does not matter whether that one writes them.
-        if (kSwap && leader) prefetch_weights<kAccs>(p, sg, row_tile * kTileM, S);
-        ptx::griddep_wait();  // no access to global memory before this, in any role
-        begun = true;
-      }
       for (int kb = sg.kb0; ok && kb < sg.kb1; ++seg) {
         const int end = min(sg.kb1, (seg + 1) * p.seg_blocks);
         const int ko = (kb - seg * p.seg_blocks) * kTileK, a_z = seg * p.a.z_segment, b_z = seg * p.b.z_segment;
@@ -800,9 +765,6 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             ptx::mbar_arrive(bar_acc_empty(ctl, acc));
         }
       };
-      int* const counter =
-          sg.whole ? nullptr : p.counters + ((size_t)(sg.tile - p.dp_tiles) * kCtas + rank) * kEpiWarps + ewarp;
-
       if constexpr (kSwap) {
         // This lane's column of the weights, and this warp's half of the tokens, 8 at a time.
         const int n = p.mma_n, end = min((half + 1) * (n / 2), p.chunks * p.box);
@@ -842,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             store_part<32>(slot, c, lane, v);
           }
           release();
+          int* const counter = p.counters + ((size_t)(sg.tile - p.dp_tiles) * kCtas + rank) * kEpiWarps + ewarp;
           if (!complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
           parts = find_parts(p, sg.tile);
           if (has_residual) fetch_residual(0);

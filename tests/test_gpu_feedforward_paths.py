@@ -30,7 +30,7 @@ def name(env):
 
 
 # shards, rows, k, n: one row to several tiles, sizes that end inside tiles and k blocks
-SIZES = [(1, 1, 1000, 264), (3, 13, 584, 136), (2, 200, 1032, 648)]
+SIZES = [(1, 1, 1000, 264), (3, 13, 584, 136), (8, 7, 520, 264), (2, 200, 1032, 648)]
 
 
 @pytest.mark.parametrize("env", ROWS + SWAP, ids=name)

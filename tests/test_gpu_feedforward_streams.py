@@ -149,3 +149,26 @@ def test_one_workspace_for_all_calls_of_a_stream(agmm):
         a.run(x, w, o.fill_(0), ws)
         b.run(u, v, v, p.fill_(0), ws)
         assert torch.equal(o, want[0]) and torch.equal(p, want[1])
+
+
+def test_plans_made_while_capturing(agmm):
+    """A plan asks the device for attributes only: it may be made inside a capture."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    new = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, w, y = new(40, 328), new(328, 152), new(40, 2056)
+    want = agmm.gated_matmul(x, w, w, "gelu"), agmm.layer_norm(y)
+    out, normed = torch.zeros_like(want[0]), torch.zeros_like(y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan = agmm.GatedPlan(328, 152, activation="gelu")
+        ws = plan.new_workspace()
+        plan.run(x, w, w, out, ws)
+        norm = agmm.LayerNormPlan(2056)
+        norm.run(y, normed)
+    for _ in range(2):
+        out.zero_()
+        normed.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(normed, want[1])
