@@ -87,8 +87,36 @@ __device__ __forceinline__ uint4 input_grad(const GradPiece& q, float rstd, floa
 
 constexpr int kWarpRowWarps = 4;
 
+// The statistics of a row that a team holds, x less its mean on return.
+template <bool kWarpRow, int kPieces>
+__device__ __forceinline__ float2 row_stats(Two (&x)[kPieces][4], int t, int team, int cols, float eps, float (&s)[2][32]) {
+  const float inv = 1.0f / (float)cols;
+  Two sum = 0, squares = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if ((t + i * team) * 8 < cols) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = add2(sum, x[i][e]);
+    }
+  }
+  const float mean = team_sum<kWarpRow>(sum2(sum), s[0]) * inv;
+  const Two minus = both(-mean);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if ((t + i * team) * 8 < cols) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[i][e] = add2(x[i][e], minus);
+        squares = fma2(x[i][e], x[i][e], squares);
+      }
+    }
+  }
+  return make_float2(mean, rsqrtf(team_sum<kWarpRow>(sum2(squares), s[1]) * inv + eps));
+}
+
+// One row to a team: short rows (a warp to each), few long ones, and the longest.
 template <bool kF16, bool kWarpRow, int kPieces>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : kPieces == 1 ? 1024 : 512) agmm_layer_norm(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : 1024) agmm_layer_norm(const __grid_constant__ NormParams p) {
   __shared__ float s[2][32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -102,33 +130,14 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : kPieces == 1 ?
     const int c = (t + i * team) * 8;
     if (c < p.cols) in[i] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + c);
   }
-  Two x[kPieces][4], sum = 0;
+  Two x[kPieces][4];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    if ((t + i * team) * 8 < p.cols) {
-      widen<kF16>(in[i], x[i]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum = add2(sum, x[i][e]);
-    }
-  }
-  const float inv = 1.0f / (float)p.cols;
-  const float mean = team_sum<kWarpRow>(sum2(sum), s[0]) * inv;
-  const Two minus = both(-mean);
-  Two squares = 0;
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    if ((t + i * team) * 8 < p.cols) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[i][e] = add2(x[i][e], minus);
-        squares = fma2(x[i][e], x[i][e], squares);
-      }
-    }
-  }
-  const float rstd = rsqrtf(team_sum<kWarpRow>(sum2(squares), s[1]) * inv + p.eps);
+  for (int i = 0; i < kPieces; ++i)
+    if ((t + i * team) * 8 < p.cols) widen<kF16>(in[i], x[i]);
+  const float2 stats = row_stats<kWarpRow>(x, t, team, p.cols, p.eps, s);
   if (t == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
+    if (p.mean) p.mean[row] = stats.x;
+    if (p.rstd) p.rstd[row] = stats.y;
   }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
@@ -136,7 +145,60 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kWarpRowWarps : kPieces == 1 ?
     if (c < p.cols) {
       const uint4 w = p.weight ? __ldg(reinterpret_cast<const uint4*>(p.weight + c)) : ones<kF16>();
       const uint4 b = p.bias ? __ldg(reinterpret_cast<const uint4*>(p.bias + c)) : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = scaled<kF16>(x[i], rstd, w, b);
+      *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = scaled<kF16>(x[i], stats.y, w, b);
+    }
+  }
+}
+
+// Weights are read again for every row (they stay in L1): held over the rows, their registers
+// would be another block's.
+__device__ __forceinline__ uint4 load_again(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Many long rows: a block walks over rows, four pieces to a thread, and loads the next row
+// beside this one's sums.  16384 x 8192: 87 us, 6.2 TB/s; a block to each row 93 us; rows through
+// shared memory 114 us; two pieces to a thread 106 us.  (Rows of 16384 values need 512 threads and
+// leave room for one block: 64 us so, 55 us with a block to each row.)
+template <bool kF16>
+__global__ void __launch_bounds__(256, 3) agmm_layer_norm_rows(const __grid_constant__ NormParams p) {
+  constexpr int kPieces = 4;
+  __shared__ float s[2][32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int t = threadIdx.x, team = blockDim.x;
+  const int64_t step = gridDim.x;
+  uint4 in[kPieces];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int c = (t + i * team) * 8;
+      if (c < p.cols) in[i] = __ldcs(reinterpret_cast<const uint4*>(p.x + row * p.ldx + c));
+    }
+  };
+  fetch(blockIdx.x);
+#pragma unroll 1
+  for (int64_t row = blockIdx.x; row < p.rows; row += step) {
+    Two x[kPieces][4];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if ((t + i * team) * 8 < p.cols) widen<kF16>(in[i], x[i]);
+    if (row + step < p.rows) fetch(row + step);
+    const float2 stats = row_stats<false>(x, t, team, p.cols, p.eps, s);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = stats.x;
+      if (p.rstd) p.rstd[row] = stats.y;
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int c = (t + i * team) * 8;
+      if (c < p.cols) {
+        const uint4 w = p.weight ? load_again(p.weight + c) : ones<kF16>();
+        const uint4 b = p.bias ? load_again(p.bias + c) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = scaled<kF16>(x[i], stats.y, w, b);
+      }
     }
   }
 }
@@ -439,7 +501,11 @@ cudaError_t launch_norm_t(const NormParams& p, int sms, cudaStream_t stream) {
   }
   if (p.rows <= 2 * sms && pieces <= 1024)
     return launch(&agmm_layer_norm<kF16, false, 1>, p, (unsigned)p.rows, round_warp(pieces), 0, stream);
-  return launch(&agmm_layer_norm<kF16, false, 4>, p, (unsigned)p.rows, round_warp((pieces + 3) / 4), 0, stream);
+  const int threads = round_warp((pieces + 3) / 4);
+  if (pieces > 1024) return launch(&agmm_layer_norm<kF16, false, 4>, p, (unsigned)p.rows, threads, 0, stream);
+  // twelve blocks to an SM, more than it holds at once: they end apart
+  const int64_t blocks = p.rows < (int64_t)sms * 12 ? p.rows : (int64_t)sms * 12;
+  return launch(&agmm_layer_norm_rows<kF16>, p, (unsigned)blocks, threads, 0, stream);
 }
 
 template <bool kF16>
