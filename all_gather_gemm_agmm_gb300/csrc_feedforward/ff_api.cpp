@@ -149,17 +149,25 @@ size_t partial_bytes(const ProductPlan* pl) { return (size_t)pl->sms * kSlots * 
 size_t workspace_bytes(const ProductPlan* pl) { return AGMM_FEEDFORWARD_HEAD_BYTES + partial_bytes(pl); }
 
 // -------------------------------------------------------------- tensor maps
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+struct TensorMapCalls {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  PFN_cuTensorMapReplaceAddress_v12000 replace = nullptr;
+};
+const TensorMapCalls& tensor_map_calls() {
+  static TensorMapCalls calls;
   static std::once_flag once;
   std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    const auto find = [](const char* name) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      return cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess
+                 ? f
+                 : nullptr;
+    };
+    calls.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(find("cuTensorMapEncodeTiled"));
+    calls.replace = reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(find("cuTensorMapReplaceAddress"));
   });
-  return fn;
+  return calls;
 }
 
 // A matrix of 16-bit values: rows of `inner` values, `stride` apart, in segments.
@@ -172,21 +180,49 @@ struct Matrix {
 // A matrix as an operand that is contracted along its rows' values (K-major), or along its rows
 // (MN-major); a tile has tile_rows of its rows or values.  128-byte swizzled, zeros outside: what lies
 // behind a segment's last row is not its neighbour's.
+//
+// Encoding takes the driver half a microsecond, and a training step has ten maps: a thread keeps
+// those of its latest layouts (sizes and strides, whatever the memory) and puts the address in.
 agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m, bool mn_major, int tile_rows, bool f16) {
-  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return fail(AGMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const TensorMapCalls& calls = tensor_map_calls();
+  if (!calls.encode || !calls.replace) return fail(AGMM_ERR_CUDA, "tensor maps are not available from the driver");
   o->mn_major = mn_major;
   o->blocked = mn_major && m.inner % 64 == 0;
-  const cuuint64_t inner = (cuuint64_t)m.inner, rows = (cuuint64_t)m.rows, step = (cuuint64_t)m.stride * 2;
-  const cuuint64_t blocks = o->blocked ? inner / 64 : 1;
-  const cuuint64_t dims[4] = {inner / blocks, rows, blocks, (cuuint64_t)m.segments};
-  const cuuint64_t strides[3] = {step, o->blocked ? 128 : step, (m.segments > 1 ? rows : 1) * step};
-  const cuuint32_t box[4] = {kTileK, (cuuint32_t)(mn_major ? 64 : tile_rows),
-                             (cuuint32_t)(o->blocked ? tile_rows / 64 : 1), 1}, one[4] = {1, 1, 1, 1};
-  const CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mn_major ? 4 : 2,
-                         const_cast<void*>(m.ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(AGMM_ERR_CUDA, "tensor map of %s: cuTensorMapEncodeTiled gave %d", m.name, (int)r);
+  struct Layout {
+    int64_t inner, rows, segments, stride, kind;
+    bool operator==(const Layout& x) const {
+      return inner == x.inner && rows == x.rows && segments == x.segments && stride == x.stride && kind == x.kind;
+    }
+  };
+  struct Known {
+    Layout layout = {};
+    CUtensorMap map;
+  };
+  constexpr int kKnown = 64;
+  thread_local Known known[kKnown];
+  const Layout l = {m.inner, m.rows, m.segments, m.stride, (int64_t)tile_rows * 4 + (mn_major ? 2 : 0) + (f16 ? 1 : 0)};
+  const uint64_t mix = ((uint64_t)l.inner * 0x9e3779b97f4a7c15ull) ^ ((uint64_t)l.rows * 0xc2b2ae3d27d4eb4full) ^
+                       ((uint64_t)l.stride * 0x165667b19e3779f9ull) ^ ((uint64_t)(l.segments * 1024 + l.kind) * 0xd6e8feb86659fd93ull);
+  Known& k = known[(mix >> 32) % kKnown];
+  CUresult r = CUDA_SUCCESS;
+  if (!(k.layout == l)) {
+    const cuuint64_t inner = (cuuint64_t)m.inner, rows = (cuuint64_t)m.rows, step = (cuuint64_t)m.stride * 2;
+    const cuuint64_t blocks = o->blocked ? inner / 64 : 1;
+    const cuuint64_t dims[4] = {inner / blocks, rows, blocks, (cuuint64_t)m.segments};
+    const cuuint64_t strides[3] = {step, o->blocked ? 128 : step, (m.segments > 1 ? rows : 1) * step};
+    const cuuint32_t box[4] = {kTileK, (cuuint32_t)(mn_major ? 64 : tile_rows), (cuuint32_t)(o->blocked ? tile_rows / 64 : 1), 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    k.layout = {};
+    r = calls.encode(&k.map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mn_major ? 4 : 2,
+                     const_cast<void*>(m.ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) k.layout = l;
+  }
+  if (r == CUDA_SUCCESS) {
+    *map = k.map;
+    r = calls.replace(map, const_cast<void*>(m.ptr));
+  }
+  if (r != CUDA_SUCCESS) return fail(AGMM_ERR_CUDA, "tensor map of %s: the driver gave %d", m.name, (int)r);
   return AGMM_OK;
 }
 

@@ -115,7 +115,8 @@ class _FeedForwardPlan(_AttentionPlan):
         if x.shape != (rows, cols) or stride[1] != 1:
             raise ValueError(f"{name} must be [{rows}, {cols}] with a contiguous last dimension, "
                              f"got {tuple(x.shape)} with strides {stride}")
-        self._check(name, x, dtype)
+        if x.dtype is not (dtype or self.dtype) or x.get_device() != self._index or x.requires_grad:
+            self._check(name, x, dtype)
         return x.data_ptr(), stride[0]
 
     def _check(self, name, x, dtype):
@@ -123,6 +124,13 @@ class _FeedForwardPlan(_AttentionPlan):
             raise ValueError(f"{name} must be {dtype or self.dtype} on {self.device}, got {x.dtype} on {x.device}")
         if x.requires_grad and self._grad_mode():
             raise ValueError(f"{name} requires grad, and nothing is recorded here: call under torch.no_grad()")
+
+    def _workspace(self, workspace):
+        if workspace.get_device() != self._index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {self.device}")
+        if workspace.nbytes < self._workspace_size:
+            raise ValueError(f"workspace needs {self._workspace_size} bytes")
+        return workspace.data_ptr()
 
     def _pair(self, names, xs, rows, cols, dtype=None):
         """(pointer, pointer, row stride) of two [rows, cols] tensors laid out alike."""
@@ -138,7 +146,8 @@ class _FeedForwardPlan(_AttentionPlan):
             return 0
         if x.shape != (size,) or not x.is_contiguous():
             raise ValueError(f"{name} must be a contiguous vector of {size}, got {tuple(x.shape)} with strides {x.stride()}")
-        self._check(name, x, dtype)
+        if x.dtype is not (dtype or self.dtype) or x.get_device() != self._index or x.requires_grad:
+            self._check(name, x, dtype)
         return x.data_ptr()
 
     def _grad_type(self, a, b):
@@ -213,11 +222,13 @@ class _ProductPlan(_FeedForwardPlan):
         if not 1 <= len(xs) <= MAX_SHARDS:
             raise ValueError(f"X must be 1 to {MAX_SHARDS} shards, got {len(xs)}")
         rows = xs[0].shape[0]
-        got = [self._matrix("a shard of X", x, rows, self.k) for x in xs]
-        stride = got[0][1]
-        if rows > 1 and any(s != stride for _, s in got):
-            raise ValueError(f"the shards of X must share one row stride, got {[s for _, s in got]}")
-        return len(xs), rows, [p for p, _ in got] + [0] * (MAX_SHARDS - len(xs)), stride
+        ptrs, stride = [0] * MAX_SHARDS, 0
+        for i, x in enumerate(xs):
+            ptrs[i], s = self._matrix("a shard of X", x, rows, self.k)
+            if i and rows > 1 and s != stride:
+                raise ValueError(f"the shards of X must share one row stride, got {stride} and {s}")
+            stride = s
+        return len(xs), rows, ptrs, stride
 
 
 class GatedPlan(_ProductPlan):
