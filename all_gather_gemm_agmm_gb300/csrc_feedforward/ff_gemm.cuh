@@ -17,14 +17,21 @@
 //                  own rows and half of the columns' operand.  Gated: the leader's half
 //                  is columns of the gate's weight, the follower's the same columns of
 //                  the other, so both products of an output value land in one thread.
-//                  Bound: the tensor cores.
+//                  Bound: the tensor cores, active in 91 to 97 % of the cycles: 8192 x 4096 x
+//                  14336 490-496 us (1.94-1.96 PFLOP/s), its gradients 490 and 496 us, in bursts;
+//                  in long runs the power limit.  Wide tiles read 64 bytes a cycle of each
+//                  SM from L2, all it gives; narrow ones would need 70, and take 340 cycles a k
+//                  block of 256.  One CTA with 128 x 128 tiles would need twice that.
 //   swapped tiles  for up to 64 tokens: 128 columns of the weights are the MMA's rows
 //                  and all tokens its columns, so that each thread of the epilogue has
 //                  one column of the weights and only the tokens that there are.
-//                  Bound: the weights' bytes.
+//                  Bound: the weights' bytes: one token of 4096 -> 2 x 7168 22 us (5.4 TB/s, 4 us
+//                  of them start and end), 64 tokens 25 us; row tiles take 39 and 28 us.  Above
+//                  64 tokens narrow row tiles win (128 tokens of 2048 -> 2 x 2048: 13 against 20 us).
 //
 // Work: cluster c takes whole tiles in turn.  Where few tiles leave SMs idle, k is shared:
-// swapped tiles by the CTAs of a cluster, whose parts meet in distributed shared memory; row
+// swapped tiles by the CTAs of a cluster, whose parts meet in distributed shared memory (1 us;
+// through L2 it was 4 us: one token of 7168 -> 4096 13 and 16 us); row
 // tiles (those of a ragged last wave and the wave before it) evenly over the clusters.  Every
 // warp of a cut row tile's epilogue leaves its float32 partial results in the workspace and
 // counts its k blocks; the warp that completes the count adds all parts and goes on to the

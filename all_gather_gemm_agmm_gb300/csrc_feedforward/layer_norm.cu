@@ -9,7 +9,10 @@
 // warp for short rows, else the block) holds a row in registers, 8 values to a piece, so
 // the variance is a sum of squares about the mean and not a difference of large numbers.
 // The backward pass keeps a team on its columns: the sums for dw and db stay in
-// registers while it walks over the rows, and each block leaves one part of them.
+// registers while it walks over the rows, and each block leaves one part of them.  Arithmetic is
+// on pairs of values: with single ones both passes were bound by instructions (2.8 of 4 a cycle).
+// Measured, 16384 x 8192: forward 88 us (6.1 TB/s), backward with a gradient to add 172 us (6.2 TB/s,
+// 5 us of it the parts' sums), without one 154 us (5.2 TB/s).
 #include "ff_math.cuh"
 #include "ptx_sm103.cuh"
 
@@ -312,7 +315,8 @@ __global__ void __launch_bounds__(32 * kWarpRowWarps) agmm_layer_norm_grad_short
 }
 
 // Other rows: a block to kRows rows, the rows streaming through shared memory.  Two rows to a
-// turn: their sums meet in one barrier, and the latency of one row's sums hides behind the other.
+// turn: their sums meet in one barrier, and the latency of one row's sums hides behind the other
+// (16384 x 8192: 177 us with one row to a turn; 236 us with four pieces to a thread and two blocks to an SM).
 template <bool kF16, int kPieces, int kRows>
 __global__ void __launch_bounds__(512, 1) agmm_layer_norm_grad(const __grid_constant__ NormGradParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
