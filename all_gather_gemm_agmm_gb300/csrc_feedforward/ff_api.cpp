@@ -32,6 +32,7 @@ struct ProductPlan {
   int device, sms;
   int pairs;                  // CTA pairs that run at once
   int clusters[kMaxSplit + 1];  // clusters of that many CTAs that do
+  int joined[kMaxPairs + 1];    // clusters of that many pairs that do
   int path, bn, cut, split;   // overrides for tests and experiments; -1: by the rules
   uint64_t wait_limit_cycles;
   int test_drop;
@@ -235,6 +236,7 @@ constexpr double kWideBlock = 512, kNarrowBlock = 340;    // a k block of a row 
 constexpr double kWideTile = 4000, kNarrowTile = 2500;    // its results, beside the next tile's main loop
 constexpr double kWideCut = 16000, kNarrowCut = 6500;     // the parts' way to L2 and back
 constexpr double kWidePart = 3000, kNarrowPart = 1400;    // ... and each part that is added
+constexpr double kJoinTile = 3500;                        // pairs' parts in distributed shared memory
 constexpr double kSwapByte = 0.019;                       // swapped tiles: a byte, for one CTA alone
 constexpr double kMemoryByte = 2.84e-4;                   // ... and for each CTA that shares the device's memory
 constexpr double kSplitTile = 1500;                       // ... the parts' way through distributed shared memory
@@ -301,6 +303,7 @@ void common_params(const ProductPlan* pl, GemmParams* p, void* workspace) {
   p->f16 = pl->f16;
   p->problems = 1;
   p->seg_blocks = p->k_blocks = 1;
+  p->split = 1;
 }
 
 // Cut tiles of full waves are worked on at different places of k, and no longer share what they
@@ -312,10 +315,10 @@ constexpr int64_t kCutBytes = 160 << 20;
 // Row tiles: their width, and the clusters that share cut ones (0: none is cut), by the shortest
 // estimate.
 struct RowChoice {
-  int bn, parts;
+  int bn, parts, split;  // split: pairs of a cluster that share a tile
 };
 RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int k_blocks, int problems, bool gated) {
-  RowChoice best = {kWideN, 0};
+  RowChoice best = {kWideN, 0, 1};
   double least = 1e300;
   const int C = pl->pairs;
   for (int bn = kWideN; bn >= kNarrowN; bn -= kWideN - kNarrowN) {
@@ -325,22 +328,31 @@ RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int 
     const bool wide = bn == kWideN;
     const double block = wide ? kWideBlock : kNarrowBlock, tile = wide ? kWideTile : kNarrowTile;
     const double cut = wide ? kWideCut : kNarrowCut, part = wide ? kWidePart : kNarrowPart;
-    const auto offer = [&](double time, int parts) {
+    const auto offer = [&](double time, int parts, int split) {
       if (time < least) {
         least = time;
-        best = {bn, parts};
+        best = {bn, parts, split};
       }
     };
+    bool joined = false;
+    if (!wide && pl->cut != 1) {
+      for (int n = 2; n <= kMaxPairs && n <= k_blocks && tiles <= pl->joined[n]; ++n) {
+        if (pl->split >= 1 && n != pl->split) continue;
+        joined = true;
+        offer(ceil_div(k_blocks, n) * block + kJoinTile, 0, n);
+      }
+    }
+    if (joined && pl->split > 1) continue;
     const int64_t bytes = (m_tiles * 2 * kTileM + cols) * problems * k_blocks * kTileK * 2;
     const bool can = can_cut(tiles, k_blocks, C) && (tiles < C || bytes <= kCutBytes) && pl->cut != 0;
-    if (!can || pl->cut != 1) offer((double)ceil_div(tiles, C) * std::max(k_blocks * block, tile), 0);
+    if (!can || pl->cut != 1) offer((double)ceil_div(tiles, C) * std::max(k_blocks * block, tile), 0, 1);
     if (!can) continue;
     if (tiles > C) {
-      offer(std::max(k_blocks * block, tile) * tiles / C + cut + 2 * part, C);
+      offer(std::max(k_blocks * block, tile) * tiles / C + cut + 2 * part, C, 1);
     } else {
       // every tile in `n` parts, or all clusters at work
-      for (int64_t n = 2; n * tiles <= C && n <= k_blocks; ++n) offer(ceil_div(k_blocks, n) * block + cut + n * part, (int)(n * tiles));
-      offer(k_blocks * block * tiles / C + cut + (double)(ceil_div(C, tiles) + 1) * part, C);
+      for (int64_t n = 2; n * tiles <= C && n <= k_blocks; ++n) offer(ceil_div(k_blocks, n) * block + cut + n * part, (int)(n * tiles), 1);
+      offer(k_blocks * block * tiles / C + cut + (double)(ceil_div(C, tiles) + 1) * part, C, 1);
     }
   }
   return best;
@@ -354,13 +366,17 @@ agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice 
   p->tiles_per_problem = p->m_tiles * p->n_tiles;
   p->num_tiles = p->tiles_per_problem * p->problems;
   p->group_m = (int)std::min<int64_t>(16, std::max<int64_t>(8, kBandBytes / ((int64_t)2 * kTileM * p->k_blocks * kTileK * 2)));
-  const bool wide = choice.bn == kWideN;
-  p->stages = wide ? kWideStages : kNarrowStages;
+  const size_t stage = kTileBytes + choice.bn * kTileK;
+  p->split = choice.split;
+  // a pair owns every split-th quarter of its rows, in two halves of the columns
+  p->recv_bytes = choice.split > 1 ? (uint32_t)(ceil_div(4, choice.split) * 2 * choice.split * 32 * 64 * sizeof(float)) : 0;
+  const size_t rest = 1024 + (size_t)kEpiWarps * kStageOutBytes + p->recv_bytes + kCtlBytes;
+  p->stages = (int)std::min<size_t>(choice.bn == kWideN ? kWideStages : kNarrowStages, (kMaxSmem - rest) / stage);
   p->tmem_cols = 2 * choice.bn;
   make_schedule(p, pl->pairs, choice.parts);
-  const int clusters = std::min(pl->pairs, std::max(p->dp_tiles, p->sk_clusters));
-  const size_t smem = 1024 + (size_t)p->stages * (kTileBytes + choice.bn * kTileK) + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
-  return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16), *p, clusters, 2, smem, stream), "product launch");
+  const int clusters = choice.split > 1 ? p->num_tiles : std::min(pl->pairs, std::max(p->dp_tiles, p->sk_clusters));
+  return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16), *p, clusters, 2 * choice.split, rest + p->stages * stage, stream),
+                    "product launch");
 }
 
 agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t features, cudaStream_t stream) {
@@ -526,6 +542,10 @@ agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int tran
     for (int bn : {kNarrowN, kWideN}) {
       AGMM_TRY(check_cuda(prepare_gemm(select_gemm(bn, epi, pl->f16), 2, &fit), "kernel attributes"));
       pl->pairs = std::min(pl->pairs, fit);
+    }
+    for (int n = 2; n <= kMaxPairs; ++n) {
+      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(kNarrowN, epi, pl->f16), 2 * n, &fit), "kernel attributes"));
+      pl->joined[n] = epi == kEpiPlain ? fit : std::min(pl->joined[n], fit);
     }
     for (int split = 1; split <= kMaxSplit; ++split) {
       AGMM_TRY(check_cuda(prepare_gemm(select_gemm(0, epi, pl->f16), split, &fit), "kernel attributes"));

@@ -29,10 +29,10 @@
 //                  of them start and end), 64 tokens 25 us; row tiles take 39 and 28 us.  Above
 //                  64 tokens narrow row tiles win (128 tokens of 2048 -> 2 x 2048: 13 against 20 us).
 //
-// Work: cluster c takes whole tiles in turn.  Where few tiles leave SMs idle, k is shared:
-// swapped tiles by the CTAs of a cluster, whose parts meet in distributed shared memory (1 us;
-// through L2 it was 4 us: one token of 7168 -> 4096 13 and 16 us); row
-// tiles (those of a ragged last wave and the wave before it) evenly over the clusters.  Every
+// Work: cluster c takes whole tiles in turn.  Where few tiles leave SMs idle, k is shared: by
+// the CTAs (narrow row tiles: two to four pairs) of a cluster, whose parts meet in distributed
+// shared memory (1 us; through L2 it was 4 us: one token of 7168 -> 4096 13 and 16 us).  Row tiles
+// of a ragged last wave, and the wave before it, are cut evenly over the clusters.  Every
 // warp of a cut row tile's epilogue leaves its float32 partial results in the workspace and
 // counts its k blocks; the warp that completes the count adds all parts and goes on to the
 // results.  Nobody waits for another cluster, and parts are added in the order of k.
@@ -125,12 +125,12 @@ __device__ __forceinline__ int first_unit(const GemmParams& p, int cluster) {
 }
 
 struct SegmentIter {
-  int u, hi, next_dp, clusters, rank, split;
+  int u, hi, next_dp, clusters, part, split;
 
-  __device__ __forceinline__ void init(const GemmParams& p, int cluster, int nclusters, int cta_rank, int splits) {
+  __device__ __forceinline__ void init(const GemmParams& p, int cluster, int nclusters, int k_part, int splits) {
     clusters = nclusters;
     next_dp = cluster;
-    rank = cta_rank;
+    part = k_part;
     split = splits;
     u = hi = 0;
     if (cluster < p.sk_clusters) {
@@ -148,8 +148,8 @@ struct SegmentIter {
       u += s.kb1 - s.kb0;
     } else if (next_dp < p.dp_tiles) {
       s.tile = next_dp;
-      s.kb0 = split > 1 ? p.k_blocks * rank / split : 0;
-      s.kb1 = split > 1 ? p.k_blocks * (rank + 1) / split : p.k_blocks;
+      s.kb0 = split > 1 ? p.k_blocks * part / split : 0;
+      s.kb1 = split > 1 ? p.k_blocks * (part + 1) / split : p.k_blocks;
       next_dp += clusters;
     } else {
       return false;
@@ -330,6 +330,37 @@ __device__ __forceinline__ void store_part(float4* slot, int col, int lane, cons
                        __uint_as_float(v[4 * i + 3])));
 }
 
+constexpr uint32_t kRowPartBytes = 32 * 64 * sizeof(float);  // narrow row tiles: a warp's part, 32 rows of 64 columns
+
+// kArrays x 32 values of this lane's row, from column `c` on, `stride` apart, summed over the pairs'
+// parts in shared memory.
+template <int kArrays>
+__device__ __forceinline__ void sum_received(const uint8_t* parts, int split, int c, int stride, int lane, uint32_t (&v)[kArrays][32]) {
+  float sum[kArrays][32];
+#pragma unroll
+  for (int t = 0; t < kArrays; ++t)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[t][i] = 0.0f;
+#pragma unroll 1
+  for (int r = 0; r < split; ++r) {
+    const float4* const src = reinterpret_cast<const float4*>(parts + (uint32_t)r * kRowPartBytes) + lane;
+#pragma unroll
+    for (int t = 0; t < kArrays; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = src[((c + t * stride) / 4 + i) * 32];
+        sum[t][4 * i] += x.x;
+        sum[t][4 * i + 1] += x.y;
+        sum[t][4 * i + 2] += x.z;
+        sum[t][4 * i + 3] += x.w;
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < kArrays; ++t)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[t][i] = __float_as_uint(sum[t][i]);
+}
+
 // A warp's staging buffer: 32 rows of 128 bytes, 16-byte pieces swizzled by the row, so
 // that both a lane's own row and four whole rows at a time are free of bank conflicts.
 __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
@@ -410,8 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
   constexpr uint32_t a_slot = (uint32_t)kAccs * kTileBytes;
   const uint32_t b_slot = (uint32_t)(kSwap ? p.mma_n : kHalf) * 128u;
   const uint32_t a0 = base, b0 = base + (uint32_t)S * a_slot;
-  const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results; swapped tiles: other CTAs' parts
-  const uint32_t ctl = out0 + (kSwap ? p.recv_bytes : (uint32_t)(kEpiWarps * kStageOutBytes));
+  const uint32_t out0 = b0 + (uint32_t)S * b_slot;  // row tiles: staged results
+  const uint32_t recv = out0 + (kSwap ? 0u : (uint32_t)(kEpiWarps * kStageOutBytes));  // other CTAs' parts
+  const uint32_t ctl = recv + p.recv_bytes;
   uint8_t* const ctl_ptr = base_ptr + (ctl - base);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(ctl_ptr + kAbortOffset);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctl_ptr + kTmemOffset);
@@ -419,10 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = p.wait_limit_cycles;
-  // swapped tiles: the CTAs of a cluster share a tile's k, or each is one of its own
-  const int split = kSwap ? p.split : 1;
-  const int rank = kPair ? (int)(blockIdx.x & 1) : (int)blockIdx.x % split;
+  // The pairs (swapped tiles: CTAs) of a cluster share a tile's k, or the cluster is one of them.
+  const int split = kBN == kWideN ? 1 : p.split;
   const int cluster = (int)blockIdx.x / (kCtas * split), clusters = (int)gridDim.x / (kCtas * split);
+  const int place = (int)blockIdx.x - cluster * kCtas * split;  // in the cluster
+  const int rank = place % kCtas, part = place / kCtas;
+  const uint32_t leader_place = (uint32_t)(place - rank);
+  const uint16_t pair_mask = (uint16_t)(3u << leader_place);
 
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   if (warp == 0) {
@@ -481,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true, dropped = p.test_drop == 0;
     SegmentIter iter;
-    iter.init(p, cluster, clusters, rank, split);
+    iter.init(p, cluster, clusters, part, split);
     Segment sg;
     const int per_tile = kSwap ? p.chunks : kTileM / p.box;  // chunks of the tokens: at most 16
     const uint32_t bytes = a_slot + (uint32_t)(kSwap ? p.chunks * p.box : kHalf) * 128u;
-    const uint32_t full0 = kPair ? ptx::map_shared_rank(bar_full(ctl, 0), 0) : bar_full(ctl, 0);
+    const uint32_t full0 = kPair ? ptx::map_shared_rank(bar_full(ctl, 0), leader_place) : bar_full(ctl, 0);
     // The loads of k blocks [kb0, kb1) of one segment, from value ko of it on.
     auto produce = [&](auto a_layout, auto b_layout, int kb0, int kb1, int ko, const CUtensorMap* a_map, int a_row, int a_z,
                        const CUtensorMap* b_map, int b_row, int b_z, const CUtensorMap* lane_map, int lane_row) {
@@ -583,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           if (!wait_drain(bar_full(ctl, s), (armed_parity >> s) & 1u, limit))
             record_failure(p, abort_flag, kWaitTimeout, kRoleDrain, s, -1);
     __syncwarp();
-    if (kSwap && split > 1) {
-      ptx::cluster_wait();
-      ptx::cluster_sync_all();
+    if (split > 1) {
+      if (kSwap) ptx::cluster_wait();
+      ptx::cluster_sync_all();  // the parts of k meet
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
@@ -600,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       uint32_t phase = 0;
       bool ok = true;
       SegmentIter iter;
-      iter.init(p, cluster, clusters, rank, split);
+      iter.init(p, cluster, clusters, part, split);
       Segment sg;
       for (; ok && iter.next(p, sg); ++it) {
         const int acc = it & 1;
@@ -642,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               }
             }
             if constexpr (kPair)
-              ptx::mma_commit_pair(bar_empty(ctl, stage), 3);
+              ptx::mma_commit_pair(bar_empty(ctl, stage), pair_mask);
             else
               ptx::mma_commit(bar_empty(ctl, stage));
           }
@@ -652,23 +687,23 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         if (!ok) break;
         if (issuer) {
           if constexpr (kPair)
-            ptx::mma_commit_pair(bar_acc_full(ctl, acc), 3);
+            ptx::mma_commit_pair(bar_acc_full(ctl, acc), pair_mask);
           else
             ptx::mma_commit(bar_acc_full(ctl, acc));
         }
       }
       if (issuer) {
         if constexpr (kPair)
-          ptx::mma_commit_pair(bar_drain(ctl), 3);
+          ptx::mma_commit_pair(bar_drain(ctl), pair_mask);
         else
           ptx::mma_commit(bar_drain(ctl));
         if (!wait_drain(bar_drain(ctl), 0, limit)) record_failure(p, abort_flag, kWaitTimeout, kRoleDrain, -1, -1);
       }
       __syncwarp();
     }
-    if (kSwap && split > 1) {
-      ptx::cluster_wait();
-      ptx::cluster_sync_all();
+    if (split > 1) {
+      if (kSwap) ptx::cluster_wait();
+      ptx::cluster_sync_all();  // the parts of k meet
     }
   } else {
     // ---------------------------------------------------------------- epilogue
@@ -676,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
     uint8_t* const stage_out = base_ptr + (out0 - base) + ewarp * kStageOutBytes;  // row tiles
     SegmentIter iter;
-    iter.init(p, cluster, clusters, rank, split);
+    iter.init(p, cluster, clusters, part, split);
     const int first_cut = p.dp_tiles + iter.u / p.k_blocks;  // the tile whose part lies in slot 0
     Segment sg;
     ptx::griddep_wait();
@@ -730,6 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       store(p.out[0], (uint32_t)p.ldo * 2u, v[0]);
       if (kEpi != kEpiPlain && p.saved[0]) store(p.saved[0], (uint32_t)p.lds * 2u, pre);
     };
+    const int owner = q % split;  // row tiles: the pair that goes on with these 32 rows
+    bool met = false;
     for (int it = 0; iter.next(p, sg); ++it) {
       const int acc = it & 1;
       // Row tiles: this lane's row, those that it reads and writes, and this warp's half of the columns.
@@ -751,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         const int in_shard = trow - shard * p.shard_chunks * p.box;
         if (shard < p.shards && in_shard < p.shard_rows) out_row = (int)(shard * p.shard_rows) + in_shard;
         block_rows(rows, out_row, lane);
-        if (has_residual && sg.whole) fetch_residual(0);  // while the products are made
+        if (has_residual && (sg.whole || (split > 1 && owner == part))) fetch_residual(0);  // while the products are made
       }
       int res = kWaitOk;
       if (lane == 0) res = wait_phase(bar_acc_full(ctl, acc), (uint32_t)(it >> 1) & 1u, abort_flag, limit);
@@ -767,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         __syncwarp();
         if (lane == 0) {
           if (kPair && rank == 1)
-            ptx::mbar_arrive_remote(ptx::map_shared_rank(bar_acc_empty(ctl, acc), 0));
+            ptx::mbar_arrive_remote(ptx::map_shared_rank(bar_acc_empty(ctl, acc), leader_place));
           else
             ptx::mbar_arrive(bar_acc_empty(ctl, acc));
         }
@@ -786,8 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           } else {
             // to the CTA that owns these tokens: group c / 8 is slot c / 8 / split of CTA c / 8 % split
             const int slot = c / 8 / split;
-            const uint32_t at = ptx::map_shared_rank(out0, (uint32_t)(c / 8 - slot * split)) +
-                                (uint32_t)((rank * p.recv_slots + slot) * kAccs) * kPartBytes + (uint32_t)(q * 32 + lane) * 16u;
+            const uint32_t at = ptx::map_shared_rank(recv, (uint32_t)(c / 8 - slot * split)) +
+                                (uint32_t)((part * p.recv_slots + slot) * kAccs) * kPartBytes + (uint32_t)(q * 32 + lane) * 16u;
 #pragma unroll
             for (int t = 0; t < kAccs; ++t) {
               st_cluster_v4(at + (uint32_t)t * kPartBytes, v[t][0], v[t][1], v[t][2], v[t][3]);
@@ -800,7 +837,11 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         const uint32_t t0 = lane_base + (uint32_t)(acc * kBN);
         Parts parts = {0, 0, 0};
         if (!sg.whole) {
-          float4* const slot = part_slot(p, cluster, kCtas, rank, sg.tile == first_cut ? 0 : 1, ewarp);
+          // to the workspace, or to the pair that owns these rows: 8 KiB for each half of each of its
+          // quarters of the rows, from each pair
+          float4* const slot = split > 1 ? nullptr : part_slot(p, cluster, kCtas, rank, sg.tile == first_cut ? 0 : 1, ewarp);
+          const uint32_t there = ptx::map_shared_rank(recv, (uint32_t)(owner * kCtas + rank)) +
+                                 (uint32_t)(((q / split) * 2 + half) * split + part) * kRowPartBytes + (uint32_t)lane * 16u;
 #pragma unroll 1
           for (int c = 0; c < kHalf; c += 32) {
             uint32_t v[32];
@@ -808,14 +849,33 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             const int col = kEpi == kEpiGated && c >= kHalf / 2 ? kHalf + first_col + c - kHalf / 2 : first_col + c;
             ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)col, v);
             ptx::tmem_ld_wait();
-            store_part<32>(slot, c, lane, v);
+            if (split > 1) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) st_cluster_v4(there + (uint32_t)(c / 4 + i) * 512u, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            } else {
+              store_part<32>(slot, c, lane, v);
+            }
           }
           release();
-          int* const counter = p.counters + ((size_t)(sg.tile - p.dp_tiles) * kCtas + rank) * kEpiWarps + ewarp;
-          if (!complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
-          parts = find_parts(p, sg.tile);
-          if (has_residual) fetch_residual(0);
+          if (split > 1) {
+            ptx::cluster_sync_all();  // the parts of k meet
+            met = true;
+            if (owner != part) continue;
+          } else {
+            int* const counter = p.counters + ((size_t)(sg.tile - p.dp_tiles) * kCtas + rank) * kEpiWarps + ewarp;
+            if (!complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
+            parts = find_parts(p, sg.tile);
+            if (has_residual) fetch_residual(0);
+          }
         }
+        // the sums over the parts of `v`'s columns from `c` on
+        auto join = [&](auto& v, int c, int stride) {
+          constexpr int kArrays = sizeof(v) / sizeof(v[0]);
+          if (split > 1)
+            sum_received<kArrays>(base_ptr + (recv - base) + ((q / split) * 2 + half) * split * kRowPartBytes, split, c, stride, lane, v);
+          else
+            sum_parts<kArrays, 32, kArrays == 1 && kEpi == kEpiPlain ? 2 : 1>(p, parts, kCtas, rank, ewarp, c, stride, lane, v);
+        };
         if constexpr (kEpi == kEpiGated) {
           constexpr int kBlocks = kHalf / 64;  // of 32 columns of results
           constexpr int kPieces = 4 * kBlocks;
@@ -833,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               ptx::tmem_ld_wait();
               if (h == kBlocks - 1) release();
             } else {
-              sum_parts<2, 32, 1>(p, parts, kCtas, rank, ewarp, 32 * h, kHalf / 2, lane, v);
+              join(v, 32 * h, kHalf / 2);
             }
             if (p.saved[0]) {
               pack32<kF16>(v[0], g16[h]);
@@ -865,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                 ptx::tmem_ld_wait();
                 if (c + 32 == kHalf) release();
               } else {
-                sum_parts<1, 32, 2>(p, parts, kCtas, rank, ewarp, c, 0, lane, v);
+                join(v, c, 0);
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -888,8 +948,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                 ptx::tmem_ld_wait();
                 if (c + 64 == kHalf) release();
               } else {
-                sum_parts<1, 32, 1>(p, parts, kCtas, rank, ewarp, c, 0, lane, w[0]);
-                sum_parts<1, 32, 1>(p, parts, kCtas, rank, ewarp, c + 32, 0, lane, w[1]);
+                join(w[0], c, 0);
+                join(w[1], c + 32, 0);
               }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
@@ -940,13 +1000,17 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         }
       }
     }
+    if (kPair && split > 1 && !met) {  // after an abort
+      __syncwarp();
+      ptx::cluster_sync_all();
+    }
     if (kSwap && split > 1) {
       // The parts are all there: the owner adds them in the order of k.
       __syncwarp();
       ptx::cluster_sync_all();
-      const uint4* const recv = reinterpret_cast<const uint4*>(base_ptr + (out0 - base)) + q * 32 + lane;
+      const uint4* const parts = reinterpret_cast<const uint4*>(base_ptr + (recv - base)) + q * 32 + lane;
       const int groups = (p.chunks * p.box + 7) / 8;
-      for (int slot = half; slot * split + rank < groups; slot += 2) {
+      for (int slot = half; slot * split + part < groups; slot += 2) {
         float sum[kAccs][8];
         uint32_t v[kAccs][8];
 #pragma unroll
@@ -959,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           for (int t = 0; t < kAccs; ++t) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint4 x = recv[(((r * p.recv_slots + slot) * kAccs + t) * 2 + h) * kTileM];
+              const uint4 x = parts[(((r * p.recv_slots + slot) * kAccs + t) * 2 + h) * kTileM];
               sum[t][4 * h] += __uint_as_float(x.x);
               sum[t][4 * h + 1] += __uint_as_float(x.y);
               sum[t][4 * h + 2] += __uint_as_float(x.z);
@@ -971,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         for (int t = 0; t < kAccs; ++t)
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[t][i] = __float_as_uint(sum[t][i]);
-        finish(v, (slot * split + rank) * 8);
+        finish(v, (slot * split + part) * 8);
       }
     }
   }

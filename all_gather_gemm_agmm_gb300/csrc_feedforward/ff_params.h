@@ -18,7 +18,8 @@ constexpr int kTileK = 64;        // one 128-byte swizzle row of 16-bit values
 constexpr int kTileBytes = kTileM * kTileK * 2;  // 16 KiB
 constexpr int kMaxStages = 12;
 constexpr int kWideStages = 6, kNarrowStages = 8;  // 192 KiB of operands beside 32 KiB of staged results
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 8;      // CTAs of a cluster that share a swapped tile's k
+constexpr int kMaxPairs = 4;      // pairs that share a narrow row tile's
 constexpr int kMaxSwapRows = 64;  // swapped tiles: token columns of a tile, at most
 constexpr int kStageOutBytes = 4096;  // row tiles: a warp's staging buffer, 32 rows x 128 bytes
 constexpr int kCtlBytes = 1024;
@@ -63,9 +64,9 @@ struct __align__(128) GemmParams {
   int chunks;                     // of all shards
   int64_t shard_rows;
   int mma_n;               // swapped tiles: token columns, a multiple of 16
-  int split;               // ... CTAs of a cluster that share a tile's k
-  int recv_slots;          // ... groups of 8 tokens that each of them owns
-  uint32_t recv_bytes;     // ... and their parts, in its shared memory
+  int recv_slots;          // ... groups of 8 tokens that each CTA of a cluster owns
+  int split;               // CTAs, or pairs, of a cluster that share a tile's k
+  uint32_t recv_bytes;     // their parts, in the shared memory of the owner
   int stages;
   uint32_t tmem_cols;
   // results

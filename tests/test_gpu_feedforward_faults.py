@@ -23,7 +23,8 @@ def agmm():
 
 
 @pytest.mark.parametrize("rows,env", [(5, {"AGMM_SPLITK": "1"}), (5, {"AGMM_SPLITK": "4"}), (300, {"AGMM_STREAMK": "0"}),
-                                      (300, {"AGMM_STREAMK": "1"})], ids=["swapped", "split", "rows", "cut"])
+                                      (300, {"AGMM_STREAMK": "1"}), (300, {"AGMM_BN": "128", "AGMM_SPLITK": "3"})],
+                         ids=["swapped", "split", "rows", "cut", "pairs"])
 def test_dropped_load_times_out_and_recovers(agmm, rows, env, monkeypatch):
     g = torch.Generator(device="cuda").manual_seed(1)
     new = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731

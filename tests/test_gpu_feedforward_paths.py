@@ -1,5 +1,5 @@
 """Every kernel variant of the feed-forward products, at small sizes: wide and narrow row tiles,
-whole and cut, and swapped tiles whose k is shared by 1 to 8 CTAs.  The rules choose among them by
+whole, cut and shared by pairs, and swapped tiles whose k is shared by 1 to 8 CTAs.  The rules choose among them by
 size; here the overrides do."""
 import pytest
 import torch
@@ -22,6 +22,7 @@ def agmm():
 
 
 ROWS = [dict(AGMM_PATH="0", AGMM_BN=bn, AGMM_STREAMK=cut) for bn in ("128", "256") for cut in ("0", "1")]
+ROWS += [dict(AGMM_PATH="0", AGMM_BN="128", AGMM_SPLITK=str(s)) for s in (2, 3, 4)]
 SWAP = [dict(AGMM_PATH="1", AGMM_SPLITK=str(s)) for s in (1, 2, 3, 4, 5, 6, 7, 8)]
 
 
@@ -79,7 +80,7 @@ def test_paths(agmm, monkeypatch, env, size, transpose):
     plan.query_status(ws)
 
 
-@pytest.mark.parametrize("env", ROWS[1::2], ids=name)
+@pytest.mark.parametrize("env", [e for e in ROWS if e.get("AGMM_STREAMK") == "1"], ids=name)
 def test_cut_tiles_behind_whole_ones(agmm, monkeypatch, env):
     """More tiles than clusters, the ragged last wave cut: parts of both slots, and whole tiles behind them."""
     for e, v in env.items():
