@@ -28,7 +28,7 @@ SOURCES = ["agmm_select_rows_a1.cu", "agmm_select_rows_a2.cu", "agmm_select_swap
 ATTENTION_SOURCES = ["norm_rope.cu", "attn_prompt.cu", "attn_tree.cu", "attn_launch.cu", "attn_api.cpp"]
 FEEDFORWARD_SOURCES = ["ff_wide_plain.cu", "ff_wide_gated.cu", "ff_wide_linear.cu", "ff_narrow_plain.cu",
                        "ff_narrow_gated.cu", "ff_narrow_linear.cu", "ff_swap_plain.cu", "ff_swap_gated.cu",
-                       "ff_swap_linear.cu", "ff_launch.cu", "ff_pointwise.cu", "layer_norm.cu", "ff_api.cpp"]
+                       "ff_swap_linear.cu", "ff_wide_two.cu", "ff_narrow_two.cu", "ff_launch.cu", "ff_pointwise.cu", "layer_norm.cu", "ff_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -33,7 +33,7 @@ struct ProductPlan {
   int pairs;                  // CTA pairs that run at once
   int clusters[kMaxSplit + 1];  // clusters of that many CTAs that do
   int joined[kMaxPairs + 1];    // clusters of that many pairs that do
-  int path, bn, cut, split;   // overrides for tests and experiments; -1: by the rules
+  int path, bn, cut, split, merge;  // overrides for tests and experiments; -1: by the rules
   uint64_t wait_limit_cycles;
   int test_drop;
 };
@@ -237,6 +237,7 @@ constexpr double kWideTile = 4000, kNarrowTile = 2500;    // its results, beside
 constexpr double kWideCut = 16000, kNarrowCut = 6500;     // the parts' way to L2 and back
 constexpr double kWidePart = 3000, kNarrowPart = 1400;    // ... and each part that is added
 constexpr double kJoinTile = 3500;                        // pairs' parts in distributed shared memory
+constexpr double kLaunch = 7000;                          // a launch's start and last results
 constexpr double kSwapByte = 0.019;                       // swapped tiles: a byte, for one CTA alone
 constexpr double kMemoryByte = 2.84e-4;                   // ... and for each CTA that shares the device's memory
 constexpr double kSplitTile = 1500;                       // ... the parts' way through distributed shared memory
@@ -263,7 +264,7 @@ bool can_cut(int64_t tiles, int k_blocks, int clusters) {
 }
 
 // How the tokens' rows lie in tiles: boxes of rows that never leave their shard.
-void chunk_rows(GemmParams* p, int shards, int64_t rows, int box) {
+void chunk_rows(Product* p, int shards, int64_t rows, int box) {
   p->shards = shards;
   p->shard_rows = rows;
   p->box = box;
@@ -316,10 +317,10 @@ constexpr int64_t kCutBytes = 160 << 20;
 // estimate.
 struct RowChoice {
   int bn, parts, split;  // split: pairs of a cluster that share a tile
+  double time;
 };
 RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int k_blocks, int problems, bool gated) {
-  RowChoice best = {kWideN, 0, 1};
-  double least = 1e300;
+  RowChoice best = {kWideN, 0, 1, 1e300};
   const int C = pl->pairs;
   for (int bn = kWideN; bn >= kNarrowN; bn -= kWideN - kNarrowN) {
     if (pl->bn >= 0 && pl->bn != bn) continue;
@@ -329,10 +330,7 @@ RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int 
     const double block = wide ? kWideBlock : kNarrowBlock, tile = wide ? kWideTile : kNarrowTile;
     const double cut = wide ? kWideCut : kNarrowCut, part = wide ? kWidePart : kNarrowPart;
     const auto offer = [&](double time, int parts, int split) {
-      if (time < least) {
-        least = time;
-        best = {bn, parts, split};
-      }
+      if (time < best.time) best = {bn, parts, split, time};
     };
     bool joined = false;
     if (!wide && pl->cut != 1) {
@@ -358,14 +356,20 @@ RowChoice choose_rows(const ProductPlan* pl, int64_t m_tiles, int64_t cols, int 
   return best;
 }
 
+// The tiles of a product; its rows' tiles are known.
+agmm_status_t lay_tiles(Product* q, int64_t m_tiles) {
+  const int64_t n_tiles = ceil_div(q->cols, q->b_tile_step);
+  if (m_tiles * n_tiles * q->problems > kMostTiles) return fail(AGMM_ERR_UNSUPPORTED, "more than 2^30 tiles of results");
+  q->m_tiles = (int)m_tiles;
+  q->n_tiles = (int)n_tiles;
+  q->tiles_per_problem = q->m_tiles * q->n_tiles;
+  q->group_m = (int)std::min<int64_t>(16, std::max<int64_t>(8, kBandBytes / ((int64_t)2 * kTileM * q->k_blocks * kTileK * 2)));
+  return AGMM_OK;
+}
+
 agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice choice, int64_t m_tiles, cudaStream_t stream) {
-  const int64_t n_tiles = ceil_div(p->cols, p->b_tile_step);
-  if (m_tiles * n_tiles * p->problems > kMostTiles) return fail(AGMM_ERR_UNSUPPORTED, "more than 2^30 tiles of results");
-  p->m_tiles = (int)m_tiles;
-  p->n_tiles = (int)n_tiles;
-  p->tiles_per_problem = p->m_tiles * p->n_tiles;
+  AGMM_TRY(lay_tiles(p, m_tiles));
   p->num_tiles = p->tiles_per_problem * p->problems;
-  p->group_m = (int)std::min<int64_t>(16, std::max<int64_t>(8, kBandBytes / ((int64_t)2 * kTileM * p->k_blocks * kTileK * 2)));
   const size_t stage = kTileBytes + choice.bn * kTileK;
   p->split = choice.split;
   // a pair owns every split-th quarter of its rows, in two halves of the columns
@@ -444,63 +448,157 @@ agmm_status_t forward(const ProductPlan* pl, GemmParams* p, int epi, int shards,
   return run_rows(pl, p, epi, choice, m_tiles, stream);
 }
 
-// dx = sum over the weights of d_i Wi^T
-agmm_status_t input_grad(const ProductPlan* pl, GemmParams* p, int weights, int64_t rows, const void* const* d, int64_t d_stride,
-                         const void* const* w, int64_t w_stride, void* dx, int64_t dx_stride, cudaStream_t stream) {
-  const int swap = pl->path == 0 ? 0 : swap_box(1, rows);
-  chunk_rows(p, 1, rows, swap ? swap : kTileM);
-  p->out[0] = dx;
-  p->ldo = dx_stride;
+// What the products of a backward pass are made of.
+struct Grads {
+  int weights, shards;
+  int64_t rows;  // of a shard
+  const void* const* x;
+  int64_t x_stride;
+  const void* const* d;  // of each weight's product
+  int64_t d_stride;
+  const void* const* w;
+  int64_t w_stride;
+  void* dx;  // NULL: not wanted
+  int64_t dx_stride;
+  void* const* dw;  // NULL: not wanted
+  int64_t dw_stride;
+  bool f32;
+};
+
+// dx = sum over the weights of d_i Wi^T; tiles of bn columns, or swapped with a box of `swap` tokens.
+agmm_status_t input_grad(const ProductPlan* pl, Product* p, const Grads& g, int swap, int bn) {
+  const int64_t tokens = g.shards * g.rows;
+  chunk_rows(p, 1, tokens, swap ? swap : kTileM);
+  p->problems = 1;
+  p->out[0] = g.dx;
+  p->ldo = g.dx_stride;
   p->cols = pl->k;
   p->seg_blocks = (int)ceil_div(pl->n, kTileK);
-  p->k_blocks = weights * p->seg_blocks;
-  const int64_t m_tiles = ceil_div(rows, 2 * kTileM);
-  const RowChoice choice = choose_rows(pl, m_tiles, pl->k, p->k_blocks, 1, false);
-  const int w_rows = swap ? kTileM : choice.bn / 2;
+  p->k_blocks = g.weights * p->seg_blocks;
+  p->b_tile_step = bn;
+  p->b_half_step = bn / 2;
   OperandParams &to = swap ? p->b : p->a, &wo = swap ? p->a : p->b;
   CUtensorMap *tm = swap ? p->b_map : p->a_map, *wm = swap ? p->a_map : p->b_map;
-  to.maps = wo.maps = weights;
+  to.maps = wo.maps = g.weights;
   to.by_segment = wo.by_segment = 1;
-  for (int i = 0; i < weights; ++i) {
-    AGMM_TRY(encode_operand(&tm[i], &to, {"a gradient", d[i], pl->n, rows, 1, d_stride}, false, p->box, pl->f16));
-    const Matrix m = pl->transpose ? Matrix{"a weight", w[i], pl->k, pl->n, 1, w_stride} : Matrix{"a weight", w[i], pl->n, pl->k, 1, w_stride};
-    AGMM_TRY(encode_operand(&wm[i], &wo, m, pl->transpose, w_rows, pl->f16));
+  for (int i = 0; i < g.weights; ++i) {
+    AGMM_TRY(encode_operand(&tm[i], &to, {"a gradient", g.d[i], pl->n, tokens, 1, g.d_stride}, false, p->box, pl->f16));
+    const Matrix m = pl->transpose ? Matrix{"a weight", g.w[i], pl->k, pl->n, 1, g.w_stride} : Matrix{"a weight", g.w[i], pl->n, pl->k, 1, g.w_stride};
+    AGMM_TRY(encode_operand(&wm[i], &wo, m, pl->transpose, swap ? kTileM : bn / 2, pl->f16));
   }
-  if (swap) return run_swap(pl, p, kEpiPlain, pl->k, stream);
-  p->b_tile_step = choice.bn;
-  p->b_half_step = choice.bn / 2;
-  return run_rows(pl, p, kEpiPlain, choice, m_tiles, stream);
+  return AGMM_OK;
 }
 
 // dWi = X^T d_i, stored like the weight; the tokens of each shard are a segment of the sum.
-agmm_status_t weight_grad(const ProductPlan* pl, GemmParams* p, int weights, int shards, int64_t rows, const void* const* x,
-                          int64_t x_stride, const void* const* d, int64_t d_stride, void* const* dw, int64_t dw_stride, bool f32,
-                          cudaStream_t stream) {
-  const int64_t out_rows = pl->transpose ? pl->n : pl->k, out_cols = pl->transpose ? pl->k : pl->n;
-  chunk_rows(p, 1, out_rows, kTileM);
-  p->problems = weights;
-  for (int i = 0; i < weights; ++i) p->out[i] = dw[i];
-  p->ldo = dw_stride;
-  p->out_f32 = f32;
-  p->cols = out_cols;
-  p->seg_blocks = (int)ceil_div(rows, kTileK);
-  if ((int64_t)p->seg_blocks * shards > INT_MAX) return fail(AGMM_ERR_UNSUPPORTED, "too many rows");
-  p->k_blocks = p->seg_blocks * shards;
-  const int64_t m_tiles = ceil_div(out_rows, 2 * kTileM);
-  const RowChoice choice = choose_rows(pl, m_tiles, out_cols, p->k_blocks, weights, false);
-  const int x_rows = pl->transpose ? choice.bn / 2 : kTileM, g_rows = pl->transpose ? kTileM : choice.bn / 2;
+agmm_status_t weight_grad(const ProductPlan* pl, Product* p, const Grads& g, int bn) {
+  chunk_rows(p, 1, pl->transpose ? pl->n : pl->k, kTileM);
+  p->problems = g.weights;
+  for (int i = 0; i < g.weights; ++i) p->out[i] = g.dw[i];
+  p->ldo = g.dw_stride;
+  p->out_f32 = g.f32;
+  p->cols = pl->transpose ? pl->k : pl->n;
+  p->seg_blocks = (int)ceil_div(g.rows, kTileK);
+  p->k_blocks = p->seg_blocks * g.shards;
+  p->b_tile_step = bn;
+  p->b_half_step = bn / 2;
+  const int x_rows = pl->transpose ? bn / 2 : kTileM, d_rows = pl->transpose ? kTileM : bn / 2;
   OperandParams &xo = pl->transpose ? p->b : p->a, &go = pl->transpose ? p->a : p->b;
   CUtensorMap *xm = pl->transpose ? p->b_map : p->a_map, *gm = pl->transpose ? p->a_map : p->b_map;
-  xo.maps = shards;
-  go.maps = weights;
+  xo.maps = g.shards;
+  go.maps = g.weights;
   xo.by_segment = 1;
   go.by_problem = 1;
   go.z_segment = 1;
-  for (int s = 0; s < shards; ++s) AGMM_TRY(encode_operand(&xm[s], &xo, {"x", x[s], pl->k, rows, 1, x_stride}, true, x_rows, pl->f16));
-  for (int i = 0; i < weights; ++i) AGMM_TRY(encode_operand(&gm[i], &go, {"a gradient", d[i], pl->n, rows, shards, d_stride}, true, g_rows, pl->f16));
-  p->b_tile_step = choice.bn;
-  p->b_half_step = choice.bn / 2;
-  return run_rows(pl, p, kEpiPlain, choice, m_tiles, stream);
+  for (int s = 0; s < g.shards; ++s) AGMM_TRY(encode_operand(&xm[s], &xo, {"x", g.x[s], pl->k, g.rows, 1, g.x_stride}, true, x_rows, pl->f16));
+  for (int i = 0; i < g.weights; ++i)
+    AGMM_TRY(encode_operand(&gm[i], &go, {"a gradient", g.d[i], pl->n, g.rows, g.shards, g.d_stride}, true, d_rows, pl->f16));
+  return AGMM_OK;
+}
+
+// Two products in one launch: how the second's tiles go round, and the estimate of its time.
+struct TwoChoice {
+  int bn, lead, ahead, each, rest;
+  bool dx_first;
+  double time;
+};
+TwoChoice choose_two(const ProductPlan* pl, int64_t dx_m_tiles, int dx_blocks, int64_t dw_m_tiles, int64_t dw_cols, int dw_blocks, int weights) {
+  TwoChoice best = {};
+  best.time = 1e300;
+  const int64_t C = pl->pairs;
+  for (int bn = kWideN; bn >= kNarrowN; bn -= kWideN - kNarrowN) {
+    if (pl->bn >= 0 && pl->bn != bn) continue;
+    const bool wide = bn == kWideN;
+    const double block = wide ? kWideBlock : kNarrowBlock, tile = wide ? kWideTile : kNarrowTile;
+    const int64_t dx_tiles = dx_m_tiles * ceil_div(pl->k, bn), dw_tiles = dw_m_tiles * ceil_div(dw_cols, bn) * weights;
+    if (dx_tiles > kMostTiles || dw_tiles > kMostTiles) continue;
+    const bool dx_first = dx_blocks >= dw_blocks;  // long tiles first
+    const int64_t t0 = dx_first ? dx_tiles : dw_tiles, t1 = dx_first ? dw_tiles : dx_tiles;
+    const double one0 = std::max((dx_first ? dx_blocks : dw_blocks) * block, tile), one1 = std::max((dx_first ? dw_blocks : dx_blocks) * block, tile);
+    TwoChoice c = {};
+    c.bn = bn;
+    c.dx_first = dx_first;
+    c.lead = (int)(t0 % C);
+    const int64_t others = C - c.lead;
+    c.ahead = c.lead ? (int)std::min<int64_t>((int64_t)(one0 / one1), t1 / others) : 0;
+    c.each = (int)((t1 - c.ahead * others) / C);
+    c.rest = (int)((t1 - c.ahead * others) % C);
+    // the last of either kind of cluster; the others take the rest first
+    const double others_end = (t0 / C) * one0 + (c.ahead + c.each + (c.rest > 0)) * one1;
+    const double lead_end = c.lead ? (t0 / C + 1) * one0 + (c.each + (c.rest > others)) * one1 : 0;
+    c.time = std::max(others_end, lead_end);
+    if (c.time < best.time) best = c;
+  }
+  return best;
+}
+
+agmm_status_t run_two(const ProductPlan* pl, const Grads& g, const TwoChoice& c, int64_t dx_m_tiles, int64_t dw_m_tiles, void* workspace,
+                      cudaStream_t stream) {
+  TwoParams p = {};
+  common_params(pl, &p, workspace);
+  Product *dx = c.dx_first ? &p : &p.second, *dw = c.dx_first ? &p.second : &p;
+  AGMM_TRY(input_grad(pl, dx, g, 0, c.bn));
+  AGMM_TRY(weight_grad(pl, dw, g, c.bn));
+  AGMM_TRY(lay_tiles(dx, dx_m_tiles));
+  AGMM_TRY(lay_tiles(dw, dw_m_tiles));
+  p.num_tiles = p.dp_tiles = p.tiles_per_problem * p.problems;
+  p.lead = c.lead;
+  p.ahead = c.ahead;
+  p.each = c.each;
+  p.rest = c.rest;
+  p.stages = c.bn == kWideN ? kWideStages : kNarrowStages;
+  p.tmem_cols = 2 * c.bn;
+  const size_t smem = 1024 + p.stages * (size_t)(kTileBytes + c.bn * kTileK) + (size_t)kEpiWarps * kStageOutBytes + kCtlBytes;
+  return check_cuda(launch_two(c.bn == kWideN ? wide_two(pl->f16) : narrow_two(pl->f16), p, pl->pairs, smem, stream), "products launch");
+}
+
+// The products of a backward pass: in one launch where that is estimated to be shorter.
+agmm_status_t run_grads(const ProductPlan* pl, const Grads& g, void* workspace, cudaStream_t stream) {
+  const int64_t tokens = g.shards * g.rows, dw_rows = pl->transpose ? pl->n : pl->k, dw_cols = pl->transpose ? pl->k : pl->n;
+  const int64_t dx_m_tiles = ceil_div(tokens, 2 * kTileM), dw_m_tiles = ceil_div(dw_rows, 2 * kTileM);
+  const int64_t dw_blocks = ceil_div(g.rows, kTileK) * g.shards, dx_blocks = g.weights * ceil_div(pl->n, kTileK);
+  if (dw_blocks > INT_MAX) return fail(AGMM_ERR_UNSUPPORTED, "too many rows");
+  const int swap = g.dx && pl->path != 0 ? swap_box(1, tokens) : 0;
+  RowChoice for_dx = {}, for_dw = {};
+  if (g.dx && !swap) for_dx = choose_rows(pl, dx_m_tiles, pl->k, (int)dx_blocks, 1, false);
+  if (g.dw) for_dw = choose_rows(pl, dw_m_tiles, dw_cols, (int)dw_blocks, g.weights, false);
+  if (g.dx && g.dw && !swap && pl->merge != 0) {
+    const TwoChoice two = choose_two(pl, dx_m_tiles, (int)dx_blocks, dw_m_tiles, dw_cols, (int)dw_blocks, g.weights);
+    if (two.time < 1e300 && (pl->merge == 1 || two.time < for_dx.time + for_dw.time + kLaunch))
+      return run_two(pl, g, two, dx_m_tiles, dw_m_tiles, workspace, stream);
+  }
+  if (g.dx) {
+    GemmParams p = {};
+    common_params(pl, &p, workspace);
+    AGMM_TRY(input_grad(pl, &p, g, swap, for_dx.bn));
+    AGMM_TRY(swap ? run_swap(pl, &p, kEpiPlain, pl->k, stream) : run_rows(pl, &p, kEpiPlain, for_dx, dx_m_tiles, stream));
+  }
+  if (g.dw) {
+    GemmParams p = {};
+    common_params(pl, &p, workspace);
+    AGMM_TRY(weight_grad(pl, &p, g, for_dw.bn));
+    AGMM_TRY(run_rows(pl, &p, kEpiPlain, for_dw, dw_m_tiles, stream));
+  }
+  return AGMM_OK;
 }
 
 agmm_status_t zero_rows(const char* name, void* p, int64_t stride, int64_t rows, int64_t cols, bool f32, cudaStream_t stream) {
@@ -535,12 +633,17 @@ agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int tran
   if (pl->bn != kNarrowN && pl->bn != kWideN) pl->bn = -1;
   pl->cut = env_int("AGMM_STREAMK", 0, 1);
   pl->split = env_int("AGMM_SPLITK", 1, kMaxSplit);
+  pl->merge = env_int("AGMM_MERGE", 0, 1);
   pl->pairs = pl->sms / 2;
   for (int split = 1; split <= kMaxSplit; ++split) pl->clusters[split] = pl->sms / split;
   for (int epi = kEpiPlain; epi <= kEpiLinear; ++epi) {
     int fit = 0;
     for (int bn : {kNarrowN, kWideN}) {
       AGMM_TRY(check_cuda(prepare_gemm(select_gemm(bn, epi, pl->f16), 2, &fit), "kernel attributes"));
+      pl->pairs = std::min(pl->pairs, fit);
+    }
+    for (TwoFn fn : {wide_two(pl->f16), narrow_two(pl->f16)}) {
+      AGMM_TRY(check_cuda(prepare_two(fn, &fit), "kernel attributes"));
       pl->pairs = std::min(pl->pairs, fit);
     }
     for (int n = 2; n <= kMaxPairs; ++n) {
@@ -790,17 +893,9 @@ agmm_status_t agmm_gated_backward(agmm_gated_t pl, const agmm_gated_grad_args_t*
   AGMM_TRY(check_cuda(launch_gated_grad(g, pl->f16, pl->sms, s), "gated backward launch"));
   const void* const d[2] = {a->d_gate, a->d_up};
   const void* const w[2] = {a->w_gate, a->w_up};
-  if (a->dx) {
-    GemmParams p = {};
-    common_params(pl, &p, a->workspace);
-    AGMM_TRY(input_grad(pl, &p, 2, tokens, d, d_stride, w, w_stride, a->dx, dx_stride, s));
-  }
-  if (a->dw_gate) {
-    GemmParams p = {};
-    common_params(pl, &p, a->workspace);
-    AGMM_TRY(weight_grad(pl, &p, 2, (int)a->shards, a->rows, a->x, x_stride, d, d_stride, dw, dw_stride, a->f32_grads != 0, s));
-  }
-  return AGMM_OK;
+  const Grads products = {2, (int)a->shards, a->rows, a->x, x_stride, d, d_stride, w, w_stride, a->dx, dx_stride, a->dw_gate ? dw : nullptr,
+                          dw_stride, a->f32_grads != 0};
+  return run_grads(pl, products, a->workspace, s);
 }
 
 // --------------------------------------------------------------------- linear
@@ -905,17 +1000,9 @@ agmm_status_t agmm_linear_backward(agmm_linear_t pl, const agmm_linear_grad_args
   }
   const void* const d = acts ? a->d_pre : a->d_out;
   if (!acts) d_stride = out_stride;
-  if (a->dx) {
-    GemmParams p = {};
-    common_params(pl, &p, a->workspace);
-    AGMM_TRY(input_grad(pl, &p, 1, tokens, &d, d_stride, &a->w, w_stride, a->dx, dx_stride, s));
-  }
-  if (a->dw) {
-    GemmParams p = {};
-    common_params(pl, &p, a->workspace);
-    AGMM_TRY(weight_grad(pl, &p, 1, (int)a->shards, a->rows, a->x, x_stride, &d, d_stride, &a->dw, dw_stride, f32, s));
-  }
-  return AGMM_OK;
+  const Grads products = {1, (int)a->shards, a->rows, a->x, x_stride, &d, d_stride, &a->w, w_stride, a->dx, dx_stride,
+                          a->dw ? &a->dw : nullptr, dw_stride, f32};
+  return run_grads(pl, products, a->workspace, s);
 }
 
 }  // extern "C"

@@ -115,7 +115,8 @@ __device__ __noinline__ void record_failure(const GemmParams& p, volatile int* a
 // A cluster's share of the work, one segment after another: its even share of the cut
 // tiles' k blocks first, so that the parts are there early, then its whole tiles.
 struct Segment {
-  int tile, problem, mt, nt;
+  int tile, problem, mt, nt;  // tile: of its product
+  bool second;
   int kb0, kb1;
   bool whole;
 };
@@ -124,10 +125,24 @@ __device__ __forceinline__ int first_unit(const GemmParams& p, int cluster) {
   return cluster * p.sk_share + min(cluster, p.sk_extra);
 }
 
+template <bool kTwo>
+using ParamsOf = std::conditional_t<kTwo, TwoParams, GemmParams>;
+
+template <bool kTwo>
+__device__ __forceinline__ const Product& product_of(const ParamsOf<kTwo>& p, const Segment& s) {
+  if constexpr (kTwo)
+    if (s.second) return p.second;
+  return p;
+}
+
+template <bool kTwo>
 struct SegmentIter {
   int u, hi, next_dp, clusters, part, split;
+  int cluster, taken;  // of the second product's tiles
 
-  __device__ __forceinline__ void init(const GemmParams& p, int cluster, int nclusters, int k_part, int splits) {
+  __device__ __forceinline__ void init(const GemmParams& p, int cluster_id, int nclusters, int k_part, int splits) {
+    cluster = cluster_id;
+    taken = 0;
     clusters = nclusters;
     next_dp = cluster;
     part = k_part;
@@ -139,7 +154,22 @@ struct SegmentIter {
     }
   }
 
-  __device__ __forceinline__ bool next(const GemmParams& p, Segment& s) {
+  // The next tile of the second product; -1 behind the last.
+  __device__ __forceinline__ int next_second(const TwoParams& p) {
+    const int others = clusters - p.lead;
+    int i = taken++;
+    if (cluster >= p.lead) {
+      if (i < p.ahead) return i * others + cluster - p.lead;
+      i -= p.ahead;
+    }
+    const int base = others * p.ahead;
+    if (i < p.each) return base + i * clusters + cluster;
+    const int place = cluster >= p.lead ? cluster - p.lead : others + cluster;
+    return i == p.each && place < p.rest ? base + p.each * clusters + place : -1;
+  }
+
+  __device__ __forceinline__ bool next(const ParamsOf<kTwo>& p, Segment& s) {
+    s.second = false;
     if (u < hi) {
       const int t = u / p.k_blocks;
       s.tile = p.dp_tiles + t;
@@ -152,15 +182,24 @@ struct SegmentIter {
       s.kb1 = split > 1 ? p.k_blocks * (part + 1) / split : p.k_blocks;
       next_dp += clusters;
     } else {
-      return false;
+      if constexpr (kTwo) {
+        s.tile = next_second(p);
+        s.second = true;
+        s.kb0 = 0;
+        s.kb1 = p.second.k_blocks;
+        if (s.tile < 0) return false;
+      } else {
+        return false;
+      }
     }
-    s.whole = s.kb0 == 0 && s.kb1 == p.k_blocks;
-    s.problem = s.tile >= p.tiles_per_problem;
+    const Product& w = product_of<kTwo>(p, s);
+    s.whole = s.kb0 == 0 && s.kb1 == w.k_blocks;
+    s.problem = s.tile >= w.tiles_per_problem;
     // bands of group_m row tiles sweep the columns together: their rows stay in L2
-    const int t = s.tile - s.problem * p.tiles_per_problem;
-    const int per_group = p.group_m * p.n_tiles;
-    const int group = t / per_group, first = group * p.group_m;
-    const int in_group = min(p.m_tiles - first, p.group_m), r = t - group * per_group;
+    const int t = s.tile - s.problem * w.tiles_per_problem;
+    const int per_group = w.group_m * w.n_tiles;
+    const int group = t / per_group, first = group * w.group_m;
+    const int in_group = min(w.m_tiles - first, w.group_m), r = t - group * per_group;
     s.nt = r / in_group;
     s.mt = first + r - s.nt * in_group;
     return true;
@@ -426,9 +465,9 @@ __device__ __forceinline__ void stage_half(uint8_t* stage, int lane, int half, c
   for (int i = 0; i < 4; ++i) *staged(stage, lane, half * 4 + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// kBN: columns of a row tile (0: swapped tiles).
-template <int kBN, int kEpi, bool kF16>
-__global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constant__ GemmParams p) {
+// kBN: columns of a row tile (0: swapped tiles).  kTwo: two products in one launch.
+template <int kBN, int kEpi, bool kF16, bool kTwo = false>
+__global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constant__ ParamsOf<kTwo> p) {
   constexpr bool kSwap = kBN == 0, kPair = !kSwap;
   constexpr int kHalf = kBN / 2;  // columns of the accumulator that a warp of the epilogue has
   constexpr int kCtas = kPair ? 2 : 1;
@@ -472,6 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     }
     if (lane < p.a.maps) ptx::prefetch_tensormap(&p.a_map[lane]);
     if (lane < p.b.maps) ptx::prefetch_tensormap(&p.b_map[lane]);
+    if constexpr (kTwo) {
+      if (lane < p.second.a.maps) ptx::prefetch_tensormap(&p.second.a_map[lane]);
+      if (lane < p.second.b.maps) ptx::prefetch_tensormap(&p.second.b_map[lane]);
+    }
     if (lane == 0) *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -515,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true, dropped = p.test_drop == 0;
-    SegmentIter iter;
+    SegmentIter<kTwo> iter;
     iter.init(p, cluster, clusters, part, split);
     Segment sg;
     const int per_tile = kSwap ? p.chunks : kTileM / p.box;  // chunks of the tokens: at most 16
@@ -573,29 +616,30 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     };
     ptx::griddep_wait();  // no access to global memory before this, in any role
     while (ok && iter.next(p, sg)) {
+      const Product& w = product_of<kTwo>(p, sg);
       const int row_tile = kPair ? sg.mt * 2 + rank : sg.mt;
       // Chunks of the tokens in a stage.  One to a stage is the elected lane's, with operands
       // that are uniform over the warp; else lane j has chunk j's map and row.  A chunk behind
       // the last lies outside its map: zeros.
       const int chunk0 = kSwap ? 0 : row_tile * per_tile;
-      const int shard0 = min(chunk0 / p.shard_chunks, p.shards - 1);
-      const int row0 = (chunk0 - shard0 * p.shard_chunks) * p.box;
-      const int chunk = chunk0 + lane, shard = min(chunk / p.shard_chunks, p.shards - 1);
-      const int lane_row = (chunk - shard * p.shard_chunks) * p.box;
-      const int b_row = kSwap ? row0 : sg.nt * p.b_tile_step + rank * p.b_half_step;
-      const int a_row = kSwap || p.a.mn_major ? row_tile * kTileM : row0;
-      int seg = sg.kb0 / p.seg_blocks;
+      const int shard0 = min(chunk0 / w.shard_chunks, w.shards - 1);
+      const int row0 = (chunk0 - shard0 * w.shard_chunks) * w.box;
+      const int chunk = chunk0 + lane, shard = min(chunk / w.shard_chunks, w.shards - 1);
+      const int lane_row = (chunk - shard * w.shard_chunks) * w.box;
+      const int b_row = kSwap ? row0 : sg.nt * w.b_tile_step + rank * w.b_half_step;
+      const int a_row = kSwap || w.a.mn_major ? row_tile * kTileM : row0;
+      int seg = sg.kb0 / w.seg_blocks;
       for (int kb = sg.kb0; ok && kb < sg.kb1; ++seg) {
-        const int end = min(sg.kb1, (seg + 1) * p.seg_blocks);
-        const int ko = (kb - seg * p.seg_blocks) * kTileK, a_z = seg * p.a.z_segment, b_z = seg * p.b.z_segment;
-        const CUtensorMap* a_map = p.a_map + sg.problem * p.a.by_problem + seg * p.a.by_segment;
-        const CUtensorMap* b_map = p.b_map + sg.problem * p.b.by_problem + seg * p.b.by_segment + rank * p.b.by_rank;
-        const CUtensorMap* const lane_map = kSwap ? b_map + shard * p.b.by_shard : a_map + shard * p.a.by_shard;
+        const int end = min(sg.kb1, (seg + 1) * w.seg_blocks);
+        const int ko = (kb - seg * w.seg_blocks) * kTileK, a_z = seg * w.a.z_segment, b_z = seg * w.b.z_segment;
+        const CUtensorMap* a_map = w.a_map + sg.problem * w.a.by_problem + seg * w.a.by_segment;
+        const CUtensorMap* b_map = w.b_map + sg.problem * w.b.by_problem + seg * w.b.by_segment + rank * w.b.by_rank;
+        const CUtensorMap* const lane_map = kSwap ? b_map + shard * w.b.by_shard : a_map + shard * w.a.by_shard;
         if (kSwap)
-          b_map += shard0 * p.b.by_shard;
+          b_map += shard0 * w.b.by_shard;
         else
-          a_map += shard0 * p.a.by_shard;
-        with_layout(p.a.mn_major, p.a.blocked, !kSwap && per_tile > 1, [&](auto a_layout) {
+          a_map += shard0 * w.a.by_shard;
+        with_layout(w.a.mn_major, w.a.blocked, !kSwap && per_tile > 1, [&](auto a_layout) {
           // swapped tiles: the tokens' rows lie along k
           if constexpr (kSwap) {
             if (per_tile > 1)
@@ -603,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             else
               produce(a_layout, Layout<kLayoutRows>(), kb, end, ko, a_map, a_row, a_z, b_map, b_row, b_z, lane_map, lane_row);
           } else {
-            with_layout(p.b.mn_major, p.b.blocked, false, [&](auto b_layout) {
+            with_layout(w.b.mn_major, w.b.blocked, false, [&](auto b_layout) {
               produce(a_layout, b_layout, kb, end, ko, a_map, a_row, a_z, b_map, b_row, b_z, lane_map, lane_row);
             });
           }
@@ -627,14 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     if (!kPair || rank == 0) {
       const bool issuer = ptx::elect_one();
       const int n = kSwap ? p.mma_n : kBN;
-      const uint32_t idesc = ptx::idesc_f16kind_f32(kPair ? 2 * kTileM : kTileM, n, p.a.mn_major != 0, p.b.mn_major != 0, kF16);
-      // a k step of 16 values: 32 bytes inside the swizzle row, or 16 rows of 128 bytes
-      const uint64_t a_step = p.a.mn_major ? 2048u / 16u : 32u / 16u, b_step = p.b.mn_major ? 2048u / 16u : 32u / 16u;
-      const uint32_t a_lbo = p.a.mn_major ? 8192u : 16u, b_lbo = p.b.mn_major ? 8192u : 16u;
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      SegmentIter iter;
+      SegmentIter<kTwo> iter;
       iter.init(p, cluster, clusters, part, split);
       Segment sg;
       for (; ok && iter.next(p, sg); ++it) {
@@ -646,6 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           break;
         }
         ptx::tc_fence_after();
+        const Product& w = product_of<kTwo>(p, sg);
+        const uint32_t idesc = ptx::idesc_f16kind_f32(kPair ? 2 * kTileM : kTileM, n, w.a.mn_major != 0, w.b.mn_major != 0, kF16);
+        // a k step of 16 values: 32 bytes inside the swizzle row, or 16 rows of 128 bytes
+        const uint64_t a_step = w.a.mn_major ? 2048u / 16u : 32u / 16u, b_step = w.b.mn_major ? 2048u / 16u : 32u / 16u;
+        const uint32_t a_lbo = w.a.mn_major ? 8192u : 16u, b_lbo = w.b.mn_major ? 8192u : 16u;
         const uint32_t d = tmem_base + (uint32_t)(acc * kAccs * n);
         bool full_ready = false;
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
@@ -710,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     const int q = warp & 3, ewarp = warp - 2, half = ewarp >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
     uint8_t* const stage_out = base_ptr + (out0 - base) + ewarp * kStageOutBytes;  // row tiles
-    SegmentIter iter;
+    SegmentIter<kTwo> iter;
     iter.init(p, cluster, clusters, part, split);
     const int first_cut = p.dp_tiles + iter.u / p.k_blocks;  // the tile whose part lies in slot 0
     Segment sg;
@@ -768,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
     const int owner = q % split;  // row tiles: the pair that goes on with these 32 rows
     bool met = false;
     for (int it = 0; iter.next(p, sg); ++it) {
+      const Product& w = product_of<kTwo>(p, sg);
       const int acc = it & 1;
       // Row tiles: this lane's row, those that it reads and writes, and this warp's half of the columns.
       int out_row = -1, rows[8];
@@ -778,15 +824,15 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       auto fetch_residual = [&](int c) {
         if constexpr (!kSwap && kEpi == kEpiLinear) {
           const int64_t at = tile_col + c + 8 * (lane & 7);
-          stage_rows(stage_out, static_cast<const uint16_t*>(p.residual) + (at < p.cols ? at : 0), (uint32_t)p.ldr * 2u, rows, at < p.cols, lane);
+          stage_rows(stage_out, static_cast<const uint16_t*>(p.residual) + (at < w.cols ? at : 0), (uint32_t)p.ldr * 2u, rows, at < w.cols, lane);
         }
       };
       const bool has_residual = kEpi == kEpiLinear && p.residual != nullptr;
       if constexpr (!kSwap) {
         const int trow = (sg.mt * 2 + rank) * kTileM + q * 32 + lane;
-        const int chunk = trow / p.box, shard = chunk / p.shard_chunks;
-        const int in_shard = trow - shard * p.shard_chunks * p.box;
-        if (shard < p.shards && in_shard < p.shard_rows) out_row = (int)(shard * p.shard_rows) + in_shard;
+        const int chunk = trow / w.box, shard = chunk / w.shard_chunks;
+        const int in_shard = trow - shard * w.shard_chunks * w.box;
+        if (shard < w.shards && in_shard < w.shard_rows) out_row = (int)(shard * w.shard_rows) + in_shard;
         block_rows(rows, out_row, lane);
         if (has_residual && (sg.whole || (split > 1 && owner == part))) fetch_residual(0);  // while the products are made
       }
@@ -811,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       };
       if constexpr (kSwap) {
         // This lane's column of the weights, and this warp's half of the tokens, 8 at a time.
-        const int n = p.mma_n, end = min((half + 1) * (n / 2), p.chunks * p.box);
+        const int n = p.mma_n, end = min((half + 1) * (n / 2), w.chunks * w.box);
         const uint32_t t0 = lane_base + (uint32_t)(acc * kAccs * n);
         for (int c = half * (n / 2); c < end; c += 8) {
           uint32_t v[kAccs][8];
@@ -880,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           constexpr int kBlocks = kHalf / 64;  // of 32 columns of results
           constexpr int kPieces = 4 * kBlocks;
           const int64_t col = tile_col + 8 * (lane % kPieces);  // of this lane's piece
-          const bool inside = col < p.cols;
+          const bool inside = col < w.cols;
           int rows[kPieces];
           block_rows(rows, out_row, lane);
           uint32_t g16[kBlocks][16], u16[kBlocks][16];
@@ -906,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             pack32<kF16>(v[0], o16);
             stage_half(stage_out, lane, h, o16);
           }
-          write_staged<kPieces>(stage_out, static_cast<uint16_t*>(p.out[0]) + col, (uint32_t)p.ldo * 2u, rows, inside, lane);
+          write_staged<kPieces>(stage_out, static_cast<uint16_t*>(w.out[0]) + col, (uint32_t)w.ldo * 2u, rows, inside, lane);
           if (p.saved[0]) {
 #pragma unroll
             for (int h = 0; h < kBlocks; ++h) stage_half(stage_out, lane, h, g16[h]);
@@ -916,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             write_staged<kPieces>(stage_out, static_cast<uint16_t*>(p.saved[1]) + col, (uint32_t)p.lds * 2u, rows, inside, lane);
           }
         } else {
-          if (kEpi == kEpiPlain && p.out_f32) {
+          if (kEpi == kEpiPlain && w.out_f32) {
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
               uint32_t v[1][32];
@@ -931,34 +977,34 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               for (int i = 0; i < 8; ++i)
                 *staged(stage_out, lane, i) = make_uint4(v[0][4 * i], v[0][4 * i + 1], v[0][4 * i + 2], v[0][4 * i + 3]);
               const int64_t col = tile_col + c + 4 * (lane & 7);
-              write_staged<8>(stage_out, static_cast<float*>(p.out[sg.problem]) + col, (uint32_t)p.ldo * 4u, rows, col < p.cols, lane);
+              write_staged<8>(stage_out, static_cast<float*>(w.out[sg.problem]) + col, (uint32_t)w.ldo * 4u, rows, col < w.cols, lane);
             }
           } else {
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 64) {
               const int64_t col = tile_col + c, at = col + 8 * (lane & 7);  // this lane's piece
-              const bool inside = at < p.cols;
+              const bool inside = at < w.cols;
               if (has_residual && c > 0) fetch_residual(c);  // beside the loads and the activation below
               uint32_t z16[2][16];
               const bool has_saved = kEpi == kEpiLinear && p.saved[0] != nullptr;
-              uint32_t w[2][1][32];
+              uint32_t x2[2][1][32];
               if (sg.whole) {
-                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), w[0][0]);
-                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c + 32), w[1][0]);
+                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), x2[0][0]);
+                ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c + 32), x2[1][0]);
                 ptx::tmem_ld_wait();
                 if (c + 64 == kHalf) release();
               } else {
-                join(w[0], c, 0);
-                join(w[1], c + 32, 0);
+                join(x2[0], c, 0);
+                join(x2[1], c + 32, 0);
               }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                uint32_t(&v)[32] = w[h][0];
+                uint32_t(&v)[32] = x2[h][0];
                 if constexpr (kEpi == kEpiLinear) {
                   if (p.bias) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                      if (col + 32 * h + 8 * i < p.cols) {
+                      if (col + 32 * h + 8 * i < w.cols) {
                         Two b[4];
                         widen<kF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col + 32 * h + 8 * i)), b);
 #pragma unroll
@@ -989,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                 pack32<kF16>(v, o16);
                 stage_half(stage_out, lane, h, o16);
               }
-              write_staged<8>(stage_out, static_cast<uint16_t*>(p.out[sg.problem]) + at, (uint32_t)p.ldo * 2u, rows, inside, lane);
+              write_staged<8>(stage_out, static_cast<uint16_t*>(w.out[sg.problem]) + at, (uint32_t)w.ldo * 2u, rows, inside, lane);
               if (has_saved) {
                 stage_half(stage_out, lane, 0, z16[0]);
                 stage_half(stage_out, lane, 1, z16[1]);

@@ -10,7 +10,10 @@ GemmFn select_gemm(int bn, int epi, bool f16) {
   return epi == kEpiGated ? swap_gated(f16) : epi == kEpiLinear ? swap_linear(f16) : swap_plain(f16);
 }
 
-cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters) {
+namespace {
+
+template <class P>
+cudaError_t prepare(void (*fn)(P), int cluster, int* clusters) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -26,7 +29,8 @@ cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters) {
   return cudaOccupancyMaxActiveClusters(clusters, fn, &cfg);
 }
 
-cudaError_t launch_gemm(GemmFn fn, const GemmParams& p, int clusters, int cluster, size_t smem, cudaStream_t stream) {
+template <class P>
+cudaError_t launch(void (*fn)(P), const P& p, int clusters, int cluster, size_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * cluster));
   cfg.blockDim = dim3(kThreads);
@@ -43,6 +47,17 @@ cudaError_t launch_gemm(GemmFn fn, const GemmParams& p, int clusters, int cluste
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+}  // namespace
+
+cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters) { return prepare(fn, cluster, clusters); }
+cudaError_t prepare_two(TwoFn fn, int* clusters) { return prepare(fn, 2, clusters); }
+cudaError_t launch_gemm(GemmFn fn, const GemmParams& p, int clusters, int cluster, size_t smem, cudaStream_t stream) {
+  return launch(fn, p, clusters, cluster, smem, stream);
+}
+cudaError_t launch_two(TwoFn fn, const TwoParams& p, int clusters, size_t smem, cudaStream_t stream) {
+  return launch(fn, p, clusters, 2, smem, stream);
 }
 
 }  // namespace ff

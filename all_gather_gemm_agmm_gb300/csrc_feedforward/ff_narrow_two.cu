@@ -1,0 +1,8 @@
+// ff_narrow_two.cu -- instantiations of the feed-forward products' kernel.
+#include "ff_gemm.cuh"
+
+namespace agmm {
+namespace ff {
+TwoFn narrow_two(bool f16) { return f16 ? &agmm_ff_gemm<kNarrowN, kEpiPlain, true, true> : &agmm_ff_gemm<kNarrowN, kEpiPlain, false, true>; }
+}  // namespace ff
+}  // namespace agmm

@@ -43,37 +43,40 @@ struct OperandParams {
   int by_problem, by_segment, by_shard, by_rank, z_segment;
 };
 
-struct __align__(128) GemmParams {
+// One matrix product (or two of one shape: the gradients of two weights).
+struct __align__(128) Product {
   CUtensorMap a_map[kMaxShards];
   CUtensorMap b_map[kMaxShards];
   OperandParams a, b;
   // Row tiles: pair tiles of 256 x 256 or 128 (gated: half of them columns of each product).
   // Swapped tiles: 128 columns of the weights, all tokens.
-  int problems;            // products that share one launch (gradients of two weights)
-  int tiles_per_problem, m_tiles, n_tiles, num_tiles, group_m;
+  int problems, tiles_per_problem, m_tiles, n_tiles, group_m;
   int b_tile_step;         // row tiles: B rows from one tile to the next
   int b_half_step;         // row tiles: ... and from the leader's half to the follower's
   int k_blocks;            // of all segments
   int seg_blocks;          // of one segment
-  int dp_tiles;            // tiles [0, dp_tiles) are worked on whole
-  int sk_clusters;         // the k blocks of the others are dealt evenly to this many clusters:
-  int sk_share, sk_extra;  // sk_share to each, and one more to the first sk_extra
   // Tokens (row tiles: the rows of A; swapped tiles: the rows of B) in chunks of
   // box rows that lie in one shard.
   int shards, box, shard_chunks;  // shard_chunks: chunks of a shard
   int chunks;                     // of all shards
   int64_t shard_rows;
+  void* out[2];            // by problem
+  int64_t ldo;
+  int out_f32;             // plain products: float32 results
+  int64_t cols;            // columns of the results
+};
+
+struct __align__(128) GemmParams : Product {
+  int num_tiles;
+  int dp_tiles;            // tiles [0, dp_tiles) are worked on whole
+  int sk_clusters;         // the k blocks of the others are dealt evenly to this many clusters:
+  int sk_share, sk_extra;  // sk_share to each, and one more to the first sk_extra
   int mma_n;               // swapped tiles: token columns, a multiple of 16
   int recv_slots;          // ... groups of 8 tokens that each CTA of a cluster owns
   int split;               // CTAs, or pairs, of a cluster that share a tile's k
   uint32_t recv_bytes;     // their parts, in the shared memory of the owner
   int stages;
   uint32_t tmem_cols;
-  // results
-  void* out[2];            // by problem
-  int64_t ldo;
-  int out_f32;             // plain products: float32 results
-  int64_t cols;            // columns of the results
   void* saved[2];          // gated: the two products; linear: the sum before the activation
   int64_t lds;
   const void* bias;
@@ -89,9 +92,20 @@ struct __align__(128) GemmParams {
   int test_drop;           // test hook: the first arrival of a producer is dropped
 };
 
+// Two products in one launch (both gradients of a layer), all tiles whole: after the first's,
+// `lead` clusters of which have one more than the others; those others take `ahead` tiles of the
+// second meanwhile, then all take `each`, and `rest` of them one more.
+struct __align__(128) TwoParams : GemmParams {
+  Product second;
+  int lead, ahead, each, rest;
+};
+
 using GemmFn = void (*)(GemmParams);
+using TwoFn = void (*)(TwoParams);
 // bn: columns of row tiles (0: swapped tiles)
 GemmFn select_gemm(int bn, int epi, bool f16);
+TwoFn wide_two(bool f16);
+TwoFn narrow_two(bool f16);
 GemmFn wide_plain(bool f16);
 GemmFn wide_gated(bool f16);
 GemmFn wide_linear(bool f16);
@@ -104,7 +118,9 @@ GemmFn swap_linear(bool f16);
 
 // Sets the shared-memory limit of a kernel and reports the clusters that fit.
 cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters);
+cudaError_t prepare_two(TwoFn fn, int* clusters);
 cudaError_t launch_gemm(GemmFn fn, const GemmParams& p, int clusters, int cluster, size_t smem, cudaStream_t stream);
+cudaError_t launch_two(TwoFn fn, const TwoParams& p, int clusters, size_t smem, cudaStream_t stream);
 
 // --------------------------------------------------------------- pointwise
 // d_gate = d_out * up * act'(gate), d_up = d_out * act(gate)

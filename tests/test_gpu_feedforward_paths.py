@@ -23,11 +23,12 @@ def agmm():
 
 ROWS = [dict(AGMM_PATH="0", AGMM_BN=bn, AGMM_STREAMK=cut) for bn in ("128", "256") for cut in ("0", "1")]
 ROWS += [dict(AGMM_PATH="0", AGMM_BN="128", AGMM_SPLITK=str(s)) for s in (2, 3, 4)]
+ROWS += [dict(AGMM_PATH="0", AGMM_BN=bn, AGMM_MERGE=m) for bn in ("128", "256") for m in ("0", "1")]
 SWAP = [dict(AGMM_PATH="1", AGMM_SPLITK=str(s)) for s in (1, 2, 3, 4, 5, 6, 7, 8)]
 
 
 def name(env):
-    return "-".join(v for v in env.values())
+    return "-".join(k[5:].lower() + v for k, v in env.items())
 
 
 # shards, rows, k, n: one row to several tiles, sizes that end inside tiles and k blocks
@@ -98,3 +99,30 @@ def test_cut_tiles_behind_whole_ones(agmm, monkeypatch, env):
         again = torch.full_like(r, float("nan"))
         plan.run(x, w, again, ws, residual=r)
         assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("sizes", [(300, 264, 4104), (2000, 4104, 72), (1500, 1032, 1544), (900, 72, 2056)], ids=str)
+@pytest.mark.parametrize("bn", ["128", "256"])
+def test_both_gradients_in_one_launch(agmm, monkeypatch, sizes, bn):
+    """Either product the longer one, few and many tiles of each, as two launches give them bit by bit
+    (none of them is cut)."""
+    t, k, n = sizes
+    g = torch.Generator(device="cuda").manual_seed(10)
+    new = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, w, d = [new(t // 2, k) for _ in range(2)], new(k, n), new(t, n)
+    monkeypatch.setenv("AGMM_BN", bn)
+    monkeypatch.setenv("AGMM_STREAMK", "0")
+    monkeypatch.setenv("AGMM_SPLITK", "1")
+    got = []
+    for merge in ("0", "1"):
+        monkeypatch.setenv("AGMM_MERGE", merge)
+        plan = agmm.LinearPlan(k, n)
+        ws = plan.new_workspace()
+        dx, dw = torch.full((t, k), float("nan"), dtype=torch.bfloat16, device="cuda"), torch.full((k, n), float("nan"), device="cuda")
+        plan.backward(d, x, w, ws, dx=dx, dw=dw)
+        plan.query_status(ws)
+        got.append((dx, dw))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    want = linear_grad(d, torch.cat(x), w, None, None, False, torch.bfloat16, torch.float32)
+    check(got[1][0], *want["dx"], "dx")
+    check(got[1][1], *want["dw"], "dw")

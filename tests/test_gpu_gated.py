@@ -118,10 +118,14 @@ def test_backward_over_the_saved_products(agmm):
     dwg, dwu, dwg2, dwu2 = (torch.empty_like(wg) for _ in range(4))
     plan.backward(d, xs, wg, wu, g, u, dg, du, ws, dx=dx, dw_gate=dwg, dw_up=dwu)
     g2, u2 = g.clone(), u.clone()
+    want = gated_grad(d, xs[0], wg, wu, g, u, "silu", True, torch.bfloat16, torch.bfloat16)
     plan.backward(d, xs, wg, wu, g, u, g, u, ws, dx=dx2)
-    assert torch.equal(g, dg) and torch.equal(u, du) and torch.equal(dx, dx2)
+    assert torch.equal(g, dg) and torch.equal(u, du)
+    check(dx2, *want["dx"], "dx")  # alone it may be cut along its sum: another order
     plan.backward(d, xs, wg, wu, g2, u2, g2, u2, ws, dw_gate=dwg2, dw_up=dwu2)
-    assert torch.equal(dwg, dwg2) and torch.equal(dwu, dwu2)
+    for name, x, y in (("dw_gate", dwg, dwg2), ("dw_up", dwu, dwu2)):
+        check(x, *want[name], name)
+        check(y, *want[name], name)
 
 
 def test_strides_and_halves(agmm):

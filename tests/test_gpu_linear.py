@@ -106,12 +106,13 @@ def test_backward(agmm, case):
         got["d_pre"] = d_pre
     for name, x in got.items():
         check(x, *want[name], name)
-    # one at a time, and over the saved sum
+    # one at a time, and over the saved sum.  A product alone may be cut along its sum, where both
+    # in one launch are not: another order of the same float32 sums, each within the bound
     for name in ("dx", "dw", "d_bias"):
         alone = torch.full_like(got[name], float("nan"))
         over = z.clone() if kind else None
         plan.backward(d, xs, w, ws, pre=over, d_pre=over, **{name: alone})
-        assert torch.equal(alone, got[name]), name
+        check(alone, *want[name], name)
 
 
 def test_strides(agmm):
