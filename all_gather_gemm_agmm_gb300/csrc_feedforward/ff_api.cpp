@@ -383,6 +383,25 @@ agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice 
                     "product launch");
 }
 
+// Swapped tiles: the CTAs of a cluster that share a tile's k, by the shortest estimate.
+struct SwapChoice {
+  int split;
+  double time;
+};
+SwapChoice choose_swap(const ProductPlan* pl, int tiles, int k_blocks, size_t stage_bytes) {
+  SwapChoice best = {1, 1e300};
+  for (int split = 1; split <= kMaxSplit; ++split) {
+    if (split > 1 && (split > k_blocks || tiles > pl->clusters[split])) break;
+    if (pl->split >= 1 && split != std::min(pl->split, k_blocks)) continue;
+    const int ctas = std::min(tiles * split, pl->clusters[1]);
+    const double time = (double)k_blocks / split * stage_bytes * std::max(kSwapByte, kMemoryByte * ctas) + (split > 1 ? kSplitTile : 0);
+    if (time < 1.02 * best.time) best = {split, time};  // of two alike the one with more copies in flight
+  }
+  return best;
+}
+
+size_t swap_stage_bytes(int accs, int token_columns) { return (size_t)accs * kTileBytes + (size_t)ceil_div(token_columns, 16) * 16 * 128; }
+
 agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t features, cudaStream_t stream) {
   p->m_tiles = (int)ceil_div(features, kTileM);
   p->n_tiles = 1;
@@ -390,20 +409,8 @@ agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t fe
   p->group_m = 1;
   p->mma_n = (int)ceil_div(p->chunks * p->box, 16) * 16;
   const int accs = epi == kEpiGated ? 2 : 1, tiles = p->num_tiles, groups = (int)ceil_div(p->chunks * p->box, 8);
-  const size_t stage = (size_t)accs * kTileBytes + (size_t)p->mma_n * 128;
-  // The CTAs of a cluster share a tile's k where that is estimated to be shorter.
-  p->split = 1;
-  double least = 1e300;
-  for (int split = 1; split <= kMaxSplit; ++split) {
-    if (split > 1 && (split > p->k_blocks || tiles > pl->clusters[split])) break;
-    if (pl->split >= 1 && split != std::min(pl->split, p->k_blocks)) continue;
-    const int ctas = std::min(tiles * split, pl->clusters[1]);
-    const double time = (double)p->k_blocks / split * stage * std::max(kSwapByte, kMemoryByte * ctas) + (split > 1 ? kSplitTile : 0);
-    if (time < 1.02 * least) {  // of two alike the one with more copies in flight
-      least = time;
-      p->split = split;
-    }
-  }
+  const size_t stage = swap_stage_bytes(accs, p->mma_n);
+  p->split = choose_swap(pl, tiles, p->k_blocks, stage).split;
   p->recv_slots = (int)ceil_div(groups, p->split);
   p->recv_bytes = p->split > 1 ? (uint32_t)(p->split * p->recv_slots * accs * kTileM * 8 * sizeof(float)) : 0;
   p->stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - 1024 - kCtlBytes - p->recv_bytes) / stage);
@@ -447,6 +454,8 @@ agmm_status_t forward(const ProductPlan* pl, GemmParams* p, int epi, int shards,
   }
   return run_rows(pl, p, epi, choice, m_tiles, stream);
 }
+
+constexpr int64_t kFewTokenBytes = 16 << 20;
 
 // What the products of a backward pass are made of.
 struct Grads {
@@ -580,8 +589,12 @@ agmm_status_t run_grads(const ProductPlan* pl, const Grads& g, void* workspace, 
   const int swap = g.dx && pl->path != 0 ? swap_box(1, tokens) : 0;
   RowChoice for_dx = {}, for_dw = {};
   if (g.dx && !swap) for_dx = choose_rows(pl, dx_m_tiles, pl->k, (int)dx_blocks, 1, false);
+  if (g.dx && swap) for_dx.time = choose_swap(pl, (int)ceil_div(pl->k, kTileM), (int)dx_blocks, swap_stage_bytes(1, swap)).time;
+  // Few tokens: row tiles read small weights as fast as swapped ones, large ones not (16 tokens, 4096 x
+  // 4096: 24.1 us in one launch, 21.1 us in two; 64 tokens, 2048 x 2048: 10.7 and 13.0 us).
+  const bool may_merge = g.dx && g.dw && pl->merge != 0 && (!swap || g.weights * pl->k * pl->n * 2 <= kFewTokenBytes);
   if (g.dw) for_dw = choose_rows(pl, dw_m_tiles, dw_cols, (int)dw_blocks, g.weights, false);
-  if (g.dx && g.dw && !swap && pl->merge != 0) {
+  if (may_merge) {
     const TwoChoice two = choose_two(pl, dx_m_tiles, (int)dx_blocks, dw_m_tiles, dw_cols, (int)dw_blocks, g.weights);
     if (two.time < 1e300 && (pl->merge == 1 || two.time < for_dx.time + for_dw.time + kLaunch))
       return run_two(pl, g, two, dx_m_tiles, dw_m_tiles, workspace, stream);
