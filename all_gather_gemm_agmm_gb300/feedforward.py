@@ -165,13 +165,20 @@ class _FeedForwardPlan(_AttentionPlan):
             _check(st)
 
 
+def _width(name, v):
+    v = int(v)
+    if not -2**31 <= v < 2**31:  # an int of the plan's description
+        raise ValueError(f"{name} must be a 32-bit number, got {v}")
+    return v
+
+
 class LayerNormPlan(_FeedForwardPlan):
     """Layer norm of rows and its backward pass (agmm_layer_norm_run, _backward)."""
 
     _name = "layer_norm"
 
     def __init__(self, columns: int, eps: float = 1e-5, f16: bool = False):
-        self.columns, self.eps = int(columns), float(eps)
+        self.columns, self.eps = _width("columns", columns), float(eps)
         self._open(_LayerNormDesc(self.columns, AGMM_F16 if f16 else AGMM_BF16, self.eps), f16)
 
     def run(self, x, out, weight=None, bias=None, mean=None, rstd=None, stream=None) -> None:
@@ -211,7 +218,7 @@ class _ProductPlan(_FeedForwardPlan):
     def __init__(self, k: int, n: int, activation: Optional[str], rhs_transpose: bool, f16: bool):
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-        self.k, self.n, self.activation, self.rhs_transpose = int(k), int(n), activation, bool(rhs_transpose)
+        self.k, self.n, self.activation, self.rhs_transpose = _width("k", k), _width("n", n), activation, bool(rhs_transpose)
         self._weight_shape = (self.n, self.k) if self.rhs_transpose else (self.k, self.n)
         self._open(_ProductDesc(self.k, self.n, ACTIVATIONS[activation], int(self.rhs_transpose), AGMM_F16 if f16 else AGMM_BF16), f16)
 

@@ -83,6 +83,14 @@ def test_null_calls(agmm_lib):
         assert getattr(lib, f"agmm_{name}_workspace_bytes")(None) == 0
 
 
+@pytest.mark.parametrize("wide", [2**31, 2**32 + 64, -2**32 + 64])
+def test_widths_past_32_bits(wide):
+    """A plan's description has them as int: 2^32 + 64 is not a plan of 64."""
+    for make in (lambda: agmm.LayerNormPlan(wide), lambda: agmm.GatedPlan(wide, 64), lambda: agmm.LinearPlan(64, wide)):
+        with pytest.raises(ValueError, match="32-bit"):
+            make()
+
+
 def test_unknown_activation():
     with pytest.raises(ValueError, match="activation"):
         agmm.GatedPlan(64, 64, activation="swish")
