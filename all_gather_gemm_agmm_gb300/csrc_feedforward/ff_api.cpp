@@ -127,7 +127,7 @@ agmm_status_t check_matrix(const char* name, const void* p, int64_t* stride, int
   return AGMM_OK;
 }
 
-// The device's peak clock.  Asked once per device: the driver takes most of a
+// The device's peak clock.  Asked once per device: CUDA takes most of a
 // millisecond to answer.
 int peak_clock_khz(int device) {
   static std::atomic<int> known[64];
@@ -182,7 +182,7 @@ struct Matrix {
 // (MN-major); a tile has tile_rows of its rows or values.  128-byte swizzled, zeros outside: what lies
 // behind a segment's last row is not its neighbour's.
 //
-// Encoding takes the driver half a microsecond, and a training step has ten maps: a thread keeps
+// Encoding takes half a microsecond, and a training step has ten maps: a thread keeps
 // those of its latest layouts (sizes and strides, whatever the memory) and puts the address in.
 agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m, bool mn_major, int tile_rows, bool f16) {
   const TensorMapCalls& calls = tensor_map_calls();
@@ -231,7 +231,7 @@ agmm_status_t encode_operand(CUtensorMap* map, OperandParams* o, const Matrix& m
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The time that a schedule takes, in cycles, as far as it differs from others: clusters that each
-// work through `blocks` k blocks.  Constants as measured (the design doc has the table).
+// work through `blocks` k blocks.  The constants were measured on this GPU, kernel by kernel.
 constexpr double kWideBlock = 512, kNarrowBlock = 340;    // a k block of a row tile's main loop
 constexpr double kWideTile = 4000, kNarrowTile = 2500;    // its results, beside the next tile's main loop
 constexpr double kWideCut = 16000, kNarrowCut = 6500;     // the parts' way to L2 and back
@@ -455,6 +455,9 @@ agmm_status_t forward(const ProductPlan* pl, GemmParams* p, int epi, int shards,
   return run_rows(pl, p, epi, choice, m_tiles, stream);
 }
 
+// Backward passes of few tokens: both gradients may share a launch of row tiles, which read small
+// weights as fast as swapped tiles do, but not large ones (16 tokens, 4096 x 4096: 24.1 us in one
+// launch, 21.1 us in two; 64 tokens, 2048 x 2048: 10.7 and 13.0 us).
 constexpr int64_t kFewTokenBytes = 16 << 20;
 
 // What the products of a backward pass are made of.
@@ -580,7 +583,10 @@ agmm_status_t run_two(const ProductPlan* pl, const Grads& g, const TwoChoice& c,
   return check_cuda(launch_two(c.bn == kWideN ? wide_two(pl->f16) : narrow_two(pl->f16), p, pl->pairs, smem, stream), "products launch");
 }
 
-// The products of a backward pass: in one launch where that is estimated to be shorter.
+// The products of a backward pass: in one launch where that is estimated to be shorter.  It saves a
+// launch and a ragged last wave, but cuts no tile along k.  (500 tokens, 2048 -> 512: 8.4 us in one
+// launch, 13.5 in two; gated, 1003 tokens, 1288 -> 2056: 36 and 47 us; 4096 tokens, 2560 -> 5120: 115
+// and 128 us; 4096 tokens, 4096 -> 14336: 495 and 524 us; 8192 tokens, 4096 -> 7168: 500 us either way.)
 agmm_status_t run_grads(const ProductPlan* pl, const Grads& g, void* workspace, cudaStream_t stream) {
   const int64_t tokens = g.shards * g.rows, dw_rows = pl->transpose ? pl->n : pl->k, dw_cols = pl->transpose ? pl->k : pl->n;
   const int64_t dx_m_tiles = ceil_div(tokens, 2 * kTileM), dw_m_tiles = ceil_div(dw_rows, 2 * kTileM);
@@ -590,8 +596,6 @@ agmm_status_t run_grads(const ProductPlan* pl, const Grads& g, void* workspace, 
   RowChoice for_dx = {}, for_dw = {};
   if (g.dx && !swap) for_dx = choose_rows(pl, dx_m_tiles, pl->k, (int)dx_blocks, 1, false);
   if (g.dx && swap) for_dx.time = choose_swap(pl, (int)ceil_div(pl->k, kTileM), (int)dx_blocks, swap_stage_bytes(1, swap)).time;
-  // Few tokens: row tiles read small weights as fast as swapped ones, large ones not (16 tokens, 4096 x
-  // 4096: 24.1 us in one launch, 21.1 us in two; 64 tokens, 2048 x 2048: 10.7 and 13.0 us).
   const bool may_merge = g.dx && g.dw && pl->merge != 0 && (!swap || g.weights * pl->k * pl->n * 2 <= kFewTokenBytes);
   if (g.dw) for_dw = choose_rows(pl, dw_m_tiles, dw_cols, (int)dw_blocks, g.weights, false);
   if (may_merge) {

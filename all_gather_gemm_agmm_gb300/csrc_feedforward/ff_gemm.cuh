@@ -35,7 +35,9 @@
 // of a ragged last wave, and the wave before it, are cut evenly over the clusters.  Every
 // warp of a cut row tile's epilogue leaves its float32 partial results in the workspace and
 // counts its k blocks; the warp that completes the count adds all parts and goes on to the
-// results.  Nobody waits for another cluster, and parts are added in the order of k.
+// results.  Nobody waits for another cluster, and parts are added in the order of k.  Both
+// gradients of a layer may be one launch (kTwo): the second product's tiles, all whole, follow
+// the first's, and clusters with one less of those take more of them.
 //
 // Every mbarrier wait is bounded; one that runs out records AGMM_ERR_TIMEOUT in the
 // status words, all roles leave their loops, wait (bounded) for their own work in
@@ -498,6 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
   const uint32_t leader_place = (uint32_t)(place - rank);
   const uint16_t pair_mask = (uint16_t)(3u << leader_place);
 
+  // A CTA takes more than half of an SM's shared memory: the next kernel's cannot come before this
+  // one's tensor memory is allocated.
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   if (warp == 0) {
     if (lane < S) {
@@ -583,6 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         }
         const int next_stage = stage + 1 == S ? 0 : stage + 1;
         const uint32_t next_phase = stage + 1 == S ? phase ^ 1u : phase;
+        // a look ahead at the next stage, by the converged warp: one access of one address, one answer
+        // (a vote on it costs 0.5 of 10.4 us for one token)
         empty_ready = kb + 1 < kb1 && ptx::mbar_test_wait(bar_empty(ctl, next_stage), next_phase ^ 1u);
         if (dropped) {
           if (!kPair || rank == 0) {
@@ -841,6 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       res = __shfl_sync(0xffffffffu, res, 0);
       if (res != kWaitOk) {
         if (lane == 0) record_failure(p, abort_flag, res, kRoleEpilogue, acc, sg.tile);
+        if (has_residual) asm volatile("cp.async.wait_all;" ::: "memory");
         break;
       }
       ptx::tc_fence_after();

@@ -128,6 +128,16 @@ __device__ __forceinline__ Two positive_two(Two z) {
   const float2 v = halves(z);
   return two(positive(v.x), positive(v.y));
 }
+// max(z, -FLT_MAX): an fp16 product past -65504 was saved as -infinity, and times 0 it would be a NaN.
+__device__ __forceinline__ float finite_below(float z) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0fff7fffff;" : "=f"(y) : "f"(z));
+  return y;
+}
+__device__ __forceinline__ Two finite_below_two(Two z) {
+  const float2 v = halves(z);
+  return two(finite_below(v.x), finite_below(v.y));
+}
 __device__ __forceinline__ Two clamp_two(Two z, float most) {
   const float2 v = halves(z);
   return two(fminf(fmaxf(v.x, -most), most), fminf(fmaxf(v.y, -most), most));
@@ -193,7 +203,7 @@ __device__ __forceinline__ void activate_with_slope(Two z, Two& a, Two& slope) {
     slope = two(v.x > 0.0f ? 1.0f : (v.x != v.x ? v.x : 0.0f), v.y > 0.0f ? 1.0f : (v.y != v.y ? v.y : 0.0f));
   } else if constexpr (kAct == kActSilu) {
     const Two s = logistic_two(mul2(z, both(-kLog2e))), rest = fma2(s, both(-1.0f), both(1.0f));
-    a = mul2(z, s);
+    a = mul2(finite_below_two(z), s);
     slope = mul2(s, fma2(clamp_two(z, 200.0f), rest, both(1.0f)));
   } else if constexpr (kAct == kActGelu) {
     Two x, gauss;
@@ -205,7 +215,7 @@ __device__ __forceinline__ void activate_with_slope(Two z, Two& a, Two& slope) {
     slope = fma2(clamp_two(z, 20.0f), mul2(gauss, both(kInvSqrt2Pi)), phi);
   } else if constexpr (kAct == kActGeluTanh) {
     const Two b = clamp_two(z, 20.0f), s = logistic_two(tanh_exponent(z)), rest = fma2(s, both(-1.0f), both(1.0f));
-    a = mul2(z, s);
+    a = mul2(finite_below_two(z), s);
     const Two dv = mul2(fma2(mul2(b, b), both(3.0f * kTanhCube), both(1.0f)), both(kTanhScale2));
     slope = fma2(mul2(b, mul2(s, rest)), dv, s);
   }

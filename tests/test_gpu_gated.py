@@ -199,3 +199,29 @@ def test_far_preactivations(agmm, kind):
     slope[-2:] = 0.0 if kind == "relu" else 0.5
     assert bool(((dg[:, 0].double() - slope).abs() <= 1e-9 + 2 ** -8 * slope).all()), dg[:, 0]
     assert torch.equal(du[:, 0], out[:, 0])
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_saved_infinities(agmm, kind):
+    """An fp16 product past 65504 is saved as infinite.  Below, the activation and its slope are 0,
+    and so are both gradients; above, the slope is 1 and the activation's own size infinite."""
+    k, n = 8, 8
+    x = torch.zeros(4, k, dtype=torch.float16, device="cuda")
+    x[:, 0], x[:, 1] = torch.tensor([-60000.0, 60000.0, -40000.0, 1.0], device="cuda"), 1
+    wg, wu = (torch.zeros(k, n, dtype=torch.float16, device="cuda") for _ in range(2))
+    wg[0], wu[1] = 2, 0.5
+    out, g, u = agmm.gated_matmul(x, wg, wu, activation=kind, return_saved=True)
+    assert g[:3, 0].tolist() == [float("-inf"), float("inf"), float("-inf")]
+    assert out[:3, 0].tolist() == [0, 60000, 0]  # of the float32 products, half of 120000 among them
+    plan = agmm.GatedPlan(k, n, activation=kind, f16=True)
+    d = torch.ones_like(out)
+    dg, du = torch.empty_like(d), torch.empty_like(d)
+    plan.backward(d, x, wg, wu, g, u, dg, du, plan.new_workspace())
+    assert dg[:3, 0].tolist() == [0, 0.5, 0]
+    assert du[:3, 0].tolist() == [0, float("inf"), 0]
+    assert bool(dg[3].isfinite().all() and du[3].isfinite().all())
+    linear = agmm.LinearPlan(k, n, activation=kind, f16=True)
+    d_pre, dx = torch.empty_like(d), torch.empty_like(x)
+    linear.backward(d, x, wg, linear.new_workspace(), pre=g, d_pre=d_pre, dx=dx)
+    assert d_pre[:3, 0].tolist() == [0, 1, 0]
+    assert bool(dx.isfinite().all())
