@@ -103,6 +103,15 @@ __device__ __forceinline__ uint4 narrow(const Two (&x)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A sum over rows, as float32 or rounded once.
+template <bool kF16>
+__device__ __forceinline__ void store_sum(void* out, int64_t col, float sum, int out_f32) {
+  if (out_f32)
+    static_cast<float*>(out)[col] = sum;
+  else
+    static_cast<uint16_t*>(out)[col] = pack1<kF16>(sum);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)

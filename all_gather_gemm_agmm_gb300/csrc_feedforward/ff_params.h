@@ -134,15 +134,17 @@ struct GatedGradParams {
 cudaError_t launch_gated_grad(const GatedGradParams& p, bool f16, int sms, cudaStream_t stream);
 
 // d_pre = d_out * act'(pre) (pre NULL: no activation, nothing is written), and the sums of
-// its columns, in parts of [blocks][cols].
+// its columns: in parts of [blocks][cols], or (few rows) the whole of them.
 struct ActGradParams {
   int64_t rows, cols;
   const uint16_t *d_out, *pre;
   uint16_t* d_pre;
   int64_t ld_out, ld_pre, ld_grad;
   int act;
-  float* part;  // NULL: no sums
+  float* part;  // NULL: no parts
   int row_blocks;
+  void* d_bias;  // few rows: the sums; NULL: no sums, or parts
+  int out_f32;
 };
 int act_grad_row_blocks(int64_t rows, int64_t cols, int sms);
 cudaError_t launch_act_grad(const ActGradParams& p, bool f16, cudaStream_t stream);
@@ -183,7 +185,13 @@ struct NormGradParams {
   int64_t ld_dx;
   float* part;  // [blocks][2][cols]: the sums of d_out * xhat and of d_out; NULL: not wanted
   int stages;   // rows in flight, where they stream
+  // few rows: the sums themselves (NULL: not wanted), and the blocks that have columns
+  void *d_weight, *d_bias;
+  int out_f32, column_blocks;
 };
+// Few rows: dx and the sums in one launch.  dx must not lie over d_out if sums are wanted.
+bool few_norm_rows(int64_t rows, int cols);
+cudaError_t launch_norm_grad_few(const NormGradParams& p, bool f16, cudaStream_t stream);
 int norm_grad_blocks(int64_t rows, int cols, int sms);
 cudaError_t launch_norm_grad(const NormGradParams& p, bool f16, int blocks, cudaStream_t stream);
 

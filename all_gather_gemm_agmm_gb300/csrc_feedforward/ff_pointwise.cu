@@ -8,8 +8,9 @@
 // Bound: device memory.  A thread keeps its 8 columns and walks down the rows, so that
 // sums of columns stay in its registers; the blocks' sums are added in a fixed order.
 // Measured: gated silu, 8192 x 7168: 88 us, 6.7 TB/s (four blocks to an SM; with three, 98 us).
-// Linear gelu with sums, 4096 x 5120: 31 us and 4 us for the parts, 4.1 TB/s: two exponentials
-// to a value take 9 us of the special-function units, and the arithmetic 11 us.
+// Linear gelu with sums, 4096 x 5120: 28 us with the parts' 4 us, 4.5 TB/s (64 registers and one wave
+// of blocks; with 80 and two waves 31 us): two exponentials to a value take 9 us of the
+// special-function units, and the arithmetic 11 us.
 #include "ff_math.cuh"
 #include "ptx_sm103.cuh"
 
@@ -70,16 +71,11 @@ __global__ void __launch_bounds__(256, 4) agmm_gated_grad(const __grid_constant_
   });
 }
 
+// Rows first, first + step, ... of 8 columns, and their sums.
 template <bool kF16>
-__global__ void __launch_bounds__(256, 3) agmm_act_grad(const __grid_constant__ ActGradParams p) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
-  if (col >= p.cols) return;
-  Two sum[4] = {0, 0, 0, 0};
+__device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t col, int64_t first, int64_t step, Two (&sum)[4]) {
   with_activation(p.act, [&](auto act) {
-    const int64_t step = gridDim.y;
-    for (int64_t r = blockIdx.y; r < p.rows; r += step * kActUnroll) {
+    for (int64_t r = first; r < p.rows; r += step * kActUnroll) {
       uint4 d[kActUnroll], z[kActUnroll];
 #pragma unroll
       for (int i = 0; i < kActUnroll; ++i) {
@@ -112,11 +108,53 @@ __global__ void __launch_bounds__(256, 3) agmm_act_grad(const __grid_constant__ 
       }
     }
   });
+}
+
+template <bool kF16>
+__global__ void __launch_bounds__(256, 4) agmm_act_grad(const __grid_constant__ ActGradParams p) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (col >= p.cols) return;
+  Two sum[4] = {0, 0, 0, 0};
+  act_grad_rows<kF16>(p, col, blockIdx.y, gridDim.y, sum);
   if (p.part) {
     ulonglong2* const dst = reinterpret_cast<ulonglong2*>(p.part + (int64_t)blockIdx.y * p.cols + col);
     dst[0] = make_ulonglong2(sum[0], sum[1]);
     dst[1] = make_ulonglong2(sum[2], sum[3]);
   }
+}
+
+// Few rows, with their sums: 64 columns to a block, four rows to a warp, whose sums meet in shared
+// memory.  No parts and no second launch.
+constexpr int kFewWarps = 16, kFewPieces = 8, kFewCols = kFewPieces * 8, kFewRowsAWarp = 32 / kFewPieces;
+static_assert(kFewWarps * 32 >= kFewCols, "a thread for each column's sum");
+
+template <bool kF16>
+__global__ void __launch_bounds__(kFewWarps * 32) agmm_act_grad_few(const __grid_constant__ ActGradParams p) {
+  __shared__ __align__(16) float s[kFewWarps][kFewCols];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, piece = lane % kFewPieces;
+  const int64_t col = ((int64_t)blockIdx.x * kFewPieces + piece) * 8;
+  Two sum[4] = {0, 0, 0, 0};
+  if (col < p.cols) act_grad_rows<kF16>(p, col, warp * kFewRowsAWarp + lane / kFewPieces, kFewWarps * kFewRowsAWarp, sum);
+#pragma unroll
+  for (int o = kFewPieces; o < 32; o *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], __shfl_xor_sync(0xffffffffu, sum[e], o));
+  if (lane < kFewPieces) {
+    ulonglong2* const mine = reinterpret_cast<ulonglong2*>(&s[warp][piece * 8]);
+    mine[0] = make_ulonglong2(sum[0], sum[1]);
+    mine[1] = make_ulonglong2(sum[2], sum[3]);
+  }
+  __syncthreads();
+  const int64_t c = (int64_t)blockIdx.x * kFewCols + threadIdx.x;
+  if (threadIdx.x >= kFewCols || c >= p.cols) return;
+  float total = s[0][threadIdx.x];
+#pragma unroll
+  for (int i = 1; i < kFewWarps; ++i) total += s[i][threadIdx.x];
+  store_sum<kF16>(p.d_bias, c, total, p.out_f32);
 }
 
 // 32 columns to a block, their parts dealt to its 16 warps.
@@ -142,10 +180,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) agmm_sum_parts(const __grid_co
   if (warp == 0 && col < p.cols) {
 #pragma unroll
     for (int i = 1; i < kSumWarps; ++i) sum += s[i][lane];
-    if (p.out_f32)
-      static_cast<float*>(p.out[blockIdx.y])[col] = sum;
-    else
-      static_cast<uint16_t*>(p.out[blockIdx.y])[col] = pack1<kF16>(sum);
+    store_sum<kF16>(p.out[blockIdx.y], col, sum, p.out_f32);
   }
 }
 
@@ -189,7 +224,7 @@ int act_grad_row_blocks(int64_t rows, int64_t cols, int sms) {
   const int64_t pieces = cols / 8;
   const int threads = threads_for(pieces);
   const int64_t x = (pieces + threads - 1) / threads;
-  int64_t y = (int64_t)sms * (2048 / threads) / x;
+  int64_t y = (int64_t)sms * (1024 / threads) / x;  // one wave: 64 registers a thread
   y = y < 1 ? 1 : y;
   const int64_t most = (rows + kUnroll - 1) / kUnroll;
   if (y > most) y = most;
@@ -197,6 +232,10 @@ int act_grad_row_blocks(int64_t rows, int64_t cols, int sms) {
 }
 
 cudaError_t launch_act_grad(const ActGradParams& p, bool f16, cudaStream_t stream) {
+  if (p.d_bias) {
+    const dim3 few((unsigned)((p.cols + kFewCols - 1) / kFewCols));
+    return launch(f16 ? &agmm_act_grad_few<true> : &agmm_act_grad_few<false>, p, few, kFewWarps * 32, stream);
+  }
   const int64_t pieces = p.cols / 8;
   const int threads = threads_for(pieces);
   const dim3 grid((unsigned)((pieces + threads - 1) / threads), (unsigned)p.row_blocks);

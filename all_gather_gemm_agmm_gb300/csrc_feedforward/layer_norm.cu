@@ -454,6 +454,136 @@ __global__ void __launch_bounds__(512, 1) agmm_layer_norm_grad(const __grid_cons
   }
 }
 
+// Few rows: some blocks have rows, for dx (a warp or a block to a row), the others 64 columns each, for
+// the sums over the rows.  Those read x and d_out again, out of L2, and need nothing of the former: the
+// statistics are there.  No parts and no second launch.  Columns come first, as they take longer, and two
+// blocks share an SM (59 registers): 512 x 4096 5.6 us; rows first 6.4, one block to an SM 7.9 us.
+constexpr int kFewWarps = 16, kFewPieces = 8, kFewCols = kFewPieces * 8, kFewRowsAWarp = 32 / kFewPieces, kFewUnroll = 3;
+static_assert(kFewWarps * 32 >= 2 * kFewCols, "a thread for each sum");
+
+template <bool kF16, int kTeamWarps, int kPieces>
+__device__ __forceinline__ void few_rows(const NormGradParams& p, int block, float2 (&s)[kFewWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int team = kTeamWarps * 32, kRows = kFewWarps / kTeamWarps;
+  const int t = threadIdx.x % team;
+  const int64_t place = (int64_t)block * kRows + threadIdx.x / team;
+  const bool there = place < p.rows;
+  const int64_t row = there ? place : p.rows - 1;  // a team without a row meets the others all the same
+  uint4 x16[kPieces], d16[kPieces], a16[kPieces], w16[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = (t + i * team) * 8;
+    a16[i] = make_uint4(0, 0, 0, 0);
+    w16[i] = ones<kF16>();
+    if (c < p.cols) {
+      x16[i] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + c);
+      d16[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + c);
+      if (p.add) a16[i] = *reinterpret_cast<const uint4*>(p.add + row * p.ld_add + c);
+      if (p.weight) w16[i] = __ldg(reinterpret_cast<const uint4*>(p.weight + c));
+    }
+  }
+  const float mean = __ldg(p.mean + row), r = __ldg(p.rstd + row), inv = 1.0f / (float)p.cols;
+  Two sum_g = 0, sum_gx = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if ((t + i * team) * 8 < p.cols) {
+      GradPiece q = grad_piece<kF16>(x16[i], d16[i], mean, r);
+      weigh<kF16>(q, w16[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum_g = add2(sum_g, q.g[e]);
+        sum_gx = fma2(q.g[e], q.x[e], sum_gx);
+      }
+    }
+  }
+  float2 v = make_float2(warp_sum(sum2(sum_g)), warp_sum(sum2(sum_gx)));
+  if constexpr (kTeamWarps > 1) {
+    if (lane == 0) s[warp] = v;
+    __syncthreads();
+    v = lane < kTeamWarps ? s[warp / kTeamWarps * kTeamWarps + lane] : make_float2(0.0f, 0.0f);
+    v = make_float2(warp_sum(v.x), warp_sum(v.y));
+  }
+  if (!there) return;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = (t + i * team) * 8;
+    if (c < p.cols) {
+      GradPiece q = grad_piece<kF16>(x16[i], d16[i], mean, r);
+      weigh<kF16>(q, w16[i]);
+      *reinterpret_cast<uint4*>(p.dx + row * p.ld_dx + c) = input_grad<kF16>(q, r, v.x * inv, v.y * inv, a16[i]);
+    }
+  }
+}
+
+template <bool kF16>
+__device__ __forceinline__ void few_columns(const NormGradParams& p, int block, float (&s)[2][kFewWarps][kFewCols]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, piece = lane % kFewPieces;
+  const int64_t col = ((int64_t)block * kFewPieces + piece) * 8;
+  constexpr int step = kFewWarps * kFewRowsAWarp;
+  Two sum[2][4] = {};
+  if (col < p.cols) {
+    for (int64_t first = warp * kFewRowsAWarp + lane / kFewPieces; first < p.rows; first += step * kFewUnroll) {
+      uint4 x16[kFewUnroll], d16[kFewUnroll];
+      float mean[kFewUnroll], r[kFewUnroll];
+#pragma unroll
+      for (int i = 0; i < kFewUnroll; ++i) {
+        const int64_t row = first + i * step;
+        if (row < p.rows) {
+          x16[i] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + col);
+          d16[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + col);
+          mean[i] = __ldg(p.mean + row);
+          r[i] = __ldg(p.rstd + row);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kFewUnroll; ++i) {
+        if (first + i * step < p.rows) {
+          const GradPiece q = grad_piece<kF16>(x16[i], d16[i], mean[i], r[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum[0][e] = fma2(q.g[e], q.x[e], sum[0][e]);
+            sum[1][e] = add2(sum[1][e], q.g[e]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int o = kFewPieces; o < 32; o *= 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[k][e] = add2(sum[k][e], __shfl_xor_sync(0xffffffffu, sum[k][e], o));
+    if (lane < kFewPieces) {
+      ulonglong2* const mine = reinterpret_cast<ulonglong2*>(&s[k][warp][piece * 8]);
+      mine[0] = make_ulonglong2(sum[k][0], sum[k][1]);
+      mine[1] = make_ulonglong2(sum[k][2], sum[k][3]);
+    }
+  }
+  __syncthreads();
+  const int k = threadIdx.x / kFewCols, c = threadIdx.x % kFewCols;
+  const int64_t at = (int64_t)block * kFewCols + c;
+  if (k >= 2 || at >= p.cols) return;
+  void* const out = k == 0 ? p.d_weight : p.d_bias;
+  if (out == nullptr) return;
+  float total = s[k][0][c];
+#pragma unroll
+  for (int i = 1; i < kFewWarps; ++i) total += s[k][i][c];
+  store_sum<kF16>(out, at, total, p.out_f32);
+}
+
+template <bool kF16, int kTeamWarps, int kPieces>
+__global__ void __launch_bounds__(kFewWarps * 32, kPieces == 4 ? 1 : 2) agmm_layer_norm_grad_few(const __grid_constant__ NormGradParams p) {
+  __shared__ __align__(16) float s[2][kFewWarps][kFewCols];
+  __shared__ float2 team_sums[kFewWarps];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if ((int)blockIdx.x < p.column_blocks)
+    few_columns<kF16>(p, (int)blockIdx.x, s);
+  else
+    few_rows<kF16, kTeamWarps, kPieces>(p, (int)blockIdx.x - p.column_blocks, team_sums);
+}
+
 template <class P>
 cudaError_t launch(void (*fn)(P), const P& p, unsigned blocks, int threads, size_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -527,7 +657,31 @@ cudaError_t launch_norm_grad_t(NormGradParams p, int blocks, cudaStream_t stream
   return launch(fn, p, (unsigned)blocks, st.threads, st.smem, stream);
 }
 
+template <bool kF16>
+cudaError_t launch_norm_grad_few_t(NormGradParams p, cudaStream_t stream) {
+  const int pieces = p.cols / 8;
+  const bool sums = p.d_weight || p.d_bias;
+  const int team = pieces <= 32 ? 1 : pieces <= 128 ? 4 : kFewWarps, rows = kFewWarps / team;  // warps to a row, rows to a block
+  p.column_blocks = sums ? (p.cols + kFewCols - 1) / kFewCols : 0;  // first: they take longer
+  const int blocks = p.column_blocks + (p.dx ? (int)((p.rows + rows - 1) / rows) : 0);
+  void (*fn)(NormGradParams) = team == 1        ? &agmm_layer_norm_grad_few<kF16, 1, 1>
+                               : team == 4      ? &agmm_layer_norm_grad_few<kF16, 4, 1>
+                               : pieces <= 512  ? &agmm_layer_norm_grad_few<kF16, kFewWarps, 1>
+                               : pieces <= 1024 ? &agmm_layer_norm_grad_few<kF16, kFewWarps, 2>
+                                                : &agmm_layer_norm_grad_few<kF16, kFewWarps, 4>;
+  return launch(fn, p, (unsigned)blocks, kFewWarps * 32, 0, stream);
+}
+
 }  // namespace
+
+// Backward with a gradient to add and the sums, few rows' way and the other: 256 columns, 768 rows 4.7 and
+// 5.0 us, 1024 rows 5.9 and 5.0; 1000 columns, 37 rows 2.1 and 4.6, 768 rows 6.2 and 7.1; 4096 columns,
+// 37 rows 2.2 and 7.1, 1024 rows 9.2 and 12.8; 16384 columns, 1024 rows 42 and 47 us.  dx alone is alike.
+bool few_norm_rows(int64_t rows, int cols) { return rows <= (cols > 1024 ? 1024 : 768); }
+
+cudaError_t launch_norm_grad_few(const NormGradParams& p, bool f16, cudaStream_t stream) {
+  return f16 ? launch_norm_grad_few_t<true>(p, stream) : launch_norm_grad_few_t<false>(p, stream);
+}
 
 cudaError_t prepare_norm(bool f16) {
   for (void (*fn)(NormGradParams) : {f16 ? &agmm_layer_norm_grad<true, 2, 2> : &agmm_layer_norm_grad<false, 2, 2>,

@@ -88,6 +88,25 @@ def test_forward_and_backward(agmm, case):
     assert torch.equal(only, db)
 
 
+@pytest.mark.parametrize("rows, columns", [(767, 1000), (768, 8), (769, 1000), (1023, 264), (1024, 1032), (1025, 2056), (65, 16384), (13, 72)])
+def test_rows_about_the_bounds_of_few(agmm, rows, columns):
+    """Sums and dx in one launch, or apart; dx in d_out's place, where one launch would read it too late."""
+    x, w, _, d, add = make(rows, columns, torch.bfloat16, 9)
+    plan = agmm.LayerNormPlan(columns)
+    _, mean, rstd = agmm.layer_norm(x, w, None, return_stats=True)
+    want = norm_grad(d, x, mean, rstd, w, add, torch.bfloat16, torch.float32)
+    ws = plan.new_workspace()
+    for over in (False, True):
+        dw, db = (torch.full((columns,), float("nan"), device="cuda") for _ in range(2))
+        d_out = torch.full((rows, columns + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+        d_out[:, :columns] = d
+        dx = d_out[:, :columns] if over else torch.full_like(d, float("nan"))
+        plan.backward(d_out[:, :columns], x, mean, rstd, dx, ws, weight=w, add=add, d_weight=dw, d_bias=db)
+        for name, got in dict(dx=dx, d_weight=dw, d_bias=db).items():
+            check(got, *want[name], name)
+        assert bool((d_out[:, columns:] == 7).all())
+
+
 def test_values_about_a_far_mean(agmm):
     """Rows far from zero: the squares are taken about the mean."""
     x, w, b, _, _ = make(20, 2048, torch.float16, 3, mean=300.0)

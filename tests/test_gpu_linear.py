@@ -115,6 +115,23 @@ def test_backward(agmm, case):
         check(alone, *want[name], name)
 
 
+@pytest.mark.parametrize("kind", [None, "gelu"])
+@pytest.mark.parametrize("rows, n", [(1, 8), (63, 72), (65, 1000), (257, 264), (384, 520), (385, 520)])
+def test_sums_of_few_rows(agmm, rows, n, kind):
+    """The bias' gradient beside the activation's, or in a launch of its own."""
+    (x,), w, _, d, z = make(1, rows, 64, n, False, torch.bfloat16, 8)
+    z = z * 2 if kind else None
+    want = linear_grad(d, x, w, z, kind, False, torch.bfloat16, torch.float32)
+    plan = agmm.LinearPlan(64, n, activation=kind)
+    d_pre = torch.full((rows + 1, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    d_bias = torch.full((n + 8,), 7.0, device="cuda")
+    plan.backward(d, x, w, plan.new_workspace(), pre=z, d_pre=d_pre[:rows] if kind else None, d_bias=d_bias[:n])
+    check(d_bias[:n], *want["d_bias"], "d_bias")
+    assert bool((d_bias[n:] == 7).all()) and bool((d_pre[rows:] == 7).all())
+    if kind:
+        check(d_pre[:rows], *want["d_pre"], "d_pre")
+
+
 def test_strides(agmm):
     k, n, t = 136, 200, 150
     g = torch.Generator(device="cuda").manual_seed(4)
