@@ -819,8 +819,9 @@ agmm_status_t agmm_layer_norm_backward(agmm_layer_norm_t pl, const agmm_layer_no
   p.rstd = a->rstd;
   p.dx = static_cast<uint16_t*>(a->dx);
   p.part = sums ? reinterpret_cast<float*>(static_cast<char*>(a->workspace) + AGMM_FEEDFORWARD_HEAD_BYTES) : nullptr;
-  // One launch has other blocks for the rows than for the sums, which may find dx in d_out's place.
-  if (few_norm_rows(a->rows, pl->columns) && !(sums && a->dx && may_overlap(a->dx, p.ld_dx, a->d_out, p.ld_out, a->rows))) {
+  // One launch has other blocks for the rows than for the sums, which would find dx in the place of what they read.
+  const bool over = sums && a->dx && (may_overlap(a->dx, p.ld_dx, a->d_out, p.ld_out, a->rows) || may_overlap(a->dx, p.ld_dx, a->x, p.ldx, a->rows));
+  if (!over && few_norm_rows(a->rows, pl->columns)) {
     p.d_weight = a->d_weight;
     p.d_bias = a->d_bias;
     p.out_f32 = a->f32_grads != 0;
