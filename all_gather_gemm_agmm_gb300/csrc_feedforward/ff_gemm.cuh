@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         phase = next_phase;
       }
     };
-    ptx::griddep_wait();  // no access to global memory before this, in any role
+    ptx::griddep_wait();  // no access to global memory and no bounded wait before this, in any role
     while (ok && iter.next(p, sg)) {
       const Product& w = product_of<kTwo>(p, sg);
       const int row_tile = kPair ? sg.mt * 2 + rank : sg.mt;
@@ -683,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       SegmentIter<kTwo> iter;
       iter.init(p, cluster, clusters, part, split);
       Segment sg;
+      ptx::griddep_wait();  // a wait's bound counts from here, and the status words are the kernel before's until now
       for (; ok && iter.next(p, sg); ++it) {
         const int acc = it & 1;
         int res = wait_phase<kPair>(bar_acc_empty(ctl, acc), (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, limit);
