@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
       bool empty_ready = false;
 #pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb, ko += kTileK) {
-        if (!empty_ready) {
+        if (!__all_sync(0xffffffffu, empty_ready)) {
           int res = wait_phase(bar_empty(ctl, stage), phase ^ 1u, abort_flag, limit);
           res = __shfl_sync(0xffffffffu, res, 0);
           if (res != kWaitOk) {
@@ -587,8 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         }
         const int next_stage = stage + 1 == S ? 0 : stage + 1;
         const uint32_t next_phase = stage + 1 == S ? phase ^ 1u : phase;
-        // a look ahead at the next stage, by the converged warp: one access of one address, one answer
-        // (a vote on it costs 0.5 of 10.4 us for one token)
+        // A look ahead at the next stage.  Lanes may get different answers; the vote on them, which
+        // every lane takes, stands where they are used: by then the looks are done, and it costs
+        // nothing (right behind the look it cost 0.5 of 10.4 us for one token).
         empty_ready = kb + 1 < kb1 && ptx::mbar_test_wait(bar_empty(ctl, next_stage), next_phase ^ 1u);
         if (dropped) {
           if (!kPair || rank == 0) {
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         const uint32_t d = tmem_base + (uint32_t)(acc * kAccs * n);
         bool full_ready = false;
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
-          if (!full_ready) {
+          if (!__all_sync(0xffffffffu, full_ready)) {
             res = wait_phase(bar_full(ctl, stage), phase, abort_flag, limit);
             res = __shfl_sync(0xffffffffu, res, 0);
             if (res != kWaitOk) {
