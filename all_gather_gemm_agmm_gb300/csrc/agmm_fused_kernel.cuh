@@ -673,10 +673,11 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_fused_sm103a(const __grid_co
         const int xrow0 = (kPath == kPathRows && nchunks > 0) ? row_j[0] : 0;
         // The next stage's empty barrier is tested while this stage's copies
         // are issued, so its latency is off the loop's critical path.
+        // Lanes may get different answers: the warp votes on them where they are used.
         bool empty_ready = false;
         for (int kb = kb0; kb < kb1; kb += A) {
           const int na = min(A, kb1 - kb);  // k blocks in this stage
-          if (!empty_ready) {
+          if (!__all_sync(0xffffffffu, empty_ready)) {
             int res = wait_phase(bar_empty(ctl, stage), phase ^ 1u, abort_flag, limit, wait_acc);
             res = __shfl_sync(0xffffffffu, res, 0);
             if (res != kWaitOk) {
@@ -863,11 +864,12 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_fused_sm103a(const __grid_co
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * mma_n);
         // The next stage's full barrier is tested while this stage's MMAs
         // are issued, so its latency is off the loop's critical path.
+        // Lanes may get different answers: the warp votes on them where they are used.
         bool full_ready = false;
         for (int kb = kb0; kb < kb1; kb += A) {
           const int na = min(A, kb1 - kb);  // k blocks in this stage
           // (a pair: this barrier also counts the follower's copies)
-          if (!full_ready) {
+          if (!__all_sync(0xffffffffu, full_ready)) {
             res = wait_phase(bar_full(ctl, stage), phase, abort_flag, limit, wf);
             res = __shfl_sync(0xffffffffu, res, 0);
             if (res != kWaitOk) {

@@ -11,7 +11,7 @@ import re
 import pytest
 
 PACKAGE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "all_gather_gemm_agmm_gb300")
-KERNELS = ["csrc_feedforward/ff_gemm.cuh"]
+KERNELS = ["csrc/agmm_fused_kernel.cuh", "csrc_feedforward/ff_gemm.cuh"]
 
 
 def code(name):
