@@ -1172,7 +1172,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_fused_sm103a(const __grid_co
     float* const stg = reinterpret_cast<float*>(base_ptr);
     if (S == 1) {
       if (warp >= 2) {
-        if (!*abort_flag) {
+        if (!__any_sync(0xffffffffu, *abort_flag)) {  // one answer for the warp's loads of tensor memory
           const uint32_t tbase = lane_base_of(tmem_base, warp);
 #pragma unroll 1
           for (int g = 0; g < groups; ++g) {
@@ -1246,7 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_fused_sm103a(const __grid_co
       const uint32_t send = base;
       const uint32_t recv = ctl + (uint32_t)kCtlBytes;
       if (warp >= 2) {
-        if (!*abort_flag) {
+        if (!__any_sync(0xffffffffu, *abort_flag)) {  // one answer for the warp's loads of tensor memory
           const uint32_t tbase = lane_base_of(tmem_base, warp);
           const uint32_t lane_off = (uint32_t)tl * 16u;
 #pragma unroll 1
@@ -1282,7 +1282,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_fused_sm103a(const __grid_co
         res = __shfl_sync(0xffffffffu, res, 0);
         if (res != kWaitOk) {
           if (lane == 0) record_failure(p, abort_flag, res, kRoleEpilogue, -5, swap_nt);
-        } else if (!*abort_flag && ptx::elect_one()) {
+        } else if (!__any_sync(0xffffffffu, *abort_flag) && ptx::elect_one()) {
           for (int o = 0; o < S; ++o) {
             const int lo = (int)(((int64_t)o * Q) / S);
             const int hi = (int)(((int64_t)(o + 1) * Q) / S);

@@ -51,3 +51,19 @@ def test_results_of_waits_come_from_one_lane(kernel):
     assert waits
     for following in waits:
         assert following == "res = __shfl_sync(0xffffffffu, res, 0)", following
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_no_collective_behind_a_lane_s_own_flag(kernel):
+    """Another warp may raise the abort flag between two lanes' reads of it: what the warp does together
+    (loads of tensor memory, elections) stands behind a vote on it."""
+    body = code(kernel).split("__global__")[-1]
+    for c in conditions(body):
+        if "*abort_flag" in c:
+            assert "elect_one" not in c or "__any_sync(0xffffffffu, *abort_flag)" in c, c
+    for m in re.finditer(r"if \(!?\*abort_flag\) \{", body):
+        depth, end = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(body[end], 0)
+            end += 1
+        assert not re.search(r"tmem_ld|elect_one|_sync\(", body[m.end():end]), body[m.start():m.start() + 200]
