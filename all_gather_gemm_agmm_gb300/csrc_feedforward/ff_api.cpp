@@ -238,7 +238,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The time that a schedule takes, in cycles, as far as it differs from others: clusters that each
 // work through `blocks` k blocks.  The constants were measured on this GPU, kernel by kernel.
-constexpr double kWideBlock = 512, kNarrowBlock = 340;    // a k block of a row tile's main loop
+constexpr double kWideBlock = 512, kNarrowBlock = 340;    // a k block of a row tile's main loop (narrow: 306 to 367, few and all pairs at work)
 constexpr double kWideTile = 4000, kNarrowTile = 2500;    // its results, beside the next tile's main loop
 constexpr double kWideCut = 16000, kNarrowCut = 6500;     // the parts' way to L2 and back
 constexpr double kWidePart = 3000, kNarrowPart = 1400;    // ... and each part that is added

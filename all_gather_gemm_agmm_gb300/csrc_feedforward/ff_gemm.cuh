@@ -19,9 +19,11 @@
 //                  the other, so both products of an output value land in one thread.
 //                  Bound: the tensor cores, active in 91 to 97 % of the cycles: 8192 x 4096 x
 //                  14336 490-496 us (1.94-1.96 PFLOP/s), its gradients 490 and 496 us, in bursts;
-//                  in long runs the power limit.  Wide tiles read 64 bytes a cycle of each
-//                  SM from L2, all it gives; narrow ones would need 70, and take 340 cycles a k
-//                  block of 256.  One CTA with 128 x 128 tiles would need twice that.
+//                  in long runs the power limit.  A k block of wide tiles takes 512 to 520 cycles,
+//                  512 of them products, and each SM reads 64 bytes a cycle from L2.  Narrow ones
+//                  would read 96 at the products' 256 cycles; they read 80 with 4 pairs at work
+//                  (306 cycles) and 67 with all 76 (367).  One CTA with 128 x 128 tiles would need
+//                  128 bytes a cycle.
 //   swapped tiles  for up to 64 tokens: 128 columns of the weights are the MMA's rows
 //                  and all tokens its columns, so that each thread of the epilogue has
 //                  one column of the weights and only the tokens that there are.

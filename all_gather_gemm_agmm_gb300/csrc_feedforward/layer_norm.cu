@@ -163,7 +163,7 @@ __device__ __forceinline__ uint4 load_again(const uint16_t* p) {
 }
 
 // Many long rows: a block walks over rows, four pieces to a thread, and loads the next row
-// beside this one's sums.  16384 x 8192: 87 us, 6.2 TB/s; a block to each row 93 us; rows through
+// beside this one's sums.  16384 x 8192: 88 us, 6.1 TB/s; a block to each row 93 us; rows through
 // shared memory 114 us; two pieces to a thread 106 us.  (Rows of 16384 values need 512 threads and
 // leave room for one block: 64 us so, 55 us with a block to each row.)
 template <bool kF16>
