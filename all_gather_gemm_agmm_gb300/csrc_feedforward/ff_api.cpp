@@ -29,6 +29,7 @@ struct ProductPlan {
   int64_t k, n;
   int act;
   bool transpose, f16;  // weights stored [n, k]; fp16
+  bool saved_f32;       // what the forward pass saves is float32
   int device, sms;
   int pairs;                  // CTA pairs that run at once
   int clusters[kMaxSplit + 1];  // clusters of that many CTAs that do
@@ -385,7 +386,7 @@ agmm_status_t run_rows(const ProductPlan* pl, GemmParams* p, int epi, RowChoice 
   p->tmem_cols = 2 * choice.bn;
   make_schedule(p, pl->pairs, choice.parts);
   const int clusters = choice.split > 1 ? p->num_tiles : std::min(pl->pairs, std::max(p->dp_tiles, p->sk_clusters));
-  return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16), *p, clusters, 2 * choice.split, rest + p->stages * stage, stream),
+  return check_cuda(launch_gemm(select_gemm(choice.bn, epi, pl->f16, pl->saved_f32 && p->saved[0]), *p, clusters, 2 * choice.split, rest + p->stages * stage, stream),
                     "product launch");
 }
 
@@ -425,7 +426,7 @@ agmm_status_t run_swap(const ProductPlan* pl, GemmParams* p, int epi, int64_t fe
   make_schedule(p, pl->clusters[1], 0);
   const int clusters = p->split > 1 ? tiles : std::min(pl->clusters[1], tiles);
   const size_t smem = 1024 + p->stages * stage + p->recv_bytes + kCtlBytes;
-  return check_cuda(launch_gemm(select_gemm(0, epi, pl->f16), *p, clusters, p->split, smem, stream), "product launch");
+  return check_cuda(launch_gemm(select_gemm(0, epi, pl->f16, pl->saved_f32 && p->saved[0]), *p, clusters, p->split, smem, stream), "product launch");
 }
 
 // X Wi for one weight or two (gated), with an epilogue.
@@ -643,6 +644,25 @@ int env_int(const char* name, int lo, int hi) {
   return i >= lo && i <= hi ? i : -1;
 }
 
+// The kernels of an epilogue: their shared memory, and the clusters of them that run at once.
+agmm_status_t prepare_kernels(ProductPlan* pl, int epi, bool save_f32) {
+  int fit = 0;
+  for (int bn : {kNarrowN, kWideN}) {
+    AGMM_TRY(check_cuda(prepare_gemm(select_gemm(bn, epi, pl->f16, save_f32), 2, &fit), "kernel attributes"));
+    pl->pairs = std::min(pl->pairs, fit);
+  }
+  for (int n = 2; n <= kMaxPairs; ++n) {
+    AGMM_TRY(check_cuda(prepare_gemm(select_gemm(kNarrowN, epi, pl->f16, save_f32), 2 * n, &fit), "kernel attributes"));
+    pl->joined[n] = std::min(pl->joined[n], fit);
+  }
+  for (int split = 1; split <= kMaxSplit; ++split) {
+    AGMM_TRY(check_cuda(prepare_gemm(select_gemm(0, epi, pl->f16, save_f32), split, &fit), "kernel attributes"));
+    pl->clusters[split] = std::min(pl->clusters[split], fit);
+  }
+  if (pl->pairs < 1 || pl->clusters[1] < 1) return fail(AGMM_ERR_UNSUPPORTED, "the kernels do not fit this device");
+  return AGMM_OK;
+}
+
 agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int transpose, int dtype) {
   pl->k = k;
   pl->n = n;
@@ -664,26 +684,13 @@ agmm_status_t fill_plan(ProductPlan* pl, int64_t k, int64_t n, int act, int tran
   pl->merge = env_int("AGMM_MERGE", 0, 1);
   pl->pairs = pl->sms / 2;
   for (int split = 1; split <= kMaxSplit; ++split) pl->clusters[split] = pl->sms / split;
-  for (int epi = kEpiPlain; epi <= kEpiLinear; ++epi) {
-    int fit = 0;
-    for (int bn : {kNarrowN, kWideN}) {
-      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(bn, epi, pl->f16), 2, &fit), "kernel attributes"));
-      pl->pairs = std::min(pl->pairs, fit);
-    }
-    for (TwoFn fn : {wide_two(pl->f16), narrow_two(pl->f16)}) {
-      AGMM_TRY(check_cuda(prepare_two(fn, &fit), "kernel attributes"));
-      pl->pairs = std::min(pl->pairs, fit);
-    }
-    for (int n = 2; n <= kMaxPairs; ++n) {
-      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(kNarrowN, epi, pl->f16), 2 * n, &fit), "kernel attributes"));
-      pl->joined[n] = epi == kEpiPlain ? fit : std::min(pl->joined[n], fit);
-    }
-    for (int split = 1; split <= kMaxSplit; ++split) {
-      AGMM_TRY(check_cuda(prepare_gemm(select_gemm(0, epi, pl->f16), split, &fit), "kernel attributes"));
-      pl->clusters[split] = std::min(pl->clusters[split], fit);
-    }
+  for (int n = 2; n <= kMaxPairs; ++n) pl->joined[n] = pl->sms / (2 * n);
+  int fit = 0;
+  for (TwoFn fn : {wide_two(pl->f16), narrow_two(pl->f16)}) {
+    AGMM_TRY(check_cuda(prepare_two(fn, &fit), "kernel attributes"));
+    pl->pairs = std::min(pl->pairs, fit);
   }
-  if (pl->pairs < 1 || pl->clusters[1] < 1) return fail(AGMM_ERR_UNSUPPORTED, "the kernels do not fit this device");
+  for (int epi = kEpiPlain; epi <= kEpiLinear; ++epi) AGMM_TRY(prepare_kernels(pl, epi, false));
   return AGMM_OK;
 }
 
@@ -706,6 +713,15 @@ agmm_status_t product_plan(int64_t k, int64_t n, int act, bool none_ok, int tran
     return st;
   }
   *out = pl;
+  return AGMM_OK;
+}
+
+agmm_status_t save_float(ProductPlan* pl, int epi, int on) {
+  if (!pl) return fail(AGMM_ERR_INVALID_ARG, "plan is NULL");
+  if (on != 0 && on != 1) return fail(AGMM_ERR_INVALID_ARG, "on must be 0 or 1: %d", on);
+  AGMM_TRY(check_plan_device(pl->device));
+  if (on) AGMM_TRY(prepare_kernels(pl, epi, true));
+  pl->saved_f32 = on != 0;
   return AGMM_OK;
 }
 
@@ -851,6 +867,8 @@ agmm_status_t agmm_gated_plan(const agmm_gated_desc_t* d, agmm_gated_t* out) {
 
 void agmm_gated_destroy(agmm_gated_t plan) { delete plan; }
 
+agmm_status_t agmm_gated_save_float(agmm_gated_t pl, int on) { return save_float(pl, kEpiGated, on); }
+
 size_t agmm_gated_workspace_bytes(agmm_gated_t pl) { return pl ? workspace_bytes(pl) : 0; }
 
 agmm_status_t agmm_gated_run(agmm_gated_t pl, const agmm_gated_args_t* a, void* stream) {
@@ -918,14 +936,15 @@ agmm_status_t agmm_gated_backward(agmm_gated_t pl, const agmm_gated_grad_args_t*
   g.rows = tokens;
   g.cols = pl->n;
   g.d_out = static_cast<const uint16_t*>(a->d_out);
-  g.gate = static_cast<const uint16_t*>(a->gate);
-  g.up = static_cast<const uint16_t*>(a->up);
+  g.gate = a->gate;
+  g.up = a->up;
   g.d_gate = static_cast<uint16_t*>(a->d_gate);
   g.d_up = static_cast<uint16_t*>(a->d_up);
   g.ld_out = out_stride;
   g.ld_saved = saved_stride;
   g.ld_grad = d_stride;
   g.act = pl->act;
+  g.saved_f32 = pl->saved_f32;
   AGMM_TRY(check_cuda(launch_gated_grad(g, pl->f16, pl->sms, s), "gated backward launch"));
   const void* const d[2] = {a->d_gate, a->d_up};
   const void* const w[2] = {a->w_gate, a->w_up};
@@ -943,6 +962,8 @@ agmm_status_t agmm_linear_plan(const agmm_linear_desc_t* d, agmm_linear_t* out) 
 }
 
 void agmm_linear_destroy(agmm_linear_t plan) { delete plan; }
+
+agmm_status_t agmm_linear_save_float(agmm_linear_t pl, int on) { return save_float(pl, kEpiLinear, on); }
 
 size_t agmm_linear_workspace_bytes(agmm_linear_t pl) { return pl ? workspace_bytes(pl) : 0; }
 
@@ -1012,12 +1033,13 @@ agmm_status_t agmm_linear_backward(agmm_linear_t pl, const agmm_linear_grad_args
     g.rows = tokens;
     g.cols = pl->n;
     g.d_out = static_cast<const uint16_t*>(a->d_out);
-    g.pre = static_cast<const uint16_t*>(a->pre);
+    g.pre = a->pre;
     g.d_pre = static_cast<uint16_t*>(a->d_pre);
     g.ld_out = out_stride;
     g.ld_pre = pre_stride;
     g.ld_grad = d_stride;
     g.act = pl->act;
+    g.saved_f32 = pl->saved_f32;
     const bool few = a->d_bias && tokens <= kFewRows;
     if (few) {
       g.d_bias = a->d_bias;

@@ -469,8 +469,9 @@ __device__ __forceinline__ void stage_half(uint8_t* stage, int lane, int half, c
   for (int i = 0; i < 4; ++i) *staged(stage, lane, half * 4 + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// kBN: columns of a row tile (0: swapped tiles).  kTwo: two products in one launch.
-template <int kBN, int kEpi, bool kF16, bool kTwo = false>
+// kBN: columns of a row tile (0: swapped tiles).  kTwo: two products in one launch.  kSaveF32: what is
+// saved is float32 (kernels of their own: as a branch it cost the others 0.5 to 2 %).
+template <int kBN, int kEpi, bool kF16, bool kTwo = false, bool kSaveF32 = false>
 __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constant__ ParamsOf<kTwo> p) {
   constexpr bool kSwap = kBN == 0, kPair = !kSwap;
   constexpr int kHalf = kBN / 2;  // columns of the accumulator that a warp of the epilogue has
@@ -816,9 +817,19 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         for (int i = 0; i < 8; ++i)
           if (row[i] >= 0) *reinterpret_cast<uint16_t*>(row_address(base, row[i], ld)) = pack1<kF16>(__uint_as_float(x[i]));
       };
-      if (kEpi == kEpiGated && p.saved[0]) store(p.saved[1], (uint32_t)p.lds * 2u, v[kAccs - 1]);
+      auto save = [&](void* out, const uint32_t (&x)[8]) {
+        if constexpr (kSaveF32) {
+          uint32_t* const base = static_cast<uint32_t*>(out) + f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (row[i] >= 0) *reinterpret_cast<uint32_t*>(row_address(base, row[i], (uint32_t)p.lds * 4u)) = x[i];
+        } else {
+          store(out, (uint32_t)p.lds * 2u, x);
+        }
+      };
+      if (kEpi == kEpiGated && p.saved[0]) save(p.saved[1], v[kAccs - 1]);
       store(p.out[0], (uint32_t)p.ldo * 2u, v[0]);
-      if (kEpi != kEpiPlain && p.saved[0]) store(p.saved[0], (uint32_t)p.lds * 2u, pre);
+      if (kEpi != kEpiPlain && p.saved[0]) save(p.saved[0], pre);
     };
     const int owner = q % split;  // row tiles: the pair that goes on with these 32 rows
     bool met = false;
@@ -838,13 +849,15 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
         }
       };
       const bool has_residual = kEpi == kEpiLinear && p.residual != nullptr;
+      // (what is saved in float32 goes through the staging buffer before the residual does)
+      const bool residual_ahead = has_residual && !kSaveF32;
       if constexpr (!kSwap) {
         const int trow = (sg.mt * 2 + rank) * kTileM + q * 32 + lane;
         const int chunk = trow / w.box, shard = chunk / w.shard_chunks;
         const int in_shard = trow - shard * w.shard_chunks * w.box;
         if (shard < w.shards && in_shard < w.shard_rows) out_row = (int)(shard * w.shard_rows) + in_shard;
         block_rows(rows, out_row, lane);
-        if (has_residual && (sg.whole || (split > 1 && owner == part))) fetch_residual(0);  // while the products are made
+        if (residual_ahead && (sg.whole || (split > 1 && owner == part))) fetch_residual(0);  // while the products are made
       }
       int res = kWaitOk;
       if (lane == 0) res = wait_phase(bar_acc_full(ctl, acc), (uint32_t)(it >> 1) & 1u, abort_flag, limit);
@@ -922,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
             int* const counter = p.counters + ((size_t)(sg.tile - p.dp_tiles) * kCtas + rank) * kEpiWarps + ewarp;
             if (!complete_tile(p, counter, sg.kb1 - sg.kb0, lane)) continue;
             parts = find_parts(p, sg.tile);
-            if (has_residual) fetch_residual(0);
+            if (residual_ahead) fetch_residual(0);
           }
         }
         // the sums over the parts of `v`'s columns from `c` on
@@ -933,7 +946,40 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
           else
             sum_parts<kArrays, 32, kArrays == 1 && kEpi == kEpiPlain ? 2 : 1>(p, parts, kCtas, rank, ewarp, c, stride, lane, v);
         };
-        if constexpr (kEpi == kEpiGated) {
+        // 32 values of this lane's row in float32, columns [col, col + 32), to `out`
+        auto write_f32 = [&](void* out, int64_t ld, int64_t col, const uint32_t (&v)[32], const int (&at_rows)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *staged(stage_out, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          const int64_t at = col + 4 * (lane & 7);
+          write_staged<8>(stage_out, static_cast<float*>(out) + at, (uint32_t)ld * 4u, at_rows, at < w.cols, lane);
+        };
+        if constexpr (kEpi == kEpiGated && kSaveF32) {
+          // 32 columns at a time through the staging buffer: both products, then the results
+#pragma unroll 1
+          for (int h = 0; h < kHalf / 64; ++h) {
+            uint32_t v[2][32], o16[16];
+            if (sg.whole) {
+              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + 32 * h), v[0]);
+              ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(kHalf + first_col + 32 * h), v[1]);
+              ptx::tmem_ld_wait();
+              if (h == kHalf / 64 - 1) release();
+            } else {
+              join(v, 32 * h, kHalf / 2);
+            }
+            write_f32(p.saved[0], p.lds, tile_col + 32 * h, v[0], rows);
+            write_f32(p.saved[1], p.lds, tile_col + 32 * h, v[1], rows);
+            with_activation(p.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) set_pair(v[0], i, mul2(activate<act.value>(pair_of(v[0], i)), pair_of(v[1], i)));
+            });
+            pack32<kF16>(v[0], o16);
+            stage_half(stage_out, lane, 0, o16);
+            int rows4[4];
+            block_rows(rows4, out_row, lane);
+            const int64_t at = tile_col + 32 * h + 8 * (lane % 4);
+            write_staged<4>(stage_out, static_cast<uint16_t*>(w.out[0]) + at, (uint32_t)w.ldo * 2u, rows4, at < w.cols, lane);
+          }
+        } else if constexpr (kEpi == kEpiGated) {
           constexpr int kBlocks = kHalf / 64;  // of 32 columns of results
           constexpr int kPieces = 4 * kBlocks;
           const int64_t col = tile_col + 8 * (lane % kPieces);  // of this lane's piece
@@ -984,20 +1030,16 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
               } else {
                 join(v, c, 0);
               }
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *staged(stage_out, lane, i) = make_uint4(v[0][4 * i], v[0][4 * i + 1], v[0][4 * i + 2], v[0][4 * i + 3]);
-              const int64_t col = tile_col + c + 4 * (lane & 7);
-              write_staged<8>(stage_out, static_cast<float*>(w.out[sg.problem]) + col, (uint32_t)w.ldo * 4u, rows, col < w.cols, lane);
+              write_f32(w.out[sg.problem], w.ldo, tile_col + c, v[0], rows);
             }
           } else {
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 64) {
               const int64_t col = tile_col + c, at = col + 8 * (lane & 7);  // this lane's piece
               const bool inside = at < w.cols;
-              if (has_residual && c > 0) fetch_residual(c);  // beside the loads and the activation below
+              if (residual_ahead && c > 0) fetch_residual(c);  // beside the loads and the activation below
               uint32_t z16[2][16];
-              const bool has_saved = kEpi == kEpiLinear && p.saved[0] != nullptr;
+              const bool has_saved = kEpi == kEpiLinear && p.saved[0] != nullptr && !kSaveF32;
               uint32_t x2[2][1][32];
               if (sg.whole) {
                 ptx::tmem_ld_32x32b_x32(t0 + (uint32_t)(first_col + c), x2[0][0]);
@@ -1008,21 +1050,31 @@ __global__ void __launch_bounds__(kThreads, 1) agmm_ff_gemm(const __grid_constan
                 join(x2[0], c, 0);
                 join(x2[1], c + 32, 0);
               }
+              auto add_bias = [&](uint32_t (&v)[32], int h) {
+                if (!p.bias) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (col + 32 * h + 8 * i < w.cols) {
+                    Two b[4];
+                    widen<kF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col + 32 * h + 8 * i)), b);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) set_pair(v, 8 * i + 2 * e, add2(pair_of(v, 8 * i + 2 * e), b[e]));
+                  }
+                }
+              };
+              if constexpr (kSaveF32) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  add_bias(x2[h][0], h);
+                  write_f32(p.saved[0], p.lds, col + 32 * h, x2[h][0], rows);
+                }
+                if (has_residual) fetch_residual(c);
+              }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 uint32_t(&v)[32] = x2[h][0];
                 if constexpr (kEpi == kEpiLinear) {
-                  if (p.bias) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      if (col + 32 * h + 8 * i < w.cols) {
-                        Two b[4];
-                        widen<kF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col + 32 * h + 8 * i)), b);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) set_pair(v, 8 * i + 2 * e, add2(pair_of(v, 8 * i + 2 * e), b[e]));
-                      }
-                    }
-                  }
+                  if (!kSaveF32) add_bias(v, h);
                   if (has_saved) pack32<kF16>(v, z16[h]);
                   with_activation(p.act, [&](auto act) {
 #pragma unroll

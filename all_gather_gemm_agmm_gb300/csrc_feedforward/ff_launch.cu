@@ -4,10 +4,10 @@
 namespace agmm {
 namespace ff {
 
-GemmFn select_gemm(int bn, int epi, bool f16) {
-  if (bn == kWideN) return epi == kEpiGated ? wide_gated(f16) : epi == kEpiLinear ? wide_linear(f16) : wide_plain(f16);
-  if (bn == kNarrowN) return epi == kEpiGated ? narrow_gated(f16) : epi == kEpiLinear ? narrow_linear(f16) : narrow_plain(f16);
-  return epi == kEpiGated ? swap_gated(f16) : epi == kEpiLinear ? swap_linear(f16) : swap_plain(f16);
+GemmFn select_gemm(int bn, int epi, bool f16, bool save_f32) {
+  if (bn == kWideN) return epi == kEpiGated ? wide_gated(f16, save_f32) : epi == kEpiLinear ? wide_linear(f16, save_f32) : wide_plain(f16);
+  if (bn == kNarrowN) return epi == kEpiGated ? narrow_gated(f16, save_f32) : epi == kEpiLinear ? narrow_linear(f16, save_f32) : narrow_plain(f16);
+  return epi == kEpiGated ? swap_gated(f16, save_f32) : epi == kEpiLinear ? swap_linear(f16, save_f32) : swap_plain(f16);
 }
 
 namespace {

@@ -3,6 +3,9 @@
 
 namespace agmm {
 namespace ff {
-GemmFn narrow_linear(bool f16) { return f16 ? &agmm_ff_gemm<kNarrowN, kEpiLinear, true> : &agmm_ff_gemm<kNarrowN, kEpiLinear, false>; }
+GemmFn narrow_linear(bool f16, bool save_f32) {
+  if (save_f32) return f16 ? &agmm_ff_gemm<kNarrowN, kEpiLinear, true, false, true> : &agmm_ff_gemm<kNarrowN, kEpiLinear, false, false, true>;
+  return f16 ? &agmm_ff_gemm<kNarrowN, kEpiLinear, true> : &agmm_ff_gemm<kNarrowN, kEpiLinear, false>;
+}
 }  // namespace ff
 }  // namespace agmm

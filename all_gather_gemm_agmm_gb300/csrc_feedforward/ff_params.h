@@ -102,19 +102,19 @@ struct __align__(128) TwoParams : GemmParams {
 
 using GemmFn = void (*)(GemmParams);
 using TwoFn = void (*)(TwoParams);
-// bn: columns of row tiles (0: swapped tiles)
-GemmFn select_gemm(int bn, int epi, bool f16);
+// bn: columns of row tiles (0: swapped tiles); save_f32: what is saved is float32 (gated, linear)
+GemmFn select_gemm(int bn, int epi, bool f16, bool save_f32);
 TwoFn wide_two(bool f16);
 TwoFn narrow_two(bool f16);
 GemmFn wide_plain(bool f16);
-GemmFn wide_gated(bool f16);
-GemmFn wide_linear(bool f16);
+GemmFn wide_gated(bool f16, bool save_f32);
+GemmFn wide_linear(bool f16, bool save_f32);
 GemmFn narrow_plain(bool f16);
-GemmFn narrow_gated(bool f16);
-GemmFn narrow_linear(bool f16);
+GemmFn narrow_gated(bool f16, bool save_f32);
+GemmFn narrow_linear(bool f16, bool save_f32);
 GemmFn swap_plain(bool f16);
-GemmFn swap_gated(bool f16);
-GemmFn swap_linear(bool f16);
+GemmFn swap_gated(bool f16, bool save_f32);
+GemmFn swap_linear(bool f16, bool save_f32);
 
 // Sets the shared-memory limit of a kernel and reports the clusters that fit.
 cudaError_t prepare_gemm(GemmFn fn, int cluster, int* clusters);
@@ -126,10 +126,11 @@ cudaError_t launch_two(TwoFn fn, const TwoParams& p, int clusters, size_t smem, 
 // d_gate = d_out * up * act'(gate), d_up = d_out * act(gate)
 struct GatedGradParams {
   int64_t rows, cols;
-  const uint16_t *d_out, *gate, *up;
+  const uint16_t* d_out;
+  const void *gate, *up;  // as the outputs, or (saved_f32) in float32
   uint16_t *d_gate, *d_up;
   int64_t ld_out, ld_saved, ld_grad;
-  int act;
+  int act, saved_f32;
 };
 cudaError_t launch_gated_grad(const GatedGradParams& p, bool f16, int sms, cudaStream_t stream);
 
@@ -137,10 +138,11 @@ cudaError_t launch_gated_grad(const GatedGradParams& p, bool f16, int sms, cudaS
 // its columns: in parts of [blocks][cols], or (few rows) the whole of them.
 struct ActGradParams {
   int64_t rows, cols;
-  const uint16_t *d_out, *pre;
+  const uint16_t* d_out;
+  const void* pre;  // as d_out, or (saved_f32) in float32
   uint16_t* d_pre;
   int64_t ld_out, ld_pre, ld_grad;
-  int act;
+  int act, saved_f32;
   float* part;  // NULL: no parts
   int row_blocks;
   void* d_bias;  // few rows: the sums; NULL: no sums, or parts

@@ -18,12 +18,39 @@ namespace agmm {
 namespace ff {
 namespace {
 
-template <bool kF16, int kAct>
-__device__ __forceinline__ void gated_grad_piece(const uint4& d16, const uint4& g16, const uint4& u16, uint4& dg, uint4& du) {
+// 8 values that the forward pass saved, in 16 bits or in float32.
+template <bool kSavedF32>
+struct Saved {
+  uint4 v[kSavedF32 ? 2 : 1];
+  // plain loads: the gradients may lie over what was saved
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    if constexpr (kSavedF32) {
+      const uint4* const q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+      v[0] = q[0];
+      v[1] = q[1];
+    } else {
+      v[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    }
+  }
+  template <bool kF16>
+  __device__ __forceinline__ void values(Two (&x)[4]) const {
+    if constexpr (kSavedF32) {
+      x[0] = two(__uint_as_float(v[0].x), __uint_as_float(v[0].y));
+      x[1] = two(__uint_as_float(v[0].z), __uint_as_float(v[0].w));
+      x[2] = two(__uint_as_float(v[1].x), __uint_as_float(v[1].y));
+      x[3] = two(__uint_as_float(v[1].z), __uint_as_float(v[1].w));
+    } else {
+      widen<kF16>(v[0], x);
+    }
+  }
+};
+
+template <bool kF16, int kAct, bool kSavedF32>
+__device__ __forceinline__ void gated_grad_piece(const uint4& d16, const Saved<kSavedF32>& gs, const Saved<kSavedF32>& us, uint4& dg, uint4& du) {
   Two d[4], g[4], u[4];
   widen<kF16>(d16, d);
-  widen<kF16>(g16, g);
-  widen<kF16>(u16, u);
+  gs.template values<kF16>(g);
+  us.template values<kF16>(u);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     Two a, slope;
@@ -35,34 +62,35 @@ __device__ __forceinline__ void gated_grad_piece(const uint4& d16, const uint4& 
   du = narrow<kF16>(u);
 }
 
-constexpr int kUnroll = 2, kActUnroll = 4;  // rows whose loads are in flight together
+constexpr int kUnroll = 2, kActUnroll = 4;  // rows whose loads are in flight together (float32: half as many)
 
-template <bool kF16>
+template <bool kF16, bool kSavedF32>
 __global__ void __launch_bounds__(256, 4) agmm_gated_grad(const __grid_constant__ GatedGradParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (col >= p.cols) return;
+  constexpr int kRows = kSavedF32 ? kUnroll / 2 : kUnroll;
   with_activation(p.act, [&](auto act) {
     const int64_t step = gridDim.y;
-    for (int64_t r = blockIdx.y; r < p.rows; r += step * kUnroll) {
-      uint4 d[kUnroll], g[kUnroll], u[kUnroll];
+    for (int64_t r = blockIdx.y; r < p.rows; r += step * kRows) {
+      uint4 d[kRows];
+      Saved<kSavedF32> g[kRows], u[kRows];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const int64_t row = r + i * step;
         if (row < p.rows) {
-          // plain loads: d_gate and d_up may lie over gate and up
           d[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + col);
-          g[i] = *reinterpret_cast<const uint4*>(p.gate + row * p.ld_saved + col);
-          u[i] = *reinterpret_cast<const uint4*>(p.up + row * p.ld_saved + col);
+          g[i].load(p.gate, row * p.ld_saved + col);
+          u[i].load(p.up, row * p.ld_saved + col);
         }
       }
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const int64_t row = r + i * step;
         if (row < p.rows) {
           uint4 dg, du;
-          gated_grad_piece<kF16, act.value>(d[i], g[i], u[i], dg, du);
+          gated_grad_piece<kF16, act.value, kSavedF32>(d[i], g[i], u[i], dg, du);
           *reinterpret_cast<uint4*>(p.d_gate + row * p.ld_grad + col) = dg;
           *reinterpret_cast<uint4*>(p.d_up + row * p.ld_grad + col) = du;
         }
@@ -72,28 +100,30 @@ __global__ void __launch_bounds__(256, 4) agmm_gated_grad(const __grid_constant_
 }
 
 // Rows first, first + step, ... of 8 columns, and their sums.
-template <bool kF16>
+template <bool kF16, bool kSavedF32>
 __device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t col, int64_t first, int64_t step, Two (&sum)[4]) {
+  constexpr int kRows = kSavedF32 ? kActUnroll / 2 : kActUnroll;
   with_activation(p.act, [&](auto act) {
-    for (int64_t r = first; r < p.rows; r += step * kActUnroll) {
-      uint4 d[kActUnroll], z[kActUnroll];
+    for (int64_t r = first; r < p.rows; r += step * kRows) {
+      uint4 d[kRows];
+      Saved<kSavedF32> z[kRows];
 #pragma unroll
-      for (int i = 0; i < kActUnroll; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const int64_t row = r + i * step;
         if (row < p.rows) {
           d[i] = *reinterpret_cast<const uint4*>(p.d_out + row * p.ld_out + col);
-          if constexpr (act.value != kActNone) z[i] = *reinterpret_cast<const uint4*>(p.pre + row * p.ld_pre + col);
+          if constexpr (act.value != kActNone) z[i].load(p.pre, row * p.ld_pre + col);
         }
       }
 #pragma unroll
-      for (int i = 0; i < kActUnroll; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const int64_t row = r + i * step;
         if (row < p.rows) {
           Two dv[4];
           widen<kF16>(d[i], dv);
           if constexpr (act.value != kActNone) {
             Two zv[4];
-            widen<kF16>(z[i], zv);
+            z[i].template values<kF16>(zv);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               Two a, slope;
@@ -110,14 +140,14 @@ __device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t co
   });
 }
 
-template <bool kF16>
+template <bool kF16, bool kSavedF32>
 __global__ void __launch_bounds__(256, 4) agmm_act_grad(const __grid_constant__ ActGradParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (col >= p.cols) return;
   Two sum[4] = {0, 0, 0, 0};
-  act_grad_rows<kF16>(p, col, blockIdx.y, gridDim.y, sum);
+  act_grad_rows<kF16, kSavedF32>(p, col, blockIdx.y, gridDim.y, sum);
   if (p.part) {
     ulonglong2* const dst = reinterpret_cast<ulonglong2*>(p.part + (int64_t)blockIdx.y * p.cols + col);
     dst[0] = make_ulonglong2(sum[0], sum[1]);
@@ -130,7 +160,7 @@ __global__ void __launch_bounds__(256, 4) agmm_act_grad(const __grid_constant__ 
 constexpr int kFewWarps = 16, kFewPieces = 8, kFewCols = kFewPieces * 8, kFewRowsAWarp = 32 / kFewPieces;
 static_assert(kFewWarps * 32 >= kFewCols, "a thread for each column's sum");
 
-template <bool kF16>
+template <bool kF16, bool kSavedF32>
 __global__ void __launch_bounds__(kFewWarps * 32) agmm_act_grad_few(const __grid_constant__ ActGradParams p) {
   __shared__ __align__(16) float s[kFewWarps][kFewCols];
   ptx::griddep_launch_dependents();
@@ -138,7 +168,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) agmm_act_grad_few(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, piece = lane % kFewPieces;
   const int64_t col = ((int64_t)blockIdx.x * kFewPieces + piece) * 8;
   Two sum[4] = {0, 0, 0, 0};
-  if (col < p.cols) act_grad_rows<kF16>(p, col, warp * kFewRowsAWarp + lane / kFewPieces, kFewWarps * kFewRowsAWarp, sum);
+  if (col < p.cols) act_grad_rows<kF16, kSavedF32>(p, col, warp * kFewRowsAWarp + lane / kFewPieces, kFewWarps * kFewRowsAWarp, sum);
 #pragma unroll
   for (int o = kFewPieces; o < 32; o *= 2)
 #pragma unroll
@@ -217,7 +247,8 @@ cudaError_t launch_gated_grad(const GatedGradParams& p, bool f16, int sms, cudaS
   if (y > most) y = most;
   if (y > 65535) y = 65535;
   const dim3 grid((unsigned)x, (unsigned)y);
-  return launch(f16 ? &agmm_gated_grad<true> : &agmm_gated_grad<false>, p, grid, threads, stream);
+  if (p.saved_f32) return launch(f16 ? &agmm_gated_grad<true, true> : &agmm_gated_grad<false, true>, p, grid, threads, stream);
+  return launch(f16 ? &agmm_gated_grad<true, false> : &agmm_gated_grad<false, false>, p, grid, threads, stream);
 }
 
 int act_grad_row_blocks(int64_t rows, int64_t cols, int sms) {
@@ -234,12 +265,14 @@ int act_grad_row_blocks(int64_t rows, int64_t cols, int sms) {
 cudaError_t launch_act_grad(const ActGradParams& p, bool f16, cudaStream_t stream) {
   if (p.d_bias) {
     const dim3 few((unsigned)((p.cols + kFewCols - 1) / kFewCols));
-    return launch(f16 ? &agmm_act_grad_few<true> : &agmm_act_grad_few<false>, p, few, kFewWarps * 32, stream);
+    if (p.saved_f32) return launch(f16 ? &agmm_act_grad_few<true, true> : &agmm_act_grad_few<false, true>, p, few, kFewWarps * 32, stream);
+    return launch(f16 ? &agmm_act_grad_few<true, false> : &agmm_act_grad_few<false, false>, p, few, kFewWarps * 32, stream);
   }
   const int64_t pieces = p.cols / 8;
   const int threads = threads_for(pieces);
   const dim3 grid((unsigned)((pieces + threads - 1) / threads), (unsigned)p.row_blocks);
-  return launch(f16 ? &agmm_act_grad<true> : &agmm_act_grad<false>, p, grid, threads, stream);
+  if (p.saved_f32) return launch(f16 ? &agmm_act_grad<true, true> : &agmm_act_grad<false, true>, p, grid, threads, stream);
+  return launch(f16 ? &agmm_act_grad<true, false> : &agmm_act_grad<false, false>, p, grid, threads, stream);
 }
 
 cudaError_t launch_sum_parts(const SumPartsParams& p, bool f16, cudaStream_t stream) {

@@ -3,6 +3,9 @@
 
 namespace agmm {
 namespace ff {
-GemmFn swap_gated(bool f16) { return f16 ? &agmm_ff_gemm<0, kEpiGated, true> : &agmm_ff_gemm<0, kEpiGated, false>; }
+GemmFn swap_gated(bool f16, bool save_f32) {
+  if (save_f32) return f16 ? &agmm_ff_gemm<0, kEpiGated, true, false, true> : &agmm_ff_gemm<0, kEpiGated, false, false, true>;
+  return f16 ? &agmm_ff_gemm<0, kEpiGated, true> : &agmm_ff_gemm<0, kEpiGated, false>;
+}
 }  // namespace ff
 }  // namespace agmm

@@ -3,6 +3,9 @@
 
 namespace agmm {
 namespace ff {
-GemmFn swap_linear(bool f16) { return f16 ? &agmm_ff_gemm<0, kEpiLinear, true> : &agmm_ff_gemm<0, kEpiLinear, false>; }
+GemmFn swap_linear(bool f16, bool save_f32) {
+  if (save_f32) return f16 ? &agmm_ff_gemm<0, kEpiLinear, true, false, true> : &agmm_ff_gemm<0, kEpiLinear, false, false, true>;
+  return f16 ? &agmm_ff_gemm<0, kEpiLinear, true> : &agmm_ff_gemm<0, kEpiLinear, false>;
+}
 }  // namespace ff
 }  // namespace agmm

@@ -30,6 +30,7 @@ from .attention import _AttentionPlan, _cached, _is_f16
 
 FEEDFORWARD_SYMBOLS = [f"agmm_{op}_{f}" for op in ("layer_norm", "gated", "linear")
                        for f in ("plan", "workspace_bytes", "run", "backward", "destroy")]
+FEEDFORWARD_SYMBOLS += ["agmm_gated_save_float", "agmm_linear_save_float"]
 MAX_SHARDS = 8
 HEAD_BYTES = 65536  # of a workspace: zero before its first use
 ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -67,6 +68,9 @@ def _library():
         for call in ("run", "backward"):
             f = getattr(lib, f"agmm_{name}_{call}")
             f.argtypes, f.restype = [vp, ctypes.c_char_p, vp], c_int
+        if name != "layer_norm":
+            f = getattr(lib, f"agmm_{name}_save_float")
+            f.argtypes, f.restype = [vp, c_int], c_int
         f = getattr(lib, f"agmm_{name}_workspace_bytes")
         f.argtypes, f.restype = [vp], ctypes.c_size_t
         f = getattr(lib, f"agmm_{name}_destroy")
@@ -215,12 +219,16 @@ class LayerNormPlan(_FeedForwardPlan):
 
 
 class _ProductPlan(_FeedForwardPlan):
-    def __init__(self, k: int, n: int, activation: Optional[str], rhs_transpose: bool, f16: bool):
+    def __init__(self, k: int, n: int, activation: Optional[str], rhs_transpose: bool, f16: bool, f32_saved: bool):
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
         self.k, self.n, self.activation, self.rhs_transpose = _width("k", k), _width("n", n), activation, bool(rhs_transpose)
         self._weight_shape = (self.n, self.k) if self.rhs_transpose else (self.k, self.n)
         self._open(_ProductDesc(self.k, self.n, ACTIVATIONS[activation], int(self.rhs_transpose), AGMM_F16 if f16 else AGMM_BF16), f16)
+        self.f32_saved = bool(f32_saved)
+        self._saved = self._float32 if self.f32_saved else self.dtype  # the type of what the forward pass saves
+        if self.f32_saved:
+            _check(getattr(self._lib, f"agmm_{self._name}_save_float")(self._h, 1))
 
     def _shards(self, xs):
         """(shards, rows, 8 pointers, row stride) of X."""
@@ -241,12 +249,14 @@ class _ProductPlan(_FeedForwardPlan):
 class GatedPlan(_ProductPlan):
     """The gated product act(X Wgate) * (X Wup) in one kernel, and its backward
     pass (agmm_gated_run, _backward).  Weights [k, n], or [n, k] with
-    rhs_transpose; activation: "silu", "gelu", "gelu_tanh" or "relu"."""
+    rhs_transpose; activation: "silu", "gelu", "gelu_tanh" or "relu".  f32_saved:
+    gate and up are float32, for gradients without their rounding."""
 
     _name = "gated"
 
-    def __init__(self, k: int, n: int, activation: str = "silu", rhs_transpose: bool = False, f16: bool = False):
-        super().__init__(k, n, activation, rhs_transpose, f16)
+    def __init__(self, k: int, n: int, activation: str = "silu", rhs_transpose: bool = False, f16: bool = False,
+                 f32_saved: bool = False):
+        super().__init__(k, n, activation, rhs_transpose, f16, f32_saved)
 
     def run(self, xs, w_gate, w_up, out, workspace, gate=None, up=None, stream=None) -> None:
         """xs: [rows, k], or up to 8 such shards; out [tokens, n].  gate and up
@@ -260,7 +270,7 @@ class GatedPlan(_ProductPlan):
         if gate is not None or up is not None:
             if gate is None or up is None:
                 raise ValueError("gate and up are given together or not at all")
-            g, u, s_s = self._pair(("gate", "up"), (gate, up), tokens, self.n)
+            g, u, s_s = self._pair(("gate", "up"), (gate, up), tokens, self.n, self._saved)
         args = _GATED_ARGS.pack(shards, rows, *xp, x_s, wg, wu, w_s, o_ptr, o_s, g, u, s_s, self._workspace(workspace))
         self._call(self._run, args, stream)
 
@@ -268,13 +278,13 @@ class GatedPlan(_ProductPlan):
                  stream=None) -> None:
         """d_out [tokens, n]; xs and the weights as the forward pass had them, gate
         and up as it wrote them.  d_gate and d_up [tokens, n]: written on the way
-        (they may be gate and up).  Outputs: dx [tokens, k], and dw_gate and dw_up
+        (they may be gate and up, unless those are float32).  Outputs: dx [tokens, k], and dw_gate and dw_up
         like the weights, of the plan's type or float32; what is None is not computed."""
         shards, rows, xp, x_s = self._shards(xs)
         tokens = shards * rows
         wg, wu, w_s = self._pair(("w_gate", "w_up"), (w_gate, w_up), *self._weight_shape)
         o_ptr, o_s = self._matrix("d_out", d_out, tokens, self.n)
-        g, u, s_s = self._pair(("gate", "up"), (gate, up), tokens, self.n)
+        g, u, s_s = self._pair(("gate", "up"), (gate, up), tokens, self.n, self._saved)
         dg, du, d_s = self._pair(("d_gate", "d_up"), (d_gate, d_up), tokens, self.n)
         dx_ptr, dx_s = (0, 0) if dx is None else self._matrix("dx", dx, tokens, self.k)
         grads = self._grad_type(dw_gate, dw_up)
@@ -291,12 +301,14 @@ class GatedPlan(_ProductPlan):
 class LinearPlan(_ProductPlan):
     """The product act(X W + bias) + residual in one kernel, and its backward pass
     (agmm_linear_run, _backward).  The weight [k, n], or [n, k] with rhs_transpose;
-    activation: None, "silu", "gelu", "gelu_tanh" or "relu"."""
+    activation: None, "silu", "gelu", "gelu_tanh" or "relu".  f32_saved: pre is
+    float32, for gradients without its rounding."""
 
     _name = "linear"
 
-    def __init__(self, k: int, n: int, activation: Optional[str] = None, rhs_transpose: bool = False, f16: bool = False):
-        super().__init__(k, n, activation, rhs_transpose, f16)
+    def __init__(self, k: int, n: int, activation: Optional[str] = None, rhs_transpose: bool = False, f16: bool = False,
+                 f32_saved: bool = False):
+        super().__init__(k, n, activation, rhs_transpose, f16, f32_saved)
 
     def run(self, xs, w, out, workspace, bias=None, residual=None, pre=None, stream=None) -> None:
         """xs: [rows, k], or up to 8 such shards; bias [n]; residual and out
@@ -307,7 +319,7 @@ class LinearPlan(_ProductPlan):
         w_ptr, w_s = self._matrix("w", w, *self._weight_shape)
         r_ptr, r_s = (0, 0) if residual is None else self._matrix("residual", residual, tokens, self.n)
         o_ptr, o_s = self._matrix("out", out, tokens, self.n)
-        p_ptr, p_s = (0, 0) if pre is None else self._matrix("pre", pre, tokens, self.n)
+        p_ptr, p_s = (0, 0) if pre is None else self._matrix("pre", pre, tokens, self.n, self._saved)
         args = _LINEAR_ARGS.pack(shards, rows, *xp, x_s, w_ptr, w_s, self._values("bias", bias, self.n), r_ptr, r_s, o_ptr, o_s, p_ptr,
                                  p_s, self._workspace(workspace))
         self._call(self._run, args, stream)
@@ -315,14 +327,14 @@ class LinearPlan(_ProductPlan):
     def backward(self, d_out, xs, w, workspace, pre=None, d_pre=None, dx=None, dw=None, d_bias=None, stream=None) -> None:
         """d_out [tokens, n]; xs and w as the forward pass had them.  With an
         activation: pre as the forward pass wrote it, and d_pre [tokens, n],
-        written on the way (it may be pre or d_out).  Outputs: dx [tokens, k], dw
+        written on the way (it may be d_out, or pre unless that is float32).  Outputs: dx [tokens, k], dw
         like the weight and d_bias [n], these two of the plan's type or both float32;
         what is None is not computed.  The residual's gradient is d_out."""
         shards, rows, xp, x_s = self._shards(xs)
         tokens = shards * rows
         w_ptr, w_s = self._matrix("w", w, *self._weight_shape)
         o_ptr, o_s = self._matrix("d_out", d_out, tokens, self.n)
-        p_ptr, p_s = (0, 0) if pre is None else self._matrix("pre", pre, tokens, self.n)
+        p_ptr, p_s = (0, 0) if pre is None else self._matrix("pre", pre, tokens, self.n, self._saved)
         d_ptr, d_s = (0, 0) if d_pre is None else self._matrix("d_pre", d_pre, tokens, self.n)
         dx_ptr, dx_s = (0, 0) if dx is None else self._matrix("dx", dx, tokens, self.k)
         grads = self._grad_type(dw, d_bias)
@@ -421,15 +433,19 @@ def _product_sizes(xs, w, rhs_transpose):
     return xs, k, n
 
 
+def _product_plan(cls, k, n, activation, rhs_transpose, x, f32_saved):
+    return _cached(cls, k, n, activation=activation, rhs_transpose=bool(rhs_transpose), f16=_is_f16(x), f32_saved=bool(f32_saved))
+
+
 def gated_matmul(xs, w_gate, w_up, activation: str = "silu", rhs_transpose: bool = False, return_saved: bool = False, out=None,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, f32_saved: bool = False):
     """act(X Wgate) * (X Wup) of X [tokens, k] or the shards of a gathered X;
     returns [tokens, n], with return_saved (out, gate, up) as the backward pass
-    reads them (GatedPlan)."""
+    reads them (GatedPlan), gate and up in float32 with f32_saved."""
     import torch
 
     xs, k, n = _product_sizes(xs, w_gate, rhs_transpose)
-    plan = _cached(GatedPlan, k, n, activation=activation, rhs_transpose=bool(rhs_transpose), f16=_is_f16(xs[0]))
+    plan = _product_plan(GatedPlan, k, n, activation, rhs_transpose, xs[0], f32_saved)
     tokens = len(xs) * xs[0].shape[0]
     gate = up = None
     with _On(stream):
@@ -437,7 +453,7 @@ def gated_matmul(xs, w_gate, w_up, activation: str = "silu", rhs_transpose: bool
         if out is None:
             out = torch.empty((tokens, n), dtype=xs[0].dtype, device=xs[0].device)
         if return_saved:
-            gate, up = (torch.empty((tokens, n), dtype=xs[0].dtype, device=xs[0].device) for _ in range(2))
+            gate, up = (torch.empty((tokens, n), dtype=plan._saved, device=xs[0].device) for _ in range(2))
         if workspace is None:
             workspace = plan.new_workspace()
     plan.run(xs, w_gate, w_up, out, workspace, gate=gate, up=up, stream=stream)
@@ -446,11 +462,11 @@ def gated_matmul(xs, w_gate, w_up, activation: str = "silu", rhs_transpose: bool
 
 def gated_matmul_backward(d_out, xs, w_gate, w_up, gate, up, activation: str = "silu", rhs_transpose: bool = False,
                           f32_grads: bool = False, workspace=None, stream=None):
-    """(dx, dw_gate, dw_up) of gated_matmul."""
+    """(dx, dw_gate, dw_up) of gated_matmul; gate and up as it saved them, in either type."""
     import torch
 
     xs, k, n = _product_sizes(xs, w_gate, rhs_transpose)
-    plan = _cached(GatedPlan, k, n, activation=activation, rhs_transpose=bool(rhs_transpose), f16=_is_f16(xs[0]))
+    plan = _product_plan(GatedPlan, k, n, activation, rhs_transpose, xs[0], gate.dtype is torch.float32)
     tokens = len(xs) * xs[0].shape[0]
     with _On(stream):
         xs, (w_gate, w_up), (gate, up) = _shard_rows(xs), _pair_rows(w_gate, w_up), _pair_rows(gate, up)
@@ -466,14 +482,15 @@ def gated_matmul_backward(d_out, xs, w_gate, w_up, gate, up, activation: str = "
 
 
 def linear_matmul(xs, w, bias=None, residual=None, activation: Optional[str] = None, rhs_transpose: bool = False,
-                  return_saved: bool = False, out=None, workspace=None, stream=None):
+                  return_saved: bool = False, out=None, workspace=None, stream=None, f32_saved: bool = False):
     """act(X W + bias) + residual of X [tokens, k] or the shards of a gathered X;
     returns [tokens, n], with return_saved (out, pre) as the backward pass reads it
-    (LinearPlan; without an activation pre is None: it reads nothing)."""
+    (LinearPlan; without an activation pre is None: it reads nothing), pre in float32
+    with f32_saved."""
     import torch
 
     xs, k, n = _product_sizes(xs, w, rhs_transpose)
-    plan = _cached(LinearPlan, k, n, activation=activation, rhs_transpose=bool(rhs_transpose), f16=_is_f16(xs[0]))
+    plan = _product_plan(LinearPlan, k, n, activation, rhs_transpose, xs[0], f32_saved)
     tokens = len(xs) * xs[0].shape[0]
     pre = None
     with _On(stream):
@@ -481,7 +498,7 @@ def linear_matmul(xs, w, bias=None, residual=None, activation: Optional[str] = N
         if out is None:
             out = torch.empty((tokens, n), dtype=xs[0].dtype, device=xs[0].device)
         if return_saved and activation is not None:
-            pre = torch.empty((tokens, n), dtype=xs[0].dtype, device=xs[0].device)
+            pre = torch.empty((tokens, n), dtype=plan._saved, device=xs[0].device)
         if workspace is None:
             workspace = plan.new_workspace()
     plan.run(xs, w, out, workspace, bias=bias, residual=residual, pre=pre, stream=stream)
@@ -490,11 +507,12 @@ def linear_matmul(xs, w, bias=None, residual=None, activation: Optional[str] = N
 
 def linear_matmul_backward(d_out, xs, w, pre=None, activation: Optional[str] = None, rhs_transpose: bool = False,
                            f32_grads: bool = False, workspace=None, stream=None):
-    """(dx, dw, d_bias) of linear_matmul; the residual's gradient is d_out."""
+    """(dx, dw, d_bias) of linear_matmul, pre as it saved it, in either type; the
+    residual's gradient is d_out."""
     import torch
 
     xs, k, n = _product_sizes(xs, w, rhs_transpose)
-    plan = _cached(LinearPlan, k, n, activation=activation, rhs_transpose=bool(rhs_transpose), f16=_is_f16(xs[0]))
+    plan = _product_plan(LinearPlan, k, n, activation, rhs_transpose, xs[0], pre is not None and pre.dtype is torch.float32)
     tokens = len(xs) * xs[0].shape[0]
     d_pre = None
     with _On(stream):

@@ -6,7 +6,8 @@
  * Types: every matrix is bf16 (AGMM_BF16) or fp16 (AGMM_F16), fixed by the
  * plan; sums, statistics and activations are held in float32 and rounded once,
  * to the nearest, at the output.  Two more roundings to that type are part of
- * the backward passes: of what the forward pass saves (gate, up, pre), and of
+ * the backward passes: of what the forward pass saves (gate, up, pre), unless the
+ * plan has it in float32 (agmm_gated_save_float, agmm_linear_save_float), and of
  * the gradients that the tensor cores multiply (d_gate, d_up, d_pre).  An fp16
  * value past 65504 is infinite there, as in any output.
  *
@@ -152,7 +153,8 @@ typedef struct {
   const void* up;
   int64_t saved_stride;
   void* d_gate;            /* out, [shards * rows, n]; may be gate  */
-  void* d_up;              /* and up, or one of them d_out          */
+  void* d_up;              /* and up (unless those are float32), or */
+                           /* one of them d_out                     */
   int64_t d_stride;
   void* dx;                /* [shards * rows, k] or NULL            */
   int64_t dx_stride;
@@ -166,6 +168,9 @@ typedef struct {
 typedef struct agmm_gated_s* agmm_gated_t;
 
 agmm_status_t agmm_gated_plan(const agmm_gated_desc_t* desc, agmm_gated_t* out_plan);
+/* gate and up of the plan's runs and backward passes are float32 (1), or of its
+ * type (0, as a new plan has it).  Before the plan is used. */
+agmm_status_t agmm_gated_save_float(agmm_gated_t plan, int on);
 size_t agmm_gated_workspace_bytes(agmm_gated_t plan);
 agmm_status_t agmm_gated_run(agmm_gated_t plan, const agmm_gated_args_t* args, void* stream);
 agmm_status_t agmm_gated_backward(agmm_gated_t plan, const agmm_gated_grad_args_t* args, void* stream);
@@ -213,7 +218,7 @@ typedef struct {
   const void* pre;         /* with an activation: as the forward pass wrote it */
   int64_t pre_stride;
   void* d_pre;             /* with an activation: out, [shards * rows, n]; may */
-  int64_t d_pre_stride;    /* be pre or d_out                       */
+  int64_t d_pre_stride;    /* be pre (unless that is float32) or d_out         */
   void* dx;                /* [shards * rows, k] or NULL            */
   int64_t dx_stride;
   void* dw;                /* like the weight, or NULL              */
@@ -226,6 +231,9 @@ typedef struct {
 typedef struct agmm_linear_s* agmm_linear_t;
 
 agmm_status_t agmm_linear_plan(const agmm_linear_desc_t* desc, agmm_linear_t* out_plan);
+/* pre of the plan's runs and backward passes is float32 (1), or of its type (0,
+ * as a new plan has it).  Before the plan is used. */
+agmm_status_t agmm_linear_save_float(agmm_linear_t plan, int on);
 size_t agmm_linear_workspace_bytes(agmm_linear_t plan);
 agmm_status_t agmm_linear_run(agmm_linear_t plan, const agmm_linear_args_t* args, void* stream);
 agmm_status_t agmm_linear_backward(agmm_linear_t plan, const agmm_linear_grad_args_t* args, void* stream);
