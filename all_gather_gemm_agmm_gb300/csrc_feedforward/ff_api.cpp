@@ -924,6 +924,8 @@ agmm_status_t agmm_gated_backward(agmm_gated_t pl, const agmm_gated_grad_args_t*
   AGMM_TRY(check_matrix("up", a->up, &saved_stride, tokens, pl->n));
   AGMM_TRY(check_matrix("d_gate", a->d_gate, &d_stride, tokens, pl->n));
   AGMM_TRY(check_matrix("d_up", a->d_up, &d_stride, tokens, pl->n));
+  if (pl->saved_f32 && (a->d_gate == a->gate || a->d_gate == a->up || a->d_up == a->gate || a->d_up == a->up))
+    return fail(AGMM_ERR_INVALID_ARG, "d_gate and d_up cannot lie over gate and up that are float32");
   if (a->dx) {
     AGMM_TRY(check_matrix("w_gate", a->w_gate, &w_stride, w_rows, w_cols));
     AGMM_TRY(check_matrix("w_up", a->w_up, &w_stride, w_rows, w_cols));
@@ -1016,6 +1018,7 @@ agmm_status_t agmm_linear_backward(agmm_linear_t pl, const agmm_linear_grad_args
   if (acts) {
     AGMM_TRY(check_matrix("pre", a->pre, &pre_stride, tokens, pl->n));
     AGMM_TRY(check_matrix("d_pre", a->d_pre, &d_stride, tokens, pl->n));
+    if (pl->saved_f32 && a->d_pre == a->pre) return fail(AGMM_ERR_INVALID_ARG, "d_pre cannot lie over a pre that is float32");
   } else if (a->pre || a->d_pre) {
     return fail(AGMM_ERR_INVALID_ARG, "pre and d_pre belong to an activation, and the plan has none");
   }

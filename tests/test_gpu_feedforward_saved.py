@@ -209,6 +209,15 @@ def test_refusals(agmm):
             plan.backward(d, x, w, ws, pre=wrong, d_pre=wide)
         with pytest.raises(ValueError, match="d_pre"):
             plan.backward(d, x, w, ws, pre=right, d_pre=f32)
+    over = torch.ones(t, 2 * n, dtype=torch.bfloat16, device="cuda")[:, :n]  # float32 rows of n, seen as 16-bit ones
+    f32 = over.as_strided((t, 2 * n), (2 * n, 1)).view(F32)
+    with pytest.raises(agmm.AgmmError, match="float32"):
+        agmm.LinearPlan(k, n, activation="relu", f32_saved=True).backward(d, x, w, ws, pre=f32, d_pre=over)
+    gated = agmm.GatedPlan(k, n, f32_saved=True)
+    for grads in ((over, wide), (wide, over)):
+        with pytest.raises(agmm.AgmmError, match="float32"):
+            plain = [torch.empty_like(over.as_strided((t, 2 * n), (2 * n, 1)))[:, :n] if y is wide else y for y in grads]
+            gated.backward(d, x, w, w, f32, f32.clone(), *plain, ws)
     plan = agmm.LinearPlan(k, n)
     with pytest.raises(agmm.AgmmError, match="none"):
         plan.backward(d, x, w, ws, pre=wide)
